@@ -29,6 +29,8 @@ __all__ = [
     "IndexerRow", "ds_rows_indexer_topk_workspace_bytes", "indexer_topk_workspace", "ds_rows_indexer_topk",
     "ds_rows_indexer_topk_queries_workspace_bytes", "ds_rows_indexer_topk_queries",
     "CompressorRow", "ds_rows_compress_kv",
+    "Rope", "ds_rows_rope", "PagedCache", "ds_rows_page_bytes", "ds_rows_append", "ds_rows_indexer_score_paged",
+    "ds_rows_sparse_attn_paged",
     "STATUS_WAIT_TIMEOUT", "STATUS_OVERFLOW", "workspace_status", "ds_rows_selftest_bounded_wait",
     "ROWS_MAX", "INDEX_HEADS", "INDEX_DIM", "TOP_K", "HEADS", "DIM",
 ]
@@ -132,6 +134,7 @@ def load():
     lib.ds_rows_compress_kv.argtypes = [i32, ctypes.POINTER(CompressorRow), vp, vp, vp, vp, ctypes.c_uint32,
                                          ctypes.c_uint32, ctypes.c_float, vp, vp]
     lib.ds_rows_compress_kv.restype = i32
+    _paged.declare(lib)
     lib.ds_rows_selftest_bounded_wait.argtypes = [vp, vp, ctypes.c_uint64, vp]
     lib.ds_rows_selftest_bounded_wait.restype = i32
     lib.ds_rows_last_error.argtypes = []
@@ -244,6 +247,13 @@ def workspace(rows, device=None) -> torch.Tensor:
     """A workspace tensor (uint8, 256-byte aligned by the caching allocator)."""
     return torch.empty(ds_rows_workspace_bytes(rows), dtype=torch.uint8,
                        device=device if device is not None else "cuda")
+
+
+def _workspace_for(rows, device, raw_stream: int) -> torch.Tensor:
+    """A workspace for one call on the stream `raw_stream`, taken from that stream's
+    memory, so that it is not handed out again while the call still runs."""
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw_stream, device=device)):
+        return workspace(rows, device)
 
 
 def workspace_status(workspace_t: torch.Tensor) -> int:
@@ -537,3 +547,12 @@ def ds_rows_compress_kv(kv_states, score_states, start_pos, kv, score, ape, norm
         tab[e] = CompressorRow(kv_states[e].data_ptr(), score_states[e].data_ptr(), int(start_pos[e]))
     _check(lib, lib.ds_rows_compress_kv(n, tab, _ptr(kv), _ptr(score), _ptr(ape), _ptr(norm), int(ratio),
                                         int(head_dim), float(epsilon), _ptr(out), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# positions and paged caches
+# ---------------------------------------------------------------------------
+
+from . import paged as _paged  # noqa: E402  (uses the names above)
+from .paged import (PagedCache, Rope, ds_rows_append, ds_rows_indexer_score_paged, ds_rows_page_bytes,  # noqa: E402
+                    ds_rows_rope, ds_rows_sparse_attn_paged)

@@ -8,8 +8,7 @@
 // and alignment. Everything is checked before anything is enqueued.
 
 #include <cudaTypedefs.h>
-#include <nvtx3/nvToolsExt.h>
-
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -17,6 +16,7 @@
 #include <string>
 
 #include "common.cuh"
+#include "host.h"
 #include "kernels.h"
 
 using namespace dsrows;
@@ -24,6 +24,10 @@ using namespace dsrows;
 namespace {
 
 thread_local std::string g_error;
+
+}  // namespace
+
+namespace dsrows {
 
 int fail(int code, const char* fmt, ...) {
     char buf[512];
@@ -39,18 +43,23 @@ int cuda_fail(cudaError_t err, const char* what) {
     return fail(DS_ECUDA, "%s failed: %s", what, cudaGetErrorString(err));
 }
 
+int num_sms() {
+    static std::atomic<int> cache[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+}  // namespace dsrows
+
+namespace {
+
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-// An NVTX range over the host-side enqueue of one stage ("dsrows.<stage>"), so
-// a profiler can attribute each launch to its stage; free without a tool.
-struct StageRange {
-    explicit StageRange(const char* name) { nvtxRangePushA(name); }
-    ~StageRange() { nvtxRangePop(); }
-    StageRange(const StageRange&) = delete;
-    StageRange& operator=(const StageRange&) = delete;
-};
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // ---- workspace layout ------------------------------------------------------
 struct Layout {
@@ -87,18 +96,6 @@ Layout make_layout(int rows, const ds_row_t* table, bool attention = true) {
 // ---- device facts and the tensor-map encoder --------------------------------
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
-
-int num_sms() {
-    static std::atomic<int> cache[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    int n = cache[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        cache[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
 
 int get_encoder() {
     std::call_once(g_encode_once, [] {
@@ -413,15 +410,11 @@ int run_topk(const ds_row_set_t* set, const float* scores, uint64_t stride, int3
     return err == cudaSuccess ? DS_OK : cuda_fail(err, "top-k select launch");
 }
 
-// Selection (decode: `given` null) or the caller's indices (`given`), then the
-// attention: one 8-CTA cluster per row.
-int run_tail(const ds_row_set_t* set, const ds_bf16* q_attn, const float* sinks, size_t sinks_row_stride,
-             float scale, ds_bf16* out, uint32_t* invalid, const float* scores, uint64_t score_stride,
-             const int32_t* given, int32_t* indices, uint8_t* ws, const Layout& L, cudaStream_t stream,
-             bool q_after_wait = false, bool attend = true, const int32_t* offsets = nullptr) {
-    StageRange range(attend ? (given ? "dsrows.attention" : "dsrows.select+attention") : "dsrows.select");
-    TailParams tp;
-    std::memset(&tp, 0, sizeof(tp));
+// The tail kernel's table (`tp` zeroed by the caller).
+void fill_tail(TailParams& tp, const ds_row_set_t* set, const ds_bf16* q_attn, const float* sinks,
+               size_t sinks_row_stride, float scale, ds_bf16* out, uint32_t* invalid, const float* scores,
+               uint64_t score_stride, const int32_t* given, int32_t* indices, uint8_t* ws, const Layout& L,
+               bool q_after_wait, bool attend, const int32_t* offsets) {
     uint32_t chunks = 0;
     for (int e = 0; e < set->rows; ++e) {
         const ds_row_t& r = set->table[e];
@@ -456,6 +449,19 @@ int run_tail(const ds_row_set_t* set, const ds_bf16* q_attn, const float* sinks,
     tp.indices = indices;
     tp.scale = scale;
     tp.rows = (uint32_t)set->rows;
+}
+
+// Selection (decode: `given` null) or the caller's indices (`given`), then the
+// attention: one 8-CTA cluster per row.
+int run_tail(const ds_row_set_t* set, const ds_bf16* q_attn, const float* sinks, size_t sinks_row_stride,
+             float scale, ds_bf16* out, uint32_t* invalid, const float* scores, uint64_t score_stride,
+             const int32_t* given, int32_t* indices, uint8_t* ws, const Layout& L, cudaStream_t stream,
+             bool q_after_wait = false, bool attend = true, const int32_t* offsets = nullptr) {
+    StageRange range(attend ? (given ? "dsrows.attention" : "dsrows.select+attention") : "dsrows.select");
+    TailParams tp;
+    std::memset(&tp, 0, sizeof(tp));
+    fill_tail(tp, set, q_attn, sinks, sinks_row_stride, scale, out, invalid, scores, score_stride, given, indices, ws,
+              L, q_after_wait, attend, offsets);
     cudaError_t err = launch_decode_tail(tp, stream, true);
     return err == cudaSuccess ? DS_OK : cuda_fail(err, given ? "attention launch" : "decode select + attention launch");
 }
@@ -590,6 +596,93 @@ int copy_async(void* dst, const void* src, size_t bytes, cudaMemcpyKind kind, cu
 }
 
 }  // namespace
+
+namespace {
+
+PagedCache paged_cache(const ds_paged_cache_t& c) {
+    PagedCache p;
+    p.pages = static_cast<uint8_t*>(c.pages);
+    p.table = c.page_table;
+    p.table_stride = c.table_stride;
+    p.entries = c.entries;
+    p.page_shift = (uint32_t)__builtin_ctz(c.page_size);
+    p.num_pages = c.num_pages;
+    p.row_bytes = page_row_bytes(c.dim, c.format);
+    return p;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+// With at most 2^31 rows, element offsets stay below 2^64.
+constexpr uint64_t kMaxStride = (uint64_t)1 << 31;
+
+// An element type and the pointers to its elements; `elem` receives its bytes.
+int check_elements(int dtype, const void* x, const void* out, size_t& elem) {
+    if (dtype != DS_BF16 && dtype != DS_F16 && dtype != DS_F32)
+        return fail(DS_EINVAL, "dtype must be DS_BF16, DS_F16 or DS_F32, got %d", dtype);
+    elem = dtype == DS_F32 ? 4 : 2;
+    if (!x || !out) return fail(DS_EINVAL, "x and out must be non-NULL");
+    if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out)) & (elem - 1))
+        return fail(DS_EALIGN, "x and out must be aligned to their element type");
+    return DS_OK;
+}
+
+int check_rope(const ds_rope_t* r, uint32_t dim, const int32_t* positions) {
+    if (!r || !r->turns) return fail(DS_EINVAL, "rope and its turns must be non-NULL");
+    if (reinterpret_cast<uintptr_t>(r->turns) & 7) return fail(DS_EALIGN, "turns must be 8-B aligned");
+    if (r->layout != DS_ROPE_INTERLEAVED && r->layout != DS_ROPE_HALF)
+        return fail(DS_EINVAL, "rope layout must be DS_ROPE_INTERLEAVED or DS_ROPE_HALF, got %d", r->layout);
+    if (r->rot_dim < 2 || r->rot_dim > DS_DIM || r->rot_dim % 2)
+        return fail(DS_EINVAL, "rot_dim must be even, 2..=%d, got %u", DS_DIM, r->rot_dim);
+    if ((uint64_t)r->first + r->rot_dim > dim)
+        return fail(DS_EINVAL, "rotated range [%u, %u + %u) exceeds the row's %u elements", r->first, r->first,
+                    r->rot_dim, dim);
+    if (r->layout == DS_ROPE_INTERLEAVED && r->first % 2)
+        return fail(DS_EINVAL, "an interleaved rotation starts at an even element, got %u", r->first);
+    if (!(r->magnitude > 0.0f) || !(r->magnitude < __builtin_huge_valf()))
+        return fail(DS_EINVAL, "rope magnitude must be finite and positive");
+    if (!positions) return fail(DS_EINVAL, "positions is NULL");
+    return DS_OK;
+}
+
+// A checked cache has a page id for every row of the table's entries.
+int check_reach(int rows, const ds_row_t* table, const ds_paged_cache_t* cache) {
+    for (int e = 0; e < rows; ++e) {
+        if (table[e].kv_len > 0x7FFFFFFFu)
+            return fail(DS_ESIZE, "row %d: kv_len %u of a paged cache must be below 2^31", e, table[e].kv_len);
+        if ((uint64_t)cache->table_stride * cache->page_size < table[e].kv_len)
+            return fail(DS_EINVAL, "row %d: kv_len %u exceeds the %u pages of %u rows of a page-table row", e,
+                        table[e].kv_len, cache->table_stride, cache->page_size);
+    }
+    return DS_OK;
+}
+
+}  // namespace
+
+namespace dsrows {
+
+uint32_t page_row_bytes(uint32_t dim, int format) {
+    return format == DS_CACHE_INT4 ? dim / 2 + dim / 16 : 2 * dim;
+}
+
+int check_cache(const ds_paged_cache_t* c, uint32_t dim, int rows) {
+    if (!c) return fail(DS_EINVAL, "paged cache is NULL");
+    if (c->dim != dim) return fail(DS_EINVAL, "paged cache rows must be %u wide, got %u", dim, c->dim);
+    if (!ds_rows_page_bytes(c->page_size, c->dim, c->format)) return DS_EINVAL;
+    if (!c->pages || !c->page_table) return fail(DS_EINVAL, "paged cache: pages and page_table must be non-NULL");
+    if (!aligned16(c->pages)) return fail(DS_EALIGN, "paged cache: pages not 16-B aligned");
+    if (reinterpret_cast<uintptr_t>(c->page_table) & 3)
+        return fail(DS_EALIGN, "paged cache: page_table not 4-B aligned");
+    if (c->entries == 0 || c->table_stride == 0 || c->num_pages == 0)
+        return fail(DS_EINVAL, "paged cache: entries, table_stride and num_pages must be nonzero");
+    if ((uint64_t)c->num_pages * c->page_size > 0x7FFFFFFFull)
+        return fail(DS_ESIZE, "paged cache: %u pages of %u rows exceed 2^31 rows", c->num_pages, c->page_size);
+    if (rows > 0 && (uint32_t)rows > c->entries)
+        return fail(DS_EINVAL, "paged cache has %u entries for %d rows", c->entries, rows);
+    return DS_OK;
+}
+
+}  // namespace dsrows
 
 extern "C" {
 
@@ -881,6 +974,218 @@ int ds_rows_indexer_topk(int rows, const ds_indexer_row_t* table, const ds_bf16*
                          size_t workspace_bytes, void* stream) {
     return ds_rows_indexer_topk_queries(rows, table, 1, index_keys, q_index, w_index, indices, workspace,
                                         workspace_bytes, stream);
+}
+
+size_t ds_rows_page_bytes(uint32_t page_size, uint32_t dim, int format) {
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) {
+        fail(DS_EINVAL, "page_size must be 16, 32, 64, 128 or 256, got %u", page_size);
+        return 0;
+    }
+    if (dim != DS_INDEX_DIM && dim != DS_DIM) {
+        fail(DS_EINVAL, "paged cache rows must be %d or %d wide, got %u", DS_INDEX_DIM, DS_DIM, dim);
+        return 0;
+    }
+    if (format != DS_CACHE_BF16 && format != DS_CACHE_INT4) {
+        fail(DS_EINVAL, "paged cache format must be DS_CACHE_BF16 or DS_CACHE_INT4, got %d", format);
+        return 0;
+    }
+    return (size_t)page_size * page_row_bytes(dim, format);
+}
+
+int ds_rows_append(const ds_paged_cache_t* cache, const void* x, uint64_t x_stride, int dtype, uint64_t tokens,
+                   const int32_t* seq, const int32_t* slot, const ds_rope_t* rope, const int32_t* positions,
+                   ds_bf16* values, uint32_t* invalid, void* stream) {
+    int rc = check_cache(cache, cache && cache->dim == DS_INDEX_DIM ? DS_INDEX_DIM : DS_DIM, 0);
+    if (rc) return rc;
+    const uint32_t dim = cache->dim;
+    size_t elem;
+    rc = check_elements(dtype, x, x, elem);
+    if (rc) return rc;
+    if (tokens > 0x7FFFFFFFull) return fail(DS_ESIZE, "tokens must be below 2^31, got %llu", (unsigned long long)tokens);
+    if (x_stride > kMaxStride) return fail(DS_ESIZE, "x_stride is out of range");
+    if (!seq || !slot) return fail(DS_EINVAL, "seq and slot must be non-NULL");
+    if (!aligned4(seq) || !aligned4(slot) || !aligned4(positions) || !aligned4(invalid))
+        return fail(DS_EALIGN, "seq, slot, positions and invalid must be 4-B aligned");
+    if (!aligned16(values)) return fail(DS_EALIGN, "values must be 16-B aligned");
+    AppendCall p;
+    std::memset(&p, 0, sizeof(p));
+    if (rope) {
+        rc = check_rope(rope, dim, positions);
+        if (rc) return rc;
+        p.rope = {rope->turns, rope->first, rope->rot_dim, rope->magnitude};
+        p.half = rope->layout == DS_ROPE_HALF;
+        p.positions = positions;
+    }
+    if (tokens == 0) return DS_OK;
+    p.cache = paged_cache(*cache);
+    p.x = x;
+    p.x_stride = x_stride;
+    p.tokens = tokens;
+    p.seq = seq;
+    p.slot = slot;
+    p.values = reinterpret_cast<__nv_bfloat16*>(values);
+    p.invalid = invalid;
+    p.wide = aligned16(x) && (x_stride * elem) % 16 == 0 ? 1u : 0u;
+    StageRange range("dsrows.append");
+    const cudaError_t err = launch_append(p, dtype, dim, cache->format, (cudaStream_t)stream, true);
+    return err == cudaSuccess ? DS_OK : cuda_fail(err, "append launch");
+}
+
+int ds_rows_rope_turns(uint32_t rot_dim, double base, double factor, uint32_t original_len, double beta_fast,
+                       double beta_slow, uint64_t* turns) {
+    if (!turns) return fail(DS_EINVAL, "turns is NULL");
+    if (rot_dim < 2 || rot_dim > DS_DIM || rot_dim % 2)
+        return fail(DS_EINVAL, "rot_dim must be even, 2..=%d, got %u", DS_DIM, rot_dim);
+    if (!(base > 1.0) || !std::isfinite(base)) return fail(DS_EINVAL, "base must be finite and above 1");
+    if (!(factor >= 1.0) || !std::isfinite(factor)) return fail(DS_EINVAL, "factor must be finite and at least 1");
+    if (original_len && (!(beta_slow > 0.0) || !(beta_fast >= beta_slow) || !std::isfinite(beta_fast)))
+        return fail(DS_EINVAL, "beta_fast >= beta_slow > 0 must be finite");
+    const double two_pi = 6.283185307179586476925;
+    double low = 0.0, high = 0.0;
+    if (original_len) {
+        auto turns_at = [&](double beta) {
+            return rot_dim * std::log(original_len / (two_pi * beta)) / (2.0 * std::log(base));
+        };
+        low = std::fmax(std::floor(turns_at(beta_fast)), 0.0);
+        high = std::fmin(std::ceil(turns_at(beta_slow)), (double)rot_dim - 1.0);
+    }
+    for (uint32_t i = 0; i < rot_dim / 2; ++i) {
+        double theta = std::pow(base, -2.0 * i / rot_dim);
+        if (factor != 1.0) {
+            // How far the pair is interpolated: fully without YaRN's ramp.
+            const double r =
+                original_len ? std::fmin(std::fmax((i - low) / std::fmax(high - low, 0.001), 0.0), 1.0) : 1.0;
+            theta = theta * (1.0 - r) + theta / factor * r;
+        }
+        turns[i] = (uint64_t)std::llrint(std::ldexp(theta / two_pi, 64));  // theta <= 1: below 2^62
+    }
+    return DS_OK;
+}
+
+int ds_rows_rope(const ds_rope_t* rope, const void* x, uint64_t x_token_stride, uint64_t x_head_stride, void* out,
+                 uint64_t out_token_stride, uint64_t out_head_stride, int dtype, uint64_t tokens, uint32_t heads,
+                 uint32_t dim, const int32_t* positions, int inverse, void* stream) {
+    if (dim < 1 || dim > 1024) return fail(DS_EINVAL, "dim must be 1..=1024, got %u", dim);
+    if (heads < 1 || heads > 65536) return fail(DS_EINVAL, "heads must be 1..=65536, got %u", heads);
+    if (tokens > 0x7FFFFFFFull / heads)
+        return fail(DS_ESIZE, "tokens x heads must be below 2^31, got %llu x %u", (unsigned long long)tokens, heads);
+    int rc = check_rope(rope, dim, positions);
+    if (rc) return rc;
+    size_t elem;
+    rc = check_elements(dtype, x, out, elem);
+    if (rc) return rc;
+    if (!aligned4(positions)) return fail(DS_EALIGN, "positions must be 4-B aligned");
+    if (x_token_stride > kMaxStride || x_head_stride > kMaxStride || out_token_stride > kMaxStride ||
+        out_head_stride > kMaxStride)
+        return fail(DS_ESIZE, "a stride is out of range");
+    const bool inplace = x == out;
+    if (inplace && ((tokens > 1 && x_token_stride != out_token_stride) || (heads > 1 && x_head_stride != out_head_stride)))
+        return fail(DS_EINVAL, "in place, the strides of x and out must be the same");
+    // The rows of out must not overlap: heads within tokens, or tokens within heads.
+    const bool heads_inner = (heads == 1 || out_head_stride >= dim) &&
+                             (tokens <= 1 || out_token_stride >= (uint64_t)(heads - 1) * out_head_stride + dim);
+    const bool tokens_inner = (tokens <= 1 || out_token_stride >= dim) &&
+                              (heads == 1 || out_head_stride >= (tokens ? tokens - 1 : 0) * out_token_stride + dim);
+    if (!heads_inner && !tokens_inner) return fail(DS_EINVAL, "rows of out overlap");
+    if (tokens == 0) return DS_OK;
+    const int sms = num_sms();
+    if (sms <= 0) return fail(DS_ECUDA, "no CUDA device");
+    RopeCall p;
+    std::memset(&p, 0, sizeof(p));
+    p.rope = {rope->turns, rope->first, rope->rot_dim, rope->magnitude};
+    p.x = x;
+    p.out = out;
+    p.positions = positions;
+    p.x_token = tokens > 1 ? x_token_stride : 0;  // a lone row's strides say nothing
+    p.x_head = heads > 1 ? x_head_stride : 0;
+    p.out_token = tokens > 1 ? out_token_stride : 0;
+    p.out_head = heads > 1 ? out_head_stride : 0;
+    p.tokens = tokens;
+    p.heads = heads;
+    p.dim = dim;
+    p.inplace = inplace ? 1u : 0u;
+    p.inverse = inverse ? 1u : 0u;
+    StageRange range("dsrows.rope");
+    const cudaError_t err = launch_rope(p, dtype, rope->layout, sms, (cudaStream_t)stream, true);
+    return err == cudaSuccess ? DS_OK : cuda_fail(err, "rope launch");
+}
+
+int ds_rows_indexer_score_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* keys,
+                                const ds_bf16* q_index, const float* w_index, float* scores, size_t score_stride,
+                                void* stream) {
+    int rc = check_table(rows, table);
+    if (rc) return rc;
+    rc = check_cache(keys, DS_INDEX_DIM, rows);
+    if (rc) return rc;
+    rc = check_reach(rows, table, keys);
+    if (rc) return rc;
+    rc = check_indexer_args(q_index, w_index);
+    if (rc) return rc;
+    if (!scores) return fail(DS_EINVAL, "scores is NULL");
+    for (int e = 0; e < rows; ++e)
+        if (score_stride < table[e].kv_len)
+            return fail(DS_EINVAL, "score_stride %zu is shorter than row %d (kv_len %u)", score_stride, e,
+                        table[e].kv_len);
+    PagedIndexerParams p;
+    std::memset(&p, 0, sizeof(p));
+    const uint32_t tile = indexer_tile_keys();
+    uint32_t tiles = 0;
+    for (int e = 0; e < rows; ++e) {
+        p.tile_begin[e] = tiles;
+        p.kv_len[e] = table[e].kv_len;
+        p.q_row[e] = table[e].q_row;
+        tiles += (table[e].kv_len - 1) / tile + 1;
+    }
+    const int sms = num_sms();
+    if (sms <= 0) return fail(DS_ECUDA, "no CUDA device");
+    if (keys->format == DS_CACHE_BF16) {
+        rc = get_encoder();
+        if (rc) return rc;
+        rc = encode_rows128(&p.kmap, keys->pages, (uint64_t)keys->num_pages * keys->page_size,
+                            keys->page_size < tile ? keys->page_size : tile, "paged indexer keys");
+        if (rc) return rc;
+    }
+    split_ctas(p.tile_begin, p.cta_begin, (uint32_t)rows, tiles, tiles < (uint32_t)sms ? tiles : (uint32_t)sms);
+    p.cache = paged_cache(*keys);
+    p.q = reinterpret_cast<const __nv_bfloat16*>(q_index);
+    p.w = w_index;
+    p.scores = scores;
+    p.score_stride = score_stride;
+    p.rows = (uint32_t)rows;
+    p.total_tiles = tiles;
+    StageRange range("dsrows.indexer_paged");
+    const cudaError_t err = launch_paged_indexer(p, keys->format, sms, (cudaStream_t)stream, true);
+    return err == cudaSuccess ? DS_OK : cuda_fail(err, "paged indexer launch");
+}
+
+int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* kv, const ds_bf16* q_attn,
+                              const float* sinks, size_t sinks_row_stride, const int32_t* indices, float scale,
+                              ds_bf16* out, uint32_t* invalid, void* workspace, size_t workspace_bytes, void* stream) {
+    const ds_row_set_t set = {rows, table, nullptr, nullptr};
+    int rc = check_set(&set, kUniqueQ);
+    if (rc) return rc;
+    rc = check_cache(kv, DS_DIM, rows);
+    if (rc) return rc;
+    rc = check_reach(rows, table, kv);
+    if (rc) return rc;
+    rc = check_attn_args(q_attn, sinks, sinks_row_stride, scale, out);
+    if (rc) return rc;
+    if (!indices) return fail(DS_EINVAL, "indices is NULL");
+    const Layout L = make_layout(rows, table);
+    rc = check_workspace(&set, workspace, workspace_bytes, L);
+    if (rc) return rc;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t err = launch_clear_stage(reinterpret_cast<uint32_t*>(ws), (uint32_t)(L.ctl_end / 4), s);
+    if (err != cudaSuccess) return cuda_fail(err, "workspace clear");
+    StageRange range("dsrows.attention_paged");
+    PagedTailParams p;
+    std::memset(static_cast<void*>(&p), 0, sizeof(p));
+    fill_tail(p, &set, q_attn, sinks, sinks_row_stride, scale, out, invalid, nullptr, 0, indices, nullptr, ws, L, false,
+              true, nullptr);
+    p.cache = paged_cache(*kv);
+    err = launch_sparse_attn_paged(p, kv->format, s, true);
+    return err == cudaSuccess ? DS_OK : cuda_fail(err, "paged attention launch");
 }
 
 int ds_rows_compress_kv(int rows, const ds_compressor_row_t* table, const float* kv, const float* score,

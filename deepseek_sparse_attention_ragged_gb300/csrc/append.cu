@@ -1,0 +1,165 @@
+// Append rows to a paged cache: rotate (optional), round to the cache's type,
+// store into the row's page.
+//
+// Bound by the bytes of the rows read and written (and, for a few rows, by the
+// launch). A lane owns 16 consecutive elements, which is one group of the 4-bit
+// type, so its scale needs no exchange: a warp holds one 512-wide row or four
+// 128-wide ones. The lanes of a row share its sines and cosines through shared
+// memory (each takes rot / 2 / lanes of them), and in the half layout the row
+// itself, whose pairs lie in different lanes.
+
+#include "int4.cuh"
+#include "rope.cuh"
+
+namespace dsrows {
+
+namespace {
+
+constexpr int kAppendThreads = 128;
+
+template <typename T>
+__device__ __forceinline__ float widen_f(T v) {
+    return (float)v;
+}
+
+}  // namespace
+
+template <typename T, int kDimOf, bool kInt4>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendCall p) {
+    constexpr int G = int4::kGroup;
+    constexpr int LANES = kDimOf / G;  // lanes of a row
+    constexpr int ROWS = kAppendThreads / LANES;
+    __shared__ float2 trig_s[ROWS][kDimOf / 2];
+    __shared__ float row_s[ROWS][G][LANES];  // element e of a row at [e mod 16][e / 16]
+    pdl_trigger();
+    const int r = threadIdx.x / LANES, g = threadIdx.x % LANES;
+    const uint64_t token = (uint64_t)blockIdx.x * ROWS + r;
+    const bool there = token < p.tokens;
+    pdl_wait();
+    // The row's place. The checks are uniform over its lanes.
+    const int32_t seq = there ? p.seq[token] : -1;
+    bool ok = false;
+    size_t page = 0;
+    uint32_t at = 0;
+    int32_t pos = 0;
+    if (there && seq != -1) {
+        const int32_t slot = p.slot[token];
+        const uint32_t page_no = (uint32_t)slot >> p.cache.page_shift;
+        ok = seq >= 0 && (uint32_t)seq < p.cache.entries && slot >= 0 && page_no < p.cache.table_stride;
+        if (ok) {
+            const int32_t id = p.cache.table[(uint64_t)seq * p.cache.table_stride + page_no];
+            ok = id >= 0 && (uint32_t)id < p.cache.num_pages;
+            page = (size_t)(uint32_t)id;
+            at = (uint32_t)slot & ((1u << p.cache.page_shift) - 1);
+        }
+        if (p.rope.rot) {
+            pos = p.positions[token];
+            ok = ok && pos >= 0;
+        }
+    }
+    if (there && g == 0 && p.invalid) p.invalid[token] = seq != -1 && !ok ? 1u : 0u;
+
+    float y[G];
+    if (ok) {
+        const T* x = static_cast<const T*>(p.x) + token * p.x_stride + g * G;
+        if (p.wide) {
+            __align__(16) T v[G];
+#pragma unroll
+            for (int i = 0; i < (int)(G * sizeof(T) / 16); ++i)
+                reinterpret_cast<uint4*>(v)[i] = reinterpret_cast<const uint4*>(x)[i];
+#pragma unroll
+            for (int i = 0; i < G; ++i) y[i] = widen_f(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < G; ++i) y[i] = widen_f(x[i]);
+        }
+    }
+    if (p.rope.rot) {
+        const uint32_t pairs = p.rope.rot / 2;
+        if (ok) {
+            for (uint32_t i = g; i < pairs; i += LANES)
+                trig_s[r][i] = rope_turn(pos, p.rope.turns[i], p.rope.magnitude, false);
+            if (p.half)
+#pragma unroll
+                for (int i = 0; i < G; ++i) row_s[r][i][g] = y[i];
+        }
+        __syncwarp();
+        if (ok) {
+            const uint32_t e0 = g * G - p.rope.first;  // this lane's elements within the range, modulo 2^32
+            if (p.half) {
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    const uint32_t e = e0 + i;
+                    if (e < p.rope.rot) {
+                        const bool low = e < pairs;
+                        const uint32_t other = (low ? e + pairs : e - pairs) + p.rope.first;
+                        const float z = row_s[r][other % G][other / G];
+                        const float2 cs = trig_s[r][low ? e : e - pairs];
+                        float a = low ? y[i] : z, b = low ? z : y[i];
+                        rope_pair(a, b, cs);
+                        y[i] = low ? a : b;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < G; i += 2)  // first is even: a pair lies in one lane
+                    if (e0 + i < p.rope.rot) rope_pair(y[i], y[i + 1], trig_s[r][(e0 + i) / 2]);
+            }
+        }
+    }
+    if (!ok) return;
+    uint8_t* base = p.cache.pages + (page << p.cache.page_shift) * p.cache.row_bytes;
+    __nv_bfloat16* held_out = p.values ? p.values + token * kDimOf + g * G : nullptr;
+    __align__(16) __nv_bfloat16 held[G];
+    if constexpr (kInt4) {
+        uint32_t word[2];
+        float h[G];
+        const uint8_t scale = int4::quantise(y, word, h);
+        if constexpr (kDimOf == kDim) {
+            uint8_t* row = base + (size_t)at * p.cache.row_bytes;
+            *reinterpret_cast<uint2*>(row + 8 * g) = make_uint2(word[0], word[1]);
+            row[kDimOf / 2 + g] = scale;
+        } else {
+            // Plane g / 2 holds 32 values of each row; then the scales.
+            const size_t size = (size_t)1 << p.cache.page_shift;
+            *reinterpret_cast<uint2*>(base + (g / 2) * size * 16 + at * 16 + (g & 1) * 8) =
+                make_uint2(word[0], word[1]);
+            base[size * (kDimOf / 2) + at * (kDimOf / G) + g] = scale;
+        }
+        if (!held_out) return;
+#pragma unroll
+        for (int i = 0; i < G; ++i) held[i] = __float2bfloat16_rn(h[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < G; ++i) held[i] = __float2bfloat16_rn(y[i]);
+        uint4* row = reinterpret_cast<uint4*>(base + (size_t)at * p.cache.row_bytes + g * G * 2);
+        row[0] = reinterpret_cast<const uint4*>(held)[0];
+        row[1] = reinterpret_cast<const uint4*>(held)[1];
+        if (!held_out) return;
+    }
+    reinterpret_cast<uint4*>(held_out)[0] = reinterpret_cast<const uint4*>(held)[0];
+    reinterpret_cast<uint4*>(held_out)[1] = reinterpret_cast<const uint4*>(held)[1];
+}
+
+template <typename T, int kDimOf>
+static cudaError_t launch_rows(const AppendCall& p, int format, cudaStream_t stream, bool pdl) {
+    constexpr uint64_t rows = kAppendThreads / (kDimOf / int4::kGroup);
+    const dim3 grid((uint32_t)((p.tokens + rows - 1) / rows));
+    if (format == DS_CACHE_INT4)
+        return launch_kernel(append_kernel<T, kDimOf, true>, grid, dim3(kAppendThreads), 0, stream, pdl, p);
+    return launch_kernel(append_kernel<T, kDimOf, false>, grid, dim3(kAppendThreads), 0, stream, pdl, p);
+}
+
+template <typename T>
+static cudaError_t launch_type(const AppendCall& p, uint32_t dim, int format, cudaStream_t stream, bool pdl) {
+    return dim == kDim ? launch_rows<T, kDim>(p, format, stream, pdl) : launch_rows<T, kIdxDim>(p, format, stream, pdl);
+}
+
+cudaError_t launch_append(const AppendCall& p, int dtype, uint32_t dim, int format, cudaStream_t stream, bool pdl) {
+    if (p.tokens == 0) return cudaSuccess;
+    if (dtype == DS_F32) return launch_type<float>(p, dim, format, stream, pdl);
+    if (dtype == DS_F16) return launch_type<__half>(p, dim, format, stream, pdl);
+    return launch_type<__nv_bfloat16>(p, dim, format, stream, pdl);
+}
+
+}  // namespace dsrows

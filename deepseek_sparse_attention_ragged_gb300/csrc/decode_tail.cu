@@ -57,6 +57,7 @@
 
 #include "attend.cuh"
 #include "common.cuh"
+#include "int4.cuh"
 #include "kernels.h"
 #include "select.cuh"
 
@@ -122,10 +123,15 @@ __device__ __forceinline__ uint32_t sw128_chunk(int r, int ch, int block) {
     return (uint32_t)((ch >> 3) * block + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
+// Where the KV rows lie: one contiguous bf16 cache per entry, or the pages of a
+// pool in bf16 or 4 bits (the caller's indices only).
+enum class Cache { kContiguous, kPagedBf16, kPagedInt4 };
+constexpr int kInt4RowBytes = kDim / 2 + kDim / int4::kGroup;
+
 }  // namespace
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
-    decode_tail_kernel(const TailParams p) {
+template <Cache kCache, class Params>
+__device__ __forceinline__ void tail_body(const Params& p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     using T = TailLayout;
@@ -157,7 +163,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     auto pub_flag = [&](uint32_t r) { return p.flags + kRowsMax * kHeads + kRowsMax + r; };
     auto pub_n = [&](uint32_t r) { return reinterpret_cast<uint32_t*>(p.pub + (size_t)kRowsMax * kTopK) + r; };
 
-    if (e >= (int)p.rows) {
+    if (kCache == Cache::kContiguous && e >= (int)p.rows) {
         // ---- one more cluster ranks the rows' winners (decode with attention):
         // CTA r waits for row r to publish its winners in index order, sorts
         // them best first and writes the row's index list. No row waits for it.
@@ -225,7 +231,31 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 
     const uint32_t first = c * kChunkSlots;
     uint32_t nsel = 0;
-    if (p.given == nullptr) {
+    if constexpr (kCache != Cache::kContiguous) {
+        // ---- the caller's indices, as below; a slot then holds its row's place in
+        // the pool instead of its index. The page ids are fetched while the indices
+        // are sorted. A page id outside the pool flags the row as an index does.
+        uint32_t* place_s = reinterpret_cast<uint32_t*>(sel);  // by the caller's position
+        const uint32_t mask = (1u << p.cache.page_shift) - 1;
+        uint64_t v = 0;
+        int32_t id = 0;
+        uint32_t at = 0;
+        if ((uint32_t)t < W) {
+            const int g = __ldcg(p.given + p.index_offset[e] + t);
+            if (g < -1 || g >= (int)L) atomicOr(&p.flags[kRowsMax * kHeads + e], 1u);
+            else if (g >= 0) {
+                v = ((uint64_t)(~(uint32_t)g) << 32) | (uint32_t)t;
+                id = __ldcg(p.cache.table + (size_t)e * p.cache.table_stride + ((uint32_t)g >> p.cache.page_shift));
+                at = (uint32_t)g & mask;
+            }
+        }
+        v = bitonic512_desc(v, reinterpret_cast<uint64_t*>(gs.h));
+        const bool paged = id >= 0 && (uint32_t)id < p.cache.num_pages;
+        if (!paged) atomicOr(&p.flags[kRowsMax * kHeads + e], 1u);
+        place_s[t] = paged ? ((uint32_t)id << p.cache.page_shift) + at : 0u;
+        __syncthreads();
+        if ((uint32_t)t - first < (uint32_t)kChunkSlots && v != 0) idx_s[t - first] = (int32_t)place_s[(uint32_t)v];
+    } else if (p.given == nullptr) {
         // ---- select: gather the candidates, then every CTA selects the same winners
         const float* s = p.scores + (size_t)e * p.score_stride;
         const Gathered gat = select_collect_all(s, L, W, p.hist + (size_t)e * kHistBins, rank, gs, regions);
@@ -257,7 +287,51 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     }
     // The gather of the chunk's KV rows starts now.
     const size_t part0_off = ((size_t)2 * p.chunk_begin[e] + (size_t)half * nchunks) * kPartFloats;
-    if (has_chunk && p.attend) {
+    if constexpr (kCache == Cache::kPagedBf16) {
+        if (has_chunk)
+            for (int k = t; k < kChunkSlots * (kDim / 8); k += kThreads) {
+                const int r = k >> 6, ch = k & 63;
+                const int i = idx_s[r];
+                uint8_t* dst = g_s + sw128_chunk(r, ch, kGBlock);
+                if (i >= 0) cp_async16(dst, p.cache.pages + (size_t)i * (2 * kDim) + ch * 16);
+                else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+            }
+    } else if constexpr (kCache == Cache::kPagedInt4) {
+        // A unit is 32 values (16 bytes) of a row and their two scales; a thread
+        // loads all of its units before it widens the first.
+        constexpr int kUnits = kChunkSlots * (kDim / 32) / kThreads;
+        if (has_chunk) {
+            uint4 d[kUnits];
+            uint32_t sc[kUnits];
+#pragma unroll
+            for (int n = 0; n < kUnits; ++n) {
+                const int k = t + n * kThreads, r = k >> 4, u = k & 15;
+                const int i = idx_s[r];
+                // An empty slot is zeros: n + 8 = 8 in every value, s = 0.
+                d[n] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                sc[n] = 0;
+                if (i >= 0) {
+                    const uint8_t* row = p.cache.pages + (size_t)i * kInt4RowBytes;
+                    d[n] = __ldcg(reinterpret_cast<const uint4*>(row + 16 * u));
+                    sc[n] = __ldcg(reinterpret_cast<const uint16_t*>(row + kDim / 2 + 2 * u));
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < kUnits; ++n) {
+                const int k = t + n * kThreads, r = k >> 4, u = k & 15;
+                const float2 s2 = int4::scales2(sc[n]);
+                const int4::Factors f[2] = {int4::factors(s2.x), int4::factors(s2.y)};
+                const uint32_t w[4] = {d[n].x, d[n].y, d[n].z, d[n].w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[4];
+                    int4::widen(w[c], f[c >> 1], o);
+                    *reinterpret_cast<uint4*>(g_s + sw128_chunk(r, 4 * u + c, kGBlock)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        }
+    } else if (has_chunk && p.attend) {
         const __nv_bfloat16* kv = p.kv[e];
         for (int k = t; k < kChunkSlots * (kDim / 8); k += kThreads) {
             const int r = k >> 6, ch = k & 63;
@@ -467,6 +541,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
+    decode_tail_kernel(const __grid_constant__ TailParams p) {
+    tail_body<Cache::kContiguous>(p);
+}
+
+// The attention of the caller's indices over a paged cache.
+template <Cache kCache>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
+    sparse_attn_paged_kernel(const __grid_constant__ PagedTailParams p) {
+    tail_body<kCache>(p);
+}
+
 size_t decode_tail_smem_bytes() { return kTailSmem; }
 
 cudaError_t launch_decode_tail(const TailParams& p, cudaStream_t stream, bool pdl) {
@@ -476,6 +562,21 @@ cudaError_t launch_decode_tail(const TailParams& p, cudaStream_t stream, bool pd
     if (p.rows == 0) return cudaSuccess;
     const uint32_t clusters = p.rows + (p.ranker ? 1u : 0u);
     return launch_kernel(decode_tail_kernel, dim3(clusters * kCluster), dim3(kThreads), kTailSmem, stream, pdl, p);
+}
+
+template <Cache kCache>
+static cudaError_t launch_paged(const PagedTailParams& p, cudaStream_t stream, bool pdl) {
+    static std::atomic<uint64_t> smem_set{0};
+    const cudaError_t err = set_smem_limit_once(sparse_attn_paged_kernel<kCache>, kTailSmem, smem_set);
+    if (err != cudaSuccess) return err;
+    return launch_kernel(sparse_attn_paged_kernel<kCache>, dim3(p.rows * kCluster), dim3(kThreads), kTailSmem, stream,
+                         pdl, p);
+}
+
+cudaError_t launch_sparse_attn_paged(const PagedTailParams& p, int format, cudaStream_t stream, bool pdl) {
+    if (p.rows == 0) return cudaSuccess;
+    return format == DS_CACHE_INT4 ? launch_paged<Cache::kPagedInt4>(p, stream, pdl)
+                                   : launch_paged<Cache::kPagedBf16>(p, stream, pdl);
 }
 
 }  // namespace dsrows

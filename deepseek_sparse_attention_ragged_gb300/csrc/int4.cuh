@@ -1,0 +1,74 @@
+// The 4-bit cache type: groups of 16 values n * s, s an e4m3 scale and n in -7..7
+// held as n + 8. A 32-bit word holds 8 values, value i at bits 4 (i / 2) + 16 (i mod 2),
+// so that one shift and one mask leave two neighbours in the halves of a word.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace dsrows {
+namespace int4 {
+
+constexpr int kGroup = 16;
+constexpr uint8_t kNanScale = 0x7F;
+
+// A group's scale s as the pair of factors of `widen`: (s, s) and (-136 s, -136 s)
+// as bf16. Both are exact: s has 4 significant bits, 136 = 8 * 17, and 17 times
+// 4 bits is 8 bits.
+struct Factors {
+    uint32_t s, c;
+};
+
+__device__ __forceinline__ uint32_t bf16_twice(float v) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(v, v);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The scales in the low two bytes of `b`.
+__device__ __forceinline__ float2 scales2(uint32_t b) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(b & 0xFFFFu), __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+__device__ __forceinline__ Factors factors(float s) { return {bf16_twice(s), bf16_twice(-136.0f * s)}; }
+
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// One word's 8 values as bf16 pairs: word j holds values 2 j and 2 j + 1. 0x4300 | (n + 8)
+// is 128 + 8 + n in bf16, so (136 + n) s - 136 s is n s, which is exact in bf16.
+__device__ __forceinline__ void widen(uint32_t word, Factors f, uint32_t* out) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[j] = fma_bf16x2(((word >> (4 * j)) & 0x000F000Fu) | 0x43004300u, f.s, f.c);
+}
+
+// Quantise a group: 16 values to two words and the scale byte; with `held` the
+// values that the cache then stands for.
+__device__ __forceinline__ uint8_t quantise(const float (&y)[kGroup], uint32_t (&word)[2], float (&held)[kGroup]) {
+    float top = 0.0f;
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+        ok = ok && finite_f(y[i]);
+        top = fmaxf(top, fabsf(y[i]));
+    }
+    const uint8_t byte = ok ? (uint8_t)__nv_cvt_float_to_fp8(top / 7.0f, __NV_SATFINITE, __NV_E4M3) : kNanScale;
+    const float s = scales2(byte).x;
+    word[0] = word[1] = 0;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+        // s = 0 (or NaN): the quotient may be anything, the value is 0 (NaN).
+        const float n = s > 0.0f ? fminf(fmaxf(rintf(y[i] / s), -7.0f), 7.0f) : 0.0f;
+        word[i >> 3] |= (uint32_t)((int)n + 8) << (4 * ((i & 7) >> 1) + 16 * (i & 1));
+        held[i] = n * s;
+    }
+    return byte;
+}
+
+}  // namespace int4
+}  // namespace dsrows

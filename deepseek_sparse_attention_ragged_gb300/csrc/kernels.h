@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -119,6 +120,85 @@ struct CompressorParams {
 };
 
 cudaError_t launch_compressor(const CompressorParams& p, cudaStream_t stream, bool pdl);
+
+// A rotation of the elements [first, first + rot) of a row (see ds_rope_t).
+struct RopeParams {
+    const uint64_t* turns;  // [rot / 2]
+    uint32_t first;
+    uint32_t rot;
+    float magnitude;
+};
+
+// Rotary positions over tokens x heads rows of `dim` elements; strides in elements.
+struct RopeCall {
+    RopeParams rope;
+    const void* x;
+    void* out;
+    const int32_t* positions;
+    uint64_t x_token, x_head, out_token, out_head;
+    uint64_t tokens;
+    uint32_t heads;
+    uint32_t dim;
+    uint32_t inplace;  // out is x: only the rotated elements are touched
+    uint32_t inverse;
+    // Set by the launcher.
+    uint32_t units;    // rotation units of a row: a thread's share of its pairs
+    uint32_t group;    // heads that one thread rotates with the same angles
+    uint32_t groups;   // head groups of a token
+    uint32_t slots;    // (token, head group) items of a block
+};
+
+// A paged cache's addressing (see ds_paged_cache_t).
+struct PagedCache {
+    uint8_t* pages;
+    const int32_t* table;
+    uint64_t table_stride;
+    uint32_t entries;
+    uint32_t page_shift;  // log2 of the page size
+    uint32_t num_pages;
+    uint32_t row_bytes;
+};
+
+struct AppendCall {
+    PagedCache cache;
+    RopeParams rope;  // rot 0: none
+    int half;         // the pairs' layout is DS_ROPE_HALF
+    const void* x;
+    uint64_t x_stride;
+    uint64_t tokens;
+    const int32_t* seq;
+    const int32_t* slot;
+    const int32_t* positions;
+    __nv_bfloat16* values;
+    uint32_t* invalid;
+    uint32_t wide;  // the rows of x start on 16-byte boundaries
+};
+
+// Indexer scores over a paged key cache, one query per entry.
+struct PagedIndexerParams {
+    CUtensorMap kmap;  // bf16 pages: [num_pages * page_size, 128], box {64, min(page_size, 128)}, 128-B swizzle
+    PagedCache cache;
+    const __nv_bfloat16* q;  // [Q, 64, 128]
+    const float* w;          // [Q, 64]
+    float* scores;           // entry e at e * score_stride
+    uint64_t score_stride;
+    uint32_t rows;
+    uint32_t total_tiles;
+    uint32_t tile_begin[DS_ROWS_MAX];
+    uint32_t cta_begin[DS_ROWS_MAX + 1];
+    uint32_t kv_len[DS_ROWS_MAX];
+    uint32_t q_row[DS_ROWS_MAX];
+};
+
+// Attention of the caller's indices over a paged cache.
+struct PagedTailParams : TailParams {
+    PagedCache cache;
+};
+
+cudaError_t launch_rope(RopeCall p, int dtype, int layout, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_append(const AppendCall& p, int dtype, uint32_t dim, int format, cudaStream_t stream, bool pdl);
+cudaError_t launch_paged_indexer(const PagedIndexerParams& p, int format, int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_sparse_attn_paged(const PagedTailParams& p, int format, cudaStream_t stream, bool pdl);
 
 uint32_t indexer_tile_keys();
 // One query per key tile (decode), or up to kIndexerGroup.

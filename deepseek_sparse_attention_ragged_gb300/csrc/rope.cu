@@ -1,0 +1,177 @@
+// Rotary positions: pair (a, b) of a row at position t becomes
+//   m (a cos x - b sin x), m (a sin x + b cos x),  x = t theta_i
+// (x negated for the inverse, which is the transpose).
+//
+// Bound by the bytes moved: 2 (in place: 2 rot / dim) of the rows. A thread owns
+// one unit of a row's rotated range: 16 bytes of interleaved pairs, or 16 bytes
+// from each half, with their angles in registers, and rotates that unit of a
+// group of heads of one token, so sine and cosine are taken once per group.
+// A row whose address, stride or range is not a multiple of 16 bytes is moved
+// by elements, one pair a unit.
+
+#include "rope.cuh"
+
+namespace dsrows {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kHeadsInFlight = 4;  // heads whose loads a thread issues before it uses the first
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+
+// N elements of a row: 16 bytes in one access, or element by element.
+template <typename T, int N>
+struct Piece {
+    T v[N];
+};
+template <typename T, int N, bool kWide>
+__device__ __forceinline__ Piece<T, N> get(const T* p) {
+    Piece<T, N> r;
+    if constexpr (kWide) {
+        static_assert(N * sizeof(T) == 16, "16 bytes");
+        *reinterpret_cast<uint4*>(r.v) = *reinterpret_cast<const uint4*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r.v[i] = p[i];
+    }
+    return r;
+}
+template <typename T, int N, bool kWide>
+__device__ __forceinline__ void put(T* p, const Piece<T, N>& r) {
+    if constexpr (kWide) {
+        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(r.v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = r.v[i];
+    }
+}
+
+// Elements of one access: with kWide 16 bytes; else one pair (interleaved) or one
+// element of each half.
+template <typename T, bool kHalf, bool kWide>
+constexpr int piece_len() {
+    return kWide ? 16 / (int)sizeof(T) : (kHalf ? 1 : 2);
+}
+
+}  // namespace
+
+template <typename T, bool kHalf, bool kWide>
+__global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeCall p) {
+    constexpr int N = piece_len<T, kHalf, kWide>();
+    constexpr int PAIRS = kHalf ? N : N / 2;
+    struct __align__(16) Unit {
+        Piece<T, N> a, b;  // b: the second half's piece (kHalf)
+    };
+    pdl_trigger();
+    const uint32_t u = threadIdx.x % p.units;
+    const uint64_t item = (uint64_t)blockIdx.x * p.slots + threadIdx.x / p.units;
+    const uint64_t token = item / p.groups;
+    if (token >= p.tokens) return;
+    const uint32_t h0 = (uint32_t)(item - token * p.groups) * p.group;
+    const uint32_t h1 = min(h0 + p.group, p.heads);
+    pdl_wait();
+    const int32_t pos = p.positions[token];
+    if (pos < 0) return;
+    const T* x = static_cast<const T*>(p.x) + token * p.x_token;
+    T* out = static_cast<T*>(p.out) + token * p.out_token;
+    const uint32_t fa = p.rope.first + u * N;
+    const uint32_t fb = fa + p.rope.rot / 2;
+    float2 cs[PAIRS];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i)
+        cs[i] = rope_turn(pos, p.rope.turns[u * PAIRS + i], p.rope.magnitude, p.inverse != 0);
+    for (uint32_t h = h0; h < h1; h += kHeadsInFlight) {
+        Unit v[kHeadsInFlight];
+#pragma unroll
+        for (int k = 0; k < kHeadsInFlight; ++k)
+            if (h + k < h1) {
+                const T* row = x + (uint64_t)(h + k) * p.x_head;
+                v[k].a = get<T, N, kWide>(row + fa);
+                if constexpr (kHalf) v[k].b = get<T, N, kWide>(row + fb);
+            }
+#pragma unroll
+        for (int k = 0; k < kHeadsInFlight; ++k)
+            if (h + k < h1) {
+                T* row = out + (uint64_t)(h + k) * p.out_head;
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    T& ta = kHalf ? v[k].a.v[i] : v[k].a.v[(2 * i) % N];
+                    T& tb = kHalf ? v[k].b.v[i] : v[k].a.v[(2 * i + 1) % N];
+                    float a = to_f(ta), b = to_f(tb);
+                    rope_pair(a, b, cs[i]);
+                    ta = from_f<T>(a);
+                    tb = from_f<T>(b);
+                }
+                put<T, N, kWide>(row + fa, v[k].a);
+                if constexpr (kHalf) put<T, N, kWide>(row + fb, v[k].b);
+            }
+    }
+    if (p.inplace) return;
+    // The elements outside the rotated range, in pieces of M.
+    constexpr int M = kWide ? N : 1;
+    const uint32_t before = p.rope.first / M, skip = p.rope.rot / M, pieces = p.dim / M - skip;
+    for (uint32_t h = h0; h < h1; ++h) {
+        const T* src = x + (uint64_t)h * p.x_head;
+        T* dst = out + (uint64_t)h * p.out_head;
+        for (uint32_t i = u; i < pieces; i += p.units) {
+            const uint32_t f = (i < before ? i : i + skip) * M;
+            put<T, M, kWide>(dst + f, get<T, M, kWide>(src + f));
+        }
+    }
+}
+
+template <typename T, bool kHalf, bool kWide>
+static cudaError_t launch(RopeCall& p, int num_sms, cudaStream_t stream, bool pdl) {
+    constexpr int N = piece_len<T, kHalf, kWide>();
+    p.units = p.rope.rot / (kHalf ? 2 * N : N);
+    // Heads per thread: as many as leave two blocks for every SM, at most 8.
+    uint32_t group = 1;
+    while (group < 8 && group < p.heads &&
+           p.tokens * ((p.heads + 2 * group - 1) / (2 * group)) * p.units >= (uint64_t)2 * num_sms * kRopeThreads)
+        group *= 2;
+    p.group = group;
+    p.groups = (p.heads + group - 1) / group;
+    p.slots = p.units >= kRopeThreads ? 1 : kRopeThreads / p.units;
+    const uint64_t items = p.tokens * p.groups;
+    const uint64_t blocks = (items + p.slots - 1) / p.slots;
+    if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+    return launch_kernel(rope_kernel<T, kHalf, kWide>, dim3((uint32_t)blocks), dim3(p.units * p.slots), 0, stream, pdl,
+                         p);
+}
+
+template <typename T>
+static cudaError_t launch_type(RopeCall& p, int layout, int num_sms, cudaStream_t stream, bool pdl) {
+    constexpr uint64_t n = 16 / sizeof(T);
+    const uint64_t strides = p.x_token | p.x_head | p.out_token | p.out_head;
+    const uint64_t range = p.rope.first | (layout == DS_ROPE_HALF ? p.rope.rot / 2 : p.rope.rot) | (p.inplace ? 0 : p.dim);
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out)) & 15) == 0 &&
+                      ((strides | range) & (n - 1)) == 0;
+    if (layout == DS_ROPE_HALF)
+        return wide ? launch<T, true, true>(p, num_sms, stream, pdl) : launch<T, true, false>(p, num_sms, stream, pdl);
+    return wide ? launch<T, false, true>(p, num_sms, stream, pdl) : launch<T, false, false>(p, num_sms, stream, pdl);
+}
+
+cudaError_t launch_rope(RopeCall p, int dtype, int layout, int num_sms, cudaStream_t stream, bool pdl) {
+    if (p.tokens == 0) return cudaSuccess;
+    if (dtype == DS_F32) return launch_type<float>(p, layout, num_sms, stream, pdl);
+    if (dtype == DS_F16) return launch_type<__half>(p, layout, num_sms, stream, pdl);
+    return launch_type<__nv_bfloat16>(p, layout, num_sms, stream, pdl);
+}
+
+}  // namespace dsrows

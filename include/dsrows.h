@@ -376,6 +376,168 @@ int ds_rows_compress_kv(int rows, const ds_compressor_row_t* table, const float*
                         const float* ape, const float* norm, uint32_t ratio, uint32_t head_dim,
                         float epsilon, ds_bf16* out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Positions and paged caches
+ *
+ * A decode step over paged caches is ds_rows_rope on the queries,
+ * ds_rows_append on the new keys and KV rows, ds_rows_indexer_score_paged,
+ * ds_rows_topk on its scores, ds_rows_sparse_attn_paged, and ds_rows_rope with
+ * `inverse` on the output where the model asks for it.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of ds_rows_rope and ds_rows_append. */
+#define DS_BF16 0
+#define DS_F16 1
+#define DS_F32 2
+
+/* Which elements of a rotated range [first, first + rot_dim) form pair i. */
+#define DS_ROPE_INTERLEAVED 0 /* first + 2 i and first + 2 i + 1 */
+#define DS_ROPE_HALF 1        /* first + i and first + rot_dim / 2 + i */
+
+/*
+ * A rotation: pair (a, b) = pair i of a row at position t becomes
+ *   m (a cos x - b sin x), m (a sin x + b cos x),  x = t theta_i.
+ *   turns      device uint64 [rot_dim / 2] (8-B aligned): theta_i / (2 pi) as a
+ *              64-bit fraction of a turn, from ds_rows_rope_turns. t * turns[i]
+ *              modulo 2^64 is the angle's exact reduction at every position.
+ *   first      first rotated element of a row (even when interleaved)
+ *   rot_dim    rotated elements: even, 2 .. 512
+ *   layout     DS_ROPE_INTERLEAVED or DS_ROPE_HALF
+ *   magnitude  m: finite and > 0 (1, or a long-context attention factor)
+ */
+typedef struct {
+    const uint64_t* turns;
+    uint32_t first;
+    uint32_t rot_dim;
+    int layout;
+    float magnitude;
+} ds_rope_t;
+
+/*
+ * The turns of a rotation, written to HOST memory [rot_dim / 2] (no GPU is
+ * used; copy them to the device once). theta_i = base^(-2 i / rot_dim), then
+ *   factor 1:                      as it is;
+ *   factor > 1, original_len 0:    theta_i / factor (linear interpolation);
+ *   factor > 1, original_len > 0:  YaRN: theta_i (1 - r_i) + theta_i / factor r_i,
+ *     r_i = clamp((i - low) / max(high - low, 0.001), 0, 1),
+ *     low = max(floor(c(beta_fast)), 0), high = min(ceil(c(beta_slow)), rot_dim - 1),
+ *     c(b) = rot_dim ln(original_len / (2 pi b)) / (2 ln base).
+ *   base > 1, factor >= 1, beta_fast >= beta_slow > 0, all finite (the betas are
+ *   used with original_len only).
+ */
+int ds_rows_rope_turns(uint32_t rot_dim, double base, double factor, uint32_t original_len, double beta_fast,
+                       double beta_slow, uint64_t* turns);
+
+/*
+ * Rotary positions of x [tokens, heads, dim], one position a token:
+ *   x, out     device, element type `dtype`; element strides *_token_stride and
+ *              *_head_stride, the dim elements of a head contiguous. `out` may be
+ *              `x` with the same strides (in place: only the rotated elements
+ *              are touched); otherwise the two must not share memory, and the
+ *              elements outside the rotated range are copied. The rows of `out`
+ *              must not overlap; those of x may (stride 0 broadcasts).
+ *   tokens     0 enqueues nothing; heads 1 .. 65536; tokens * heads < 2^31
+ *   dim        1 .. 1024; first + rot_dim <= dim. Strides are at most 2^31.
+ *   positions  device int32 [tokens]; a negative position marks padding: its
+ *              rows of `out` are left as they are.
+ *   inverse    nonzero: the angles are negated. This is the transpose of the
+ *              rotation, so it maps the gradient of `out` to the gradient of x
+ *              (m is the same factor, not its reciprocal).
+ * The angle is reduced exactly, sine and cosine are taken and the products are
+ * summed in 32 bits, and the result is rounded once to `dtype`. Pointers need
+ * the type's alignment; with 16-byte aligned rows and ranges the call is fastest.
+ */
+int ds_rows_rope(const ds_rope_t* rope, const void* x, uint64_t x_token_stride, uint64_t x_head_stride, void* out,
+                 uint64_t out_token_stride, uint64_t out_head_stride, int dtype, uint64_t tokens, uint32_t heads,
+                 uint32_t dim, const int32_t* positions, int inverse, void* stream);
+
+/* Types of a paged cache. */
+#define DS_CACHE_BF16 0
+#define DS_CACHE_INT4 1
+
+/*
+ * A paged cache of `dim`-wide rows (128: indexer keys, 512: shared K/V rows).
+ * Entry e's row j lies in page id = page_table[e * table_stride + j / page_size],
+ * at place j mod page_size. Entries may share pages.
+ *   pages       device, num_pages pages one after another (16-B aligned), each of
+ *               ds_rows_page_bytes(page_size, dim, format) bytes:
+ *     DS_CACHE_BF16  bf16 [page_size][dim].
+ *     DS_CACHE_INT4  a row is dim / 16 groups of 16 values n s: s an e4m3 scale,
+ *                    n an integer in -7 .. 7 held as n + 8 in 4 bits. A 32-bit
+ *                    word holds 8 values, value i at bits 4 (i / 2) + 16 (i mod 2);
+ *                    a scale byte of 0x7F (NaN) makes its group NaN.
+ *                    dim 512: [page_size][256 bytes of values, 32 scales].
+ *                    dim 128: 4 planes [page_size][16 bytes], plane c with values
+ *                    32 c .. 32 c + 31 of each row, then [page_size][8 scales]
+ *                    (a plane is read by consecutive threads without bank conflicts).
+ *   page_table  device int32 [entries, table_stride] (4-B aligned)
+ *   page_size   rows of a page: 16, 32, 64, 128 or 256
+ *   num_pages   pages of the pool; num_pages * page_size < 2^31
+ */
+typedef struct {
+    void* pages;
+    const int32_t* page_table;
+    uint32_t entries;
+    uint32_t table_stride;
+    uint32_t page_size;
+    uint32_t num_pages;
+    uint32_t dim;
+    int format;
+} ds_paged_cache_t;
+
+/* Bytes of one page; 0 when the arguments are invalid (see ds_rows_last_error). */
+size_t ds_rows_page_bytes(uint32_t page_size, uint32_t dim, int format);
+
+/*
+ * Append rows to a paged cache, rotated on the way: row i of x [tokens, dim]
+ * becomes row slot[i] of entry seq[i].
+ *   x          device, element type `dtype`, rows x_stride elements apart (the
+ *              elements of a row contiguous); must not share memory with the pages
+ *   tokens     below 2^31; 0 enqueues nothing. x_stride is at most 2^31.
+ *   seq, slot  device int32 [tokens]. seq -1 marks padding: the row is skipped.
+ *              The (seq, slot) pairs of a call, and the places they map to, must
+ *              be distinct: of two rows for one place, any mix may remain.
+ *   rope       NULL: no rotation; else rotates as ds_rows_rope with
+ *   positions  device int32 [tokens]: the rotation's position, >= 0 (not the slot:
+ *              a compressed row stands for several tokens); unused without rope
+ *   values     optional bf16 [tokens, dim] (16-B aligned): the row as the cache
+ *              now holds it (what later reads will see); skipped rows are left
+ *   invalid    optional uint32 [tokens]: 1 where the row was not written because
+ *              seq, slot, its page id or its position is out of range, else 0
+ * The rotated row is kept in 32 bits and rounded once. DS_CACHE_BF16: to nearest
+ * even. DS_CACHE_INT4, per group of 16 values y: s = e4m3(min(max|y| / 7, 448)) to
+ * nearest even, n = y / s to the nearest integer (even on ties) within -7 .. 7
+ * (s = 0: n = 0); a group with a non-finite value is stored as NaN. n s is exact
+ * in bf16 and in fp16.
+ */
+int ds_rows_append(const ds_paged_cache_t* cache, const void* x, uint64_t x_stride, int dtype, uint64_t tokens,
+                   const int32_t* seq, const int32_t* slot, const ds_rope_t* rope, const int32_t* positions,
+                   ds_bf16* values, uint32_t* invalid, void* stream);
+
+/*
+ * ds_rows_indexer_score with the keys in a paged cache (dim 128): entry e of the
+ * table reads entry e of the cache. 4-bit keys are widened exactly, so the scores
+ * are those of the bf16 keys that the cache stands for. A key whose page id is
+ * not in [0, num_pages), or with a NaN scale, scores -inf. DS_EINVAL when the
+ * cache has fewer entries than rows, or a table row cannot reach kv_len; kv_len
+ * is below 2^31.
+ */
+int ds_rows_indexer_score_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* keys,
+                                const ds_bf16* q_index, const float* w_index, float* scores, size_t score_stride,
+                                void* stream);
+
+/*
+ * ds_rows_sparse_attn with the KV rows in a paged cache (dim 512): entry e of the
+ * table reads entry e of the cache. 4-bit rows are widened to bf16 exactly, so
+ * the output is bitwise that of ds_rows_sparse_attn on the bf16 rows that the
+ * cache stands for. A selected row whose page id is not in [0, num_pages) zeroes
+ * every head of its entry, as an index out of range does; a NaN scale zeroes the
+ * heads as a non-finite KV element does. Workspace as for ds_rows_sparse_attn.
+ */
+int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* kv, const ds_bf16* q_attn,
+                              const float* sinks, size_t sinks_row_stride, const int32_t* indices, float scale,
+                              ds_bf16* out, uint32_t* invalid, void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * Self-test of the device-side failure detection, on the current device. One
  * CTA runs the library's bounded mbarrier wait twice on a shared-memory
