@@ -319,8 +319,8 @@ __device__ __forceinline__ void tail_body(const Params& p) {
 #pragma unroll
             for (int n = 0; n < kUnits; ++n) {
                 const int k = t + n * kThreads, r = k >> 4, u = k & 15;
-                const float2 s2 = int4::scales2(sc[n]);
-                const int4::Factors f[2] = {int4::factors(s2.x), int4::factors(s2.y)};
+                int4::Factors f[2];
+                int4::factors2<0>(sc[n], f[0], f[1]);
                 const uint32_t w[4] = {d[n].x, d[n].y, d[n].z, d[n].w};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {

@@ -51,4 +51,45 @@ __device__ __forceinline__ float head_sum(const uint32_t (&x)[64], const float* 
     return (s4[0] + s4[1]) + (s4[2] + s4[3]);
 }
 
+// The same sum, 32 heads at a time with the weights in shared memory. With kAdd,
+// x + |x| = 2 max(0, x) takes the place of the maximum, and half the total is the
+// sum, bit for bit while nothing overflows: the addition runs on the FMA pipe, the
+// maximum on the integer pipe at half its rate. An infinite product makes that form
+// NaN or infinite where the maximum may be finite: a total that is not finite says
+// nothing, and is taken again without kAdd.
+template <bool kAdd>
+struct HeadSum {
+    float2 s01 = {0.0f, 0.0f}, s23 = {0.0f, 0.0f};
+    static __device__ __forceinline__ float relu(uint32_t bits) {
+        const float x = __uint_as_float(bits);
+        return kAdd ? x + fabsf(x) : relu_nan(x);
+    }
+    __device__ __forceinline__ void add(const uint32_t (&x)[32], const float* w_s) {
+#pragma unroll
+        for (int h = 0; h < 32; h += 4) {
+            const float4 w4 = *reinterpret_cast<const float4*>(w_s + h);
+            s01 = fma2(make_float2(relu(x[h]), relu(x[h + 1])), make_float2(w4.x, w4.y), s01);
+            s23 = fma2(make_float2(relu(x[h + 2]), relu(x[h + 3])), make_float2(w4.z, w4.w), s23);
+        }
+    }
+    __device__ __forceinline__ float total() const {
+        const float t = (s01.x + s01.y) + (s23.x + s23.y);
+        return kAdd ? 0.5f * t : t;
+    }
+};
+
+// The score of a key from its 64 head dot products in TMEM (one lane, 64 columns).
+template <bool kAdd>
+__device__ __forceinline__ float head_sum_tmem(uint32_t taddr, const float* w_s) {
+    HeadSum<kAdd> sum;
+    uint32_t v[32];
+    tmem_ld_x32(taddr, v);
+    tmem_ld_wait();
+    sum.add(v, w_s);
+    tmem_ld_x32(taddr + 32, v);
+    tmem_ld_wait();
+    sum.add(v, w_s + 32);
+    return sum.total();
+}
+
 }  // namespace dsrows

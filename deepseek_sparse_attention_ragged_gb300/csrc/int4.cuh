@@ -21,18 +21,11 @@ struct Factors {
     uint32_t s, c;
 };
 
-__device__ __forceinline__ uint32_t bf16_twice(float v) {
-    const __nv_bfloat162 r = __floats2bfloat162_rn(v, v);
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // The scales in the low two bytes of `b`.
 __device__ __forceinline__ float2 scales2(uint32_t b) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(b & 0xFFFFu), __NV_E4M3);
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-
-__device__ __forceinline__ Factors factors(float s) { return {bf16_twice(s), bf16_twice(-136.0f * s)}; }
 
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
@@ -40,11 +33,32 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
     return d;
 }
 
+// The factors of two scales, bytes `at` and `at` + 1 of `b`. A byte's exponent and mantissa
+// in a bf16's places are s 2^-120 (the types' biases are 7 and 127; subnormals agree
+// too), so one exact product gives s. The byte of NaN would give 480: 480 (145/128) 2^119
+// is past the largest bf16 while 448 is not, and infinity times 0 makes it NaN.
+template <int at>
+__device__ __forceinline__ void factors2(uint32_t b, Factors& f0, Factors& f1) {
+    constexpr uint32_t kScale = 0x7B807B80u, kFar = 0x7B117B11u, kMinus136 = 0xC308C308u;
+    const uint32_t x = __byte_perm(b, 0, at == 0 ? 0x4140 : 0x4342) * 16u;
+    uint32_t s = fma_bf16x2(x, kScale, 0x80008000u);
+    s = fma_bf16x2(fma_bf16x2(s, kFar, 0x80008000u), 0u, s);
+    const uint32_t c = fma_bf16x2(s, kMinus136, 0x80008000u);
+    f0 = {__byte_perm(s, 0, 0x1010), __byte_perm(c, 0, 0x1010)};
+    f1 = {__byte_perm(s, 0, 0x3232), __byte_perm(c, 0, 0x3232)};
+}
+
 // One word's 8 values as bf16 pairs: word j holds values 2 j and 2 j + 1. 0x4300 | (n + 8)
-// is 128 + 8 + n in bf16, so (136 + n) s - 136 s is n s, which is exact in bf16.
+// is 128 + 8 + n in bf16, so (136 + n) s - 136 s is n s, which is exact in bf16. The mask
+// and the exponent are one instruction (with both as constants it became two: 64 of the
+// 311 ALU instructions of a key in the indexer).
 __device__ __forceinline__ void widen(uint32_t word, Factors f, uint32_t* out) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) out[j] = fma_bf16x2(((word >> (4 * j)) & 0x000F000Fu) | 0x43004300u, f.s, f.c);
+    for (int j = 0; j < 4; ++j) {
+        uint32_t t;
+        asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(t) : "r"(word >> (4 * j)), "r"(0x43004300u));
+        out[j] = fma_bf16x2(t, f.s, f.c);
+    }
 }
 
 // Quantise a group: 16 values to two words and the scale byte; with `held` the

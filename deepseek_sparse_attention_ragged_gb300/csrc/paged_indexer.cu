@@ -13,16 +13,22 @@
 // straight into the swizzled operand layout.
 //
 // 4-bit pages: 72 bytes a key instead of 256, so the tile's work in the SM counts
-// as much as the stream. Bulk copies bring whole pages (or a page's 128-row
+// more than the stream. Bulk copies bring whole pages (or a page's 128-row
 // slices) into a ring; a thread reads one key's values and scales, widens them to
-// bf16 (one shift, one mask and one packed FMA for two values, exact) and stores
-// them into TMEM, where they are the A operand of the MMAs: the widened key never
+// bf16 (a shift, a mask and a packed FMA for two values, exact) and stores them
+// into TMEM, where they are the A operand of the MMAs: the widened key never
 // passes through shared memory, whose bandwidth (32 KB written and 32 KB read
-// again a tile) would be the bound otherwise. Two sets of four widening warps take
-// alternate tiles, each with its own A and accumulator columns.
+// again a tile) would be the bound otherwise. The instructions of the widening
+// and of the head sums are the bound: 8 x 131072 keys take 20.8 us, of which the
+// loads alone are 14.6 us (75.5 MB: 11.1 us at the measured copy bandwidth), and
+// 17.0 us without the head sums; the MMAs hardly count (21.1 us with one of
+// eight). Steps, in us: one issuing thread 34.7; the issuer's warp kept uniform 26.6
+// (a divergent thread took 80 cycles an MMA, a uniform warp 25); four widening sets
+// and two issuers 25.3; the mask and exponent of a value in one instruction 23.1;
+// the polling loads 21.5; shared-space pointers and running indexes 20.8.
 //
-// Warp roles: 0 loads, 1 owns TMEM and issues the MMAs, 2..5 run the epilogue,
-// 6..13 widen (4-bit pages).
+// Warp roles: 0 loads, the next kIssuers issue the MMAs (warp 1 owns TMEM), then
+// kEpiSets epilogue sets of four warps and (4-bit pages) kWideSets widening sets.
 
 #include "common.cuh"
 #include "head_sum.cuh"
@@ -40,34 +46,45 @@ constexpr int kQHalf = kIdxHeads * 64 * 2;         // one 64-column block of the
 constexpr int kInt4Row = kIdxDim / 2 + kIdxDim / int4::kGroup;  // 72 bytes
 constexpr int kInt4Tile = kTileKeys * kInt4Row;
 constexpr int kKeyWords = kIdxDim / 2;             // TMEM columns of a widened key (bf16 pairs)
-constexpr int kEpiWarps = 4;
+constexpr int kIssuers = 2;   // warps that issue MMAs, each every second tile
+constexpr int kEpiSets = 2;   // of four epilogue warps, each every second tile
+constexpr int kWideSets = 4;  // of four widening warps, each every fourth tile
+constexpr int kBufs = 4;    // accumulators, and widened tiles
 
 template <bool kInt4>
 struct Shape {
     static constexpr int kStages = kInt4 ? 12 : 4;
+    static constexpr int kLap = 4;  // tiles whose loads are in the lanes' hands
     static constexpr int kStageBytes = kInt4 ? kInt4Tile : kBf16Tile;
-    static constexpr int kSets = 2;                // of four widening warps
-    static constexpr int kThreads = 64 + 32 * kEpiWarps + (kInt4 ? 32 * 4 * kSets : 0);
+    static constexpr int kThreads = 32 * (1 + kIssuers) + 128 * (kEpiSets + (kInt4 ? kWideSets : 0));
     static constexpr uint32_t kAccCols = kIdxHeads;
-    static constexpr uint32_t kKeyCol = 2 * kAccCols;  // widened keys: kSets * kKeyWords columns
-    static constexpr uint32_t kTmemCols = kInt4 ? 256 : 128;
+    static constexpr uint32_t kKeyCol = kBufs * kAccCols;  // widened keys: kBufs * kKeyWords columns
+    static constexpr uint32_t kTmemCols = kInt4 ? 512 : 256;
     static constexpr size_t keys = 0;
     static constexpr size_t q = keys + (size_t)kStages * kStageBytes;
-    static constexpr size_t bars = q + 2 * (size_t)kQHalf;
+    static constexpr size_t w = q + 2 * (size_t)kQHalf;
+    static constexpr size_t bars = w + kIdxHeads * 4;
 };
+// A buffer's tiles all belong to one issuer and one set each: a wait on its barrier is then
+// never more than one phase ahead.
+static_assert(Shape<true>::kStages % Shape<true>::kLap == 0 && Shape<false>::kStages % Shape<false>::kLap == 0, "phases");
+static_assert(kBufs % kIssuers == 0 && kBufs % kEpiSets == 0 && kBufs % kWideSets == 0, "phases");
+static_assert(Shape<true>::kStages % kWideSets == 0 && Shape<true>::kStages % kIssuers == 0 &&
+                  Shape<false>::kStages % kIssuers == 0,
+              "phases");
+static_assert(Shape<true>::kKeyCol + kBufs * kKeyWords <= 512, "TMEM columns");
 static_assert(Shape<true>::q % 1024 == 0 && Shape<false>::q % 1024 == 0, "the swizzled query is 1-KiB aligned");
 
 template <bool kInt4>
 struct __align__(8) Bars {
     uint64_t full[Shape<kInt4>::kStages];
     uint64_t empty[Shape<kInt4>::kStages];
-    uint64_t key_full[2];   // a widened tile is in TMEM
-    uint64_t key_empty[2];  // its MMAs are done
-    uint64_t acc_full[2];
-    uint64_t acc_empty[2];
+    uint64_t key_full[kBufs];   // a widened tile is in TMEM
+    uint64_t key_empty[kBufs];  // its MMAs are done
+    uint64_t acc_full[kBufs];
+    uint64_t acc_empty[kBufs];
     uint32_t bad[Shape<kInt4>::kStages];  // sub-pages of the tile without a page
     uint32_t tmem_base;
-    uint32_t abort_flag;
 };
 
 template <bool kInt4>
@@ -85,6 +102,24 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
+// mbar_wait whose first tries read no timer, for waits of a few hundred cycles.
+__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity) {
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, nullptr);
+}
 
 // D[tmem] (+)= A[tmem] * B[smem desc]^T: A's rows are the TMEM lanes, two bf16 a column.
 __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -104,11 +139,13 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
     paged_indexer_kernel(const __grid_constant__ PagedIndexerParams p) {
     using S = Shape<kInt4>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // Aligned by an offset, so that the pointers stay in the shared address space.
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* keys_s = smem + S::keys;
     uint8_t* q_s = smem + S::q;
+    float* w_s = reinterpret_cast<float*>(smem + S::w);
     Bars<kInt4>* bar = reinterpret_cast<Bars<kInt4>*>(smem + S::bars);
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);  // known to be uniform
     const int lane = threadIdx.x & 31;
 
     // This CTA's entry and tiles: first, first + step, ... below n_tiles.
@@ -131,13 +168,12 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
             mbar_init(&bar->empty[s], kInt4 ? 4 : 1);
             bar->bad[s] = 0;
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < kBufs; ++a) {
             mbar_init(&bar->key_full[a], 4);
             mbar_init(&bar->key_empty[a], 1);
             mbar_init(&bar->acc_full[a], 1);
-            mbar_init(&bar->acc_empty[a], kEpiWarps);
+            mbar_init(&bar->acc_empty[a], 4);
         }
-        bar->abort_flag = 0;
         fence_barrier_init();
         if (!kInt4) tma_prefetch_map(&p.kmap);
     }
@@ -154,96 +190,101 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
             const int h = i >> 4, ch = i & 15;
             *reinterpret_cast<uint4*>(q_s + (ch >> 3) * kQHalf + h * 128 + (((ch & 7) ^ (h & 7)) << 4)) = q[i];
         }
+        if (threadIdx.x < kIdxHeads) w_s[threadIdx.x] = p.w[(size_t)p.q_row[e] * kIdxHeads + threadIdx.x];
         fence_proxy_async_smem();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bar->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem_base, 0);
 
     if (warp == 0) {
-        // ---- loads: a lane holds the page id of (tile, sub-page) of the next tiles ----
-        const uint32_t batch = 32 / subs;
+        // ---- loads: a lane owns one sub-page of every lap-th tile: it holds that page's id, issues
+        // its copy as soon as the tile's stage is free, and goes on to its next tile, whose id it
+        // fetched a lap before. The lanes poll together (one tile at a time, this loop took 680
+        // cycles a tile and set the kernel's pace). A lap divides the stages, so the tile that
+        // used a lane's stage last was the lane's own, and no wait is more than one phase ahead.
+        constexpr uint32_t lap = S::kLap;  // tiles of up to 8 sub-pages each: 32 lanes
+        const uint32_t my_tile = lane / subs, my_sub = lane % subs;
+        const uint32_t group = ((1u << subs) - 1) << (my_tile * subs);  // the tile's lanes; subs <= 8
+        const uint32_t sub_bytes = sub_rows * (kInt4 ? kInt4Row : kIdxDim * 2);
         const int32_t* table = p.cache.table + (size_t)e * p.cache.table_stride;
-        auto page_ids = [&](uint32_t k0) -> int32_t {
-            const uint32_t k = k0 + lane / subs;
-            if (k >= mine) return -1;
-            const uint32_t key = (first + k * step) * kTileKeys + (lane % subs) * sub_rows;
-            return key < kv_len ? table[key >> shift] : -1;
-        };
         const uint64_t policy = l2_policy_evict_first();
-        int32_t next = page_ids(0), ids = 0;
+        const uint32_t tiles = my_tile < lap ? mine : 0;  // the other lanes have none
+        auto first_key = [&](uint32_t it) { return (first + it * step) * kTileKeys + my_sub * sub_rows; };
+        auto wants = [&](uint32_t it) { return it < tiles && first_key(it) < kv_len; };
+        auto page_id = [&](uint32_t it) -> int32_t { return wants(it) ? table[first_key(it) >> shift] : -1; };
+        uint32_t it = my_tile, s = my_tile, parity = 1;
+        int32_t id = page_id(it), next = page_id(it + lap);
+        uint64_t start = 0;
         bool ok = true;
-        uint32_t it = 0;
-        for (; it < mine; ++it) {
-            if (it % batch == 0) {
-                ids = next;
-                next = page_ids(it + batch);
+        for (uint32_t tries = 0; ok && __any_sync(0xFFFFFFFFu, it < tiles); ++tries) {
+            const bool want = wants(it);
+            const bool have = want && id >= 0 && (uint32_t)id < p.cache.num_pages;
+            const bool ready = it < tiles && mbar_try_wait(&bar->empty[s], parity);
+            const uint32_t have_bits = __ballot_sync(0xFFFFFFFFu, have) & group;
+            const uint32_t bad_bits = __ballot_sync(0xFFFFFFFFu, want && !have) & group;
+            if ((__ballot_sync(0xFFFFFFFFu, ready) & group) == group) {
+                if (my_sub == 0) {
+                    bar->bad[s] = bad_bits >> (my_tile * subs);
+                    mbar_arrive_expect_tx(&bar->full[s], __popc(have_bits) * sub_bytes);
+                }
+                if (have) {
+                    uint8_t* dst = keys_s + s * S::kStageBytes + my_sub * (kInt4 ? sub_bytes : sub_rows * 128);
+                    const uint32_t in_page = shift <= 7 ? 0u : first_key(it) & ((1u << shift) - 1);
+                    if (!kInt4) {
+                        const int y = (int)(((uint32_t)id << shift) + in_page);
+                        tma_load_2d(dst, &p.kmap, &bar->full[s], 0, y, policy);
+                        tma_load_2d(dst + kHalfBytes, &p.kmap, &bar->full[s], 64, y, policy);
+                    } else {
+                        const uint8_t* page = p.cache.pages + ((size_t)(uint32_t)id << shift) * p.cache.row_bytes;
+                        if (shift <= 7) {
+                            bulk_copy_g2s(dst, page, sub_bytes, &bar->full[s]);
+                        } else {
+                            // A 128-row slice of each plane, and its scales.
+                            for (uint32_t c = 0; c < 5; ++c)
+                                bulk_copy_g2s(dst + c * kTileKeys * 16,
+                                              page + ((size_t)c << shift) * 16 + (size_t)in_page * (c < 4 ? 16 : 8),
+                                              kTileKeys * (c < 4 ? 16 : 8), &bar->full[s]);
+                        }
+                    }
+                }
+                it += lap;
+                if ((s += lap) >= S::kStages) s -= S::kStages, parity ^= 1;
+                id = next;
+                next = page_id(it + lap);
+                start = 0;
             }
-            const uint32_t s = it % S::kStages;
-            ok = mbar_wait(&bar->empty[s], ((it / S::kStages) & 1) ^ 1, nullptr);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
-                ok = false;
-                break;
-            }
-            const uint32_t key0 = (first + it * step) * kTileKeys;
-            const uint32_t in_page = shift < 7 ? 0u : key0 & ((1u << shift) - 1);  // the slice's first row
-            // Lane `sub` has sub-page `sub`'s id.
-            const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, (it % batch) * subs + lane % subs);
-            const bool wanted = (uint32_t)lane < subs && key0 + lane * sub_rows < kv_len;
-            const bool have = wanted && id >= 0 && (uint32_t)id < p.cache.num_pages;
-            const uint32_t have_bits = __ballot_sync(0xFFFFFFFFu, have);
-            const uint32_t bad_bits = __ballot_sync(0xFFFFFFFFu, wanted && !have);
-            const uint32_t sub_bytes = sub_rows * (kInt4 ? kInt4Row : kIdxDim * 2);
-            uint8_t* dst = keys_s + (size_t)s * S::kStageBytes;
-            if (lane == 0) {
-                bar->bad[s] = bad_bits;
-                mbar_arrive_expect_tx(&bar->full[s], __popc(have_bits) * sub_bytes);
+            if ((tries & 63) == 63) {  // bounded, as every wait
+                const uint64_t now = global_timer_ns();
+                if (start == 0) start = now;
+                ok = !__any_sync(0xFFFFFFFFu, it < tiles && now - start > kWaitBudgetNs);
             }
             __syncwarp();
-            if (kInt4) {
-                if (shift < 7) {
-                    if (have)
-                        bulk_copy_g2s(dst + lane * sub_bytes, p.cache.pages + (size_t)(uint32_t)id * sub_bytes,
-                                      sub_bytes, &bar->full[s]);
-                } else if (have_bits && lane < 5) {
-                    // The slice's rows of each plane, and their scales.
-                    const uint8_t* page = p.cache.pages + ((size_t)(uint32_t)id << shift) * kInt4Row;
-                    const uint32_t width = lane < 4 ? 16 : 8;
-                    bulk_copy_g2s(dst + lane * kTileKeys * 16,
-                                  page + ((size_t)lane << shift) * 16 + (size_t)in_page * width, kTileKeys * width,
-                                  &bar->full[s]);
-                }
-            } else if (have) {
-                const int y = (int)(((uint32_t)id << shift) + in_page);
-                uint8_t* d = dst + lane * sub_rows * 128;
-                tma_load_2d(d, &p.kmap, &bar->full[s], 0, y, policy);
-                tma_load_2d(d + kHalfBytes, &p.kmap, &bar->full[s], 64, y, policy);
-            }
         }
-        if (!ok && lane == 0) atomicExch(&bar->abort_flag, 1u);
-        // Every load this warp issued has landed before the CTA exits.
-        for (uint32_t k = it > (uint32_t)S::kStages ? it - S::kStages : 0; k < it; ++k)
-            (void)mbar_wait(&bar->full[k % S::kStages], (k / S::kStages) & 1, nullptr);
-    } else if (warp == 1) {
-        // ---- MMA issuer -------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_bf16_f32(kTileKeys, kIdxHeads);
-            const uint32_t b_base = smem_u32(q_s);
-            uint32_t it = 0;
-            for (; it < mine; ++it) {
-                if (*(volatile uint32_t*)&bar->abort_flag) break;
-                const uint32_t a = it & 1, ph = (it >> 1) & 1;
-                const uint32_t s = it % S::kStages;
-                if (kInt4) {
-                    if (!mbar_wait(&bar->key_full[a], ph, nullptr)) break;
-                } else {
-                    if (!mbar_wait(&bar->full[s], (it / S::kStages) & 1, nullptr)) break;
-                }
-                if (!mbar_wait(&bar->acc_empty[a], ph ^ 1, nullptr)) break;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem + a * S::kAccCols;
-                const uint32_t a_base = smem_u32(keys_s + (size_t)s * S::kStageBytes);
+        // Every load has landed before the CTA exits: each lane waits for its last tile of each stage.
+        for (uint32_t k = 0; k < S::kStages / lap && it >= lap && my_tile < lap; ++k) {
+            it -= lap;
+            s = it % S::kStages;
+            (void)mbar_wait(&bar->full[s], (it / S::kStages) & 1, nullptr);
+        }
+    } else if (warp <= kIssuers) {
+        // ---- MMA issuer: the whole warp runs the loop, so that addresses and descriptors
+        // stay in uniform registers, and one elected lane executes each MMA -----------------
+        constexpr uint32_t idesc = idesc_bf16_f32(kTileKeys, kIdxHeads);
+        const uint32_t b_base = smem_u32(q_s);
+        uint32_t it = warp - 1, a = it, s = it, ph = 0, sph = 0;  // tile, buffer, stage, their phases
+        for (; it < mine; it += kIssuers) {
+            if (!wait_short(&bar->acc_empty[a], ph ^ 1)) break;
+            if (kInt4) {
+                if (!wait_short(&bar->key_full[a], ph)) break;
+            } else {
+                if (!wait_short(&bar->full[s], sph)) break;
+            }
+            tc_fence_after();
+            const uint32_t d_tmem = tmem + a * S::kAccCols;
+            const uint32_t a_base = smem_u32(keys_s + (size_t)s * S::kStageBytes);
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kIdxDim / 16; ++kk) {
                     const uint32_t koff = (uint32_t)(kk & 3) * 32;  // 16 bf16 inside the 128-byte row
@@ -257,77 +298,72 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
                 umma_commit(kInt4 ? &bar->key_empty[a] : &bar->empty[s]);
                 umma_commit(&bar->acc_full[a]);
             }
-            // The MMAs issued are done before TMEM is freed.
-            for (uint32_t k = it > 2 ? it - 2 : 0; k < it; ++k)
-                (void)mbar_wait(&bar->acc_full[k & 1], (k >> 1) & 1, nullptr);
+            __syncwarp();
+            if ((a += kIssuers) >= kBufs) a -= kBufs, ph ^= 1;
+            if ((s += kIssuers) >= S::kStages) s -= S::kStages, sph ^= 1;
         }
-        __syncwarp();
-    } else if (warp < 2 + kEpiWarps) {
-        // ---- epilogue: one key per thread ---------------------------------------------
+        // The MMAs issued are done before TMEM is freed.
+        for (uint32_t k = it > kBufs ? it - kBufs : warp - 1; k < it; k += kIssuers)
+            (void)mbar_wait(&bar->acc_full[k % kBufs], (k / kBufs) & 1, nullptr);
+    } else if (warp < 1 + kIssuers + 4 * kEpiSets) {
+        // ---- epilogue: one key per thread, alternate tiles per set -----------------------
+        const int set = (warp - 1 - kIssuers) >> 2;
         const int quarter = warp & 3;
         const uint64_t keep = l2_policy_evict_last();  // the top-k reads the scores next
-        float wr[kIdxHeads];
-        const float4* w = reinterpret_cast<const float4*>(p.w + (size_t)p.q_row[e] * kIdxHeads);
-        const bool w16 = (reinterpret_cast<uintptr_t>(p.w) & 15) == 0;
-#pragma unroll
-        for (int h = 0; h < kIdxHeads; h += 4) {
-            if (w16) {
-                *reinterpret_cast<float4*>(&wr[h]) = w[h / 4];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) wr[h + i] = reinterpret_cast<const float*>(w)[h + i];
-            }
-        }
         float* out = p.scores + (size_t)e * p.score_stride;
-        for (uint32_t it = 0; it < mine; ++it) {
-            const uint32_t a = it & 1, ph = (it >> 1) & 1;
-            const uint32_t j = (first + it * step) * kTileKeys + quarter * 32 + lane;
+        uint32_t a = set, ph = 0;  // buffer and its phase
+        uint32_t j = (first + set * step) * kTileKeys + quarter * 32 + lane;
+        for (uint32_t it = set; it < mine; it += kEpiSets, j += kEpiSets * step * kTileKeys) {
             // A bf16 key without a page is left out here (a widened one is NaN).
             bool have = true;
             if (!kInt4 && j < kv_len) {
                 const int32_t id = p.cache.table[(size_t)e * p.cache.table_stride + (j >> shift)];
                 have = id >= 0 && (uint32_t)id < p.cache.num_pages;
             }
-            if (!mbar_wait(&bar->acc_full[a], ph, nullptr)) break;
+            if (!wait_short(&bar->acc_full[a], ph)) break;
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * S::kAccCols;
-            uint32_t v[64];
-            tmem_ld_x32(taddr, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-            tmem_ld_x32(taddr + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-            tmem_ld_wait();
+            float sc = head_sum_tmem<true>(taddr, w_s);
+            if (__any_sync(0xFFFFFFFFu, !finite_f(sc))) {
+                const float again = head_sum_tmem<false>(taddr, w_s);
+                sc = finite_f(sc) ? sc : again;
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar->acc_empty[a]);
-            const float sc = head_sum(v, wr, nullptr);
             if (j < kv_len) st_global_hint(out + j, finite_f(sc) && have ? sc : -INFINITY, keep);
+            if ((a += kEpiSets) >= kBufs) a -= kBufs, ph ^= 1;
         }
     } else {
         // ---- widening: one key per thread, alternate tiles per set ----------------------
-        const int set = (warp - 2 - kEpiWarps) >> 2;
+        const int set = (warp - 1 - kIssuers - 4 * kEpiSets) >> 2;
         const int quarter = warp & 3;
         const uint32_t key = quarter * 32 + lane;
         const uint32_t sub = key / sub_rows, row = key % sub_rows;
-        const uint32_t base = sub * sub_rows * kInt4Row;
-        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + S::kKeyCol + set * kKeyWords;
-        for (uint32_t it = set; it < mine; it += S::kSets) {
-            const uint32_t s = it % S::kStages;
-            if (!mbar_wait(&bar->full[s], (it / S::kStages) & 1, nullptr)) break;
-            const uint8_t* src = keys_s + (size_t)s * S::kStageBytes + base;
+        const uint8_t* row_s = keys_s + sub * sub_rows * kInt4Row + row * 16;
+        const uint8_t* scale_s = keys_s + (sub * kInt4Row + kIdxDim / 2) * sub_rows + row * 8;
+        const uint32_t tcol = tmem + ((uint32_t)(quarter * 32) << 16) + S::kKeyCol;
+        uint32_t a = set, s = set, ph = 0, sph = 0;  // buffer, stage, their phases
+        for (uint32_t it = set; it < mine; it += kWideSets) {
+            const uint32_t taddr = tcol + a * kKeyWords;
+            if (!wait_short(&bar->full[s], sph)) break;
             uint4 d[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) d[c] = *reinterpret_cast<const uint4*>(src + (c * sub_rows + row) * 16);
-            const uint2 sc = *reinterpret_cast<const uint2*>(src + sub_rows * (kIdxDim / 2) + row * 8);
-            const bool bad = (bar->bad[s] >> sub) & 1;
+            for (int c = 0; c < 4; ++c)
+                d[c] = *reinterpret_cast<const uint4*>(row_s + s * S::kStageBytes + c * sub_rows * 16);
+            uint2 sc = *reinterpret_cast<const uint2*>(scale_s + s * S::kStageBytes);
+            // A key without a page becomes NaN (its score -inf).
+            if ((bar->bad[s] >> sub) & 1) sc.x = sc.y = 0x7F7F7F7Fu;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar->empty[s]);
-            if (!mbar_wait(&bar->key_empty[set], ((it >> 1) & 1) ^ 1, nullptr)) break;
+            if (!wait_short(&bar->key_empty[a], ph ^ 1)) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                // Two groups a plane. A key without a page becomes NaN (its score -inf).
-                const float2 s2 = int4::scales2((c & 1 ? (c & 2 ? sc.y : sc.x) >> 16 : (c & 2 ? sc.y : sc.x)));
-                const int4::Factors f0 = int4::factors(bad ? __int_as_float(0x7FC00000) : s2.x);
-                const int4::Factors f1 = int4::factors(bad ? __int_as_float(0x7FC00000) : s2.y);
+                int4::Factors f0, f1;  // two groups a plane
+                const uint32_t b = c < 2 ? sc.x : sc.y;
+                if (c % 2 == 0) int4::factors2<0>(b, f0, f1);
+                else int4::factors2<2>(b, f0, f1);
                 uint32_t r[16];
                 int4::widen(d[c].x, f0, r);
                 int4::widen(d[c].y, f0, r + 4);
@@ -338,7 +374,9 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->key_full[set]);
+            if (lane == 0) mbar_arrive(&bar->key_full[a]);
+            if ((a += kWideSets) >= kBufs) a -= kBufs, ph ^= 1;
+            if ((s += kWideSets) >= S::kStages) s -= S::kStages, sph ^= 1;
         }
     }
 

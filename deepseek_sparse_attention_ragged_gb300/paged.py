@@ -8,13 +8,15 @@ check tensor types, sizes and devices, and enqueue on the tensors' device.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+from array import array
+from itertools import chain
+from operator import add
 from typing import Optional
 
 import torch
 
-from . import DIM, HEADS, INDEX_DIM, INDEX_HEADS, Row, _check, _table, _workspace_for, load
+from . import DIM, DS_OK, HEADS, INDEX_DIM, INDEX_HEADS, _check, _table, _workspace_for, load
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # DS_BF16, DS_F16, DS_F32
 _LAYOUTS = {"interleaved": 0, "half": 1}                           # DS_ROPE_*
@@ -37,14 +39,13 @@ def declare(lib) -> None:
     vp, sz, i32, u32, u64, f32, f64 = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint32,
                                        ctypes.c_uint64, ctypes.c_float, ctypes.c_double)
     rope, cache = ctypes.POINTER(_Rope), ctypes.POINTER(_PagedCache)
-    rows = ctypes.POINTER(Row)
     lib.ds_rows_rope_turns.argtypes = [u32, f64, f64, u32, f64, f64, vp]
     lib.ds_rows_rope.argtypes = [rope, vp, u64, u64, vp, u64, u64, i32, u64, u32, u32, vp, i32, vp]
     lib.ds_rows_page_bytes.argtypes = [u32, u32, i32]
     lib.ds_rows_page_bytes.restype = sz
     lib.ds_rows_append.argtypes = [cache, vp, u64, i32, u64, vp, vp, rope, vp, vp, vp, vp]
-    lib.ds_rows_indexer_score_paged.argtypes = [i32, rows, cache, vp, vp, vp, sz, vp]
-    lib.ds_rows_sparse_attn_paged.argtypes = [i32, rows, cache, vp, vp, sz, vp, f32, vp, vp, vp, sz, vp]
+    lib.ds_rows_indexer_score_paged.argtypes = [i32, vp, cache, vp, vp, vp, sz, vp]
+    lib.ds_rows_sparse_attn_paged.argtypes = [i32, vp, cache, vp, vp, sz, vp, f32, vp, vp, vp, sz, vp]
     for f in (lib.ds_rows_rope_turns, lib.ds_rows_rope, lib.ds_rows_append, lib.ds_rows_indexer_score_paged,
               lib.ds_rows_sparse_attn_paged):
         f.restype = i32
@@ -54,14 +55,14 @@ def declare(lib) -> None:
 # argument checks
 # ---------------------------------------------------------------------------
 
-def _tensor(t, name: str, dtype, device, numel: int):
-    """`t` must be a contiguous tensor of `dtype` on `device` holding >= numel elements."""
+def _tensor(t, name: str, dtype, index: int, numel: int):
+    """The address of `t`: a contiguous tensor of `dtype` on CUDA device `index` holding >= numel elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if t.numel() < numel:
@@ -69,29 +70,41 @@ def _tensor(t, name: str, dtype, device, numel: int):
     return t.data_ptr()
 
 
-def _cuda(t, name: str) -> torch.device:
+def _cuda(t, name: str) -> int:
+    """The index of a CUDA tensor's device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return index
 
 
-def _stream_of(stream, device: torch.device) -> int:
+# The current stream's handle by device index, without building a Stream object where
+# this torch has the call for it (2 us of a call's host time).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _stream_of(stream, index: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current_raw_stream(index)
     if isinstance(stream, torch.cuda.Stream):
-        if stream.device != device:
-            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+        if stream.device.index != index:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{index}")
         return stream.cuda_stream
     return int(stream)
 
 
-def _on(device: torch.device):
-    """The device of the call's tensors as the current one."""
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _call(index: int, fn, *args) -> None:
+    """Call an entry point with the tensors' device as the current one."""
+    if torch.cuda.current_device() == index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args)
+    if rc != DS_OK:
+        _check(load(), rc)
 
 
 def _code(table, value, name: str) -> int:
@@ -102,12 +115,15 @@ def _code(table, value, name: str) -> int:
 
 
 def _rows(rows):
-    """A row table (an array of Row) and its entries as tuples."""
-    rows = list(rows)
-    if all(type(r) is tuple and len(r) == 4 for r in rows) and rows:
-        return (Row * len(rows))(*rows), rows
-    tab, n = _table(rows)
-    return tab, [(tab[e].kv_len, tab[e].width, tab[e].index_offset, tab[e].q_row) for e in range(n)]
+    """A row table as ds_row_t words, and its columns (kv_len, width, index_offset, q_row)."""
+    try:
+        words = array("I", chain.from_iterable(rows))
+    except TypeError:  # Row structures, or objects with their fields
+        tab, n = _table(rows)
+        words = array("I", chain.from_iterable((r.kv_len, r.width, r.index_offset, r.q_row) for r in tab[:n]))
+    if len(words) == 0 or len(words) % 4:
+        raise ValueError("rows must be a nonempty list of (kv_len, width, index_offset, q_row)")
+    return words, words[0::4], words[1::4], words[2::4], words[3::4]
 
 
 # ---------------------------------------------------------------------------
@@ -133,7 +149,7 @@ class Rope:
         _check(lib, lib.ds_rows_rope_turns(int(rot_dim), float(base), float(factor), int(original_len),
                                            float(beta_fast), float(beta_slow), host.data_ptr()))
         self.turns = host.to(torch.device(device if device is not None else "cuda"))
-        self.device = _cuda(self.turns, "the rotation's table")
+        self.device_index = _cuda(self.turns, "the rotation's table")
         self.rot_dim, self.first, self.layout, self.magnitude = int(rot_dim), int(first), layout, float(magnitude)
         self._c = _Rope(self.turns.data_ptr(), self.first, self.rot_dim, code, self.magnitude)
         self._ref = ctypes.byref(self._c)
@@ -149,26 +165,27 @@ def ds_rows_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, out: torc
     of out to that of x."""
     lib = load()
     dev = _cuda(x, "x")
-    _cuda(out, "out")
-    if rope.device != dev or out.device != dev:
-        raise ValueError(f"x is on {dev}, the rotation on {rope.device} and out on {out.device}")
-    if x.dim() not in (2, 3):
-        raise ValueError(f"x must be [tokens, heads, dim] or [tokens, dim], got {tuple(x.shape)}")
-    if out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out must have the shape and type of x")
+    if _cuda(out, "out") != dev or rope.device_index != dev:
+        raise ValueError(f"x is on {x.device}, out on {out.device} and the rotation on {rope.turns.device}")
     code = _code(_DTYPES, x.dtype, "the type of x")
-    tokens, dim = x.shape[0], x.shape[-1]
-    heads = x.shape[1] if x.dim() == 3 else 1
-    xs, os_ = x.stride(), out.stride()
+    shape, xs, os_ = x.shape, x.stride(), out.stride()
+    if out.shape != shape or out.dtype != x.dtype:
+        raise ValueError("out must have the shape and type of x")
+    if len(shape) == 3:
+        tokens, heads, dim = shape
+        xh, oh = xs[1], os_[1]
+    elif len(shape) == 2:
+        tokens, dim = shape
+        heads, xh, oh = 1, 0, 0
+    else:
+        raise ValueError(f"x must be [tokens, heads, dim] or [tokens, dim], got {tuple(shape)}")
     if dim > 1 and (xs[-1] != 1 or os_[-1] != 1):
         raise ValueError("the elements of a row of x and out must be contiguous")
     ptr = _tensor(positions, "positions", torch.int32, dev, tokens)
     if tokens == 0 or heads == 0:
         return
-    xh, oh = (xs[1], os_[1]) if x.dim() == 3 else (0, 0)
-    with _on(dev):
-        _check(lib, lib.ds_rows_rope(rope._ref, x.data_ptr(), xs[0], xh, out.data_ptr(), os_[0], oh, code, tokens,
-                                     heads, dim, ptr, 1 if inverse else 0, _stream_of(stream, dev)))
+    _call(dev, lib.ds_rows_rope, rope._ref, x.data_ptr(), xs[0], xh, out.data_ptr(), os_[0], oh, code, tokens, heads,
+          dim, ptr, 1 if inverse else 0, _stream_of(stream, dev))
 
 
 # ---------------------------------------------------------------------------
@@ -193,7 +210,7 @@ class PagedCache:
 
     def __init__(self, pages: torch.Tensor, page_table: torch.Tensor, page_size: int, dim: int, fmt: str):
         size = ds_rows_page_bytes(page_size, dim, fmt)
-        self.device = _cuda(pages, "pages")
+        self.device_index = _cuda(pages, "pages")
         if not pages.is_contiguous():
             raise ValueError("pages must be contiguous")
         total = pages.numel() * pages.element_size()
@@ -201,7 +218,7 @@ class PagedCache:
             raise ValueError(f"pages holds {total} bytes, not a whole number of {size}-byte pages")
         if page_table.dim() != 2 or page_table.numel() == 0:
             raise ValueError("page_table must be [entries, pages per entry]")
-        _tensor(page_table, "page_table", torch.int32, self.device, 1)
+        _tensor(page_table, "page_table", torch.int32, self.device_index, 1)
         self.pages, self.page_table = pages, page_table
         self.page_size, self.dim, self.format, self.num_pages = int(page_size), int(dim), fmt, total // size
         self._c = _PagedCache(pages.data_ptr(), page_table.data_ptr(), page_table.shape[0], page_table.shape[1],
@@ -228,12 +245,13 @@ def ds_rows_append(cache: PagedCache, x: torch.Tensor, seq: torch.Tensor, slot: 
     them; invalid (optional, int32 [tokens]) 1 where a row could not be written."""
     lib = load()
     dev = _cuda(x, "x")
-    if cache.device != dev or (rope is not None and rope.device != dev):
-        raise ValueError(f"x is on {dev}, the cache on {cache.device}"
-                         + (f", the rotation on {rope.device}" if rope is not None else ""))
+    if cache.device_index != dev or (rope is not None and rope.device_index != dev):
+        raise ValueError(f"x is on {x.device}, the cache on {cache.pages.device}"
+                         + (f", the rotation on {rope.turns.device}" if rope is not None else ""))
     if x.dim() != 2 or x.shape[1] != cache.dim:
         raise ValueError(f"x must be [tokens, {cache.dim}], got {tuple(x.shape)}")
-    if x.stride(1) != 1:
+    row, element = x.stride()
+    if element != 1:
         raise ValueError("the elements of a row of x must be contiguous")
     code = _code(_DTYPES, x.dtype, "the type of x")
     n = x.shape[0]
@@ -244,26 +262,24 @@ def ds_rows_append(cache: PagedCache, x: torch.Tensor, seq: torch.Tensor, slot: 
     pi = None if invalid is None else _tensor(invalid, "invalid", i32, dev, n)
     if n == 0:
         return
-    with _on(dev):
-        _check(lib, lib.ds_rows_append(cache._ref, x.data_ptr(), x.stride(0) if n > 1 else 0, code, n, ps, pl,
-                                       None if rope is None else rope._ref, pp, pv, pi, _stream_of(stream, dev)))
+    _call(dev, lib.ds_rows_append, cache._ref, x.data_ptr(), row if n > 1 else 0, code, n, ps, pl,
+          None if rope is None else rope._ref, pp, pv, pi, _stream_of(stream, dev))
 
 
 def ds_rows_indexer_score_paged(rows, q_index: torch.Tensor, w_index: torch.Tensor, keys: PagedCache,
                                 scores: torch.Tensor, score_stride: Optional[int] = None, stream=None) -> None:
     """ds_rows_indexer_score with entry e's keys in entry e of a paged cache (dim 128)."""
     lib = load()
-    dev = keys.device
-    tab, rl = _rows(rows)
-    q_rows, longest = max(r[3] for r in rl) + 1, max(r[0] for r in rl)
+    dev = keys.device_index
+    words, kv_len, _, _, q_row = _rows(rows)
+    n, q_rows = len(kv_len), max(q_row) + 1
     if score_stride is None:
-        score_stride = scores.shape[-1] if scores.dim() > 1 else longest
+        score_stride = scores.shape[-1] if scores.dim() > 1 else max(kv_len)
     pq = _tensor(q_index, "q_index", torch.bfloat16, dev, q_rows * INDEX_HEADS * INDEX_DIM)
     pw = _tensor(w_index, "w_index", torch.float32, dev, q_rows * INDEX_HEADS)
-    po = _tensor(scores, "scores", torch.float32, dev, (len(rl) - 1) * score_stride + rl[-1][0])
-    with _on(dev):
-        _check(lib, lib.ds_rows_indexer_score_paged(len(rl), tab, keys._ref, pq, pw, po, score_stride,
-                                                    _stream_of(stream, dev)))
+    po = _tensor(scores, "scores", torch.float32, dev, (n - 1) * score_stride + kv_len[-1])
+    _call(dev, lib.ds_rows_indexer_score_paged, n, words.buffer_info()[0], keys._ref, pq, pw, po, score_stride,
+          _stream_of(stream, dev))
 
 
 def ds_rows_sparse_attn_paged(rows, q_attn: torch.Tensor, sinks: torch.Tensor, sinks_row_stride: int,
@@ -272,20 +288,19 @@ def ds_rows_sparse_attn_paged(rows, q_attn: torch.Tensor, sinks: torch.Tensor, s
                               stream=None) -> None:
     """ds_rows_sparse_attn with entry e's KV rows in entry e of a paged cache (dim 512)."""
     lib = load()
-    dev = kv.device
-    tab, rl = _rows(rows)
-    q_rows = max(r[3] for r in rl) + 1
+    dev = kv.device_index
+    words, kv_len, width, offset, q_row = _rows(rows)
+    n, q_rows = len(kv_len), max(q_row) + 1
     bf16 = torch.bfloat16
     pq = _tensor(q_attn, "q_attn", bf16, dev, q_rows * HEADS * DIM)
     po = _tensor(out, "out", bf16, dev, q_rows * HEADS * DIM)
     ps = _tensor(sinks, "sinks", torch.float32, dev,
                  HEADS if sinks_row_stride == 0 else (q_rows - 1) * sinks_row_stride + HEADS)
-    px = _tensor(indices, "indices", torch.int32, dev, max(r[2] + r[1] for r in rl))
+    px = _tensor(indices, "indices", torch.int32, dev, max(map(add, offset, width)))
     pi = None if invalid is None else _tensor(invalid, "invalid", torch.int32, dev, q_rows * HEADS)
-    with _on(dev):
-        raw = _stream_of(stream, dev)
-        if workspace_t is None:
-            workspace_t = _workspace_for(rl, dev, raw)
-        pw = _tensor(workspace_t, "workspace", torch.uint8, dev, 0)
-        _check(lib, lib.ds_rows_sparse_attn_paged(len(rl), tab, kv._ref, pq, ps, sinks_row_stride, px, scale, po, pi,
-                                                  pw, workspace_t.numel(), raw))
+    raw = _stream_of(stream, dev)
+    if workspace_t is None:
+        workspace_t = _workspace_for(list(zip(kv_len, width, offset, q_row)), kv.pages.device, raw)
+    pw = _tensor(workspace_t, "workspace", torch.uint8, dev, 0)
+    _call(dev, lib.ds_rows_sparse_attn_paged, n, words.buffer_info()[0], kv._ref, pq, ps, sinks_row_stride, px, scale,
+          po, pi, pw, workspace_t.numel(), raw)
