@@ -29,8 +29,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     constexpr int G = int4::kGroup;
     constexpr int LANES = kDimOf / G;  // lanes of a row
     constexpr int ROWS = kAppendThreads / LANES;
-    __shared__ float2 trig_s[ROWS][kDimOf / 2];
-    __shared__ float row_s[ROWS][G][LANES];  // element e of a row at [e mod 16][e / 16]
+    // Pair i of a row at [i mod 16][i / 16] and element e at [e mod 16][e / 16], padded: lanes read
+    // with strides of 8 or 16 pairs and 16 elements, and the rows of a warp lie in different banks.
+    constexpr int W = kDimOf / 32 + 1;
+    constexpr int PAD = LANES == 32 ? 0 : 4;
+    __shared__ float2 trig_s[ROWS][16 * W + PAD];
+    __shared__ float row_s[ROWS][G * LANES + 2 * PAD];
+    auto pair_at = [](uint32_t i) { return (i % 16) * W + i / 16; };
+    auto element_at = [](uint32_t e) { return (e % G) * LANES + e / G; };
     pdl_trigger();
     const int r = threadIdx.x / LANES, g = threadIdx.x % LANES;
     const uint64_t token = (uint64_t)blockIdx.x * ROWS + r;
@@ -78,10 +84,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         const uint32_t pairs = p.rope.rot / 2;
         if (ok) {
             for (uint32_t i = g; i < pairs; i += LANES)
-                trig_s[r][i] = rope_turn(pos, p.rope.turns[i], p.rope.magnitude, false);
+                trig_s[r][pair_at(i)] = rope_turn(pos, p.rope.turns[i], p.rope.magnitude, false);
             if (p.half)
 #pragma unroll
-                for (int i = 0; i < G; ++i) row_s[r][i][g] = y[i];
+                for (int i = 0; i < G; ++i) row_s[r][element_at(g * G + i)] = y[i];
         }
         __syncwarp();
         if (ok) {
@@ -93,8 +99,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
                     if (e < p.rope.rot) {
                         const bool low = e < pairs;
                         const uint32_t other = (low ? e + pairs : e - pairs) + p.rope.first;
-                        const float z = row_s[r][other % G][other / G];
-                        const float2 cs = trig_s[r][low ? e : e - pairs];
+                        const float z = row_s[r][element_at(other)];
+                        const float2 cs = trig_s[r][pair_at(low ? e : e - pairs)];
                         float a = low ? y[i] : z, b = low ? z : y[i];
                         rope_pair(a, b, cs);
                         y[i] = low ? a : b;
@@ -103,7 +109,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             } else {
 #pragma unroll
                 for (int i = 0; i < G; i += 2)  // first is even: a pair lies in one lane
-                    if (e0 + i < p.rope.rot) rope_pair(y[i], y[i + 1], trig_s[r][(e0 + i) / 2]);
+                    if (e0 + i < p.rope.rot) rope_pair(y[i], y[i + 1], trig_s[r][pair_at((e0 + i) / 2)]);
             }
         }
     }

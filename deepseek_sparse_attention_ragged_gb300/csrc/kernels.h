@@ -142,7 +142,8 @@ struct RopeCall {
     uint32_t inplace;  // out is x: only the rotated elements are touched
     uint32_t inverse;
     // Set by the launcher.
-    uint32_t units;    // rotation units of a row: a thread's share of its pairs
+    uint32_t units;    // threads of a row that rotate its pairs
+    uint32_t copies;   // threads of a row that copy the elements outside the range (not in place)
     uint32_t group;    // heads that one thread rotates with the same angles
     uint32_t groups;   // head groups of a token
     uint32_t slots;    // (token, head group) items of a block

@@ -16,6 +16,9 @@ namespace dsrows {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeThreadsMax = 544;   // one row a block: 1024 / 2 units and one more, in whole warps
+constexpr uint32_t kGroupMax = 16;
+constexpr uint32_t kFull = 512;        // threads an SM keeps busy with
 constexpr int kHeadsInFlight = 4;  // heads whose loads a thread issues before it uses the first
 
 template <typename T>
@@ -72,15 +75,14 @@ constexpr int piece_len() {
 }  // namespace
 
 template <typename T, bool kHalf, bool kWide>
-__global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeCall p) {
+__global__ void __launch_bounds__(kRopeThreadsMax) rope_kernel(const __grid_constant__ RopeCall p) {
     constexpr int N = piece_len<T, kHalf, kWide>();
+    constexpr int M = kWide ? N : 1;  // a piece outside the range
     constexpr int PAIRS = kHalf ? N : N / 2;
-    struct __align__(16) Unit {
-        Piece<T, N> a, b;  // b: the second half's piece (kHalf)
-    };
     pdl_trigger();
-    const uint32_t u = threadIdx.x % p.units;
-    const uint64_t item = (uint64_t)blockIdx.x * p.slots + threadIdx.x / p.units;
+    const uint32_t units = p.units + p.copies;
+    const uint32_t u = threadIdx.x % units;
+    const uint64_t item = (uint64_t)blockIdx.x * p.slots + threadIdx.x / units;
     const uint64_t token = item / p.groups;
     if (token >= p.tokens) return;
     const uint32_t h0 = (uint32_t)(item - token * p.groups) * p.group;
@@ -90,6 +92,31 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeC
     if (pos < 0) return;
     const T* x = static_cast<const T*>(p.x) + token * p.x_token;
     T* out = static_cast<T*>(p.out) + token * p.out_token;
+    if (u >= p.units) {
+        // Pieces q and q + copies of the elements outside the range.
+        const uint32_t before = p.rope.first / M, skip = p.rope.rot / M, pieces = p.dim / M - skip;
+        const uint32_t q = u - p.units, q2 = q + p.copies;
+        const bool two = q2 < pieces;
+        const uint32_t fa = (q < before ? q : q + skip) * M, fb = two ? (q2 < before ? q2 : q2 + skip) * M : fa;
+        for (uint32_t h = h0; h < h1; h += kHeadsInFlight) {
+            Piece<T, M> a[kHeadsInFlight], b[kHeadsInFlight];
+#pragma unroll
+            for (int k = 0; k < kHeadsInFlight; ++k)
+                if (h + k < h1) {
+                    const T* row = x + (uint64_t)(h + k) * p.x_head;
+                    a[k] = get<T, M, kWide>(row + fa);
+                    if (two) b[k] = get<T, M, kWide>(row + fb);
+                }
+#pragma unroll
+            for (int k = 0; k < kHeadsInFlight; ++k)
+                if (h + k < h1) {
+                    T* row = out + (uint64_t)(h + k) * p.out_head;
+                    put<T, M, kWide>(row + fa, a[k]);
+                    if (two) put<T, M, kWide>(row + fb, b[k]);
+                }
+        }
+        return;
+    }
     const uint32_t fa = p.rope.first + u * N;
     const uint32_t fb = fa + p.rope.rot / 2;
     float2 cs[PAIRS];
@@ -97,13 +124,13 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeC
     for (int i = 0; i < PAIRS; ++i)
         cs[i] = rope_turn(pos, p.rope.turns[u * PAIRS + i], p.rope.magnitude, p.inverse != 0);
     for (uint32_t h = h0; h < h1; h += kHeadsInFlight) {
-        Unit v[kHeadsInFlight];
+        Piece<T, N> a[kHeadsInFlight], b[kHeadsInFlight];  // b: the second half's piece (kHalf)
 #pragma unroll
         for (int k = 0; k < kHeadsInFlight; ++k)
             if (h + k < h1) {
                 const T* row = x + (uint64_t)(h + k) * p.x_head;
-                v[k].a = get<T, N, kWide>(row + fa);
-                if constexpr (kHalf) v[k].b = get<T, N, kWide>(row + fb);
+                a[k] = get<T, N, kWide>(row + fa);
+                if constexpr (kHalf) b[k] = get<T, N, kWide>(row + fb);
             }
 #pragma unroll
         for (int k = 0; k < kHeadsInFlight; ++k)
@@ -111,47 +138,38 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeC
                 T* row = out + (uint64_t)(h + k) * p.out_head;
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) {
-                    T& ta = kHalf ? v[k].a.v[i] : v[k].a.v[(2 * i) % N];
-                    T& tb = kHalf ? v[k].b.v[i] : v[k].a.v[(2 * i + 1) % N];
-                    float a = to_f(ta), b = to_f(tb);
-                    rope_pair(a, b, cs[i]);
-                    ta = from_f<T>(a);
-                    tb = from_f<T>(b);
+                    T& ta = kHalf ? a[k].v[i] : a[k].v[(2 * i) % N];
+                    T& tb = kHalf ? b[k].v[i] : a[k].v[(2 * i + 1) % N];
+                    float va = to_f(ta), vb = to_f(tb);
+                    rope_pair(va, vb, cs[i]);
+                    ta = from_f<T>(va);
+                    tb = from_f<T>(vb);
                 }
-                put<T, N, kWide>(row + fa, v[k].a);
-                if constexpr (kHalf) put<T, N, kWide>(row + fb, v[k].b);
+                put<T, N, kWide>(row + fa, a[k]);
+                if constexpr (kHalf) put<T, N, kWide>(row + fb, b[k]);
             }
-    }
-    if (p.inplace) return;
-    // The elements outside the rotated range, in pieces of M.
-    constexpr int M = kWide ? N : 1;
-    const uint32_t before = p.rope.first / M, skip = p.rope.rot / M, pieces = p.dim / M - skip;
-    for (uint32_t h = h0; h < h1; ++h) {
-        const T* src = x + (uint64_t)h * p.x_head;
-        T* dst = out + (uint64_t)h * p.out_head;
-        for (uint32_t i = u; i < pieces; i += p.units) {
-            const uint32_t f = (i < before ? i : i + skip) * M;
-            put<T, M, kWide>(dst + f, get<T, M, kWide>(src + f));
-        }
     }
 }
 
 template <typename T, bool kHalf, bool kWide>
 static cudaError_t launch(RopeCall& p, int num_sms, cudaStream_t stream, bool pdl) {
     constexpr int N = piece_len<T, kHalf, kWide>();
+    constexpr int M = kWide ? N : 1;
     p.units = p.rope.rot / (kHalf ? 2 * N : N);
-    // Heads per thread: as many as leave two blocks for every SM, at most 8.
+    p.copies = p.inplace ? 0 : (p.dim / M - p.rope.rot / M + 1) / 2;
+    const uint32_t units = p.units + p.copies;  // at most dim / 2 + 1
+    // Heads per thread: as many as leave kFull threads for every SM, at most kGroupMax.
     uint32_t group = 1;
-    while (group < 8 && group < p.heads &&
-           p.tokens * ((p.heads + 2 * group - 1) / (2 * group)) * p.units >= (uint64_t)2 * num_sms * kRopeThreads)
+    while (group < kGroupMax && group < p.heads &&
+           p.tokens * ((p.heads + 2 * group - 1) / (2 * group)) * units >= (uint64_t)kFull * num_sms)
         group *= 2;
     p.group = group;
     p.groups = (p.heads + group - 1) / group;
-    p.slots = p.units >= kRopeThreads ? 1 : kRopeThreads / p.units;
+    p.slots = units >= kRopeThreads ? 1 : kRopeThreads / units;
     const uint64_t items = p.tokens * p.groups;
     const uint64_t blocks = (items + p.slots - 1) / p.slots;
     if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
-    return launch_kernel(rope_kernel<T, kHalf, kWide>, dim3((uint32_t)blocks), dim3(p.units * p.slots), 0, stream, pdl,
+    return launch_kernel(rope_kernel<T, kHalf, kWide>, dim3((uint32_t)blocks), dim3(units * p.slots), 0, stream, pdl,
                          p);
 }
 
