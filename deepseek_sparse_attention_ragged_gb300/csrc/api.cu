@@ -1013,7 +1013,8 @@ int ds_rows_append(const ds_paged_cache_t* cache, const void* x, uint64_t x_stri
         rc = check_rope(rope, dim, positions);
         if (rc) return rc;
         p.rope = {rope->turns, rope->first, rope->rot_dim, rope->magnitude};
-        p.half = rope->layout == DS_ROPE_HALF;
+        p.half = rope->layout == DS_ROPE_HALF ? 1u : 0u;
+        p.whole = rope->first % 16 == 0 && rope->rot_dim % (p.half ? 32 : 16) == 0 ? 1u : 0u;
         p.positions = positions;
     }
     if (tokens == 0) return DS_OK;

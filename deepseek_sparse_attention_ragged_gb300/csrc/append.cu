@@ -42,6 +42,22 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     const uint64_t token = (uint64_t)blockIdx.x * ROWS + r;
     const bool there = token < p.tokens;
     pdl_wait();
+    // The row is fetched while its place is looked up.
+    float y[G];
+    if (there) {
+        const T* x = static_cast<const T*>(p.x) + token * p.x_stride + g * G;
+        if (p.wide) {
+            __align__(16) T v[G];
+#pragma unroll
+            for (int i = 0; i < (int)(G * sizeof(T) / 16); ++i)
+                reinterpret_cast<uint4*>(v)[i] = reinterpret_cast<const uint4*>(x)[i];
+#pragma unroll
+            for (int i = 0; i < G; ++i) y[i] = widen_f(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < G; ++i) y[i] = widen_f(x[i]);
+        }
+    }
     // The row's place. The checks are uniform over its lanes.
     const int32_t seq = there ? p.seq[token] : -1;
     bool ok = false;
@@ -65,21 +81,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     }
     if (there && g == 0 && p.invalid) p.invalid[token] = seq != -1 && !ok ? 1u : 0u;
 
-    float y[G];
-    if (ok) {
-        const T* x = static_cast<const T*>(p.x) + token * p.x_stride + g * G;
-        if (p.wide) {
-            __align__(16) T v[G];
-#pragma unroll
-            for (int i = 0; i < (int)(G * sizeof(T) / 16); ++i)
-                reinterpret_cast<uint4*>(v)[i] = reinterpret_cast<const uint4*>(x)[i];
-#pragma unroll
-            for (int i = 0; i < G; ++i) y[i] = widen_f(v[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < G; ++i) y[i] = widen_f(x[i]);
-        }
-    }
     if (p.rope.rot) {
         const uint32_t pairs = p.rope.rot / 2;
         if (ok) {
@@ -90,27 +91,44 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
                 for (int i = 0; i < G; ++i) row_s[r][element_at(g * G + i)] = y[i];
         }
         __syncwarp();
-        if (ok) {
-            const uint32_t e0 = g * G - p.rope.first;  // this lane's elements within the range, modulo 2^32
-            if (p.half) {
+        const uint32_t e0 = g * G - p.rope.first;  // this lane's elements within the range, modulo 2^32
+        if (!ok) {
+        } else if (p.whole) {
+            // The range begins and ends with lanes' groups, and so do its halves.
+            if (e0 < p.rope.rot) {
+                if (p.half) {
+                    const bool low = e0 < pairs;
+                    const float2* trig = &trig_s[r][pair_at(low ? e0 : e0 - pairs)];
+                    const float* other = &row_s[r][low ? g + pairs / G : g - pairs / G];
 #pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    const uint32_t e = e0 + i;
-                    if (e < p.rope.rot) {
-                        const bool low = e < pairs;
-                        const uint32_t other = (low ? e + pairs : e - pairs) + p.rope.first;
-                        const float z = row_s[r][element_at(other)];
-                        const float2 cs = trig_s[r][pair_at(low ? e : e - pairs)];
-                        float a = low ? y[i] : z, b = low ? z : y[i];
+                    for (int i = 0; i < G; ++i) {
+                        const float2 cs = trig[i * W];
+                        float a = low ? y[i] : other[i * LANES], b = low ? other[i * LANES] : y[i];
                         rope_pair(a, b, cs);
                         y[i] = low ? a : b;
                     }
-                }
-            } else {
+                } else {
+                    const float2* trig = &trig_s[r][pair_at(e0 / 2)];
 #pragma unroll
-                for (int i = 0; i < G; i += 2)  // first is even: a pair lies in one lane
-                    if (e0 + i < p.rope.rot) rope_pair(y[i], y[i + 1], trig_s[r][pair_at((e0 + i) / 2)]);
+                    for (int i = 0; i < G; i += 2) rope_pair(y[i], y[i + 1], trig[i / 2 * W]);
+                }
             }
+        } else if (p.half) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const uint32_t e = e0 + i;
+                if (e < p.rope.rot) {
+                    const bool low = e < pairs;
+                    const float z = row_s[r][element_at((low ? e + pairs : e - pairs) + p.rope.first)];
+                    float a = low ? y[i] : z, b = low ? z : y[i];
+                    rope_pair(a, b, trig_s[r][pair_at(low ? e : e - pairs)]);
+                    y[i] = low ? a : b;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < G; i += 2)  // first is even: a pair lies in one lane
+                if (e0 + i < p.rope.rot) rope_pair(y[i], y[i + 1], trig_s[r][pair_at((e0 + i) / 2)]);
         }
     }
     if (!ok) return;

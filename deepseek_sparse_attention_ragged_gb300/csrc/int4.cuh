@@ -65,29 +65,38 @@ __device__ __forceinline__ void widen(uint32_t word, Factors f, uint32_t* out) {
 // values that the cache then stands for. The quotients are correctly rounded by
 // Markstein's theorem (q0 = y r with r = 1 / s rounded to nearest, q = q0 + (y - q0 s) r
 // with fused products), 3 FMA instructions instead of a division each; adding and
-// taking away 1.5 * 2^23 rounds to the nearest integer, even on ties.
+// taking away 1.5 * 2^23 rounds to the nearest integer, even on ties. Four values of a
+// half word are packed as one sum below 2^16 in fp32.
 __device__ __forceinline__ uint8_t quantise(const float (&y)[kGroup], uint32_t (&word)[2], float (&held)[kGroup]) {
     constexpr float kToInt = 12582912.0f;
-    float top = 0.0f;
-    bool ok = true;
+    uint32_t top = 0;  // of the magnitudes as integers: infinity and NaN are the largest
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i) {
-        ok = ok && finite_f(y[i]);
-        top = fmaxf(top, fabsf(y[i]));
-    }
-    const uint8_t byte = ok ? (uint8_t)__nv_cvt_float_to_fp8(top / 7.0f, __NV_SATFINITE, __NV_E4M3) : kNanScale;
+    for (int i = 0; i < kGroup; ++i) top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+    const uint8_t byte = top < 0x7F800000u
+                             ? (uint8_t)__nv_cvt_float_to_fp8(__uint_as_float(top) / 7.0f, __NV_SATFINITE, __NV_E4M3)
+                             : kNanScale;
     const float s = scales2(byte).x;
-    // s = 0 (or NaN): every n is 0 and every value 0 (NaN).
+    // s = 0: every n is 0. s = NaN: every n is -7 (what fmaxf makes of NaN), every value NaN.
     const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
-    word[0] = word[1] = 0;
+    float n[kGroup];
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) {
-        const float v = r > 0.0f ? y[i] : 0.0f;
-        const float q0 = v * r;
-        const float q = fmaf(fmaf(-q0, r > 0.0f ? s : 0.0f, v), r, q0);
-        const float n = fminf(fmaxf(q, -7.0f), 7.0f) + kToInt;  // integer in the low bits
-        word[i >> 3] |= ((__float_as_uint(n) + 8u) & 15u) << (4 * ((i & 7) >> 1) + 16 * (i & 1));
-        held[i] = (n - kToInt) * s;
+        const float q0 = y[i] * r;
+        const float q = fmaf(fmaf(-q0, s, y[i]), r, q0);
+        n[i] = (fminf(fmaxf(q, -7.0f), 7.0f) + kToInt) - kToInt;
+        held[i] = n[i] * s;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t half[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float* c = n + 8 * k + h;
+            // (n + 8) of values h, h + 2, h + 4, h + 6 at bits 0, 4, 8, 12: the eights sum to 0x8888.
+            const float sum = fmaf(fmaf(fmaf(c[6], 16.0f, c[4]), 16.0f, c[2]), 16.0f, c[0]) + (float)0x8888;
+            half[h] = __float_as_uint(sum + 8388608.0f);
+        }
+        word[k] = __byte_perm(half[0], half[1], 0x5410);
     }
     return byte;
 }

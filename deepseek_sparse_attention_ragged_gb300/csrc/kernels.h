@@ -163,7 +163,8 @@ struct PagedCache {
 struct AppendCall {
     PagedCache cache;
     RopeParams rope;  // rot 0: none
-    int half;         // the pairs' layout is DS_ROPE_HALF
+    uint32_t half;    // the pairs' layout is DS_ROPE_HALF
+    uint32_t whole;   // the rotated range (and each half of it) is whole groups of 16 elements
     const void* x;
     uint64_t x_stride;
     uint64_t tokens;
