@@ -128,10 +128,47 @@ __device__ __forceinline__ uint32_t sw128_chunk(int r, int ch, int block) {
 enum class Cache { kContiguous, kPagedBf16, kPagedInt4 };
 constexpr int kInt4RowBytes = kDim / 2 + kDim / int4::kGroup;
 
+constexpr uint32_t kNoIndex = 0xFFFFFFFFu;
+
+// Sort 512 values in ascending order, one per thread, as bitonic512_desc does; `between`
+// runs after the stages inside the warps (it hides a load's latency behind them).
+template <class F>
+__device__ __forceinline__ uint32_t bitonic512_asc(uint32_t x, uint32_t* buf, F&& between) {
+    const uint32_t t = threadIdx.x;
+    int b = 0;
+#pragma unroll
+    for (uint32_t k = 2; k <= 512; k <<= 1) {
+        if (k == 64) between();
+#pragma unroll
+        for (uint32_t j = k >> 1; j > 0; j >>= 1) {
+            uint32_t y;
+            if (j >= 32) {
+                buf[b * 512 + t] = x;
+                __syncthreads();
+                y = buf[b * 512 + (t ^ j)];
+                b ^= 1;
+            } else {
+                y = __shfl_xor_sync(0xFFFFFFFFu, x, j);
+            }
+            const bool keep_min = ((t & j) == 0) == ((t & k) == 0);
+            x = keep_min ? min(x, y) : max(x, y);
+        }
+    }
+    return x;
+}
+
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 }  // namespace
 
+// The paged instantiations differ from the contiguous one up to the gather, and in when
+// they wait for the previous kernel: it is the workspace's clear, which starts after all
+// earlier work is complete, so the inputs may be read at once; what the clear zeroes, and
+// the partials, are touched only after the wait, while the tensor cores run P G.
 template <Cache kCache, class Params>
 __device__ __forceinline__ void tail_body(const Params& p) {
+    constexpr bool kPaged = kCache != Cache::kContiguous;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     using T = TailLayout;
@@ -163,7 +200,7 @@ __device__ __forceinline__ void tail_body(const Params& p) {
     auto pub_flag = [&](uint32_t r) { return p.flags + kRowsMax * kHeads + kRowsMax + r; };
     auto pub_n = [&](uint32_t r) { return reinterpret_cast<uint32_t*>(p.pub + (size_t)kRowsMax * kTopK) + r; };
 
-    if (kCache == Cache::kContiguous && e >= (int)p.rows) {
+    if (!kPaged && e >= (int)p.rows) {
         // ---- one more cluster ranks the rows' winners (decode with attention):
         // CTA r waits for row r to publish its winners in index order, sorts
         // them best first and writes the row's index list. No row waits for it.
@@ -223,38 +260,49 @@ __device__ __forceinline__ void tail_body(const Params& p) {
     };
     if (p.attend && !p.q_after_wait) fetch_inputs();
     tc_fence_before();
-    cluster.sync();  // every CTA's counters are set before anyone stores into them
+    if (kPaged) __syncthreads();
+    else cluster.sync();  // every CTA's counters are set before anyone stores into them
     tc_fence_after();
     const uint32_t tmem = p.attend ? *tmem_s : 0u;
-    pdl_wait();  // scores and histogram (decode) or indices (caller) come from earlier work
+    if (!kPaged) pdl_wait();  // scores and histogram (decode) or indices (caller) come from earlier work
     if (p.attend && p.q_after_wait) fetch_inputs();
 
     const uint32_t first = c * kChunkSlots;
     uint32_t nsel = 0;
-    if constexpr (kCache != Cache::kContiguous) {
-        // ---- the caller's indices, as below; a slot then holds its row's place in
-        // the pool instead of its index. The page ids are fetched while the indices
-        // are sorted. A page id outside the pool flags the row as an index does.
-        uint32_t* place_s = reinterpret_cast<uint32_t*>(sel);  // by the caller's position
-        const uint32_t mask = (1u << p.cache.page_shift) - 1;
-        uint64_t v = 0;
-        int32_t id = 0;
-        uint32_t at = 0;
+    bool bad_row = false;  // an index or a page id out of range (paged)
+    if constexpr (kPaged) {
+        // ---- the caller's indices in ascending order (-1 last), as below. A slot of this
+        // chunk then holds its row's place in the pool instead of its index.
+        const int32_t* table = p.cache.table + (size_t)e * p.cache.table_stride;
+        const uint32_t shift = p.cache.page_shift;
+        auto place_of = [&](uint32_t g) -> int32_t {
+            const int32_t id = table[g >> shift];
+            if (id < 0 || (uint32_t)id >= p.cache.num_pages) return -1;
+            return (int32_t)(((uint32_t)id << shift) + (g & ((1u << shift) - 1)));
+        };
+        uint32_t g = kNoIndex;
         if ((uint32_t)t < W) {
-            const int g = __ldcg(p.given + p.index_offset[e] + t);
-            if (g < -1 || g >= (int)L) atomicOr(&p.flags[kRowsMax * kHeads + e], 1u);
-            else if (g >= 0) {
-                v = ((uint64_t)(~(uint32_t)g) << 32) | (uint32_t)t;
-                id = __ldcg(p.cache.table + (size_t)e * p.cache.table_stride + ((uint32_t)g >> p.cache.page_shift));
-                at = (uint32_t)g & mask;
-            }
+            const int i = __ldcg(p.given + p.index_offset[e] + t);
+            if (i < -1 || i >= (int)L) bad_row = true;
+            else if (i >= 0) g = (uint32_t)i;
         }
-        v = bitonic512_desc(v, reinterpret_cast<uint64_t*>(gs.h));
-        const bool paged = id >= 0 && (uint32_t)id < p.cache.num_pages;
-        if (!paged) atomicOr(&p.flags[kRowsMax * kHeads + e], 1u);
-        place_s[t] = paged ? ((uint32_t)id << p.cache.page_shift) + at : 0u;
-        __syncthreads();
-        if ((uint32_t)t - first < (uint32_t)kChunkSlots && v != 0) idx_s[t - first] = (int32_t)place_s[(uint32_t)v];
+        // Every CTA sorts the whole list. On the way each fetches an eighth of the rows into L2
+        // (a thread's own index), and the page ids into L1, where the chunk's threads find them.
+        const uint32_t mine = g;
+        if (mine != kNoIndex) prefetch_l1(table + (mine >> shift));
+        g = bitonic512_asc(g, reinterpret_cast<uint32_t*>(gs.h), [&] {
+            if (((uint32_t)t >> 6) == rank && mine != kNoIndex) {
+                const int32_t at = place_of(mine);
+                if (at >= 0)
+                    for (uint32_t o = 0; o < p.cache.row_bytes; o += 128)
+                        prefetch_l2(p.cache.pages + (size_t)at * p.cache.row_bytes + o);
+            }
+        });
+        if ((uint32_t)t - first < (uint32_t)kChunkSlots && g != kNoIndex) {
+            const int32_t at = place_of(g);
+            bad_row = bad_row || at < 0;
+            idx_s[t - first] = max(at, 0);
+        }
     } else if (p.given == nullptr) {
         // ---- select: gather the candidates, then every CTA selects the same winners
         const float* s = p.scores + (size_t)e * p.score_stride;
@@ -297,28 +345,32 @@ __device__ __forceinline__ void tail_body(const Params& p) {
                 else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
             }
     } else if constexpr (kCache == Cache::kPagedInt4) {
-        // A unit is 32 values (16 bytes) of a row and their two scales; a thread
-        // loads all of its units before it widens the first.
-        constexpr int kUnits = kChunkSlots * (kDim / 32) / kThreads;
+        // A unit is 32 values (16 bytes) of a row and their two scales. A warp has eight rows,
+        // and per step four neighbouring units of each: whole sectors are read, and eight
+        // lanes store into eight rows, which the swizzle puts into different banks. All loads
+        // are issued before the first unit is widened.
+        constexpr int kUnits = kDim / 32 / 4;
+        static_assert(8 * (kThreads / 32) == kChunkSlots, "eight rows a warp");
         if (has_chunk) {
+            const int r = 8 * warp + (lane & 7);
+            const int i = idx_s[r];
+            const uint8_t* row = p.cache.pages + (size_t)max(i, 0) * kInt4RowBytes;
             uint4 d[kUnits];
             uint32_t sc[kUnits];
 #pragma unroll
             for (int n = 0; n < kUnits; ++n) {
-                const int k = t + n * kThreads, r = k >> 4, u = k & 15;
-                const int i = idx_s[r];
+                const int u = 4 * n + (lane >> 3);
                 // An empty slot is zeros: n + 8 = 8 in every value, s = 0.
                 d[n] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
                 sc[n] = 0;
                 if (i >= 0) {
-                    const uint8_t* row = p.cache.pages + (size_t)i * kInt4RowBytes;
                     d[n] = __ldcg(reinterpret_cast<const uint4*>(row + 16 * u));
                     sc[n] = __ldcg(reinterpret_cast<const uint16_t*>(row + kDim / 2 + 2 * u));
                 }
             }
 #pragma unroll
             for (int n = 0; n < kUnits; ++n) {
-                const int k = t + n * kThreads, r = k >> 4, u = k & 15;
+                const int u = 4 * n + (lane >> 3);
                 int4::Factors f[2];
                 int4::factors2<0>(sc[n], f[0], f[1]);
                 const uint32_t w[4] = {d[n].x, d[n].y, d[n].z, d[n].w};
@@ -382,19 +434,27 @@ __device__ __forceinline__ void tail_body(const Params& p) {
         st_release_gpu(pub_flag(e), 1u);
     }
 
+    // The issuing thread of warps 0..3. Paged: elected in a warp known to be uniform, which
+    // keeps the descriptors in uniform registers (25 cycles an MMA instead of 80).
+    const int uwarp = kPaged ? __shfl_sync(0xFFFFFFFFu, warp, 0) : warp;
+    auto issuer = [&]() -> bool {
+        if (kPaged) return uwarp < kIssuers && elect_one();
+        return lane == 0 && warp < kIssuers;
+    };
+
     // `alive`: every tensor-core wait of this CTA has succeeded (uniform over the
     // CTA); `pending`: the mma_bar phase of MMAs whose completion was not seen.
     bool alive = true;
     int pending = -1;
     if (has_chunk) {
         const uint32_t g_addr = smem_u32(g_s), q_addr = smem_u32(q_s);
-        if (lane == 0 && warp < kIssuers) {
+        if (issuer()) {
             // Accumulator a = warp takes the K-steps kk = 4 j + a.
             constexpr uint32_t idesc = idesc_bf16_f32(128, kHalfHeads);
-            const uint32_t koff = (uint32_t)warp * 32;  // 16 bf16 = 32 B inside the 128-B row
+            const uint32_t koff = (uint32_t)uwarp * 32;  // 16 bf16 = 32 B inside the 128-B row
 #pragma unroll
             for (int j = 0; j < kDim / 64; ++j)
-                umma_bf16(tmem + 32 * warp, smem_desc_sw128_kmajor(g_addr + j * kGBlock + koff),
+                umma_bf16(tmem + 32 * uwarp, smem_desc_sw128_kmajor(g_addr + j * kGBlock + koff),
                           smem_desc_sw128_kmajor(q_addr + j * kQBlock + koff), idesc, j > 0 ? 1u : 0u);
             umma_commit(mma_bar);
         }
@@ -453,11 +513,11 @@ __device__ __forceinline__ void tail_body(const Params& p) {
         __syncthreads();
         tc_fence_after();
         const uint32_t g_addr = smem_u32(g_s);
-        if (lane == 0 && warp < kIssuers) {
+        if (issuer()) {
             // Feature block b = warp: features [128 b, 128 b + 128).
             constexpr uint32_t idesc = idesc_bf16_f32(128, 2 * kHalfHeads) | kIdescAMnMajor;
             const uint32_t p_addr = smem_u32(p_s);
-            const int b = warp;
+            const int b = uwarp;
 #pragma unroll
             for (int ks = 0; ks < kChunkSlots / 16; ++ks) {
                 // A: features [128 b, 128 b + 128) x slots [16 ks, 16 ks + 16), MN-major.
@@ -478,6 +538,7 @@ __device__ __forceinline__ void tail_body(const Params& p) {
             for (int i = 0; i < 8; ++i) red_sum[qt * kHalfHeads + 8 * hg + i] = sum[i];
         __syncthreads();
         float* part = p.part + part0_off + (size_t)c * kPartFloats;
+        if (kPaged) pdl_wait();
         if (t < kHalfHeads) {
             const float mh = fmaxf(fmaxf(red_max[t], red_max[kHalfHeads + t]),
                                    fmaxf(red_max[2 * kHalfHeads + t], red_max[3 * kHalfHeads + t]));
@@ -514,7 +575,11 @@ __device__ __forceinline__ void tail_body(const Params& p) {
     }
     // A CTA whose tensor-core wait gave up has no valid partial: the whole row
     // is written as zeros.
-    if (!alive && t == 0) atomicOr(&p.flags[kRowsMax * kHeads + e], 1u);
+    if (kPaged) {
+        pdl_wait();  // nothing more to wait for where it ran above
+        if (!alive && t == 0) atomicOr(p.status, kStatusWaitTimeout);  // it may have been reported before the clear
+    }
+    if ((!alive && t == 0) || bad_row) atomicOr(&p.flags[kRowsMax * kHeads + e], 1u);
     tc_fence_before();
     // Every chunk's partial and flags are visible to the cluster after this
     // barrier; the best-first ranks are written while it completes.

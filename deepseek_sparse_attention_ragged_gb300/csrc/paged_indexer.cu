@@ -103,17 +103,6 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t one;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xFFFFFFFF;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(one));
-    return one != 0;
-}
-
 // mbar_wait whose first tries read no timer, for waits of a few hundred cycles.
 __device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity) {
     for (int i = 0; i < 64; ++i)

@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeThreadsMax = 544;   // one row a block: 1024 / 2 units and one more, in whole warps
-constexpr uint32_t kGroupMax = 8; 
+constexpr uint32_t kGroupMax = 8;
 constexpr uint32_t kFull = 512;        // threads an SM keeps busy with
 
 template <typename T>
