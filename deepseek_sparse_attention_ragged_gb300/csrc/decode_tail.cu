@@ -109,12 +109,27 @@ static_assert(TailLayout::misc % 8 == 0, "alignment");
 constexpr size_t kTailSmem = TailLayout::total + 1024;  // + slack to align the swizzled buffers to 1 KiB
 static_assert(kTailSmem <= 227 * 1024, "shared memory");
 
-// Maximum over the warp, in the integer reduction unit: finite values and
-// -inf map order-preservingly to int (no NaN reaches here).
-__device__ __forceinline__ float warp_max(float x) {
-    const int i = __float_as_int(x);
-    const int r = __reduce_max_sync(0xFFFFFFFFu, i >= 0 ? i : i ^ 0x7FFFFFFF);
-    return __int_as_float(r >= 0 ? r : r ^ 0x7FFFFFFF);
+// Reduce 8 values over the warp by a butterfly that halves what a lane holds: the first
+// three steps exchange 4, 2 and 1 values, so 9 shuffles do the work of 40, in the order
+// of the plain butterfly (lane distances 16, 8, 4, 2, 1: the same bits). Returns the
+// reduction of value reduced_of(lane).
+__device__ __forceinline__ int reduced_of(int lane) { return (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1); }
+template <class Op>
+__device__ __forceinline__ float warp_reduce8(const float (&x)[8], int lane, Op op) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = x[k];
+#pragma unroll
+    for (int n = 4; n > 0; n >>= 1) {
+        const bool upper = lane & (4 * n);
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const float other = __shfl_xor_sync(0xFFFFFFFFu, upper ? v[k] : v[k + n], 4 * n);
+            v[k] = op(upper ? v[k + n] : v[k], other);
+        }
+    }
+    v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 2));
+    return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
 }
 
 // Byte offset of 16-byte chunk ch (0..63) of row r in a K-major SW128 buffer of
@@ -473,7 +488,7 @@ __device__ __forceinline__ void tail_body(const Params& p) {
         for (int a = 0; a < 4; ++a) tmem_ld_x8(tmem + ((uint32_t)(32 * qt) << 16) + 32 * a + 8 * hg, v[a]);
         tmem_ld_wait();
         const bool live = idx_s[slot] >= 0;
-        float l[8], m[8];
+        float l[8];
         uint32_t bad_bits = 0;  // head i of this warp's 8 has a non-finite live logit
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -482,15 +497,14 @@ __device__ __forceinline__ void tail_body(const Params& p) {
             const bool ok = live && finite_f(l[i]);
             bad_bits |= (live && !ok) ? 1u << i : 0u;
             if (!ok) l[i] = -INFINITY;
-            m[i] = warp_max(l[i]);
         }
         bad_bits = __reduce_or_sync(0xFFFFFFFFu, bad_bits);
-        if (lane == 0)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                red_max[qt * kHalfHeads + 8 * hg + i] = m[i];
-                red_bad[qt * kHalfHeads + 8 * hg + i] = (bad_bits >> i) & 1u;
-            }
+        const float m = warp_reduce8(l, lane, [](float a, float b) { return fmaxf(a, b); });
+        const int red_at = qt * kHalfHeads + 8 * hg + reduced_of(lane);
+        if ((lane & 3) == 0) {
+            red_max[red_at] = m;
+            red_bad[red_at] = (bad_bits >> reduced_of(lane)) & 1u;
+        }
         __syncthreads();
         float sum[8];
 #pragma unroll
@@ -529,13 +543,8 @@ __device__ __forceinline__ void tail_body(const Params& p) {
         }
         // While the tensor cores run P G: the chunk's sum per head (a fixed warp
         // tree, then the four quarters) and the head flags.
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], o);
-        if (lane == 0)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) red_sum[qt * kHalfHeads + 8 * hg + i] = sum[i];
+        const float total = warp_reduce8(sum, lane, [](float a, float b) { return a + b; });
+        if ((lane & 3) == 0) red_sum[red_at] = total;
         __syncthreads();
         float* part = p.part + part0_off + (size_t)c * kPartFloats;
         if (kPaged) pdl_wait();
