@@ -1175,17 +1175,13 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
     const Layout L = make_layout(rows, table);
     rc = check_workspace(&set, workspace, workspace_bytes, L);
     if (rc) return rc;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t err = launch_clear_stage(reinterpret_cast<uint32_t*>(ws), (uint32_t)(L.ctl_end / 4), s);
-    if (err != cudaSuccess) return cuda_fail(err, "workspace clear");
     StageRange range("dsrows.attention_paged");
     PagedTailParams p;
     std::memset(static_cast<void*>(&p), 0, sizeof(p));
-    fill_tail(p, &set, q_attn, sinks, sinks_row_stride, scale, out, invalid, nullptr, 0, indices, nullptr, ws, L, false,
-              true, nullptr);
+    fill_tail(p, &set, q_attn, sinks, sinks_row_stride, scale, out, invalid, nullptr, 0, indices, nullptr,
+              static_cast<uint8_t*>(workspace), L, false, true, nullptr);
     p.cache = paged_cache(*kv);
-    err = launch_sparse_attn_paged(p, kv->format, s, true);
+    const cudaError_t err = launch_sparse_attn_paged(p, kv->format, (cudaStream_t)stream, true);
     return err == cudaSuccess ? DS_OK : cuda_fail(err, "paged attention launch");
 }
 

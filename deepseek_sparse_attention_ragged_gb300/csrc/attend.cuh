@@ -19,6 +19,52 @@ __device__ __forceinline__ void cp_async_wait_all() {
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 
+// A thread's part of the combine: FPT features of one head from the partials of n chunks.
+template <int FPT, int kChunks>
+__device__ __forceinline__ void combine_finish(const float4 (&v)[kChunks][FPT / 4], const float (&mc)[kChunks],
+                                               const float (&lc)[kChunks], int n, bool flagged, float sink,
+                                               __nv_bfloat16* dst, uint32_t* invalid) {
+    float m = sink;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+        if (c < n) m = fmaxf(m, mc[c]);
+    float den = finite_f(sink) ? expf(sink - m) : 0.0f;
+    float fac[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+        if (c < n) {
+            fac[c] = mc[c] == -INFINITY ? 0.0f : expf(mc[c] - m);
+            den = fmaf(lc[c], fac[c], den);
+        }
+    const bool zero = flagged || !finite_f(sink) || !finite_f(den) || !(den > 0.0f) || !finite_f(m);
+    if (invalid) *invalid = zero ? 1u : 0u;
+    const float inv_den = 1.0f / den;
+    float r[FPT];
+#pragma unroll
+    for (int i = 0; i < FPT; ++i) r[i] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        if (c < n) {
+            const float w = fac[c];
+#pragma unroll
+            for (int u = 0; u < FPT / 4; ++u) {
+                r[4 * u] = fmaf(v[c][u].x, w, r[4 * u]);
+                r[4 * u + 1] = fmaf(v[c][u].y, w, r[4 * u + 1]);
+                r[4 * u + 2] = fmaf(v[c][u].z, w, r[4 * u + 2]);
+                r[4 * u + 3] = fmaf(v[c][u].w, w, r[4 * u + 3]);
+            }
+        }
+    }
+    __align__(16) __nv_bfloat16 o[FPT];
+#pragma unroll
+    for (int i = 0; i < FPT; ++i) {
+        const float x = r[i] * inv_den;
+        o[i] = __float2bfloat16_rn(!zero && finite_f(x) ? x : 0.0f);
+    }
+    if (FPT == 8) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
+    else *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o);
+}
+
 // Combine feature columns [f0, f0 + F) of H heads over the n chunk partials of
 // one row (or head half) with NT threads: thread -> one head and F H / NT
 // consecutive features. A partial is m[H], l[H], acc[H][512] (fp32), `stride`
@@ -65,47 +111,32 @@ __device__ __forceinline__ void combine_slice(const float* part0, size_t stride,
             lc[c] = __ldcg(pc + H + h);
         }
     const uint32_t flagged = __ldcg(flags + h) | __ldcg(row_flag);
-    const float sink = sinks[h];
-    float m = sink;
+    combine_finish<FPT>(v, mc, lc, n, flagged != 0, sinks[h], out + (size_t)h * kDim + f,
+                        invalid && t % TPH == 0 ? invalid + h : nullptr);
+}
+
+// The same combine for a row whose partials are in this CTA's shared memory: chunk c's block
+// of these columns at block(c) ([H][F] floats), its maxima and sums at ml + 2 H c; head
+// h of a row is flagged by bit h of bad_heads.
+template <int H, int NT, int F, class Block>
+__device__ __forceinline__ void combine_shared(Block&& block, const float* ml, int n, int f0, uint32_t bad_heads,
+                                               const float* sinks, __nv_bfloat16* out, uint32_t* invalid) {
+    constexpr int FPT = F * H / NT, TPH = F / FPT, kChunks = kTopK / 128;
+    static_assert(H <= 32 && FPT % 4 == 0, "flags in a word, whole float4s");
+    const int t = threadIdx.x, h = t / TPH, fl = (t % TPH) * FPT;
+    float4 v[kChunks][FPT / 4];
+    float mc[kChunks], lc[kChunks];
 #pragma unroll
-    for (int c = 0; c < kAttnChunksMax; ++c)
-        if (c < n) m = fmaxf(m, mc[c]);
-    float den = finite_f(sink) ? expf(sink - m) : 0.0f;
-    float fac[kAttnChunksMax];
-#pragma unroll
-    for (int c = 0; c < kAttnChunksMax; ++c)
+    for (int c = 0; c < kChunks; ++c)
         if (c < n) {
-            fac[c] = mc[c] == -INFINITY ? 0.0f : expf(mc[c] - m);
-            den = fmaf(lc[c], fac[c], den);
+#pragma unroll
+            for (int u = 0; u < FPT / 4; ++u)
+                v[c][u] = *reinterpret_cast<const float4*>(block(c) + h * F + fl + 4 * u);
+            mc[c] = ml[2 * H * c + h];
+            lc[c] = ml[2 * H * c + H + h];
         }
-    const bool zero = flagged != 0 || !finite_f(sink) || !finite_f(den) || !(den > 0.0f) || !finite_f(m);
-    if (invalid && t % TPH == 0) invalid[h] = zero ? 1u : 0u;
-    const float inv_den = 1.0f / den;
-    float r[FPT];
-#pragma unroll
-    for (int i = 0; i < FPT; ++i) r[i] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < kAttnChunksMax; ++c) {
-        if (c < n) {
-            const float w = fac[c];
-#pragma unroll
-            for (int u = 0; u < FPT / 4; ++u) {
-                r[4 * u] = fmaf(v[c][u].x, w, r[4 * u]);
-                r[4 * u + 1] = fmaf(v[c][u].y, w, r[4 * u + 1]);
-                r[4 * u + 2] = fmaf(v[c][u].z, w, r[4 * u + 2]);
-                r[4 * u + 3] = fmaf(v[c][u].w, w, r[4 * u + 3]);
-            }
-        }
-    }
-    __align__(16) __nv_bfloat16 o[FPT];
-#pragma unroll
-    for (int i = 0; i < FPT; ++i) {
-        const float x = r[i] * inv_den;
-        o[i] = __float2bfloat16_rn(!zero && finite_f(x) ? x : 0.0f);
-    }
-    __nv_bfloat16* dst = out + (size_t)h * kDim + f;
-    if (FPT == 8) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
-    else *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o);
+    combine_finish<FPT>(v, mc, lc, n, (bad_heads >> h & 1) != 0, sinks[h], out + (size_t)h * kDim + f0 + fl,
+                        invalid && t % TPH == 0 ? invalid + h : nullptr);
 }
 
 }  // namespace attend

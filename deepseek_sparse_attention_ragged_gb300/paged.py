@@ -116,12 +116,14 @@ def _code(table, value, name: str) -> int:
 
 def _rows(rows):
     """A row table as ds_row_t words, and its columns (kv_len, width, index_offset, q_row)."""
+    if not isinstance(rows, (list, tuple)):
+        rows = list(rows)
     try:
         words = array("I", chain.from_iterable(rows))
     except TypeError:  # Row structures, or objects with their fields
         tab, n = _table(rows)
         words = array("I", chain.from_iterable((r.kv_len, r.width, r.index_offset, r.q_row) for r in tab[:n]))
-    if len(words) == 0 or len(words) % 4:
+    if len(rows) == 0 or len(words) != 4 * len(rows):
         raise ValueError("rows must be a nonempty list of (kv_len, width, index_offset, q_row)")
     return words, words[0::4], words[1::4], words[2::4], words[3::4]
 

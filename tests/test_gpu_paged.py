@@ -712,6 +712,34 @@ def test_two_streams_at_once():
         assert all(torch.equal(w, x) for x in o)
 
 
+def test_captured_calls_of_two_graphs_without_a_workspace():
+    """Two graphs whose workspaces the binding takes during capture, replayed in turn and
+    on two streams at once."""
+    rng = np.random.default_rng(14)
+    lens = [900, 64]
+    rows = row_table(lens)
+    cache, values = make_cache(rng, lens, 512, "int4", 32)
+    idx = i32(np.concatenate([np.r_[rng.permutation(n)[:512], np.full(max(0, 512 - n), -1)] for n in lens]))
+    sinks = torch.zeros(64, device="cuda")
+    qs = [queries(rng, 2, 512) for _ in range(2)]
+    want = [attend(rows, q, sinks, 0, idx, cache, values)[0] for q in qs]
+    outs = [torch.zeros_like(q) for q in qs]
+    graphs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for q, o, st in zip(qs, outs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for _ in range(4):
+                ds.ds_rows_sparse_attn_paged(rows, q, sinks, 0, idx, SCALE, o, cache)
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(w, o) for w, o in zip(want, outs))
+
+
 def test_cache_refusals_of_the_binding():
     pages = torch.zeros(18432 * 2, dtype=torch.uint8, device="cuda")
     table = torch.zeros(1, 2, dtype=torch.int32, device="cuda")

@@ -273,3 +273,16 @@ def test_binding_refuses_host_tensors():
         ds.Rope(64, device="cpu")
     with pytest.raises(ds.DsRowsError, match="rot_dim"):
         ds.Rope(63, device="cpu")
+
+
+def test_row_tables_of_every_kind():
+    want = [(600, 512, 0, 0), (7, 7, 512, 3)]
+    for rows in (want, tuple(want), iter(want), [ds.Row(*r) for r in want], (ds.Row(*r) for r in want),
+                 [list(r) for r in want]):
+        words, *columns = paged._rows(rows)
+        assert list(zip(*columns)) == want and len(words) == 8
+    for bad in ([], [(1, 2), (3, 4)], [(1, 2, 3)], [(1, 2, 3, 4, 5)]):
+        with pytest.raises(ValueError, match="nonempty list"):
+            paged._rows(bad)
+    with pytest.raises(OverflowError):
+        paged._rows([(-1, 1, 0, 0)])
