@@ -5,8 +5,9 @@
 // launch). A lane owns 16 consecutive elements, which is one group of the 4-bit
 // type, so its scale needs no exchange: a warp holds one 512-wide row or four
 // 128-wide ones. The lanes of a row share its sines and cosines through shared
-// memory (each takes rot / 2 / lanes of them), and in the half layout the row
-// itself, whose pairs lie in different lanes.
+// memory (each takes rot / 2 / lanes of them); in the half layout a pair's other
+// element comes from its lane by a shuffle where the halves are whole groups, and is
+// read again where they are not.
 
 #include "int4.cuh"
 #include "rope.cuh"
@@ -29,14 +30,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     constexpr int G = int4::kGroup;
     constexpr int LANES = kDimOf / G;  // lanes of a row
     constexpr int ROWS = kAppendThreads / LANES;
-    // Pair i of a row at [i mod 16][i / 16] and element e at [e mod 16][e / 16], padded: lanes read
-    // with strides of 8 or 16 pairs and 16 elements, and the rows of a warp lie in different banks.
+    // Pair i of a row at [i mod 16][i / 16], padded: lanes read with strides of 8 or 16 pairs, and
+    // the rows of a warp lie in different banks.
     constexpr int W = kDimOf / 32 + 1;
     constexpr int PAD = LANES == 32 ? 0 : 4;
     __shared__ float2 trig_s[ROWS][16 * W + PAD];
-    __shared__ float row_s[ROWS][G * LANES + 2 * PAD];
     auto pair_at = [](uint32_t i) { return (i % 16) * W + i / 16; };
-    auto element_at = [](uint32_t e) { return (e % G) * LANES + e / G; };
     pdl_trigger();
     const int r = threadIdx.x / LANES, g = threadIdx.x % LANES;
     const uint64_t token = (uint64_t)blockIdx.x * ROWS + r;
@@ -44,8 +43,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     pdl_wait();
     // The row is fetched while its place is looked up.
     float y[G];
+    const T* x = static_cast<const T*>(p.x) + token * p.x_stride + g * G;
     if (there) {
-        const T* x = static_cast<const T*>(p.x) + token * p.x_stride + g * G;
         if (p.wide) {
             __align__(16) T v[G];
 #pragma unroll
@@ -83,49 +82,43 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 
     if (p.rope.rot) {
         const uint32_t pairs = p.rope.rot / 2;
-        if (ok) {
+        if (ok)
             for (uint32_t i = g; i < pairs; i += LANES)
                 trig_s[r][pair_at(i)] = rope_turn(pos, p.rope.turns[i], p.rope.magnitude, false);
-            if (p.half)
-#pragma unroll
-                for (int i = 0; i < G; ++i) row_s[r][element_at(g * G + i)] = y[i];
-        }
         __syncwarp();
         const uint32_t e0 = g * G - p.rope.first;  // this lane's elements within the range, modulo 2^32
-        if (!ok) {
-        } else if (p.whole) {
+        const bool inside = e0 < p.rope.rot, low = e0 < pairs;
+        if (p.whole) {
             // The range begins and ends with lanes' groups, and so do its halves.
-            if (e0 < p.rope.rot) {
-                if (p.half) {
-                    const bool low = e0 < pairs;
-                    const float2* trig = &trig_s[r][pair_at(low ? e0 : e0 - pairs)];
-                    const float* other = &row_s[r][low ? g + pairs / G : g - pairs / G];
+            if (p.half) {
+                const int other = (threadIdx.x & 31) + (!inside ? 0 : low ? (int)pairs / G : -((int)pairs / G));
+                const float2* trig = &trig_s[r][pair_at(!inside ? 0 : low ? e0 : e0 - pairs)];
 #pragma unroll
-                    for (int i = 0; i < G; ++i) {
+                for (int i = 0; i < G; ++i) {
+                    const float z = __shfl_sync(0xFFFFFFFFu, y[i], other);
+                    if (inside && ok) {
                         const float2 cs = trig[i * W];
-                        float a = low ? y[i] : other[i * LANES], b = low ? other[i * LANES] : y[i];
-                        rope_pair(a, b, cs);
-                        y[i] = low ? a : b;
+                        y[i] = low ? y[i] * cs.x - z * cs.y : z * cs.y + y[i] * cs.x;
                     }
-                } else {
-                    const float2* trig = &trig_s[r][pair_at(e0 / 2)];
-#pragma unroll
-                    for (int i = 0; i < G; i += 2) rope_pair(y[i], y[i + 1], trig[i / 2 * W]);
                 }
+            } else if (inside && ok) {
+                const float2* trig = &trig_s[r][pair_at(e0 / 2)];
+#pragma unroll
+                for (int i = 0; i < G; i += 2) rope_pair(y[i], y[i + 1], trig[i / 2 * W]);
             }
-        } else if (p.half) {
+        } else if (ok && p.half) {
 #pragma unroll
             for (int i = 0; i < G; ++i) {
                 const uint32_t e = e0 + i;
                 if (e < p.rope.rot) {
-                    const bool low = e < pairs;
-                    const float z = row_s[r][element_at((low ? e + pairs : e - pairs) + p.rope.first)];
-                    float a = low ? y[i] : z, b = low ? z : y[i];
-                    rope_pair(a, b, trig_s[r][pair_at(low ? e : e - pairs)]);
-                    y[i] = low ? a : b;
+                    const bool first = e < pairs;
+                    const float z = widen_f(x[first ? i + (int)pairs : i - (int)pairs]);
+                    float a = first ? y[i] : z, b = first ? z : y[i];
+                    rope_pair(a, b, trig_s[r][pair_at(first ? e : e - pairs)]);
+                    y[i] = first ? a : b;
                 }
             }
-        } else {
+        } else if (ok) {
 #pragma unroll
             for (int i = 0; i < G; i += 2)  // first is even: a pair lies in one lane
                 if (e0 + i < p.rope.rot) rope_pair(y[i], y[i + 1], trig_s[r][pair_at((e0 + i) / 2)]);
