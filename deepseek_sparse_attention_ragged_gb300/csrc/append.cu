@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
                     const float z = __shfl_sync(0xFFFFFFFFu, y[i], other);
                     if (inside && ok) {
                         const float2 cs = trig[i * W];
-                        y[i] = low ? y[i] * cs.x - z * cs.y : z * cs.y + y[i] * cs.x;
+                        y[i] = low ? rope_first(y[i], z, cs) : rope_second(z, y[i], cs);
                     }
                 }
             } else if (inside && ok) {

@@ -8,10 +8,14 @@
 // group of heads of one token, so sine and cosine are taken once per group; out of
 // place, threads of their own copy two pieces each of what is not rotated. The
 // heads of a group are interleaved over the block, so that its accesses at one time
-// cover whole rows side by side. 4096 x 64 bf16 rows of 128, out of place: 22.4 us
-// (134 MB; a plain copy of them takes 21.0 us here); with consecutive heads per
-// thread 27.6 us, without the streaming hints 24.5 us, with the copies in the
-// rotating threads 31.5 us. Eight rows of 64 heads in place: 1.6 us.
+// cover whole rows side by side. 4096 x 64 bf16 rows of 128, half of each rotated, out
+// of place (134 MB): 27.3 us with inputs that are not in L2, 22.4 us replayed on the same
+// ones (a plain copy of them: 21.1 us); replayed, with consecutive heads per thread
+// 27.6 us, without the streaming hints 24.5 us, with the copies in the rotating threads
+// 31.5 us. What is left is that an access takes 64 bytes of a line (23.3 us if it took
+// all 128); threads that read whole lines and share the angles through shared memory
+// needed a barrier and twice the loads, and took 44 us. Eight rows of 64 heads in
+// place: 1.6 us; 1021 x 64 fp32 rows in place 4.2 us.
 // A row whose address, stride or range is not a multiple of 16 bytes is moved
 // by elements, one pair a unit.
 

@@ -19,11 +19,14 @@ __device__ __forceinline__ float2 rope_turn(int32_t pos, uint64_t turns, float m
     return make_float2(c * m, (inverse ? -s : s) * m);
 }
 
-// The rotation of one pair, in fp32.
+// The rotation of a pair (x, y) in fp32, each element with one rounded and one fused
+// product, so that every path gives the same bits.
+__device__ __forceinline__ float rope_first(float x, float y, float2 cs) { return fmaf(x, cs.x, -__fmul_rn(y, cs.y)); }
+__device__ __forceinline__ float rope_second(float x, float y, float2 cs) { return fmaf(x, cs.y, __fmul_rn(y, cs.x)); }
 __device__ __forceinline__ void rope_pair(float& a, float& b, float2 cs) {
     const float x = a, y = b;
-    a = x * cs.x - y * cs.y;
-    b = x * cs.y + y * cs.x;
+    a = rope_first(x, y, cs);
+    b = rope_second(x, y, cs);
 }
 
 }  // namespace dsrows
