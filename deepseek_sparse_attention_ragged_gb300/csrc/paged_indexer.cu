@@ -19,10 +19,10 @@
 // into TMEM, where they are the A operand of the MMAs: the widened key never
 // passes through shared memory, whose bandwidth (32 KB written and 32 KB read
 // again a tile) would be the bound otherwise. The instructions of the widening
-// and of the head sums are the bound: 8 x 131072 keys take 20.8 us, of which the
-// loads alone are 14.6 us (75.5 MB: 11.1 us at the measured copy bandwidth), and
-// 17.0 us without the head sums; the MMAs hardly count (21.1 us with one of
-// eight). Steps, in us: one issuing thread 34.7; the issuer's warp kept uniform 26.6
+// and of the head sums are the bound: 8 x 131072 keys take 20.8 us (22.8 us when
+// nothing is in L2), of which the loads alone are 14.6 us (75.5 MB: 11.1 us at the
+// measured copy bandwidth), and 17.0 us without the head sums; the MMAs hardly count
+// (21.1 us with one of eight). Steps, in us: one issuing thread 34.7; the issuer's warp kept uniform 26.6
 // (a divergent thread took 80 cycles an MMA, a uniform warp 25); four widening sets
 // and two issuers 25.3; the mask and exponent of a value in one instruction 23.1;
 // the polling loads 21.5; shared-space pointers and running indexes 20.8.
@@ -49,7 +49,7 @@ constexpr int kKeyWords = kIdxDim / 2;             // TMEM columns of a widened 
 constexpr int kIssuers = 2;   // warps that issue MMAs, each every second tile
 constexpr int kEpiSets = 2;   // of four epilogue warps, each every second tile
 constexpr int kWideSets = 4;  // of four widening warps, each every fourth tile
-constexpr int kBufs = 4;    // accumulators, and widened tiles
+constexpr int kBufs = 4;      // accumulators, and widened tiles
 
 template <bool kInt4>
 struct Shape {
@@ -65,8 +65,9 @@ struct Shape {
     static constexpr size_t w = q + 2 * (size_t)kQHalf;
     static constexpr size_t bars = w + kIdxHeads * 4;
 };
-// A buffer's tiles all belong to one issuer and one set each: a wait on its barrier is then
-// never more than one phase ahead.
+// The tiles of a buffer belong to one issuer and one set of each kind, and those of a stage to
+// one lane of the loading warp, one issuer and one widening set: a wait for a parity is then
+// never more than one phase ahead of its barrier.
 static_assert(Shape<true>::kStages % Shape<true>::kLap == 0 && Shape<false>::kStages % Shape<false>::kLap == 0, "phases");
 static_assert(kBufs % kIssuers == 0 && kBufs % kEpiSets == 0 && kBufs % kWideSets == 0, "phases");
 static_assert(Shape<true>::kStages % kWideSets == 0 && Shape<true>::kStages % kIssuers == 0 &&

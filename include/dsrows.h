@@ -492,7 +492,7 @@ size_t ds_rows_page_bytes(uint32_t page_size, uint32_t dim, int format);
  * Append rows to a paged cache, rotated on the way: row i of x [tokens, dim]
  * becomes row slot[i] of entry seq[i].
  *   x          device, element type `dtype`, rows x_stride elements apart (the
- *              elements of a row contiguous); must not share memory with the pages
+ *              elements of a row contiguous); must not share memory with the pages or `values`
  *   tokens     below 2^31; 0 enqueues nothing. x_stride is at most 2^31.
  *   seq, slot  device int32 [tokens]. seq -1 marks padding: the row is skipped.
  *              The (seq, slot) pairs of a call, and the places they map to, must
