@@ -35,8 +35,9 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 
 // The factors of two scales, bytes `at` and `at` + 1 of `b`. A byte's exponent and mantissa
 // in a bf16's places are s 2^-120 (the types' biases are 7 and 127; subnormals agree
-// too), so one exact product gives s. The byte of NaN would give 480: 480 (145/128) 2^119
-// is past the largest bf16 while 448 is not, and infinity times 0 makes it NaN.
+// too), so one exact product gives s. The byte of NaN would give 480, bytes with a sign 512 and
+// more: from 480 on, s (145/128) 2^119 is past the largest bf16, up to 448 it is not, and
+// infinity times 0 makes it NaN.
 template <int at>
 __device__ __forceinline__ void factors2(uint32_t b, Factors& f0, Factors& f1) {
     constexpr uint32_t kScale = 0x7B807B80u, kFar = 0x7B117B11u, kMinus136 = 0xC308C308u;

@@ -277,6 +277,8 @@ def ds_rows_indexer_score_paged(rows, q_index: torch.Tensor, w_index: torch.Tens
     n, q_rows = len(kv_len), max(q_row) + 1
     if score_stride is None:
         score_stride = scores.shape[-1] if scores.dim() > 1 else max(kv_len)
+    elif score_stride < 0:
+        raise ValueError(f"score_stride must not be negative, got {score_stride}")
     pq = _tensor(q_index, "q_index", torch.bfloat16, dev, q_rows * INDEX_HEADS * INDEX_DIM)
     pw = _tensor(w_index, "w_index", torch.float32, dev, q_rows * INDEX_HEADS)
     po = _tensor(scores, "scores", torch.float32, dev, (n - 1) * score_stride + kv_len[-1])
@@ -293,6 +295,8 @@ def ds_rows_sparse_attn_paged(rows, q_attn: torch.Tensor, sinks: torch.Tensor, s
     dev = kv.device_index
     words, kv_len, width, offset, q_row = _rows(rows)
     n, q_rows = len(kv_len), max(q_row) + 1
+    if sinks_row_stride < 0:
+        raise ValueError(f"sinks_row_stride must not be negative, got {sinks_row_stride}")
     bf16 = torch.bfloat16
     pq = _tensor(q_attn, "q_attn", bf16, dev, q_rows * HEADS * DIM)
     po = _tensor(out, "out", bf16, dev, q_rows * HEADS * DIM)

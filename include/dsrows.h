@@ -465,7 +465,7 @@ int ds_rows_rope(const ds_rope_t* rope, const void* x, uint64_t x_token_stride, 
  *     DS_CACHE_INT4  a row is dim / 16 groups of 16 values n s: s an e4m3 scale,
  *                    n an integer in -7 .. 7 held as n + 8 in 4 bits. A 32-bit
  *                    word holds 8 values, value i at bits 4 (i / 2) + 16 (i mod 2);
- *                    a scale byte of 0x7F (NaN) makes its group NaN.
+ *                    a scale byte above 0x7E (NaN, or a sign) makes its group NaN.
  *                    dim 512: [page_size][256 bytes of values, 32 scales].
  *                    dim 128: 4 planes [page_size][16 bytes], plane c with values
  *                    32 c .. 32 c + 31 of each row, then [page_size][8 scales]

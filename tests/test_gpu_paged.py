@@ -68,6 +68,7 @@ def check_rope(got, x, pos, rope_kw, first, layout, inverse, magnitude, dtype):
 @pytest.mark.parametrize("tokens,heads,dim,rot,first", [
     (1, 1, 2, 2, 0), (3, 1, 64, 64, 0), (8, 64, 512, 64, 448), (5, 7, 128, 64, 64), (33, 2, 96, 86, 10),
     (2, 3, 130, 6, 4), (1, 5, 1024, 512, 512), (300, 16, 128, 128, 0), (17, 64, 64, 2, 62), (40, 9, 192, 48, 96),
+    (2, 2, 1023, 510, 512), (1, 1, 1024, 512, 2),
 ])
 @pytest.mark.parametrize("inplace", [False, True])
 def test_rope(layout, dtype, tokens, heads, dim, rot, first, inplace):
@@ -478,6 +479,33 @@ def test_scores_of_bad_pages_and_values(fmt, page):
     assert np.all(err <= SCORE_RTOL * score_bound(*args)[~gone])
 
 
+def test_every_scale_byte():
+    """Keys and KV rows of one value n = 1 in every group, row r with scale byte r: the scores
+    and outputs of the value, NaN (so -inf, and zero heads) from byte 0x7F on."""
+    page, w = 256, torch.zeros(1, 64, device="cuda")
+    w[0, 0] = 1.0
+    for dim in (128, 512):
+        data = np.zeros(ds.ds_rows_page_bytes(page, dim, "int4"), np.uint8)
+        n = np.ones((page, dim), np.int64)
+        ref.write_int4_page(data, dim, page, n, np.repeat(np.arange(256, dtype=np.uint8)[:, None], dim // 16, 1))
+        cache = ds.PagedCache(torch.from_numpy(data).cuda(), i32([[0]]), page, dim, "int4")
+        q = torch.zeros(1, 64, dim, dtype=BF16, device="cuda")
+        q[0, 0, dim - 1] = 1.0
+        if dim == 128:
+            scores = torch.zeros(256, device="cuda")
+            ds.ds_rows_indexer_score_paged([(256, 256, 0, 0)], q, w, cache, scores)
+            got = f64(scores)
+            np.testing.assert_array_equal(got[:127], ref.E4M3)
+            assert np.all(np.isneginf(got[127:]))
+            continue
+        out = torch.zeros_like(q)
+        for r in (0, 1, 7, 8, 63, 126, 127, 128, 200, 255):
+            ds.ds_rows_sparse_attn_paged([(256, 1, 0, 0)], q, torch.full((64,), -1e30, device="cuda"), 0, i32([r]), SCALE,
+                                         out, cache)
+            want = ref.E4M3[r] if r < 127 else 0.0
+            assert (out == want).all(), r
+
+
 def test_scores_with_weights_off_16_bytes():
     rng = np.random.default_rng(3)
     cache, values = make_cache(rng, [200], 128, "int4", 32)
@@ -753,6 +781,11 @@ def test_cache_refusals_of_the_binding():
     q, out = (torch.zeros(1, 64, 512, dtype=BF16, device="cuda") for _ in range(2))
     idx = torch.zeros(512, dtype=torch.int32, device="cuda")
     sinks = torch.zeros(64, device="cuda")
+    with pytest.raises(ValueError, match="negative"):
+        ds.ds_rows_sparse_attn_paged([(100, 10, 0, 0)], q, sinks, -64, idx, SCALE, out, cache)
+    with pytest.raises(ValueError, match="negative"):
+        ds.ds_rows_indexer_score_paged([(100, 100, 0, 0)] * 2, q, torch.zeros(1, 64, device="cuda"), cache,
+                                       torch.zeros(100, device="cuda"), score_stride=-100)
     with pytest.raises(ds.DsRowsError, match="exceeds the 2 pages"):
         ds.ds_rows_sparse_attn_paged([(129, 10, 0, 0)], q, sinks, 0, idx, SCALE, out, cache)
     with pytest.raises(ValueError, match="q_attn"):
