@@ -91,8 +91,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     if (p.rope.rot) {
         const uint32_t pairs = p.rope.rot / 2;
         if (ok)
-            for (uint32_t i = g; i < pairs; i += LANES)
-                trig_s[r][pair_at(i)] = rope_turn(pos, p.rope.turns[i], p.rope.magnitude, false);
+            for (uint32_t i0 = g; i0 < pairs; i0 += 4 * LANES) {
+                uint64_t turns[4];  // four pairs' loads together
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (i0 + k * LANES < pairs) turns[k] = p.rope.turns[i0 + k * LANES];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (i0 + k * LANES < pairs)
+                        trig_s[r][pair_at(i0 + k * LANES)] = rope_turn(pos, turns[k], p.rope.magnitude, false);
+            }
         __syncwarp();
         const uint32_t e0 = g * G - p.rope.first;  // this lane's elements within the range, modulo 2^32
         const bool inside = e0 < p.rope.rot, low = e0 < pairs;
@@ -101,12 +109,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             if (p.half) {
                 const int other = (threadIdx.x & 31) + (!inside ? 0 : low ? (int)pairs / G : -((int)pairs / G));
                 const float2* trig = &trig_s[r][pair_at(!inside ? 0 : low ? e0 : e0 - pairs)];
+                const uint32_t flip = low ? 0x80000000u : 0u;
 #pragma unroll
                 for (int i = 0; i < G; ++i) {
                     const float z = __shfl_sync(0xFFFFFFFFu, y[i], other);
                     if (inside && ok) {
+                        // rope_first or rope_second, by the sine's sign.
                         const float2 cs = trig[i * W];
-                        y[i] = low ? rope_first(y[i], z, cs) : rope_second(z, y[i], cs);
+                        y[i] = fmaf(y[i], cs.x, __fmul_rn(z, __uint_as_float(__float_as_uint(cs.y) ^ flip)));
                     }
                 }
             } else if (inside && ok) {

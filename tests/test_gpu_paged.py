@@ -3,9 +3,9 @@ ds_rows_append, ds_rows_indexer_score_paged and ds_rows_sparse_attn_paged agains
 the float64 oracle, and against the contiguous entry points on the bf16 rows that
 a cache stands for.
 
-Tolerances. Rotation: the angle's fp32 word is off by 2^-25 of half a turn
-(9.4e-8), sincospif by two ulps of a number at most 1 (1.2e-7), and three
-roundings of 2^-24 follow (the magnitude, the product, the sum): 4e-7 of
+Tolerances. Rotation: the remainder within a quarter turn is at most pi/4, rounded twice (2^-24 of
+itself: 4.7e-8), the polynomials' last step rounds by 2^-25 to 2^-24 (6e-8), their next terms are
+below 3e-8, and three roundings of 2^-24 follow (the magnitude, the product, the sum): 3.2e-7 of
 m (|a| + |b|), taken as 5e-7, plus half a step of the output's type.
 Scores: sums of 128 products and of 64 heads in fp32, 192 roundings of 2^-24 of
 T = sum |w| sum |q k|: 1.2e-5 T. Attention: the bars of parity.check_out.
