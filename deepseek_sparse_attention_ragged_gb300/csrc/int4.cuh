@@ -83,8 +83,16 @@ __device__ __forceinline__ uint8_t quantise(const float (&y)[kGroup], uint32_t (
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) {
         const float q0 = y[i] * r;
-        const float q = fmaf(fmaf(-q0, s, y[i]), r, q0);
-        n[i] = (fminf(fmaxf(q, -7.0f), 7.0f) + kToInt) - kToInt;
+        n[i] = fmaf(fmaf(-q0, s, y[i]), r, q0);
+    }
+    // A normal s is at least 16/17 of top / 7, so |q| <= 7.44 rounds to 7 at most; a subnormal,
+    // saturated or NaN one says nothing.
+    if (byte < 0x08 || byte >= 0x7E)
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) n[i] = fminf(fmaxf(n[i], -7.0f), 7.0f);
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+        n[i] = (n[i] + kToInt) - kToInt;
         held[i] = n[i] * s;
     }
 #pragma unroll
