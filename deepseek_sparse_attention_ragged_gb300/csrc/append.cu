@@ -12,10 +12,10 @@
 //
 // Eight 512-wide rows: 2.4 us. 8191 fp32 rows of 512 into bf16 pages (25 MB): 6.0 us, 6.7 us
 // with nothing in L2 (3.7 us at the measured copy bandwidth). 32768 rows of 128 into 4-bit
-// pages, half of each rotated, with the values written too (19 MB, 2.9 us): 8.4 us, bound by
-// instructions (800 a warp of four rows, a quarter of them sines and cosines; 14.3 us with
-// divisions for quotients and per-element index arithmetic). More blocks on an SM than the
-// 48 registers allow made it slower (8.9 us at 40 registers, 11.2 us at 32).
+// pages, half of each rotated, with the values written too (19 MB, 2.9 us): 7.4 us, bound by
+// instructions (700 a warp of four rows: quotients, rotation, angles); 14.3 us with divisions
+// for quotients and per-element index arithmetic. More blocks on an SM than the 48 registers
+// allow made it slower (8.9 us at 40 registers, 11.2 us at 32, against 8.4).
 
 #include "int4.cuh"
 #include "rope.cuh"

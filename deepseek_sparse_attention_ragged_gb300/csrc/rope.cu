@@ -2,22 +2,24 @@
 //   m (a cos x - b sin x), m (a sin x + b cos x),  x = t theta_i
 // (x negated for the inverse, which is the transpose).
 //
-// Bound by the bytes moved: 2 (in place: 2 rot / dim) of the rows. A thread owns
-// one unit of a row's rotated range: 16 bytes of interleaved pairs, or 16 bytes
-// from each half, with their angles in registers, and rotates that unit of a
-// group of heads of one token, so sine and cosine are taken once per group; out of
-// place, threads of their own copy two pieces each of what is not rotated. The
-// heads of a group are interleaved over the block, so that its accesses at one time
-// cover whole rows side by side. 4096 x 64 bf16 rows of 128, half of each rotated, out
-// of place (134 MB): 27.3 us with inputs that are not in L2, 22.4 us replayed on the same
-// ones (a plain copy of them: 21.1 us); replayed, with consecutive heads per thread
-// 27.6 us, without the streaming hints 24.5 us, with the copies in the rotating threads
-// 31.5 us. What is left is that an access takes 64 bytes of a line (23.3 us if it took
-// all 128); threads that read whole lines and share the angles through shared memory
-// needed a barrier and twice the loads, and took 44 us. Eight rows of 64 heads in
-// place: 1.6 us; 1021 x 64 fp32 rows in place 4.2 us.
-// A row whose address, stride or range is not a multiple of 16 bytes is moved
-// by elements, one pair a unit.
+// Bound by the bytes moved: 2 (in place: 2 rot / dim) of the rows.
+//
+// Out of place (rope_rows_kernel) a thread moves the same 16 bytes of up to 16 heads of a
+// token and its neighbours the rest of those rows, so that an access of a warp covers whole
+// lines; the heads of a group are interleaved over the block, so that its rows at one time
+// lie side by side. The angles of a thread's pairs stay in its registers, and in the half
+// layout a pair's other element comes by shuffles. 4096 x 64 bf16 rows of 128, half of each
+// rotated (134 MB, nothing in L2): 23.4 us, where a plain copy of them takes 21.1 us; 23.9
+// with 8 heads a thread, 28.9 with 4. A thread per pair of halves took 27.0 us (each access
+// 64 bytes of a line), the angles shared through shared memory 44 us (a barrier).
+//
+// In place (rope_kernel) a thread owns one unit of a row's rotated range, 16 bytes of
+// interleaved pairs or 16 bytes from each half, for up to 8 heads: nobody else reads what
+// it writes. 1021 x 64 fp32 rows of 512, 64 rotated: 4.5 us (33 MB); eight tokens of 64
+// heads: 1.6 us. The same kernel serves half layouts whose range crosses a warp of
+// rope_rows_kernel (rows of 12 or 24 pieces, say), and moves rows whose address, stride or
+// range is not a multiple of 16 bytes element by element, one pair a unit; threads of
+// their own then copy what is not rotated.
 
 #include "rope.cuh"
 
@@ -27,7 +29,8 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeThreadsMax = 544;   // one row a block: 1024 / 2 units and one more, in whole warps
-constexpr uint32_t kGroupMax = 8;
+constexpr uint32_t kGroupMax = 8;      // heads of a thread, at most: in place
+constexpr uint32_t kRowsGroupMax = 16; // ... and out of place
 constexpr uint32_t kFull = 512;        // threads an SM keeps busy with
 
 template <typename T>
@@ -47,8 +50,8 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 
-// N elements of a row: 16 bytes in one access, or element by element. kStream: the rows
-// go by once (out of place), so they are the first to leave the L2.
+// N elements of a row: 16 bytes in one access, or element by element. kStream: what goes
+// by once (out of place) is the first to leave the L2.
 template <typename T, int N>
 struct Piece {
     T v[N];
@@ -79,7 +82,7 @@ __device__ __forceinline__ void put(T* p, const Piece<T, N>& r) {
 }
 
 // Heads h, h + step, ... (H of them) of a token: one or two pieces of each row.
-template <typename T, int N, int H, bool kWide, bool kStream>
+template <typename T, int N, int H, bool kWide>
 struct Step {
     Piece<T, N> a[H], b[H];
     __device__ __forceinline__ void load(const T* x, uint64_t stride, uint32_t h, uint32_t h1, uint32_t step,
@@ -88,8 +91,8 @@ struct Step {
         for (int k = 0; k < H; ++k)
             if (h + k * step < h1) {
                 const T* row = x + (uint64_t)(h + k * step) * stride;
-                a[k] = get<T, N, kWide, kStream>(row + fa);
-                if (two) b[k] = get<T, N, kWide, kStream>(row + fb);
+                a[k] = get<T, N, kWide, false>(row + fa);
+                if (two) b[k] = get<T, N, kWide, false>(row + fb);
             }
     }
     __device__ __forceinline__ void store(T* out, uint64_t stride, uint32_t h, uint32_t h1, uint32_t step,
@@ -98,8 +101,8 @@ struct Step {
         for (int k = 0; k < H; ++k)
             if (h + k * step < h1) {
                 T* row = out + (uint64_t)(h + k * step) * stride;
-                put<T, N, kWide, kStream>(row + fa, a[k]);
-                if (two) put<T, N, kWide, kStream>(row + fb, b[k]);
+                put<T, N, kWide, false>(row + fa, a[k]);
+                if (two) put<T, N, kWide, false>(row + fb, b[k]);
             }
     }
 };
@@ -113,14 +116,13 @@ constexpr int piece_len() {
 
 }  // namespace
 
-template <typename T, bool kHalf, bool kWide, bool kStream>
+template <typename T, bool kHalf, bool kWide>
 __global__ void __launch_bounds__(kRopeThreadsMax) rope_kernel(const __grid_constant__ RopeCall p) {
     constexpr int N = piece_len<T, kHalf, kWide>();
     constexpr int M = kWide ? N : 1;  // a piece outside the range
     constexpr int PAIRS = kHalf ? N : N / 2;
     // Heads of a step: four pieces of 16 bytes a thread. With two heads the interleaved rotation
-    // of 1021 x 64 fp32 rows in place took 5.7 us instead of 4.2; with four the half layout's
-    // 4096 x 64 bf16 rows out of place 24.5 us instead of 22.4.
+    // of 1021 x 64 fp32 rows in place took 5.7 us instead of 4.2.
     constexpr int H = kHalf ? 2 : 4;
     pdl_trigger();
     const uint32_t units = p.units + p.copies;
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kRopeThreadsMax) rope_kernel(const __grid_cons
         const uint32_t q = u - p.units, q2 = q + p.copies;
         const bool two = q2 < pieces;
         const uint32_t fa = (q < before ? q : q + skip) * M, fb = two ? (q2 < before ? q2 : q2 + skip) * M : fa;
-        Step<T, M, H, kWide, kStream> now;
+        Step<T, M, H, kWide> now;
         now.load(x, p.x_head, h0, h1, step, fa, fb, two);
         if (p.positions[token] < 0) return;
         for (uint32_t h = h0; h < h1; h += H * step) {
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kRopeThreadsMax) rope_kernel(const __grid_cons
     }
     const uint32_t fa = p.rope.first + u * N;
     const uint32_t fb = fa + p.rope.rot / 2;
-    Step<T, N, H, kWide, kStream> now;  // b: the second half's piece (kHalf)
+    Step<T, N, H, kWide> now;  // b: the second half's piece (kHalf)
     now.load(x, p.x_head, h0, h1, step, fa, fb, kHalf);
     const int32_t pos = p.positions[token];
     if (pos < 0) return;
@@ -179,7 +181,99 @@ __global__ void __launch_bounds__(kRopeThreadsMax) rope_kernel(const __grid_cons
     }
 }
 
-template <typename T, bool kHalf, bool kWide, bool kStream>
+// Out of place, rows, strides and ranges in pieces of 16 bytes: a thread moves piece v of
+// p.group heads of a token, so that an access of a warp covers whole lines. In the half
+// layout a pair's other element comes from its lane by shuffles: the launcher sees to it
+// that a row's range lies in one warp.
+template <typename T, bool kHalf>
+__global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_constant__ RopeCall p) {
+    constexpr int N = 16 / (int)sizeof(T);
+    constexpr int PAIRS = kHalf ? N : N / 2;
+    constexpr int H = 4;  // heads whose loads are in flight together
+    pdl_trigger();
+    const uint32_t v = threadIdx.x % p.units, pairs = p.rope.rot / 2;
+    const uint64_t item = (uint64_t)blockIdx.x * p.slots + threadIdx.x / p.units;
+    const uint64_t token = item / p.groups;
+    const bool there = token < p.tokens;
+    const uint32_t step = p.groups, h0 = there ? (uint32_t)(item - token * p.groups) : 0u, h1 = there ? p.heads : 0u;
+    const uint32_t f = v * N, e = f - p.rope.first;  // e: within the range, modulo 2^32
+    const bool turns = e < p.rope.rot, low = e < pairs;
+    const T* x = static_cast<const T*>(p.x) + (there ? token : 0) * p.x_token + f;
+    T* out = static_cast<T*>(p.out) + (there ? token : 0) * p.out_token + f;
+    pdl_wait();
+    Piece<T, N> a[H];
+    auto load = [&](uint32_t h) {
+#pragma unroll
+        for (int k = 0; k < H; ++k)
+            if (h + k * step < h1) a[k] = get<T, N, true, true>(x + (uint64_t)(h + k * step) * p.x_head);
+    };
+    load(h0);
+    const int32_t pos = there ? p.positions[token] : -1;
+    float2 cs[PAIRS];
+    if (turns) {
+        const uint64_t* t = p.rope.turns + (!kHalf ? e / 2 : low ? e : e - pairs);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) cs[i] = rope_turn(pos, t[i], p.rope.magnitude, p.inverse != 0);
+    }
+    const int lane = threadIdx.x & 31;
+    const int other = lane + (!turns ? 0 : low ? (int)(pairs / N) : -(int)(pairs / N));
+    const uint32_t flip = low ? 0x80000000u : 0u;
+    // Every lane of the warp goes round as often (the shuffles), by the same count of heads.
+    for (uint32_t n = 0; n < p.group; n += H) {
+        const uint32_t h = h0 + n * step;
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            if constexpr (kHalf) {
+                Piece<T, N> b;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    reinterpret_cast<uint32_t*>(b.v)[i] =
+                        __shfl_sync(0xFFFFFFFFu, reinterpret_cast<const uint32_t*>(a[k].v)[i], other);
+                if (turns)
+#pragma unroll
+                    for (int i = 0; i < N; ++i)  // rope_first or rope_second, by the sine's sign
+                        a[k].v[i] = from_f<T>(fmaf(to_f(a[k].v[i]), cs[i].x,
+                                                   __fmul_rn(to_f(b.v[i]), __uint_as_float(__float_as_uint(cs[i].y) ^ flip))));
+            } else if (turns) {
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    float va = to_f(a[k].v[2 * i]), vb = to_f(a[k].v[2 * i + 1]);
+                    rope_pair(va, vb, cs[i]);
+                    a[k].v[2 * i] = from_f<T>(va);
+                    a[k].v[2 * i + 1] = from_f<T>(vb);
+                }
+            }
+            if (h + k * step < h1 && pos >= 0) put<T, N, true, true>(out + (uint64_t)(h + k * step) * p.out_head, a[k]);
+        }
+        load(h + H * step);
+    }
+}
+
+template <typename T, bool kHalf>
+static cudaError_t launch_rows(RopeCall& p, int num_sms, cudaStream_t stream, bool pdl) {
+    p.units = p.dim / (16 / (uint32_t)sizeof(T));
+    p.slots = kRopeThreads / p.units;
+    uint32_t group = 1;
+    while (group < kRowsGroupMax && group < p.heads &&
+           p.tokens * ((p.heads + 2 * group - 1) / (2 * group)) * p.units >= (uint64_t)kFull * num_sms)
+        group *= 2;
+    p.group = group;
+    p.groups = (p.heads + group - 1) / group;
+    const uint64_t blocks = (p.tokens * p.groups + p.slots - 1) / p.slots;
+    if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+    return launch_kernel(rope_rows_kernel<T, kHalf>, dim3((uint32_t)blocks), dim3(p.units * p.slots), 0, stream, pdl, p);
+}
+
+// Whether rope_rows_kernel takes the half layout of these rows: whole rows in a warp, or the
+// range within one warp of a row of whole warps.
+template <typename T>
+static bool range_in_a_warp(const RopeCall& p) {
+    constexpr uint32_t n = 16 / sizeof(T);
+    const uint32_t pieces = p.dim / n, first = p.rope.first / n, last = first + p.rope.rot / n - 1;
+    return 32 % pieces == 0 || (pieces % 32 == 0 && first / 32 == last / 32);
+}
+
+template <typename T, bool kHalf, bool kWide>
 static cudaError_t launch(RopeCall& p, int num_sms, cudaStream_t stream, bool pdl) {
     constexpr int N = piece_len<T, kHalf, kWide>();
     constexpr int M = kWide ? N : 1;
@@ -197,7 +291,7 @@ static cudaError_t launch(RopeCall& p, int num_sms, cudaStream_t stream, bool pd
     const uint64_t items = p.tokens * p.groups;
     const uint64_t blocks = (items + p.slots - 1) / p.slots;
     if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
-    return launch_kernel(rope_kernel<T, kHalf, kWide, kStream>, dim3((uint32_t)blocks), dim3(units * p.slots), 0, stream, pdl,
+    return launch_kernel(rope_kernel<T, kHalf, kWide>, dim3((uint32_t)blocks), dim3(units * p.slots), 0, stream, pdl,
                          p);
 }
 
@@ -208,13 +302,13 @@ static cudaError_t launch_type(RopeCall& p, int layout, int num_sms, cudaStream_
     const uint64_t range = p.rope.first | (layout == DS_ROPE_HALF ? p.rope.rot / 2 : p.rope.rot) | (p.inplace ? 0 : p.dim);
     const bool wide = ((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out)) & 15) == 0 &&
                       ((strides | range) & (n - 1)) == 0;
+    if (wide && !p.inplace) {
+        if (layout == DS_ROPE_INTERLEAVED) return launch_rows<T, false>(p, num_sms, stream, pdl);
+        if (range_in_a_warp<T>(p)) return launch_rows<T, true>(p, num_sms, stream, pdl);
+    }
     if (layout == DS_ROPE_HALF)
-        return !wide ? launch<T, true, false, false>(p, num_sms, stream, pdl)
-               : p.inplace ? launch<T, true, true, false>(p, num_sms, stream, pdl)
-                           : launch<T, true, true, true>(p, num_sms, stream, pdl);
-    return !wide ? launch<T, false, false, false>(p, num_sms, stream, pdl)
-           : p.inplace ? launch<T, false, true, false>(p, num_sms, stream, pdl)
-                       : launch<T, false, true, true>(p, num_sms, stream, pdl);
+        return wide ? launch<T, true, true>(p, num_sms, stream, pdl) : launch<T, true, false>(p, num_sms, stream, pdl);
+    return wide ? launch<T, false, true>(p, num_sms, stream, pdl) : launch<T, false, false>(p, num_sms, stream, pdl);
 }
 
 cudaError_t launch_rope(RopeCall p, int dtype, int layout, int num_sms, cudaStream_t stream, bool pdl) {
