@@ -30,7 +30,7 @@ __all__ = [
     "ds_rows_indexer_topk_queries_workspace_bytes", "ds_rows_indexer_topk_queries",
     "CompressorRow", "ds_rows_compress_kv",
     "Rope", "ds_rows_rope", "PagedCache", "ds_rows_page_bytes", "ds_rows_append", "ds_rows_indexer_score_paged",
-    "ds_rows_sparse_attn_paged",
+    "ds_rows_sparse_attn_paged", "PAGED_WORKSPACE_BYTES",
     "STATUS_WAIT_TIMEOUT", "STATUS_OVERFLOW", "workspace_status", "ds_rows_selftest_bounded_wait",
     "ROWS_MAX", "INDEX_HEADS", "INDEX_DIM", "TOP_K", "HEADS", "DIM",
 ]
@@ -247,13 +247,6 @@ def workspace(rows, device=None) -> torch.Tensor:
     """A workspace tensor (uint8, 256-byte aligned by the caching allocator)."""
     return torch.empty(ds_rows_workspace_bytes(rows), dtype=torch.uint8,
                        device=device if device is not None else "cuda")
-
-
-def _workspace_for(rows, device, raw_stream: int) -> torch.Tensor:
-    """A workspace for one call on the stream `raw_stream`, taken from that stream's
-    memory, so that it is not handed out again while the call still runs."""
-    with torch.cuda.stream(torch.cuda.ExternalStream(raw_stream, device=device)):
-        return workspace(rows, device)
 
 
 def workspace_status(workspace_t: torch.Tensor) -> int:
@@ -554,5 +547,5 @@ def ds_rows_compress_kv(kv_states, score_states, start_pos, kv, score, ape, norm
 # ---------------------------------------------------------------------------
 
 from . import paged as _paged  # noqa: E402  (uses the names above)
-from .paged import (PagedCache, Rope, ds_rows_append, ds_rows_indexer_score_paged, ds_rows_page_bytes,  # noqa: E402
+from .paged import (PAGED_WORKSPACE_BYTES, PagedCache, Rope, ds_rows_append, ds_rows_indexer_score_paged, ds_rows_page_bytes,  # noqa: E402
                     ds_rows_rope, ds_rows_sparse_attn_paged)

@@ -1172,7 +1172,8 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
     rc = check_attn_args(q_attn, sinks, sinks_row_stride, scale, out);
     if (rc) return rc;
     if (!indices) return fail(DS_EINVAL, "indices is NULL");
-    const Layout L = make_layout(rows, table);
+    Layout L;  // the status word only
+    L.total = DS_PAGED_WORKSPACE_BYTES;
     rc = check_workspace(&set, workspace, workspace_bytes, L);
     if (rc) return rc;
     StageRange range("dsrows.attention_paged");
@@ -1180,6 +1181,9 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
     std::memset(static_cast<void*>(&p), 0, sizeof(p));
     fill_tail(p, &set, q_attn, sinks, sinks_row_stride, scale, out, invalid, nullptr, 0, indices, nullptr,
               static_cast<uint8_t*>(workspace), L, false, true, nullptr);
+    p.part = nullptr;  // partials and flags stay in shared memory
+    p.flags = nullptr;
+    p.hist = nullptr;
     p.cache = paged_cache(*kv);
     const cudaError_t err = launch_sparse_attn_paged(p, kv->format, (cudaStream_t)stream, true);
     return err == cudaSuccess ? DS_OK : cuda_fail(err, "paged attention launch");

@@ -16,8 +16,9 @@ from typing import Optional
 
 import torch
 
-from . import DIM, DS_OK, HEADS, INDEX_DIM, INDEX_HEADS, _check, _table, _workspace_for, load
+from . import DIM, DS_OK, HEADS, INDEX_DIM, INDEX_HEADS, _check, _table, load
 
+PAGED_WORKSPACE_BYTES = 256  # DS_PAGED_WORKSPACE_BYTES
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # DS_BF16, DS_F16, DS_F32
 _LAYOUTS = {"interleaved": 0, "half": 1}                           # DS_ROPE_*
 _FORMATS = {"bf16": 0, "int4": 1}                                  # DS_CACHE_*
@@ -105,6 +106,13 @@ def _call(index: int, fn, *args) -> None:
             rc = fn(*args)
     if rc != DS_OK:
         _check(load(), rc)
+
+
+def _status_word_for(device: torch.device, raw_stream: int) -> torch.Tensor:
+    """A workspace for one call on the stream `raw_stream`, taken from that stream's
+    memory, so that it is not handed out again while the call still runs."""
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw_stream, device=device)):
+        return torch.empty(PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
 
 
 def _code(table, value, name: str) -> int:
@@ -290,7 +298,9 @@ def ds_rows_sparse_attn_paged(rows, q_attn: torch.Tensor, sinks: torch.Tensor, s
                               indices: torch.Tensor, scale: float, out: torch.Tensor, kv: PagedCache,
                               invalid: Optional[torch.Tensor] = None, workspace_t: Optional[torch.Tensor] = None,
                               stream=None) -> None:
-    """ds_rows_sparse_attn with entry e's KV rows in entry e of a paged cache (dim 512)."""
+    """ds_rows_sparse_attn with entry e's KV rows in entry e of a paged cache (dim 512).
+    workspace_t (optional): any workspace of at least PAGED_WORKSPACE_BYTES; it holds the
+    call's status word."""
     lib = load()
     dev = kv.device_index
     words, kv_len, width, offset, q_row = _rows(rows)
@@ -306,7 +316,7 @@ def ds_rows_sparse_attn_paged(rows, q_attn: torch.Tensor, sinks: torch.Tensor, s
     pi = None if invalid is None else _tensor(invalid, "invalid", torch.int32, dev, q_rows * HEADS)
     raw = _stream_of(stream, dev)
     if workspace_t is None:
-        workspace_t = _workspace_for(list(zip(kv_len, width, offset, q_row)), kv.pages.device, raw)
+        workspace_t = _status_word_for(kv.pages.device, raw)
     pw = _tensor(workspace_t, "workspace", torch.uint8, dev, 0)
     _call(dev, lib.ds_rows_sparse_attn_paged, n, words.buffer_info()[0], kv._ref, pq, ps, sinks_row_stride, px, scale,
           po, pi, pw, workspace_t.numel(), raw)

@@ -532,8 +532,11 @@ int ds_rows_indexer_score_paged(int rows, const ds_row_t* table, const ds_paged_
  * the output is bitwise that of ds_rows_sparse_attn on the bf16 rows that the
  * cache stands for. A selected row whose page id is not in [0, num_pages) zeroes
  * every head of its entry, as an index out of range does; a NaN scale zeroes the
- * heads as a non-finite KV element does. Workspace as for ds_rows_sparse_attn.
+ * heads as a non-finite KV element does. The workspace (256-byte aligned, at least
+ * DS_PAGED_WORKSPACE_BYTES; any other workspace of this library will do) holds the
+ * call's status word only.
  */
+#define DS_PAGED_WORKSPACE_BYTES 256
 int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* kv, const ds_bf16* q_attn,
                               const float* sinks, size_t sinks_row_stride, const int32_t* indices, float scale,
                               ds_bf16* out, uint32_t* invalid, void* workspace, size_t workspace_bytes, void* stream);

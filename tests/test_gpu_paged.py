@@ -718,6 +718,41 @@ def test_pools_past_32_bits(fmt, dim):
     assert got[0][0].any() and torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+def test_the_longest_rows(fmt):
+    """kv_len 2^31 - 1, one page under every place of the table: the page's scores over and
+    over (the second row's begin past 2^33 bytes), and its rows under the last indices."""
+    n, page = 2 ** 31 - 1, 256
+    places = -(-n // page)
+    rng = np.random.default_rng(15)
+    table = torch.zeros(2, places, dtype=torch.int32, device="cuda")
+    one, values = make_cache(rng, [page], 128, fmt, page)
+    keys = ds.PagedCache(one.pages, table + one.page_table[0, 0], page, 128, fmt)
+    q, w = queries(rng, 2, 128), torch.rand(2, 64, device="cuda")
+    short = torch.zeros(2, page, device="cuda")
+    both = ds.PagedCache(one.pages, one.page_table[:, :1].expand(2, 1).contiguous(), page, 128, fmt)
+    ds.ds_rows_indexer_score_paged(row_table([page, page]), q, w, both, short)
+    scores = torch.zeros(n + 1 + 999, device="cuda")
+    ds.ds_rows_indexer_score_paged([(n, 512, 0, 0), (999, 512, 512, 1)], q, w, keys, scores, score_stride=n + 1)
+    assert scores[n] == 0 and torch.equal(scores[n + 1:], short[1].repeat(4)[:999])
+    assert torch.equal(scores[n - 255:n], short[0, :255])
+    body = scores[:n - 255].view(-1, page)
+    assert all(torch.equal(part, short[0].expand_as(part)) for part in body.split(1 << 20))
+    del scores, body
+    one, values = make_cache(rng, [page], 512, fmt, page)
+    kv = ds.PagedCache(one.pages, table[:1] + one.page_table[0, 0], page, 512, fmt)
+    idx = np.r_[n - 1 - rng.permutation(300)[:99], 0]
+    q, sinks = queries(rng, 1, 512), torch.zeros(64, device="cuda")
+    out = torch.zeros_like(q)
+    ws = torch.full((ds.PAGED_WORKSPACE_BYTES,), 255, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ds.DsRowsError, match="workspace holds"):
+        ds.ds_rows_sparse_attn_paged([(n, 100, 0, 0)], q, sinks, 0, i32(idx), SCALE, out, kv, workspace_t=ws[:255])
+    ds.ds_rows_sparse_attn_paged([(n, 100, 0, 0)], q, sinks, 0, i32(idx), SCALE, out, kv, workspace_t=ws)
+    assert ds.workspace_status(ws) == 0 and (ws[4:] == 255).all()
+    want, _ = oracle.sparse_attention(f64(q[0]), values[0].astype(np.float64), np.sort(idx) % page, f64(sinks), SCALE)
+    check_out(f64(out[0]), want)
+
+
 def test_two_streams_at_once():
     """Calls on two streams with their own outputs and workspaces, interleaved; one
     stream given as an argument, its workspace left to the binding."""

@@ -257,8 +257,7 @@ def test_attention_refusals(lib):
     for scale in (0.0, float("nan"), float("inf")):
         assert _attn(lib, scale=scale) == -1 and "scale" in _err(lib)
     assert _attn(lib, [(8, 8, 0, 3), (9, 9, 8, 3)]) == -1 and "used twice" in _err(lib)
-    need = ds.ds_rows_workspace_bytes([(600, 512, 0, 0)])
-    assert _attn(lib, ws_bytes=need - 1) == -2 and "workspace holds" in _err(lib)
+    assert _attn(lib, ws_bytes=ds.PAGED_WORKSPACE_BYTES - 1) == -2 and "workspace holds" in _err(lib)
     assert _attn(lib, ws=FAKE + 16) == -3 and _attn(lib, ws=None) == -1
 
 
