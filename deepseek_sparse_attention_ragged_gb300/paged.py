@@ -81,8 +81,9 @@ def _cuda(t, name: str) -> int:
     return index
 
 
-# The current stream's handle by device index, without building a Stream object where
-# this torch has the call for it (2 us of a call's host time).
+# The current device, and the current stream's handle by device index without building a
+# Stream object, where this torch has the calls for it (2 us of a call's host time).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -99,7 +100,7 @@ def _stream_of(stream, index: int) -> int:
 
 def _call(index: int, fn, *args) -> None:
     """Call an entry point with the tensors' device as the current one."""
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = fn(*args)
     else:
         with torch.cuda.device(index):
