@@ -42,6 +42,11 @@
 // same ascending order, so the decode's output is bitwise the attention of
 // its own best-first index list.
 //
+// Over a paged cache (sparse_attn_paged_kernel) the rows come from the pages of a pool, in
+// bf16 or widened from 4 bits as they are gathered, and the partials cross the cluster in
+// distributed shared memory; every reduction is the same, so the output is bitwise that of
+// the rows that the cache stands for.
+//
 // Fail-closed rules: a caller's index < -1 or >= kv_len flags the whole row; a
 // non-finite logit (non-finite q or KV element, or overflow) flags its head;
 // a non-finite sink or denominator flags the head; a flagged head is written
