@@ -10,13 +10,12 @@ from __future__ import annotations
 
 import ctypes
 from array import array
-from itertools import chain
 from operator import add
 from typing import Optional
 
 import torch
 
-from . import DIM, DS_OK, HEADS, INDEX_DIM, INDEX_HEADS, _check, _table, load
+from . import DIM, DS_OK, HEADS, INDEX_DIM, INDEX_HEADS, _check, load
 
 PAGED_WORKSPACE_BYTES = 256  # DS_PAGED_WORKSPACE_BYTES
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # DS_BF16, DS_F16, DS_F32
@@ -123,16 +122,23 @@ def _code(table, value, name: str) -> int:
     return code
 
 
+def _four(kv_len, width, index_offset, q_row):
+    return kv_len, width, index_offset, q_row
+
+
 def _rows(rows):
     """A row table as ds_row_t words, and its columns (kv_len, width, index_offset, q_row)."""
     if not isinstance(rows, (list, tuple)):
         rows = list(rows)
     try:
-        words = array("I", chain.from_iterable(rows))
-    except TypeError:  # Row structures, or objects with their fields
-        tab, n = _table(rows)
-        words = array("I", chain.from_iterable((r.kv_len, r.width, r.index_offset, r.q_row) for r in tab[:n]))
-    if len(rows) == 0 or len(words) != 4 * len(rows):
+        try:
+            words = array("I", [x for n, w, o, q in rows for x in (n, w, o, q)])  # four fields in every row
+        except TypeError:  # Row structures, or objects with their fields
+            words = array("I", [x for r in rows for x in
+                                ((r.kv_len, r.width, r.index_offset, r.q_row) if hasattr(r, "kv_len") else _four(*r))])
+    except (TypeError, ValueError):
+        words = None
+    if not words:
         raise ValueError("rows must be a nonempty list of (kv_len, width, index_offset, q_row)")
     return words, words[0::4], words[1::4], words[2::4], words[3::4]
 
