@@ -115,6 +115,14 @@ def _status_word_for(device: torch.device, raw_stream: int) -> torch.Tensor:
         return torch.empty(PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
 
 
+def _u32(value, name: str) -> int:
+    """A whole number that a C uint32 holds (ctypes would cut it to 32 bits without a word)."""
+    n = int(value)
+    if n != value or not 0 <= n < 1 << 32:
+        raise ValueError(f"{name} must be a whole number in 0 .. 2^32 - 1, got {value}")
+    return n
+
+
 def _code(table, value, name: str) -> int:
     code = table.get(value)
     if code is None:
@@ -162,12 +170,14 @@ class Rope:
                  magnitude: float = 1.0, device=None):
         lib = load()
         code = _code(_LAYOUTS, layout, "layout")
-        host = torch.zeros(max(1, int(rot_dim) // 2), dtype=torch.int64)
-        _check(lib, lib.ds_rows_rope_turns(int(rot_dim), float(base), float(factor), int(original_len),
+        rot_dim, first = _u32(rot_dim, "rot_dim"), _u32(first, "first")
+        host = torch.zeros(DIM // 2, dtype=torch.int64)  # the longest table; the library checks rot_dim
+        _check(lib, lib.ds_rows_rope_turns(rot_dim, float(base), float(factor), _u32(original_len, "original_len"),
                                            float(beta_fast), float(beta_slow), host.data_ptr()))
+        host = host[: rot_dim // 2]
         self.turns = host.to(torch.device(device if device is not None else "cuda"))
         self.device_index = _cuda(self.turns, "the rotation's table")
-        self.rot_dim, self.first, self.layout, self.magnitude = int(rot_dim), int(first), layout, float(magnitude)
+        self.rot_dim, self.first, self.layout, self.magnitude = rot_dim, first, layout, float(magnitude)
         self._c = _Rope(self.turns.data_ptr(), self.first, self.rot_dim, code, self.magnitude)
         self._ref = ctypes.byref(self._c)
 
@@ -212,7 +222,8 @@ def ds_rows_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, out: torc
 def ds_rows_page_bytes(page_size: int, dim: int, fmt: str) -> int:
     """Bytes of one page of `page_size` rows of `dim` (128 or 512) elements held as "bf16" or "int4"."""
     lib = load()
-    n = lib.ds_rows_page_bytes(int(page_size), int(dim), _code(_FORMATS, fmt, "the cache's format"))
+    n = lib.ds_rows_page_bytes(_u32(page_size, "page_size"), _u32(dim, "dim"),
+                               _code(_FORMATS, fmt, "the cache's format"))
     if n == 0:
         _check(lib, -1)
     return int(n)

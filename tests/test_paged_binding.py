@@ -27,3 +27,21 @@ def test_rows_of_numpy_words_and_mixed_kinds():
     for bad in ([(1.5, 1, 0, 0)], ["abcd"], [None], 7 * [3]):
         with pytest.raises(ValueError, match="nonempty list"):
             paged._rows(bad)
+
+
+@pytest.mark.parametrize("kw", [dict(first=1 << 32), dict(first=-2), dict(first=0.5), dict(original_len=-1, factor=2.0),
+                                dict(original_len=1 << 32, factor=2.0), dict(rot_dim=(1 << 32) + 64), dict(rot_dim=-64),
+                                dict(rot_dim=63.5)])
+def test_rotations_beyond_32_bits_are_refused(kw):
+    """ctypes cuts what it is given to 32 bits: 2^32 would have been 0, -1 a context of 2^32 - 1."""
+    ds.build()
+    with pytest.raises(ValueError, match="whole number"):
+        ds.Rope(kw.pop("rot_dim", 64), device="cpu", **kw)
+
+
+@pytest.mark.parametrize("page,dim", [((1 << 32) + 64, 128), (64, (1 << 32) + 512), (-64, 128), (64.5, 128)])
+def test_page_sizes_beyond_32_bits_are_refused(page, dim):
+    ds.build()
+    with pytest.raises(ValueError, match="whole number"):
+        ds.ds_rows_page_bytes(page, dim, "bf16")
+    assert ds.ds_rows_page_bytes(64.0, np.int64(128), "bf16") == 16384
