@@ -21,6 +21,7 @@ PAGED_WORKSPACE_BYTES = 256  # DS_PAGED_WORKSPACE_BYTES
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # DS_BF16, DS_F16, DS_F32
 _LAYOUTS = {"interleaved": 0, "half": 1}                           # DS_ROPE_*
 _FORMATS = {"bf16": 0, "int4": 1}                                  # DS_CACHE_*
+_U32_MAX = 0xFFFFFFFF
 
 
 class _Rope(ctypes.Structure):
@@ -118,7 +119,7 @@ def _status_word_for(device: torch.device, raw_stream: int) -> torch.Tensor:
 def _u32(value, name: str) -> int:
     """A whole number that a C uint32 holds (ctypes would cut it to 32 bits without a word)."""
     n = int(value)
-    if n != value or not 0 <= n < 1 << 32:
+    if n != value or not 0 <= n <= _U32_MAX:
         raise ValueError(f"{name} must be a whole number in 0 .. 2^32 - 1, got {value}")
     return n
 
@@ -206,6 +207,8 @@ def ds_rows_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, out: torc
         heads, xh, oh = 1, 0, 0
     else:
         raise ValueError(f"x must be [tokens, heads, dim] or [tokens, dim], got {tuple(shape)}")
+    if heads > _U32_MAX or dim > _U32_MAX:
+        raise ValueError(f"x {tuple(shape)} has more than 2^32 - 1 heads or elements a head")
     if dim > 1 and (xs[-1] != 1 or os_[-1] != 1):
         raise ValueError("the elements of a row of x and out must be contiguous")
     ptr = _tensor(positions, "positions", torch.int32, dev, tokens)
@@ -249,8 +252,9 @@ class PagedCache:
         _tensor(page_table, "page_table", torch.int32, self.device_index, 1)
         self.pages, self.page_table = pages, page_table
         self.page_size, self.dim, self.format, self.num_pages = int(page_size), int(dim), fmt, total // size
-        self._c = _PagedCache(pages.data_ptr(), page_table.data_ptr(), page_table.shape[0], page_table.shape[1],
-                              self.page_size, self.num_pages, self.dim, _FORMATS[fmt])
+        entries, per_entry = (_u32(n, "a side of page_table") for n in page_table.shape)
+        self._c = _PagedCache(pages.data_ptr(), page_table.data_ptr(), entries, per_entry, self.page_size,
+                              self.num_pages, self.dim, _FORMATS[fmt])
         self._ref = ctypes.byref(self._c)
 
     @classmethod
