@@ -1002,6 +1002,7 @@ int ds_rows_append(const ds_paged_cache_t* cache, const void* x, uint64_t x_stri
     rc = check_elements(dtype, x, x, elem);
     if (rc) return rc;
     if (tokens > 0x7FFFFFFFull) return fail(DS_ESIZE, "tokens must be below 2^31, got %llu", (unsigned long long)tokens);
+    if (tokens <= 1) x_stride = 0;  // a lone row's stride says nothing
     if (x_stride > kMaxStride) return fail(DS_ESIZE, "x_stride is out of range");
     if (!seq || !slot) return fail(DS_EINVAL, "seq and slot must be non-NULL");
     if (!aligned4(seq) || !aligned4(slot) || !aligned4(positions) || !aligned4(invalid))
@@ -1076,11 +1077,14 @@ int ds_rows_rope(const ds_rope_t* rope, const void* x, uint64_t x_token_stride, 
     rc = check_elements(dtype, x, out, elem);
     if (rc) return rc;
     if (!aligned4(positions)) return fail(DS_EALIGN, "positions must be 4-B aligned");
+    // The strides of a side of one say nothing.
+    if (tokens <= 1) x_token_stride = out_token_stride = 0;
+    if (heads == 1) x_head_stride = out_head_stride = 0;
     if (x_token_stride > kMaxStride || x_head_stride > kMaxStride || out_token_stride > kMaxStride ||
         out_head_stride > kMaxStride)
         return fail(DS_ESIZE, "a stride is out of range");
     const bool inplace = x == out;
-    if (inplace && ((tokens > 1 && x_token_stride != out_token_stride) || (heads > 1 && x_head_stride != out_head_stride)))
+    if (inplace && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
         return fail(DS_EINVAL, "in place, the strides of x and out must be the same");
     // The rows of out must not overlap: heads within tokens, or tokens within heads.
     const bool heads_inner = (heads == 1 || out_head_stride >= dim) &&
@@ -1097,10 +1101,10 @@ int ds_rows_rope(const ds_rope_t* rope, const void* x, uint64_t x_token_stride, 
     p.x = x;
     p.out = out;
     p.positions = positions;
-    p.x_token = tokens > 1 ? x_token_stride : 0;  // a lone row's strides say nothing
-    p.x_head = heads > 1 ? x_head_stride : 0;
-    p.out_token = tokens > 1 ? out_token_stride : 0;
-    p.out_head = heads > 1 ? out_head_stride : 0;
+    p.x_token = x_token_stride;
+    p.x_head = x_head_stride;
+    p.out_token = out_token_stride;
+    p.out_head = out_head_stride;
     p.tokens = tokens;
     p.heads = heads;
     p.dim = dim;

@@ -437,7 +437,8 @@ int ds_rows_rope_turns(uint32_t rot_dim, double base, double factor, uint32_t or
  *              elements outside the rotated range are copied. The rows of `out`
  *              must not overlap; those of x may (stride 0 broadcasts).
  *   tokens     0 enqueues nothing; heads 1 .. 65536; tokens * heads < 2^31
- *   dim        1 .. 1024; first + rot_dim <= dim. Strides are at most 2^31.
+ *   dim        1 .. 1024; first + rot_dim <= dim. Strides are at most 2^31
+ *              (the stride of a side of one is not looked at).
  *   positions  device int32 [tokens]; a negative position marks padding: its
  *              rows of `out` are left as they are.
  *   inverse    nonzero: the angles are negated. This is the transpose of the
@@ -493,7 +494,7 @@ size_t ds_rows_page_bytes(uint32_t page_size, uint32_t dim, int format);
  * becomes row slot[i] of entry seq[i].
  *   x          device, element type `dtype`, rows x_stride elements apart (the
  *              elements of a row contiguous); must not share memory with the pages or `values`
- *   tokens     below 2^31; 0 enqueues nothing. x_stride is at most 2^31.
+ *   tokens     below 2^31; 0 enqueues nothing. x_stride is at most 2^31 (of a lone row: not looked at).
  *   seq, slot  device int32 [tokens]. seq -1 marks padding: the row is skipped.
  *              The (seq, slot) pairs of a call, and the places they map to, must
  *              be distinct: of two rows for one place, any mix may remain.

@@ -41,3 +41,24 @@ def test_cache_refuses_tables_past_32_bits():
     table = torch.empty(1, (1 << 32) + 1, dtype=torch.int32, device="cuda")  # would have been one page an entry
     with pytest.raises(ValueError, match="side of page_table"):
         ds.PagedCache(pages, table, 16, 128, "int4")
+
+
+# ---------------------------------------------------------------------------
+# strides
+# ---------------------------------------------------------------------------
+
+def test_rope_of_a_lone_token_of_a_wide_buffer():
+    """A token taken from a buffer whose tokens lie 2^32 elements apart, and one head of such a buffer."""
+    rope, pos = ds.Rope(64), i32([77])
+    data = torch.randn(4, 64, device="cuda")
+    want = torch.empty(1, 4, 64, device="cuda")
+    ds.ds_rows_rope(rope, data[None], pos, want)
+    x = torch.as_strided(data, (1, 4, 64), (1 << 32, 64, 1))
+    out = torch.empty_like(want)
+    ds.ds_rows_rope(rope, x, pos, out)
+    assert torch.equal(out, want)
+    x = torch.as_strided(data, (4, 1, 64), (64, 1 << 32, 1))
+    ds.ds_rows_rope(rope, x, pos.repeat(4), out.view(4, 1, 64))
+    assert torch.equal(out, want)
+    ds.ds_rows_rope(rope, torch.as_strided(data, (1, 4, 64), (1 << 40, 64, 1)), pos, data.view(1, 4, 64))
+    assert torch.equal(data, want[0])
