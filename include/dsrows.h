@@ -521,7 +521,8 @@ int ds_rows_append(const ds_paged_cache_t* cache, const void* x, uint64_t x_stri
  * are those of the bf16 keys that the cache stands for. A key whose page id is
  * not in [0, num_pages), or with a NaN scale, scores -inf. DS_EINVAL when the
  * cache has fewer entries than rows, or a table row cannot reach kv_len; kv_len
- * is below 2^31.
+ * is below 2^31. There is no status word: keys that a bounded device-side wait
+ * gave up on (see DS_STATUS_WAIT_TIMEOUT) score -inf.
  */
 int ds_rows_indexer_score_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* keys,
                                 const ds_bf16* q_index, const float* w_index, float* scores, size_t score_stride,
@@ -555,6 +556,17 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
  *   result   device uint32 [2]
  */
 int ds_rows_selftest_bounded_wait(uint32_t* status, uint32_t* result, uint64_t budget_ns, void* stream);
+
+/*
+ * Self-test of what ds_rows_indexer_score_paged leaves when its waits give up:
+ * the same call, whose blocks load only the first `tiles` of their 128-key tiles
+ * (a block takes every n-th tile of an entry) and whose waits give up after
+ * `budget_ns` (1,000 to 10,000,000,000). Keys of loaded tiles score as ever,
+ * the others -inf. Nothing faults and the device stays usable.
+ */
+int ds_rows_selftest_score_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* keys, const ds_bf16* q_index,
+                                 const float* w_index, float* scores, size_t score_stride, uint32_t tiles,
+                                 uint64_t budget_ns, void* stream);
 
 /* Message of the last failed call on this host thread ("" if none). */
 const char* ds_rows_last_error(void);

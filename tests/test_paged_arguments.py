@@ -1,4 +1,4 @@
-"""Strides of the rotation and the append without a GPU (calls of no tokens: checked, nothing enqueued)."""
+"""Arguments of the rotation, append and score entry points without a GPU (refused, or calls of no tokens: nothing enqueued)."""
 
 import ctypes
 
@@ -36,3 +36,13 @@ def test_append_of_a_lone_row_from_anywhere(lib):
                                              None, None)
     assert call(0) == 0
     assert call(2) == -2 and "x_stride" in lib.ds_rows_last_error().decode()
+
+
+def test_score_selftest_validation(lib):
+    tab, n = ds._table([(600, 512, 0, 0)])
+    c = paged._PagedCache(FAKE, FAKE, 8, 64, 64, 1000, 128, 1)
+    call = lambda out, budget: lib.ds_rows_selftest_score_paged(n, tab, ctypes.byref(c), FAKE, FAKE, out, 600, 1,  # noqa: E731
+                                                                budget, None)
+    assert call(FAKE, 999) == -1 and "budget_ns" in lib.ds_rows_last_error().decode()
+    assert call(FAKE, 10_000_000_001) == -1
+    assert call(None, 1000) == -1 and "scores is NULL" in lib.ds_rows_last_error().decode()
