@@ -7,15 +7,19 @@
 namespace dsrows {
 
 // Cosine and sine of `pos` * theta times m, where `turns` is theta / (2 pi) as a 64-bit
-// fraction of a turn: the product modulo 2^64 is the angle's fraction of a turn exactly
-// (far positions lose nothing). Its high word is split into the nearest quarter turn and a
-// remainder r in [-pi/4, pi/4], again exactly, and the Taylor polynomials of sine (to r^9, the
-// next term is below 2e-9) and cosine (to r^8, 3e-8) give both: half the instructions of
-// reducing and evaluating a general argument, which were a quarter of the append's.
+// fraction of a turn: the product modulo 2^64 is the angle's fraction of a turn, with no error
+// but the table's half step of 2^-64 times the position. It is split into the nearest quarter
+// turn and a remainder, exactly, whose 64 bits both words of r = [-pi/4, pi/4] are taken from:
+// small angles keep their relative accuracy (with the high word alone the sine of 10^-4 was
+// off by 10^-5 of itself). The Taylor polynomials of sine (to r^9, the next term is below
+// 2e-9) and cosine (to r^8, 3e-8) give both: half the instructions of reducing and evaluating
+// a general argument, which were a quarter of the append's.
 __device__ __forceinline__ float2 rope_turn(int32_t pos, uint64_t turns, float m, bool inverse) {
-    const uint32_t phase = (uint32_t)(((uint64_t)(uint32_t)pos * turns) >> 32);
-    const uint32_t quarter = (phase + 0x20000000u) >> 30;
-    const float r = (float)(int32_t)(phase - (quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const uint64_t phase = (uint64_t)(uint32_t)pos * turns;
+    const uint32_t high = (uint32_t)(phase >> 32);
+    const uint32_t quarter = (high + 0x20000000u) >> 30;
+    constexpr float kHigh = 1.4629180792671596e-9f, kLow = kHigh / 4294967296.0f;  // 2 pi / 2^32, 2 pi / 2^64
+    const float r = fmaf((float)(int32_t)(high - (quarter << 30)), kHigh, (float)(uint32_t)phase * kLow);
     const float r2 = r * r;
     float s = fmaf(r2, 2.7557319e-6f, -1.9841270e-4f);  // 1/9!, -1/7!
     s = fmaf(r2, s, 8.3333333e-3f);                     // 1/5!

@@ -65,6 +65,38 @@ def test_rope_of_a_lone_token_of_a_wide_buffer():
 
 
 # ---------------------------------------------------------------------------
+# angles
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("rot,base,factor", [(64, 1e4, 1.0), (64, 1e4, 40.0), (128, 5e6, 1.0), (512, 5e5, 8.0), (6, 1e4, 1.0)])
+def test_sines_of_small_angles(layout, inverse, rot, base, factor):
+    """Pairs (1, 0) at near positions: cosine and sine to 3e-7 of themselves, however small.
+    The remainder is rounded twice and its constant once (two steps of 2^-24 and 2.8e-8: 1.5e-7 of
+    r, so at most 1.5e-7 of a sine and 1.2e-7 of a cosine), the polynomial's last step 2^-24 of a
+    sine and 4.2e-8 of a cosine, its inner steps 3e-8 and 5e-8, the terms left out 3e-9 and
+    3.5e-8; products with 1 and 0 are exact: 2.5e-7 at most. 1e-16: the low word's rounding where
+    the high one is -1."""
+    pos = np.r_[np.arange(1, 40), 100, 1000, 4097, 30000]
+    theta = base ** (-2.0 * np.arange(rot // 2) / rot) / factor
+    angle = pos[:, None] * theta
+    # Both sides round the angle in 64 bits: 2^-52 of it, whatever the size of its sine; the
+    # table's half step is 2 pi 2^-65 a position.
+    x = torch.zeros(len(pos), 1, rot, device="cuda")
+    a, b = (slice(0, rot, 2), slice(1, rot, 2)) if layout == "interleaved" else (slice(0, rot // 2), slice(rot // 2, rot))
+    x[..., a] = 1.0
+    rope = ds.Rope(rot, layout=layout, base=base, factor=factor)
+    for out in (torch.empty_like(x), x):
+        ds.ds_rows_rope(rope, x, i32(pos), out, inverse=inverse)
+        got = out[:, 0].double().cpu().numpy()
+        for part, want in ((a, np.cos(angle)), (b, np.sin(-angle if inverse else angle))):
+            err = np.abs(got[:, part] - want)
+            bound = 3e-7 * np.abs(want) + 1e-16 + angle * 2.0 ** -52 + pos[:, None] * 2.0 ** -62
+            assert np.all(err <= bound), np.max(err / np.abs(want))
+
+
+# ---------------------------------------------------------------------------
 # indexer scores
 # ---------------------------------------------------------------------------
 
