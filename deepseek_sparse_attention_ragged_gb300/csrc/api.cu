@@ -8,7 +8,6 @@
 // and alignment. Everything is checked before anything is enqueued.
 
 #include <cudaTypedefs.h>
-#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -1086,37 +1085,6 @@ int ds_rows_append(const ds_paged_cache_t* cache, const void* x, uint64_t x_stri
     StageRange range("dsrows.append");
     const cudaError_t err = launch_append(p, dtype, dim, cache->format, (cudaStream_t)stream, true);
     return err == cudaSuccess ? DS_OK : cuda_fail(err, "append launch");
-}
-
-int ds_rows_rope_turns(uint32_t rot_dim, double base, double factor, uint32_t original_len, double beta_fast,
-                       double beta_slow, uint64_t* turns) {
-    if (!turns) return fail(DS_EINVAL, "turns is NULL");
-    if (rot_dim < 2 || rot_dim > DS_DIM || rot_dim % 2)
-        return fail(DS_EINVAL, "rot_dim must be even, 2..=%d, got %u", DS_DIM, rot_dim);
-    if (!(base > 1.0) || !std::isfinite(base)) return fail(DS_EINVAL, "base must be finite and above 1");
-    if (!(factor >= 1.0) || !std::isfinite(factor)) return fail(DS_EINVAL, "factor must be finite and at least 1");
-    if (original_len && (!(beta_slow > 0.0) || !(beta_fast >= beta_slow) || !std::isfinite(beta_fast)))
-        return fail(DS_EINVAL, "beta_fast >= beta_slow > 0 must be finite");
-    const double two_pi = 6.283185307179586476925;
-    double low = 0.0, high = 0.0;
-    if (original_len) {
-        auto turns_at = [&](double beta) {
-            return rot_dim * std::log(original_len / (two_pi * beta)) / (2.0 * std::log(base));
-        };
-        low = std::fmax(std::floor(turns_at(beta_fast)), 0.0);
-        high = std::fmin(std::ceil(turns_at(beta_slow)), (double)rot_dim - 1.0);
-    }
-    for (uint32_t i = 0; i < rot_dim / 2; ++i) {
-        double theta = std::pow(base, -2.0 * i / rot_dim);
-        if (factor != 1.0) {
-            // How far the pair is interpolated: fully without YaRN's ramp.
-            const double r =
-                original_len ? std::fmin(std::fmax((i - low) / std::fmax(high - low, 0.001), 0.0), 1.0) : 1.0;
-            theta = theta * (1.0 - r) + theta / factor * r;
-        }
-        turns[i] = (uint64_t)std::llrint(std::ldexp(theta / two_pi, 64));  // theta <= 1: below 2^62
-    }
-    return DS_OK;
 }
 
 int ds_rows_rope(const ds_rope_t* rope, const void* x, uint64_t x_token_stride, uint64_t x_head_stride, void* out,

@@ -397,9 +397,10 @@ int ds_rows_compress_kv(int rows, const ds_compressor_row_t* table, const float*
 /*
  * A rotation: pair (a, b) = pair i of a row at position t becomes
  *   m (a cos x - b sin x), m (a sin x + b cos x),  x = t theta_i.
- *   turns      device uint64 [rot_dim / 2] (8-B aligned): theta_i / (2 pi) as a
- *              64-bit fraction of a turn, from ds_rows_rope_turns. t * turns[i]
- *              modulo 2^64 is the angle's exact reduction at every position.
+ *   turns      device uint64 [rot_dim / 2] (8-B aligned): theta_i / (2 pi) as the
+ *              nearest 64-bit fraction of a turn, from ds_rows_rope_turns.
+ *              t * turns[i] modulo 2^64 is the reduced angle, off by t half steps
+ *              of 2^-64 of a turn: 4e-10 at the last position.
  *   first      first rotated element of a row (even when interleaved)
  *   rot_dim    rotated elements: even, 2 .. 512
  *   layout     DS_ROPE_INTERLEAVED or DS_ROPE_HALF
@@ -415,7 +416,9 @@ typedef struct {
 
 /*
  * The turns of a rotation, written to HOST memory [rot_dim / 2] (no GPU is
- * used; copy them to the device once). theta_i = base^(-2 i / rot_dim), then
+ * used; copy them to the device once), each the nearest to its formula's value
+ * (taken with 100 bits; YaRN's low and high, whole numbers, in 64-bit floating
+ * point). theta_i = base^(-2 i / rot_dim), then
  *   factor 1:                      as it is;
  *   factor > 1, original_len 0:    theta_i / factor (linear interpolation);
  *   factor > 1, original_len > 0:  YaRN: theta_i (1 - r_i) + theta_i / factor r_i,
@@ -444,8 +447,8 @@ int ds_rows_rope_turns(uint32_t rot_dim, double base, double factor, uint32_t or
  *   inverse    nonzero: the angles are negated. This is the transpose of the
  *              rotation, so it maps the gradient of `out` to the gradient of x
  *              (m is the same factor, not its reciprocal).
- * The angle is reduced exactly, sine and cosine are taken and the products are
- * summed in 32 bits, and the result is rounded once to `dtype`. Pointers need
+ * The angle is reduced in 64-bit integers, sine and cosine are taken and the
+ * products are summed in 32 bits, and the result is rounded once to `dtype`. Pointers need
  * the type's alignment; with 16-byte aligned rows and ranges the call is fastest.
  */
 int ds_rows_rope(const ds_rope_t* rope, const void* x, uint64_t x_token_stride, uint64_t x_head_stride, void* out,

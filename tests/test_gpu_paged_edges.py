@@ -1,11 +1,14 @@
 """Rotary positions and paged caches at the edges of what their documentation allows: shapes,
 strides and streams that tests/test_gpu_paged.py leaves out."""
 
+from decimal import Decimal
+
 import numpy as np
 import pytest
 import torch
 
 import deepseek_sparse_attention_ragged_gb300 as ds
+from test_rope_table import TWO_PI, exact_turns
 
 pytestmark = pytest.mark.gpu
 
@@ -94,6 +97,28 @@ def test_sines_of_small_angles(layout, inverse, rot, base, factor):
             err = np.abs(got[:, part] - want)
             bound = 3e-7 * np.abs(want) + 1e-16 + angle * 2.0 ** -52 + pos[:, None] * 2.0 ** -62
             assert np.all(err <= bound), np.max(err / np.abs(want))
+
+
+@pytest.mark.parametrize("rot,kw", [(64, dict(base=1e4)), (512, dict(base=1e4)), (128, dict(base=5e5, factor=8.0)),
+                                    (64, dict(base=1e4, factor=16.0, original_len=65536))])
+def test_sines_at_the_last_positions(rot, kw):
+    """The bound of test_sines_of_small_angles at positions up to 2^31 - 1, against angles reduced
+    in 60 decimal digits; the table's half step is 2 pi 2^-65 a position (3.7e-10 at the last)."""
+    pos = np.r_[2 ** 31 - 1 - np.arange(20), 2 ** 30 + 12345, 10 ** 9, 123456789, 2 ** 24 + 1]
+    full = [int(t * 2 ** 128) for t in exact_turns(rot, kw["base"], kw.get("factor", 1.0), kw.get("original_len", 0))]
+    turn = np.array([[float(Decimal(int(p) * f % 2 ** 128) / 2 ** 128) for f in full] for p in pos])
+    near = np.round(4 * turn)  # quarter turns, and the rest in radians: each value to 2^-52 of itself
+    angle = np.array([[float((Decimal(int(p) * f % 2 ** 128) / 2 ** 128 - Decimal(k / 4)) * TWO_PI)
+                       for f, k in zip(full, ks)] for p, ks in zip(pos, near)])
+    c, s = np.cos(angle), np.sin(angle)
+    k = near.astype(int) % 4
+    cos, sin = np.choose(k, [c, -s, -c, s]), np.choose(k, [s, c, -s, -c])
+    x = torch.zeros(len(pos), 1, rot, device="cuda")
+    x[..., : rot // 2] = 1.0
+    ds.ds_rows_rope(ds.Rope(rot, layout="half", **kw), x, i32(pos), x)
+    got = x[:, 0].double().cpu().numpy()
+    for part, want in ((got[:, : rot // 2], cos), (got[:, rot // 2:], sin)):
+        assert np.all(np.abs(part - want) <= 3e-7 * np.abs(want) + 1e-16 + pos[:, None] * 2.0 ** -62)
 
 
 # ---------------------------------------------------------------------------
