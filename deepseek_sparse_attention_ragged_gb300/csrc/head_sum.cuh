@@ -51,12 +51,12 @@ __device__ __forceinline__ float head_sum(const uint32_t (&x)[64], const float* 
     return (s4[0] + s4[1]) + (s4[2] + s4[3]);
 }
 
-// The same sum, 32 heads at a time with the weights in shared memory. With kAdd,
-// x + |x| = 2 max(0, x) takes the place of the maximum, and half the total is the
-// sum, bit for bit while nothing overflows: the addition runs on the FMA pipe, the
-// maximum on the integer pipe at half its rate. An infinite product makes that form
-// NaN or infinite where the maximum may be finite: a total that is not finite says
-// nothing, and is taken again without kAdd.
+// The same sum, 32 heads at a time with the weights in shared memory. With kAdd, x + |x| =
+// 2 max(0, x) takes the place of the maximum and w holds half the weights: the products and so
+// the sums are the same, bit for bit, where the half weights are exact (halvable()) and no 2 x
+// overflows. The addition runs on the FMA pipe, the maximum on the integer pipe at half its
+// rate. An overflowing 2 x makes the total NaN or infinite where the maximum's may be finite: a
+// total that is not finite says nothing, and is taken again without kAdd.
 template <bool kAdd>
 struct HeadSum {
     float2 s01 = {0.0f, 0.0f}, s23 = {0.0f, 0.0f};
@@ -72,11 +72,11 @@ struct HeadSum {
             s23 = fma2(make_float2(relu(x[h + 2]), relu(x[h + 3])), make_float2(w4.z, w4.w), s23);
         }
     }
-    __device__ __forceinline__ float total() const {
-        const float t = (s01.x + s01.y) + (s23.x + s23.y);
-        return kAdd ? 0.5f * t : t;
-    }
+    __device__ __forceinline__ float total() const { return (s01.x + s01.y) + (s23.x + s23.y); }
 };
+
+// Whether half of a weight is exact: below 2^-125 the half may lose its last bit.
+__device__ __forceinline__ bool halvable(float w) { return w == 0.0f || !(fabsf(w) < 0x1p-125f); }
 
 // The score of a key from its 64 head dot products in TMEM (one lane, 64 columns).
 template <bool kAdd>

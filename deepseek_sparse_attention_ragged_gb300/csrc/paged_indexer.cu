@@ -63,7 +63,7 @@ struct Shape {
     static constexpr size_t keys = 0;
     static constexpr size_t q = keys + (size_t)kStages * kStageBytes;
     static constexpr size_t w = q + 2 * (size_t)kQHalf;
-    static constexpr size_t bars = w + kIdxHeads * 4;
+    static constexpr size_t bars = w + 2 * kIdxHeads * 4;  // behind the weights and their halves
 };
 // The tiles of a buffer belong to one issuer and one set of each kind, and those of a stage to
 // one lane of the loading warp, one issuer and one widening set: a wait for a parity is then
@@ -185,7 +185,11 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
             const int h = i >> 4, ch = i & 15;
             *reinterpret_cast<uint4*>(q_s + (ch >> 3) * kQHalf + h * 128 + (((ch & 7) ^ (h & 7)) << 4)) = q[i];
         }
-        if (threadIdx.x < kIdxHeads) w_s[threadIdx.x] = p.w[(size_t)p.q_row[e] * kIdxHeads + threadIdx.x];
+        if (threadIdx.x < kIdxHeads) {
+            const float w = p.w[(size_t)p.q_row[e] * kIdxHeads + threadIdx.x];
+            w_s[threadIdx.x] = w;
+            w_s[kIdxHeads + threadIdx.x] = 0.5f * w;
+        }
         fence_proxy_async_smem();
     }
     tc_fence_before();
@@ -307,6 +311,7 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
         const int quarter = warp & 3;
         const uint64_t keep = l2_policy_evict_last();  // the top-k reads the scores next
         float* out = p.scores + (size_t)e * p.score_stride;
+        const bool halves = __all_sync(0xFFFFFFFFu, halvable(w_s[lane]) && halvable(w_s[lane + 32]));
         uint32_t a = set, ph = 0;  // buffer and its phase
         uint32_t j = (first + set * step) * kTileKeys + quarter * 32 + lane;
         for (uint32_t it = set; it < mine; it += kEpiSets, j += kEpiSets * step * kTileKeys) {
@@ -324,7 +329,8 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
             }
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + a * S::kAccCols;
-            float sc = head_sum_tmem<true>(taddr, w_s);
+            float sc = INFINITY;
+            if (halves) sc = head_sum_tmem<true>(taddr, w_s + kIdxHeads);
             if (__any_sync(0xFFFFFFFFu, !finite_f(sc))) {
                 const float again = head_sum_tmem<false>(taddr, w_s);
                 sc = finite_f(sc) ? sc : again;

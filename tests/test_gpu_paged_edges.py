@@ -125,17 +125,19 @@ def test_sines_at_the_last_positions(rot, kw):
 # indexer scores
 # ---------------------------------------------------------------------------
 
-def random_cache(seed, lens, dim, fmt, page):
-    """A cache whose entries' rows were appended, its pages in no order."""
+def appended(lens, fmt, page, seed):
+    """A cache of random keys, its pages in no order, and the bf16 keys that it stands for."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     places = -(-max(lens) // page)
     table = torch.randperm(len(lens) * places, generator=g, device="cuda").to(torch.int32).view(len(lens), places)
-    cache = ds.PagedCache.empty(len(lens) * places, table, page, dim, fmt)
+    cache = ds.PagedCache.empty(len(lens) * places, table, page, 128, fmt)
+    held = []
     for e, n in enumerate(lens):
-        x = torch.randn(n, dim, generator=g, device="cuda")
-        ds.ds_rows_append(cache, x, torch.full((n,), e, dtype=torch.int32, device="cuda"),
-                          torch.arange(n, dtype=torch.int32, device="cuda"))
-    return cache, g
+        held.append(torch.empty(n, 128, dtype=BF16, device="cuda"))
+        ds.ds_rows_append(cache, torch.randn(n, 128, generator=g, device="cuda"),
+                          torch.full((n,), e, dtype=torch.int32, device="cuda"),
+                          torch.arange(n, dtype=torch.int32, device="cuda"), values=held[-1])
+    return cache, held, g
 
 
 def row_table(lens):
@@ -149,7 +151,7 @@ def test_scores_of_waits_that_give_up(fmt, page):
     the others as ever, and the next call is whole."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     n = 128 * (4 * sms + 7) - 5  # one entry: block b takes tiles b, b + sms, ...
-    cache, g = random_cache(21, [n], 128, fmt, page)
+    cache, _, g = appended([n], fmt, page, 21)
     q = torch.randn(1, 64, 128, generator=g, device="cuda").to(BF16)
     w = torch.randn(1, 64, generator=g, device="cuda")
     want = torch.full((n + 9,), 123.0, device="cuda")
@@ -171,7 +173,7 @@ def test_scores_of_waits_that_give_up(fmt, page):
 
 def test_keys_given_up_on_are_not_selected():
     lens = [900, 300]
-    cache, g = random_cache(22, lens, 128, "int4", 64)
+    cache, _, g = appended(lens, "int4", 64, 22)
     q = torch.randn(2, 64, 128, generator=g, device="cuda").to(BF16)
     w = torch.randn(2, 64, generator=g, device="cuda")
     scores = torch.rand(2, 900, device="cuda")
@@ -181,3 +183,42 @@ def test_keys_given_up_on_are_not_selected():
                                                   900, 0, 20_000_000, torch.cuda.current_stream().cuda_stream) == 0
     ds.ds_rows_topk(row_table(lens), scores, 900, idx, ds.workspace(row_table(lens)))
     assert (idx[:812] == -1).all()
+
+
+def scores_both_ways(cache, held, lens, q, w):
+    out = [torch.full((len(lens), max(lens)), 123.0, device="cuda") for _ in range(2)]
+    ds.ds_rows_indexer_score_paged(row_table(lens), q, w, cache, out[0])
+    ds.ds_rows_indexer_score(row_table(lens), q, w, held, out[1])
+    return out
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+@pytest.mark.parametrize("power", [1, -100, -124, -126, -130, -140, -148, 120, 126])
+def test_scores_with_weights_of_any_size(fmt, power):
+    """Bitwise the contiguous scores of the keys that the cache stands for, where products fall
+    below the normal range, where weights themselves do, and where sums overflow."""
+    lens = [3000, 129]
+    cache, held, g = appended(lens, fmt, 64, 23)
+    q = torch.randn(2, 64, 128, generator=g, device="cuda").to(BF16)
+    w = (torch.randn(2, 64, generator=g, device="cuda").double() * 2.0 ** power).float()
+    paged, plain = scores_both_ways(cache, held, lens, q, w)
+    assert torch.equal(paged, plain)
+    w[0, 5:] = 0  # one head alone, and one of ordinary size beside the small ones
+    w[1, 7] = 1.0
+    paged, plain = scores_both_ways(cache, held, lens, q, w)
+    assert torch.equal(paged, plain)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+def test_scores_of_products_that_overflow(fmt):
+    """Dot products near the largest float (and infinite ones), under weights of every sign and zero."""
+    lens = [1500]
+    cache, held, g = appended(lens, fmt, 64, 24)
+    q = torch.randn(1, 64, 128, generator=g, device="cuda") * 2.0 ** torch.randint(118, 128, (1, 64, 1), generator=g,
+                                                                                 device="cuda")
+    w = torch.randn(1, 64, generator=g, device="cuda") * 2.0 ** -8
+    w[0, ::3] = 0
+    for x in (q, q.clamp(-1e38, 1e38) / 16):
+        paged, plain = scores_both_ways(cache, held, lens, x.to(BF16), w)
+        assert torch.equal(paged, plain)
+    assert torch.isfinite(plain).any() and torch.isneginf(paged).sum() < 1500
