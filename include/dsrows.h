@@ -520,8 +520,8 @@ int ds_rows_append(const ds_paged_cache_t* cache, const void* x, uint64_t x_stri
 
 /*
  * ds_rows_indexer_score with the keys in a paged cache (dim 128): entry e of the
- * table reads entry e of the cache. 4-bit keys are widened exactly, so the scores
- * are those of the bf16 keys that the cache stands for. A key whose page id is
+ * table reads entry e of the cache. 4-bit keys are widened exactly, and the scores
+ * are bitwise those of the bf16 keys that the cache stands for. A key whose page id is
  * not in [0, num_pages), or with a NaN scale, scores -inf. DS_EINVAL when the
  * cache has fewer entries than rows, or a table row cannot reach kv_len; kv_len
  * is below 2^31. There is no status word: keys that a bounded device-side wait

@@ -193,6 +193,17 @@ def scores_both_ways(cache, held, lens, q, w):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "int4"])
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("lens", [[1], [15, 16, 17, 127, 128, 129, 255, 257], [30000, 3, 4097]])
+def test_scores_are_those_of_the_rows_held(fmt, page, lens):
+    cache, held, g = appended(lens, fmt, page, 25)
+    q = torch.randn(len(lens), 64, 128, generator=g, device="cuda").to(BF16)
+    w = torch.randn(len(lens), 64, generator=g, device="cuda") / 8
+    paged, plain = scores_both_ways(cache, held, lens, q, w)
+    assert torch.equal(paged, plain) and torch.isfinite(paged).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
 @pytest.mark.parametrize("power", [1, -100, -124, -126, -130, -140, -148, 120, 126])
 def test_scores_with_weights_of_any_size(fmt, power):
     """Bitwise the contiguous scores of the keys that the cache stands for, where products fall
