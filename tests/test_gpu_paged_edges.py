@@ -68,6 +68,82 @@ def test_rope_of_a_lone_token_of_a_wide_buffer():
 
 
 # ---------------------------------------------------------------------------
+# many heads: a thread rotates several of them
+# ---------------------------------------------------------------------------
+
+ROPE_RTOL = 5e-7  # of m (|a| + |b|), derived at the head of tests/test_gpu_paged.py
+
+
+def check_rotated(got, x, pos, rot, first, layout, magnitude, inverse, fill):
+    """Every element of got against 64-bit arithmetic on x; rows of negative positions hold `fill`."""
+    dtype, half = x.dtype, rot // 2
+    theta = torch.from_numpy(10000.0 ** (-2.0 * np.arange(half) / rot)).cuda()
+    angle = pos.double()[:, None, None] * theta * (-1.0 if inverse else 1.0)
+    c, s = magnitude * angle.cos(), magnitude * angle.sin()
+    at = torch.arange(half, device="cuda")
+    a, b = (first + 2 * at, first + 2 * at + 1) if layout == "interleaved" else (first + at, first + half + at)
+    xa, xb = x[..., a].double(), x[..., b].double()
+    live = pos >= 0
+    tiny = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    size = ROPE_RTOL * magnitude * (xa.abs() + xb.abs()) + tiny
+    for part, want in ((a, xa * c - xb * s), (b, xa * s + xb * c)):
+        bound = size + want.abs() * (torch.finfo(dtype).eps / 2) * (1 + 1e-6)
+        bad = (got[..., part].double() - want).abs() > bound
+        assert not bad[live].any(), torch.nonzero(bad & live[:, None, None])[0].tolist()
+    rest = torch.ones(x.shape[-1], dtype=torch.bool, device="cuda")
+    rest[first:first + rot] = False
+    assert torch.equal(got[live][..., rest], x[live][..., rest]) and torch.equal(got[~live], fill[~live])
+
+
+# Shapes by what they reach on 152 SMs, where a thread takes twice the heads while 512 threads an SM
+# are left: heads a thread, and whether the groups divide the heads.
+@pytest.mark.parametrize("dtype,tokens,heads,dim,rot,first,shift", [
+    (F32, 160, 33, 128, 64, 64, 0),      # 2 (out of place)
+    (F32, 300, 64, 128, 128, 0, 0),      # 4
+    (BF16, 700, 64, 128, 64, 64, 0),     # 8
+    (BF16, 4900, 13, 128, 64, 64, 0),    # 16, one group of 13
+    (BF16, 1300, 65, 128, 64, 0, 0),     # 16, the last one short; in place 4 or 8
+    (F16, 2500, 65, 64, 64, 0, 0),       # 16; in place 8
+    (F32, 1021, 64, 512, 64, 448, 0),    # 16; in place 4 or 8
+    (BF16, 13000, 7, 96, 64, 32, 0),     # 8 (rows of 12 pieces: the half layout's out of place too)
+    (BF16, 4000, 7, 41, 16, 2, 1),       # 8, element by element (in place 2)
+    (F32, 2500, 13, 70, 64, 4, 1),       # 8, element by element
+    (F16, 1300, 65, 129, 6, 122, 1),     # the same, most of a row copied
+])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope_of_many_heads(dtype, tokens, heads, dim, rot, first, shift, layout, inplace, inverse):
+    g = torch.Generator(device="cuda").manual_seed(tokens + dim)
+    wide = dim + 8 if shift else dim
+    x = torch.randn(tokens, heads, wide, generator=g, device="cuda").to(dtype)[..., shift:shift + dim]
+    pos = torch.randint(0, 1 << 20, (tokens,), generator=g, device="cuda", dtype=torch.int32)
+    pos[5::97] = -1
+    rope = ds.Rope(rot, first=first, layout=layout, magnitude=1.25)
+    keep = x.clone()
+    out = x if inplace else torch.full((tokens, heads, wide), 7.0, dtype=dtype, device="cuda")[..., shift:shift + dim]
+    fill = out.clone()
+    ds.ds_rows_rope(rope, x, pos, out, inverse=inverse)
+    check_rotated(out, keep, pos, rot, first, layout, 1.25, inverse, fill)
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_rope_of_many_heads_outside_the_tokens(layout, inplace):
+    """Heads that lie outside the tokens, rows inside wider ones, sixteen (in place eight) a thread."""
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x = torch.randn(21, 3000, 192, generator=g, device="cuda").to(BF16).transpose(0, 1)[..., 32:160]
+    pos = torch.randint(0, 1 << 20, (3000,), generator=g, device="cuda", dtype=torch.int32)
+    pos[::41] = -9
+    base = torch.full((21, 3000, 136), 7.0, dtype=BF16, device="cuda")
+    keep = x.clone()
+    out = x if inplace else base.transpose(0, 1)[..., 8:]
+    fill = out.clone()
+    ds.ds_rows_rope(ds.Rope(64, first=32, layout=layout), x, pos, out)
+    check_rotated(out, keep, pos, 64, 32, layout, 1.0, False, fill)
+    assert (base[..., :8] == 7.0).all()
+
+# ---------------------------------------------------------------------------
 # angles
 # ---------------------------------------------------------------------------
 
