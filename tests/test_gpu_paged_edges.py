@@ -309,3 +309,51 @@ def test_scores_of_products_that_overflow(fmt):
         paged, plain = scores_both_ways(cache, held, lens, x.to(BF16), w)
         assert torch.equal(paged, plain)
     assert torch.isfinite(plain).any() and torch.isneginf(paged).sum() < 1500
+
+
+# ---------------------------------------------------------------------------
+# beside the contiguous calls
+# ---------------------------------------------------------------------------
+
+def test_contiguous_calls_behind_a_rotation_in_place():
+    """A long rotation in place, whose last rows the next call of the stream takes as its query: the
+    contiguous calls fetch their query early, and the rotation lets the next launch begin early."""
+    g = torch.Generator(device="cuda").manual_seed(41)
+    tokens, lens = 4096, [3000, 700, 64]
+    first = tokens - len(lens)
+    rows = [(n, min(n, 512), 512 * e, first + e) for e, n in enumerate(lens)]
+    keys = [torch.randn(n, 128, generator=g, device="cuda").to(BF16) for n in lens]
+    kv = [torch.randn(n, 512, generator=g, device="cuda").to(BF16) for n in lens]
+    qi = torch.randn(tokens, 64, 128, generator=g, device="cuda").to(BF16)
+    qa = torch.randn(tokens, 64, 512, generator=g, device="cuda").to(BF16)
+    w = torch.randn(tokens, 64, generator=g, device="cuda") / 8
+    sinks = torch.randn(64, generator=g, device="cuda")
+    pos = torch.randint(0, 1 << 20, (tokens,), generator=g, device="cuda", dtype=torch.int32)
+    ri, ra = ds.Rope(64, first=64, layout="half"), ds.Rope(64, first=448)
+    ws = ds.workspace(rows)
+
+    def results(pause):
+        a, b = qi.clone(), qa.clone()
+        scores = torch.zeros(3, 3000, device="cuda")
+        idx = torch.full((3 * 512,), -1, dtype=torch.int32, device="cuda")
+        out, attn = (torch.zeros_like(qa[first:]) for _ in range(2))
+        full = [torch.zeros(tokens, 64, 512, dtype=BF16, device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+        ds.ds_rows_rope(ri, a, pos, a)
+        pause()
+        ds.ds_rows_indexer_score(rows, a, w, keys, scores)
+        ds.ds_rows_rope(ra, b, pos, b)
+        pause()
+        ds.ds_rows_decode(rows, a, w, keys, b, kv, sinks, 0, 512 ** -0.5, full[0], indices=idx, workspace_t=ws)
+        ds.ds_rows_rope(ra, b, pos, b, inverse=True)
+        pause()
+        ds.ds_rows_sparse_attn(rows, b, sinks, 0, idx, 512 ** -0.5, full[1], kv, workspace_t=ws)
+        torch.cuda.synchronize()
+        assert ds.workspace_status(ws) == 0
+        out.copy_(full[0][first:]), attn.copy_(full[1][first:])
+        return scores, idx, out, attn
+
+    want = results(torch.cuda.synchronize)
+    assert all(t.any() for t in want)
+    for _ in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(results(lambda: None), want))
