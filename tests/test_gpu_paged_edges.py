@@ -201,16 +201,16 @@ def test_sines_at_the_last_positions(rot, kw):
 # indexer scores
 # ---------------------------------------------------------------------------
 
-def appended(lens, fmt, page, seed):
-    """A cache of random keys, its pages in no order, and the bf16 keys that it stands for."""
+def appended(lens, fmt, page, seed, dim=128):
+    """A cache of random rows, its pages in no order, and the bf16 rows that it stands for."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     places = -(-max(lens) // page)
     table = torch.randperm(len(lens) * places, generator=g, device="cuda").to(torch.int32).view(len(lens), places)
-    cache = ds.PagedCache.empty(len(lens) * places, table, page, 128, fmt)
+    cache = ds.PagedCache.empty(len(lens) * places, table, page, dim, fmt)
     held = []
     for e, n in enumerate(lens):
-        held.append(torch.empty(n, 128, dtype=BF16, device="cuda"))
-        ds.ds_rows_append(cache, torch.randn(n, 128, generator=g, device="cuda"),
+        held.append(torch.empty(n, dim, dtype=BF16, device="cuda"))
+        ds.ds_rows_append(cache, torch.randn(n, dim, generator=g, device="cuda"),
                           torch.full((n,), e, dtype=torch.int32, device="cuda"),
                           torch.arange(n, dtype=torch.int32, device="cuda"), values=held[-1])
     return cache, held, g
@@ -309,6 +309,41 @@ def test_scores_of_products_that_overflow(fmt):
         paged, plain = scores_both_ways(cache, held, lens, x.to(BF16), w)
         assert torch.equal(paged, plain)
     assert torch.isfinite(plain).any() and torch.isneginf(paged).sum() < 1500
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+@pytest.mark.parametrize("size", [1.0, 1e4, 1e37])
+def test_attention_of_values_at_the_ends(fmt, size):
+    """Queries, sinks and logits that are infinite, NaN, the lowest and past the range: bitwise the
+    contiguous call on the rows held, flags among it."""
+    lens = [700, 600, 129, 128, 127, 2, 1, 513]
+    widths = [512, 385, 129, 128, 127, 2, 1, 384]
+    cache, held, g = appended(lens, fmt, 32, 51, 512)
+    rows = [(n, w, 512 * e, e) for e, (n, w) in enumerate(zip(lens, widths))]
+    idx = torch.full((8 * 512,), -1, dtype=torch.int32, device="cuda")
+    for e, (n, w) in enumerate(zip(lens, widths)):
+        idx[512 * e: 512 * e + w] = torch.randperm(n, generator=g, device="cuda")[:w]
+    idx[512 + 100: 512 + 385] = -1  # chunks with no row at all
+    q = (torch.randn(8, 64, 512, generator=g, device="cuda") * size).to(BF16)
+    inf, nan = float("inf"), float("nan")
+    for e in range(8):
+        q[e, e, 3], q[e, 9 + e, 500], q[e, 18 + e, 7] = nan, inf, -inf
+    sinks = torch.randn(8, 64, generator=g, device="cuda")
+    low = torch.finfo(F32).min
+    sinks[:, 30:38] = torch.tensor([inf, -inf, nan, low, -low, 0.0, 1e30, -1e30], device="cuda")
+    ws = ds.workspace(rows)
+    for scale in (512 ** -0.5, 1e30, 1e-30):
+        out, plain = (torch.full_like(q, 4.0) for _ in range(2))
+        bad, bad_plain = (torch.full((8, 64), 4, dtype=torch.int32, device="cuda") for _ in range(2))
+        ds.ds_rows_sparse_attn_paged(rows, q, sinks, 64, idx, scale, out, cache, invalid=bad, workspace_t=ws)
+        assert ds.workspace_status(ws) == 0
+        ds.ds_rows_sparse_attn(rows, q, sinks, 64, idx, scale, plain, held, invalid=bad_plain, workspace_t=ws)
+        assert torch.equal(out, plain) and torch.equal(bad, bad_plain)
+        assert torch.isfinite(out).all() and bad[0, [0, 30, 32]].all() and not out[0, 0].any()
 
 
 # ---------------------------------------------------------------------------
