@@ -10,12 +10,18 @@
 // read again where they are not. The row is fetched while its place is looked up
 // (index, page id, page: three dependent loads).
 //
-// Eight 512-wide rows: 2.4 us. 8191 fp32 rows of 512 into bf16 pages (25 MB): 6.0 us, 6.7 us
-// with nothing in L2 (3.7 us at the measured copy bandwidth). 32768 rows of 128 into 4-bit
-// pages, half of each rotated, with the values written too (19 MB, 2.9 us): 7.4 us, bound by
-// instructions (700 a warp of four rows: quotients, rotation, angles); 14.3 us with divisions
-// for quotients and per-element index arithmetic. More blocks on an SM than the 48 registers
-// allow made it slower (8.9 us at 40 registers, 11.2 us at 32, against 8.4).
+// Eight 512-wide rows: 2.5 us. Long runs, over three sets of inputs (most of them in L2) and over
+// sets of 300 MB and more, with the bytes' time at the measured copy bandwidth:
+//   32768 x 128, bf16 into 4-bit pages, half of each rotated, and the values   7.6 / 10.2 us (2.9)
+//   32768 x 128, bf16 into bf16 pages                                          6.2 /  8.9 us (2.5)
+//   8191 x 512, bf16 into 4-bit pages, and the values                          6.3 /  8.9 us (2.8)
+//   8191 x 512, fp32 into bf16 pages                                           6.2 /  8.2 us (3.7)
+// Waits for loads are the largest stall in all of them (half of the issue slots are used on 4-bit
+// keys, a quarter on fp32 rows): a warp's one set of rows waits for its dependent look-ups, which only
+// other warps hide, and a lane's 16-byte accesses lie 32 or 64 bytes apart from its neighbour's.
+// The instructions count next: 14.3 us on the keys with divisions for quotients and per-element
+// index arithmetic. More blocks on an SM than the 48 registers allow made it slower (8.9 us at 40
+// registers, 11.2 us at 32, against 8.4).
 
 #include "int4.cuh"
 #include "rope.cuh"

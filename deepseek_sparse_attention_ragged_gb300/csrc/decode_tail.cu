@@ -549,7 +549,8 @@ __device__ __forceinline__ void tail_body(const Params& p) {
             const float w = l[i] == -INFINITY ? 0.0f : expf(l[i] - mh);
             const __nv_bfloat16 hi = __float2bfloat16_rn(w);
             const __nv_bfloat16 lo = __float2bfloat16_rn(w - __bfloat162float(hi));
-            // Row h holds P_hi, row 32 + h P_lo (same swizzle phase: 32 is a multiple of 8).
+            // 16 bits of each weight reach the product, twice the output's 8. Row h holds
+            // P_hi, row 32 + h P_lo (same swizzle phase: 32 is a multiple of 8).
             const uint32_t off = (uint32_t)((slot >> 6) * kPBlock + h * 128 +
                                             ((((slot & 63) >> 3) ^ (h & 7)) << 4) + ((slot & 7) << 1));
             *reinterpret_cast<__nv_bfloat16*>(p_s + off) = hi;

@@ -18,11 +18,14 @@
 // bf16 (a shift, a mask and a packed FMA for two values, exact) and stores them
 // into TMEM, where they are the A operand of the MMAs: the widened key never
 // passes through shared memory, whose bandwidth (32 KB written and 32 KB read
-// again a tile) would be the bound otherwise. The instructions of the widening
-// and of the head sums are the bound: 8 x 131072 keys take 20.8 us (22.8 us when
-// nothing is in L2), of which the loads alone are 14.6 us (75.5 MB: 11.1 us at the
-// measured copy bandwidth), and 17.0 us without the head sums; the MMAs hardly count
-// (21.1 us with one of eight). Steps, in us: one issuing thread 34.7; the issuer's warp kept uniform 26.6
+// again a tile) would be the bound otherwise. 8 x 131072 keys take 20.8 us (22.8 us
+// when nothing is in L2), of which the loads alone are 14.6 us (75.5 MB: 11.1 us at
+// the measured copy bandwidth); it is 17.0 us without the head sums, and the MMAs
+// hardly count (21.1 us with one of eight). No unit is full: 2.3 of 4 instructions
+// issued a cycle, integer and FMA pipes at 41% and 39%, tensor pipe 31%, and the
+// largest stall is one role waiting on another's results (TMEM loads, barriers); the
+// first page comes only after the query's copy and a block barrier. Steps, in us: one
+// issuing thread 34.7; the issuer's warp kept uniform 26.6
 // (a divergent thread took 80 cycles an MMA, a uniform warp 25); four widening sets
 // and two issuers 25.3; the mask and exponent of a value in one instruction 23.1;
 // the polling loads 21.5; shared-space pointers and running indexes 20.8.
