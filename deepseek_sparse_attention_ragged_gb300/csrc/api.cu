@@ -698,6 +698,7 @@ int score_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* keys, c
     rc = check_indexer_args(q_index, w_index);
     if (rc) return rc;
     if (!scores) return fail(DS_EINVAL, "scores is NULL");
+    if (!aligned4(w_index) || !aligned4(scores)) return fail(DS_EALIGN, "w_index and scores must be 4-B aligned");
     for (int e = 0; e < rows; ++e)
         if (score_stride < table[e].kv_len)
             return fail(DS_EINVAL, "score_stride %zu is shorter than row %d (kv_len %u)", score_stride, e,
@@ -1165,6 +1166,8 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
     rc = check_attn_args(q_attn, sinks, sinks_row_stride, scale, out);
     if (rc) return rc;
     if (!indices) return fail(DS_EINVAL, "indices is NULL");
+    if (!aligned4(sinks) || !aligned4(indices) || !aligned4(invalid))
+        return fail(DS_EALIGN, "sinks, indices and invalid must be 4-B aligned");
     Layout L;  // the status word only
     L.total = DS_PAGED_WORKSPACE_BYTES;
     rc = check_workspace(&set, workspace, workspace_bytes, L);

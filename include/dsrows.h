@@ -524,7 +524,7 @@ int ds_rows_append(const ds_paged_cache_t* cache, const void* x, uint64_t x_stri
  * are bitwise those of the bf16 keys that the cache stands for. A key whose page id is
  * not in [0, num_pages), or with a NaN scale, scores -inf. DS_EINVAL when the
  * cache has fewer entries than rows, or a table row cannot reach kv_len; kv_len
- * is below 2^31. There is no status word: keys that a bounded device-side wait
+ * is below 2^31; w_index and scores are 4-B aligned (DS_EALIGN). There is no status word: keys that a bounded device-side wait
  * gave up on (see DS_STATUS_WAIT_TIMEOUT) score -inf.
  */
 int ds_rows_indexer_score_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* keys,
@@ -539,7 +539,7 @@ int ds_rows_indexer_score_paged(int rows, const ds_row_t* table, const ds_paged_
  * every head of its entry, as an index out of range does; a NaN scale zeroes the
  * heads as a non-finite KV element does. The workspace (256-byte aligned, at least
  * DS_PAGED_WORKSPACE_BYTES; any other workspace of this library will do) holds the
- * call's status word only.
+ * call's status word only. sinks, indices and invalid are 4-B aligned (DS_EALIGN).
  */
 #define DS_PAGED_WORKSPACE_BYTES 256
 int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* kv, const ds_bf16* q_attn,

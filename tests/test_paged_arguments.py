@@ -46,3 +46,16 @@ def test_score_selftest_validation(lib):
     assert call(FAKE, 999) == -1 and "budget_ns" in lib.ds_rows_last_error().decode()
     assert call(FAKE, 10_000_000_001) == -1
     assert call(None, 1000) == -1 and "scores is NULL" in lib.ds_rows_last_error().decode()
+
+
+def test_reads_need_aligned_words(lib):
+    """Words off 4 bytes would be misaligned accesses on the device."""
+    tab, n = ds._table([(600, 512, 0, 0)])
+    keys, kv = (paged._PagedCache(FAKE, FAKE, 8, 64, 64, 1000, dim, 1) for dim in (128, 512))
+    for w, out in ((FAKE + 2, FAKE), (FAKE, FAKE + 1)):
+        assert lib.ds_rows_indexer_score_paged(n, tab, ctypes.byref(keys), FAKE, w, out, 600, None) == -3
+        assert "4-B" in lib.ds_rows_last_error().decode()
+    for sinks, idx, invalid in ((FAKE + 2, FAKE, None), (FAKE, FAKE + 3, None), (FAKE, FAKE, FAKE + 2)):
+        assert lib.ds_rows_sparse_attn_paged(n, tab, ctypes.byref(kv), FAKE, sinks, 0, idx, 0.04, FAKE, invalid, FAKE, 256,
+                                             None) == -3
+        assert "4-B" in lib.ds_rows_last_error().decode()
