@@ -144,6 +144,49 @@ def test_rope_of_many_heads_outside_the_tokens(layout, inplace):
     assert (base[..., :8] == 7.0).all()
 
 # ---------------------------------------------------------------------------
+# the largest calls
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("tokens,heads,dim", [(2 ** 31 - 1, 1, 2), (32767, 65536, 8), (2 ** 31 // 65535, 65535, 8)])
+def test_rope_of_the_most_rows(layout, tokens, heads, dim):
+    """2^31 - 1 rows at most, in place: the first and the last as in small calls, others between
+    them; one row more is refused."""
+    x = torch.ones(tokens, heads, dim, dtype=BF16, device="cuda")
+    pos = torch.full((tokens,), 3, dtype=torch.int32, device="cuda")
+    pos[-2:] = 77
+    pos[-1] = -1
+    rope = ds.Rope(dim, layout=layout)
+    small = torch.ones(3, 1, dim, dtype=BF16, device="cuda")
+    ds.ds_rows_rope(rope, small, i32([3, 77, -1]), small)
+    ds.ds_rows_rope(rope, x, pos, x)
+    assert torch.equal(x[-2], small[1].expand(heads, dim)) and torch.equal(x[-1], torch.ones_like(x[-1]))
+    assert all((part == small[0]).all() for part in x[:-2].split(max(1, (1 << 28) // heads)))
+    del x
+    more = torch.empty(1, 1, dim, dtype=BF16, device="cuda").expand(2 ** 31 // heads + 1, heads, dim)
+    with pytest.raises(ds.DsRowsError, match="below 2"):
+        ds.ds_rows_rope(rope, more, torch.empty(more.shape[0], dtype=torch.int32, device="cuda"), more)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+def test_append_of_the_most_rows(fmt):
+    """2^31 - 1 rows from one broadcast row, all padding but the first and the last two."""
+    n = 2 ** 31 - 1
+    x = torch.randn(1, 128, device="cuda").to(BF16)
+    seq = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    slot = torch.zeros(n, dtype=torch.int32, device="cuda")
+    seq[0] = seq[-2] = seq[-1] = 0
+    slot[-2], slot[-1] = 17, 33
+    pages = [torch.full((3, ds.ds_rows_page_bytes(16, 128, fmt)), 90, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    table = i32([[2, 0, 1]])
+    invalid = torch.full((n,), 9, dtype=torch.int32, device="cuda")
+    ds.ds_rows_append(ds.PagedCache(pages[0], table, 16, 128, fmt), x.expand(n, 128), seq, slot, invalid=invalid)
+    assert not invalid.any()
+    ds.ds_rows_append(ds.PagedCache(pages[1], table, 16, 128, fmt), x.expand(3, 128), i32([0, 0, 0]), i32([0, 17, 33]))
+    assert torch.equal(pages[0], pages[1]) and (pages[0] != 90).any()
+
+
+# ---------------------------------------------------------------------------
 # angles
 # ---------------------------------------------------------------------------
 
