@@ -9,14 +9,14 @@
 // lines; the heads of a group are interleaved over the block, so that its rows at one time
 // lie side by side. The angles of a thread's pairs stay in its registers, and in the half
 // layout a pair's other element comes by shuffles. 4096 x 64 bf16 rows of 128, half of each
-// rotated (134 MB, nothing in L2): 23.4 us, where a plain copy of them takes 21.1 us; 23.9
+// rotated (134 MB, nothing in L2): 23.6 us, where a plain copy of them takes 21.1 us; 23.9
 // with 8 heads a thread, 28.9 with 4. A thread per pair of halves took 27.0 us (each access
 // 64 bytes of a line), the angles shared through shared memory 44 us (a barrier).
 //
 // In place (rope_kernel) a thread owns one unit of a row's rotated range, 16 bytes of
 // interleaved pairs or 16 bytes from each half, for up to 8 heads: nobody else reads what
-// it writes. 1021 x 64 fp32 rows of 512, 64 rotated: 4.5 us (33 MB); eight tokens of 64
-// heads: 1.6 us. The same kernel serves half layouts whose range crosses a warp of
+// it writes. 1021 x 64 fp32 rows of 512, 64 rotated: 4.2 us (33 MB, partly in L2); eight tokens of 64
+// heads: 1.7 us. The same kernel serves half layouts whose range crosses a warp of
 // rope_rows_kernel (rows of 12 or 24 pieces, say), and moves rows whose address, stride or
 // range is not a multiple of 16 bytes element by element, one pair a unit; threads of
 // their own then copy what is not rotated (the two cases above with rows off by one
