@@ -683,62 +683,6 @@ int check_cache(const ds_paged_cache_t* c, uint32_t dim, int rows) {
 
 }  // namespace dsrows
 
-namespace {
-
-// ds_rows_indexer_score_paged; with give_up_ns the self-test of its waits.
-int score_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* keys, const ds_bf16* q_index,
-                const float* w_index, float* scores, size_t score_stride, uint32_t give_up_tiles, uint64_t give_up_ns,
-                void* stream) {
-    int rc = check_table(rows, table);
-    if (rc) return rc;
-    rc = check_cache(keys, DS_INDEX_DIM, rows);
-    if (rc) return rc;
-    rc = check_reach(rows, table, keys);
-    if (rc) return rc;
-    rc = check_indexer_args(q_index, w_index);
-    if (rc) return rc;
-    if (!scores) return fail(DS_EINVAL, "scores is NULL");
-    if (!aligned4(w_index) || !aligned4(scores)) return fail(DS_EALIGN, "w_index and scores must be 4-B aligned");
-    for (int e = 0; e < rows; ++e)
-        if (score_stride < table[e].kv_len)
-            return fail(DS_EINVAL, "score_stride %zu is shorter than row %d (kv_len %u)", score_stride, e,
-                        table[e].kv_len);
-    PagedIndexerParams p;
-    std::memset(&p, 0, sizeof(p));
-    const uint32_t tile = indexer_tile_keys();
-    uint32_t tiles = 0;
-    for (int e = 0; e < rows; ++e) {
-        p.tile_begin[e] = tiles;
-        p.kv_len[e] = table[e].kv_len;
-        p.q_row[e] = table[e].q_row;
-        tiles += (table[e].kv_len - 1) / tile + 1;
-    }
-    const int sms = num_sms();
-    if (sms <= 0) return fail(DS_ECUDA, "no CUDA device");
-    if (keys->format == DS_CACHE_BF16) {
-        rc = get_encoder();
-        if (rc) return rc;
-        rc = encode_rows128(&p.kmap, keys->pages, (uint64_t)keys->num_pages * keys->page_size,
-                            keys->page_size < tile ? keys->page_size : tile, "paged indexer keys");
-        if (rc) return rc;
-    }
-    split_ctas(p.tile_begin, p.cta_begin, (uint32_t)rows, tiles, tiles < (uint32_t)sms ? tiles : (uint32_t)sms);
-    p.cache = paged_cache(*keys);
-    p.q = reinterpret_cast<const __nv_bfloat16*>(q_index);
-    p.w = w_index;
-    p.scores = scores;
-    p.score_stride = score_stride;
-    p.rows = (uint32_t)rows;
-    p.total_tiles = tiles;
-    p.give_up_tiles = give_up_tiles;
-    p.give_up_ns = give_up_ns;
-    StageRange range("dsrows.indexer_paged");
-    const cudaError_t err = launch_paged_indexer(p, keys->format, sms, (cudaStream_t)stream, true);
-    return err == cudaSuccess ? DS_OK : cuda_fail(err, "paged indexer launch");
-}
-
-}  // namespace
-
 extern "C" {
 
 size_t ds_rows_workspace_bytes(int rows, const ds_row_t* table) {
@@ -1142,15 +1086,50 @@ int ds_rows_rope(const ds_rope_t* rope, const void* x, uint64_t x_token_stride, 
 int ds_rows_indexer_score_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* keys,
                                 const ds_bf16* q_index, const float* w_index, float* scores, size_t score_stride,
                                 void* stream) {
-    return score_paged(rows, table, keys, q_index, w_index, scores, score_stride, 0, 0, stream);
-}
-
-int ds_rows_selftest_score_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* keys, const ds_bf16* q_index,
-                                 const float* w_index, float* scores, size_t score_stride, uint32_t tiles,
-                                 uint64_t budget_ns, void* stream) {
-    if (budget_ns < 1000 || budget_ns > 10000000000ull)
-        return fail(DS_EINVAL, "budget_ns must be 1000..=10000000000, got %llu", (unsigned long long)budget_ns);
-    return score_paged(rows, table, keys, q_index, w_index, scores, score_stride, tiles, budget_ns, stream);
+    int rc = check_table(rows, table);
+    if (rc) return rc;
+    rc = check_cache(keys, DS_INDEX_DIM, rows);
+    if (rc) return rc;
+    rc = check_reach(rows, table, keys);
+    if (rc) return rc;
+    rc = check_indexer_args(q_index, w_index);
+    if (rc) return rc;
+    if (!scores) return fail(DS_EINVAL, "scores is NULL");
+    if (!aligned4(w_index) || !aligned4(scores)) return fail(DS_EALIGN, "w_index and scores must be 4-B aligned");
+    for (int e = 0; e < rows; ++e)
+        if (score_stride < table[e].kv_len)
+            return fail(DS_EINVAL, "score_stride %zu is shorter than row %d (kv_len %u)", score_stride, e,
+                        table[e].kv_len);
+    PagedIndexerParams p;
+    std::memset(&p, 0, sizeof(p));
+    const uint32_t tile = indexer_tile_keys();
+    uint32_t tiles = 0;
+    for (int e = 0; e < rows; ++e) {
+        p.tile_begin[e] = tiles;
+        p.kv_len[e] = table[e].kv_len;
+        p.q_row[e] = table[e].q_row;
+        tiles += (table[e].kv_len - 1) / tile + 1;
+    }
+    const int sms = num_sms();
+    if (sms <= 0) return fail(DS_ECUDA, "no CUDA device");
+    if (keys->format == DS_CACHE_BF16) {
+        rc = get_encoder();
+        if (rc) return rc;
+        rc = encode_rows128(&p.kmap, keys->pages, (uint64_t)keys->num_pages * keys->page_size,
+                            keys->page_size < tile ? keys->page_size : tile, "paged indexer keys");
+        if (rc) return rc;
+    }
+    split_ctas(p.tile_begin, p.cta_begin, (uint32_t)rows, tiles, tiles < (uint32_t)sms ? tiles : (uint32_t)sms);
+    p.cache = paged_cache(*keys);
+    p.q = reinterpret_cast<const __nv_bfloat16*>(q_index);
+    p.w = w_index;
+    p.scores = scores;
+    p.score_stride = score_stride;
+    p.rows = (uint32_t)rows;
+    p.total_tiles = tiles;
+    StageRange range("dsrows.indexer_paged");
+    const cudaError_t err = launch_paged_indexer(p, keys->format, sms, (cudaStream_t)stream, true);
+    return err == cudaSuccess ? DS_OK : cuda_fail(err, "paged indexer launch");
 }
 
 int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* kv, const ds_bf16* q_attn,

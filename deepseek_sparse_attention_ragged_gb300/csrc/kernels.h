@@ -190,8 +190,6 @@ struct PagedIndexerParams {
     uint32_t cta_begin[DS_ROWS_MAX + 1];
     uint32_t kv_len[DS_ROWS_MAX];
     uint32_t q_row[DS_ROWS_MAX];
-    uint32_t give_up_tiles;  // self-test of the waits (give_up_ns nonzero): tiles that each CTA loads
-    uint64_t give_up_ns;     // ... and the budget of each wait
 };
 
 // Attention of the caller's indices over a paged cache.

@@ -37,6 +37,7 @@
 #include "head_sum.cuh"
 #include "int4.cuh"
 #include "kernels.h"
+#include "unscored.cuh"
 
 namespace dsrows {
 
@@ -108,10 +109,10 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // mbar_wait whose first tries read no timer, for waits of a few hundred cycles.
-__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity, uint64_t budget_ns) {
+__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity) {
     for (int i = 0; i < 64; ++i)
         if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity, nullptr, budget_ns);
+    return mbar_wait(bar, parity, nullptr);
 }
 
 // D[tmem] (+)= A[tmem] * B[smem desc]^T: A's rows are the TMEM lanes, two bf16 a column.
@@ -129,13 +130,11 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
 
 // A wait that gives up ends its role, so every later wait on its work gives up too, and the
 // epilogue writes -inf for the keys that it has no sums for: the caller's buffer never keeps
-// another call's scores. kGiveUp (the self-test): the loads end after p.give_up_tiles tiles,
-// and every wait has p.give_up_ns.
-template <bool kInt4, bool kGiveUp>
+// another call's scores.
+template <bool kInt4>
 __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
     paged_indexer_kernel(const __grid_constant__ PagedIndexerParams p) {
     using S = Shape<kInt4>;
-    const uint64_t budget = kGiveUp ? p.give_up_ns : kWaitBudgetNs;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // Aligned by an offset, so that the pointers stay in the shared address space.
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -212,8 +211,7 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
         const uint32_t sub_bytes = sub_rows * (kInt4 ? kInt4Row : kIdxDim * 2);
         const int32_t* table = p.cache.table + (size_t)e * p.cache.table_stride;
         const uint64_t policy = l2_policy_evict_first();
-        const uint32_t loaded = kGiveUp ? min(mine, p.give_up_tiles) : mine;
-        const uint32_t tiles = my_tile < lap ? loaded : 0;  // the other lanes have none
+        const uint32_t tiles = my_tile < lap ? mine : 0;  // the other lanes have none
         auto first_key = [&](uint32_t it) { return (first + it * step) * kTileKeys + my_sub * sub_rows; };
         auto wants = [&](uint32_t it) { return it < tiles && first_key(it) < kv_len; };
         auto page_id = [&](uint32_t it) -> int32_t { return wants(it) ? table[first_key(it) >> shift] : -1; };
@@ -261,7 +259,7 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
             if ((tries & 63) == 63) {  // bounded, as every wait
                 const uint64_t now = global_timer_ns();
                 if (start == 0) start = now;
-                ok = !__any_sync(0xFFFFFFFFu, it < tiles && now - start > budget);
+                ok = !__any_sync(0xFFFFFFFFu, it < tiles && now - start > kWaitBudgetNs);
             }
             __syncwarp();
         }
@@ -269,7 +267,7 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
         for (uint32_t k = 0; k < S::kStages / lap && it >= lap && my_tile < lap; ++k) {
             it -= lap;
             s = it % S::kStages;
-            (void)mbar_wait(&bar->full[s], (it / S::kStages) & 1, nullptr, budget);
+            (void)mbar_wait(&bar->full[s], (it / S::kStages) & 1, nullptr);
         }
     } else if (warp <= kIssuers) {
         // ---- MMA issuer: the whole warp runs the loop, so that addresses and descriptors
@@ -278,11 +276,11 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
         const uint32_t b_base = smem_u32(q_s);
         uint32_t it = warp - 1, a = it, s = it, ph = 0, sph = 0;  // tile, buffer, stage, their phases
         for (; it < mine; it += kIssuers) {
-            if (!wait_short(&bar->acc_empty[a], ph ^ 1, budget)) break;
+            if (!wait_short(&bar->acc_empty[a], ph ^ 1)) break;
             if (kInt4) {
-                if (!wait_short(&bar->key_full[a], ph, budget)) break;
+                if (!wait_short(&bar->key_full[a], ph)) break;
             } else {
-                if (!wait_short(&bar->full[s], sph, budget)) break;
+                if (!wait_short(&bar->full[s], sph)) break;
             }
             tc_fence_after();
             const uint32_t d_tmem = tmem + a * S::kAccCols;
@@ -307,7 +305,7 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
         }
         // The MMAs issued are done before TMEM is freed.
         for (uint32_t k = it > kBufs ? it - kBufs : warp - 1; k < it; k += kIssuers)
-            (void)mbar_wait(&bar->acc_full[k % kBufs], (k / kBufs) & 1, nullptr, budget);
+            (void)mbar_wait(&bar->acc_full[k % kBufs], (k / kBufs) & 1, nullptr);
     } else if (warp < 1 + kIssuers + 4 * kEpiSets) {
         // ---- epilogue: one key per thread, alternate tiles per set -----------------------
         const int set = (warp - 1 - kIssuers) >> 2;
@@ -324,10 +322,8 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
                 const int32_t id = p.cache.table[(size_t)e * p.cache.table_stride + (j >> shift)];
                 have = id >= 0 && (uint32_t)id < p.cache.num_pages;
             }
-            if (!wait_short(&bar->acc_full[a], ph, budget)) {
-#pragma unroll 1
-                for (; it < mine; it += kEpiSets, j += kEpiSets * step * kTileKeys)
-                    if (j < kv_len) out[j] = -INFINITY;
+            if (!wait_short(&bar->acc_full[a], ph)) {
+                unscored(out, it, mine, kEpiSets, j, kEpiSets * step * kTileKeys, kv_len);
                 break;
             }
             tc_fence_after();
@@ -356,7 +352,7 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
         uint32_t a = set, s = set, ph = 0, sph = 0;  // buffer, stage, their phases
         for (uint32_t it = set; it < mine; it += kWideSets) {
             const uint32_t taddr = tcol + a * kKeyWords;
-            if (!wait_short(&bar->full[s], sph, budget)) break;
+            if (!wait_short(&bar->full[s], sph)) break;
             uint4 d[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -366,7 +362,7 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
             if ((bar->bad[s] >> sub) & 1) sc.x = sc.y = 0x7F7F7F7Fu;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar->empty[s]);
-            if (!wait_short(&bar->key_empty[a], ph ^ 1, budget)) break;
+            if (!wait_short(&bar->key_empty[a], ph ^ 1)) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -398,23 +394,18 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
     }
 }
 
-template <bool kInt4, bool kGiveUp>
+template <bool kInt4>
 static cudaError_t launch(const PagedIndexerParams& p, int num_sms, cudaStream_t stream, bool pdl) {
     static std::atomic<uint64_t> smem_set{0};
     constexpr size_t bytes = smem_bytes<kInt4>();
-    const cudaError_t err = set_smem_limit_once(paged_indexer_kernel<kInt4, kGiveUp>, bytes, smem_set);
+    const cudaError_t err = set_smem_limit_once(paged_indexer_kernel<kInt4>, bytes, smem_set);
     if (err != cudaSuccess) return err;
     const uint32_t grid = p.total_tiles < (uint32_t)num_sms ? p.total_tiles : (uint32_t)num_sms;
-    return launch_kernel(paged_indexer_kernel<kInt4, kGiveUp>, dim3(grid), dim3(Shape<kInt4>::kThreads), bytes, stream,
-                         pdl, p);
+    return launch_kernel(paged_indexer_kernel<kInt4>, dim3(grid), dim3(Shape<kInt4>::kThreads), bytes, stream, pdl, p);
 }
 
 cudaError_t launch_paged_indexer(const PagedIndexerParams& p, int format, int num_sms, cudaStream_t stream, bool pdl) {
-    if (p.give_up_ns)
-        return format == DS_CACHE_INT4 ? launch<true, true>(p, num_sms, stream, pdl)
-                                       : launch<false, true>(p, num_sms, stream, pdl);
-    return format == DS_CACHE_INT4 ? launch<true, false>(p, num_sms, stream, pdl)
-                                   : launch<false, false>(p, num_sms, stream, pdl);
+    return format == DS_CACHE_INT4 ? launch<true>(p, num_sms, stream, pdl) : launch<false>(p, num_sms, stream, pdl);
 }
 
 }  // namespace dsrows

@@ -46,10 +46,9 @@ def declare(lib) -> None:
     lib.ds_rows_page_bytes.restype = sz
     lib.ds_rows_append.argtypes = [cache, vp, u64, i32, u64, vp, vp, rope, vp, vp, vp, vp]
     lib.ds_rows_indexer_score_paged.argtypes = [i32, vp, cache, vp, vp, vp, sz, vp]
-    lib.ds_rows_selftest_score_paged.argtypes = [i32, vp, cache, vp, vp, vp, sz, u32, u64, vp]
     lib.ds_rows_sparse_attn_paged.argtypes = [i32, vp, cache, vp, vp, sz, vp, f32, vp, vp, vp, sz, vp]
     for f in (lib.ds_rows_rope_turns, lib.ds_rows_rope, lib.ds_rows_append, lib.ds_rows_indexer_score_paged,
-              lib.ds_rows_selftest_score_paged, lib.ds_rows_sparse_attn_paged):
+              lib.ds_rows_sparse_attn_paged):
         f.restype = i32
 
 

@@ -560,17 +560,6 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
  */
 int ds_rows_selftest_bounded_wait(uint32_t* status, uint32_t* result, uint64_t budget_ns, void* stream);
 
-/*
- * Self-test of what ds_rows_indexer_score_paged leaves when its waits give up:
- * the same call, whose blocks load only the first `tiles` of their 128-key tiles
- * (a block takes every n-th tile of an entry) and whose waits give up after
- * `budget_ns` (1,000 to 10,000,000,000). Keys of loaded tiles score as ever,
- * the others -inf. Nothing faults and the device stays usable.
- */
-int ds_rows_selftest_score_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* keys, const ds_bf16* q_index,
-                                 const float* w_index, float* scores, size_t score_stride, uint32_t tiles,
-                                 uint64_t budget_ns, void* stream);
-
 /* Message of the last failed call on this host thread ("" if none). */
 const char* ds_rows_last_error(void);
 

@@ -263,47 +263,6 @@ def row_table(lens):
     return [(n, min(512, n), 512 * e, e) for e, n in enumerate(lens)]
 
 
-@pytest.mark.parametrize("fmt", ["bf16", "int4"])
-@pytest.mark.parametrize("page", [16, 128, 256])
-def test_scores_of_waits_that_give_up(fmt, page):
-    """Blocks that never load their later tiles: those keys score -inf, whatever the buffer held,
-    the others as ever, and the next call is whole."""
-    sms = torch.cuda.get_device_properties(0).multi_processor_count
-    n = 128 * (4 * sms + 7) - 5  # one entry: block b takes tiles b, b + sms, ...
-    cache, _, g = appended([n], fmt, page, 21)
-    q = torch.randn(1, 64, 128, generator=g, device="cuda").to(BF16)
-    w = torch.randn(1, 64, generator=g, device="cuda")
-    want = torch.full((n + 9,), 123.0, device="cuda")
-    ds.ds_rows_indexer_score_paged(row_table([n]), q, w, cache, want, score_stride=n + 9)
-    assert torch.isfinite(want).all() and (want[n:] == 123.0).all()
-    lib, (tab, rows) = ds.load(), ds._table(row_table([n]))
-    for tiles in (0, 1, 2, 3, 5):
-        scores = torch.full((n + 9,), 123.0, device="cuda")
-        rc = lib.ds_rows_selftest_score_paged(rows, tab, cache._ref, q.data_ptr(), w.data_ptr(), scores.data_ptr(), n + 9,
-                                              tiles, 20_000_000, torch.cuda.current_stream().cuda_stream)
-        assert rc == 0, lib.ds_rows_last_error()
-        done = min(n, 128 * sms * tiles)
-        assert torch.equal(scores[:done], want[:done]) and torch.isneginf(scores[done:n]).all()
-        assert (scores[n:] == 123.0).all()
-        again = torch.full((n + 9,), 123.0, device="cuda")
-        ds.ds_rows_indexer_score_paged(row_table([n]), q, w, cache, again, score_stride=n + 9)
-        assert torch.equal(again, want)
-
-
-def test_keys_given_up_on_are_not_selected():
-    lens = [900, 300]
-    cache, _, g = appended(lens, "int4", 64, 22)
-    q = torch.randn(2, 64, 128, generator=g, device="cuda").to(BF16)
-    w = torch.randn(2, 64, generator=g, device="cuda")
-    scores = torch.rand(2, 900, device="cuda")
-    idx = torch.zeros(1024, dtype=torch.int32, device="cuda")
-    tab, rows = ds._table(row_table(lens))
-    assert ds.load().ds_rows_selftest_score_paged(rows, tab, cache._ref, q.data_ptr(), w.data_ptr(), scores.data_ptr(),
-                                                  900, 0, 20_000_000, torch.cuda.current_stream().cuda_stream) == 0
-    ds.ds_rows_topk(row_table(lens), scores, 900, idx, ds.workspace(row_table(lens)))
-    assert (idx[:812] == -1).all()
-
-
 def scores_both_ways(cache, held, lens, q, w):
     out = [torch.full((len(lens), max(lens)), 123.0, device="cuda") for _ in range(2)]
     ds.ds_rows_indexer_score_paged(row_table(lens), q, w, cache, out[0])

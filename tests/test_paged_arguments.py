@@ -38,16 +38,6 @@ def test_append_of_a_lone_row_from_anywhere(lib):
     assert call(2) == -2 and "x_stride" in lib.ds_rows_last_error().decode()
 
 
-def test_score_selftest_validation(lib):
-    tab, n = ds._table([(600, 512, 0, 0)])
-    c = paged._PagedCache(FAKE, FAKE, 8, 64, 64, 1000, 128, 1)
-    call = lambda out, budget: lib.ds_rows_selftest_score_paged(n, tab, ctypes.byref(c), FAKE, FAKE, out, 600, 1,  # noqa: E731
-                                                                budget, None)
-    assert call(FAKE, 999) == -1 and "budget_ns" in lib.ds_rows_last_error().decode()
-    assert call(FAKE, 10_000_000_001) == -1
-    assert call(None, 1000) == -1 and "scores is NULL" in lib.ds_rows_last_error().decode()
-
-
 def test_reads_need_aligned_words(lib):
     """Words off 4 bytes would be misaligned accesses on the device."""
     tab, n = ds._table([(600, 512, 0, 0)])
