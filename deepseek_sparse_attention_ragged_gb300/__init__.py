@@ -29,7 +29,8 @@ __all__ = [
     "IndexerRow", "ds_rows_indexer_topk_workspace_bytes", "indexer_topk_workspace", "ds_rows_indexer_topk",
     "ds_rows_indexer_topk_queries_workspace_bytes", "ds_rows_indexer_topk_queries",
     "CompressorRow", "ds_rows_compress_kv",
-    "Rope", "ds_rows_rope", "PagedCache", "ds_rows_page_bytes", "ds_rows_append", "ds_rows_indexer_score_paged",
+    "Rope", "ds_rows_rope", "PagedCache", "ds_rows_page_bytes", "ds_rows_append", "ds_rows_fetch",
+    "ds_rows_indexer_score_paged",
     "ds_rows_sparse_attn_paged", "PAGED_WORKSPACE_BYTES",
     "STATUS_WAIT_TIMEOUT", "STATUS_OVERFLOW", "workspace_status", "ds_rows_selftest_bounded_wait",
     "ROWS_MAX", "INDEX_HEADS", "INDEX_DIM", "TOP_K", "HEADS", "DIM",
@@ -547,5 +548,6 @@ def ds_rows_compress_kv(kv_states, score_states, start_pos, kv, score, ape, norm
 # ---------------------------------------------------------------------------
 
 from . import paged as _paged  # noqa: E402  (uses the names above)
-from .paged import (PAGED_WORKSPACE_BYTES, PagedCache, Rope, ds_rows_append, ds_rows_indexer_score_paged, ds_rows_page_bytes,  # noqa: E402
+from .paged import (PAGED_WORKSPACE_BYTES, PagedCache, Rope, ds_rows_append, ds_rows_fetch,  # noqa: E402
+                    ds_rows_indexer_score_paged, ds_rows_page_bytes,
                     ds_rows_rope, ds_rows_sparse_attn_paged)

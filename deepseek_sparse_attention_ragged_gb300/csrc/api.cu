@@ -661,6 +661,7 @@ int check_reach(int rows, const ds_row_t* table, const ds_paged_cache_t* cache) 
 namespace dsrows {
 
 uint32_t page_row_bytes(uint32_t dim, int format) {
+    if (format == DS_CACHE_FP8) return dim + dim / 128;
     return format == DS_CACHE_INT4 ? dim / 2 + dim / 16 : 2 * dim;
 }
 
@@ -984,8 +985,8 @@ size_t ds_rows_page_bytes(uint32_t page_size, uint32_t dim, int format) {
         fail(DS_EINVAL, "paged cache rows must be %d or %d wide, got %u", DS_INDEX_DIM, DS_DIM, dim);
         return 0;
     }
-    if (format != DS_CACHE_BF16 && format != DS_CACHE_INT4) {
-        fail(DS_EINVAL, "paged cache format must be DS_CACHE_BF16 or DS_CACHE_INT4, got %d", format);
+    if (format != DS_CACHE_BF16 && format != DS_CACHE_INT4 && format != DS_CACHE_FP8) {
+        fail(DS_EINVAL, "paged cache format must be DS_CACHE_BF16, DS_CACHE_INT4 or DS_CACHE_FP8, got %d", format);
         return 0;
     }
     return (size_t)page_size * page_row_bytes(dim, format);
@@ -1030,6 +1031,35 @@ int ds_rows_append(const ds_paged_cache_t* cache, const void* x, uint64_t x_stri
     StageRange range("dsrows.append");
     const cudaError_t err = launch_append(p, dtype, dim, cache->format, (cudaStream_t)stream, true);
     return err == cudaSuccess ? DS_OK : cuda_fail(err, "append launch");
+}
+
+int ds_rows_fetch(const ds_paged_cache_t* cache, const int32_t* seq, const int32_t* slot, void* out,
+                  uint64_t out_stride, int dtype, uint64_t tokens, uint32_t* invalid, void* stream) {
+    int rc = check_cache(cache, cache && cache->dim == DS_INDEX_DIM ? DS_INDEX_DIM : DS_DIM, 0);
+    if (rc) return rc;
+    size_t elem;
+    rc = check_elements(dtype, out, out, elem);
+    if (rc) return rc;
+    if (tokens > 0x7FFFFFFFull) return fail(DS_ESIZE, "tokens must be below 2^31, got %llu", (unsigned long long)tokens);
+    if (tokens <= 1) out_stride = cache->dim;  // a lone row's stride says nothing
+    if (out_stride > kMaxStride) return fail(DS_ESIZE, "out_stride is out of range");
+    if (out_stride < cache->dim) return fail(DS_EINVAL, "rows of out overlap");
+    if (!seq || !slot) return fail(DS_EINVAL, "seq and slot must be non-NULL");
+    if (!aligned4(seq) || !aligned4(slot) || !aligned4(invalid))
+        return fail(DS_EALIGN, "seq, slot and invalid must be 4-B aligned");
+    if (tokens == 0) return DS_OK;
+    FetchCall p;
+    p.cache = paged_cache(*cache);
+    p.out = out;
+    p.out_stride = out_stride;
+    p.tokens = tokens;
+    p.seq = seq;
+    p.slot = slot;
+    p.invalid = invalid;
+    p.wide = aligned16(out) && (out_stride * elem) % 16 == 0 ? 1u : 0u;
+    StageRange range("dsrows.fetch");
+    const cudaError_t err = launch_fetch(p, dtype, cache->dim, cache->format, (cudaStream_t)stream, true);
+    return err == cudaSuccess ? DS_OK : cuda_fail(err, "fetch launch");
 }
 
 int ds_rows_rope(const ds_rope_t* rope, const void* x, uint64_t x_token_stride, uint64_t x_head_stride, void* out,
@@ -1090,6 +1120,7 @@ int ds_rows_indexer_score_paged(int rows, const ds_row_t* table, const ds_paged_
     if (rc) return rc;
     rc = check_cache(keys, DS_INDEX_DIM, rows);
     if (rc) return rc;
+    if (keys->format == DS_CACHE_FP8) return fail(DS_EINVAL, "scores over 8-bit pages are not built");
     rc = check_reach(rows, table, keys);
     if (rc) return rc;
     rc = check_indexer_args(q_index, w_index);
@@ -1140,6 +1171,7 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
     if (rc) return rc;
     rc = check_cache(kv, DS_DIM, rows);
     if (rc) return rc;
+    if (kv->format == DS_CACHE_FP8) return fail(DS_EINVAL, "attention over 8-bit pages are not built");
     rc = check_reach(rows, table, kv);
     if (rc) return rc;
     rc = check_attn_args(q_attn, sinks, sinks_row_stride, scale, out);

@@ -3,8 +3,8 @@
 //
 // Bound by the bytes of the rows read and written (and, for a few rows, by the
 // launch). A lane owns 16 consecutive elements, which is one group of the 4-bit
-// type, so its scale needs no exchange: a warp holds one 512-wide row or four
-// 128-wide ones. The lanes of a row share its sines and cosines through shared
+// type, so its scale needs no exchange (a block of the 8-bit type is eight lanes, whose
+// magnitudes meet in three shuffles): a warp holds one 512-wide row or four 128-wide ones. The lanes of a row share its sines and cosines through shared
 // memory (each takes rot / 2 / lanes of them); in the half layout a pair's other
 // element comes from its lane by a shuffle where the halves are whole groups, and is
 // read again where they are not. The row is fetched while its place is looked up
@@ -23,6 +23,7 @@
 // index arithmetic. More blocks on an SM than the 48 registers allow made it slower (8.9 us at 40
 // registers, 11.2 us at 32, against 8.4).
 
+#include "fp8.cuh"
 #include "int4.cuh"
 #include "rope.cuh"
 
@@ -39,7 +40,7 @@ __device__ __forceinline__ float widen_f(T v) {
 
 }  // namespace
 
-template <typename T, int kDimOf, bool kInt4>
+template <typename T, int kDimOf, int kFormat>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendCall p) {
     constexpr int G = int4::kGroup;
     constexpr int LANES = kDimOf / G;  // lanes of a row
@@ -148,11 +149,18 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
                 if (e0 + i < p.rope.rot) rope_pair(y[i], y[i + 1], trig_s[r][pair_at((e0 + i) / 2)]);
         }
     }
+    uint32_t top = 0;  // 8 bits: the largest magnitude of the block, over its eight lanes
+    if constexpr (kFormat == DS_CACHE_FP8) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = 1; o < fp8::kBlock / G; o *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    }
     if (!ok) return;
     uint8_t* base = p.cache.pages + (page << p.cache.page_shift) * p.cache.row_bytes;
     __nv_bfloat16* held_out = p.values ? p.values + token * kDimOf + g * G : nullptr;
     __align__(16) __nv_bfloat16 held[G];
-    if constexpr (kInt4) {
+    if constexpr (kFormat == DS_CACHE_INT4) {
         uint32_t word[2];
         float h[G];
         const uint8_t scale = int4::quantise(y, word, h);
@@ -170,6 +178,19 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         if (!held_out) return;
 #pragma unroll
         for (int i = 0; i < G; ++i) held[i] = __float2bfloat16_rn(h[i]);
+    } else if constexpr (kFormat == DS_CACHE_FP8) {
+        const uint32_t byte = fp8::exponent_byte(top);
+        uint32_t word[4];
+        fp8::quantise(y, byte, word);
+        const size_t size = (size_t)1 << p.cache.page_shift;
+        uint8_t* values = kDimOf == kDim ? base + (size_t)at * kDimOf + g * G : base + (g * size + at) * G;
+        *reinterpret_cast<uint4*>(values) = make_uint4(word[0], word[1], word[2], word[3]);
+        if (g % (fp8::kBlock / G) == 0)
+            base[size * kDimOf + (size_t)at * (kDimOf / fp8::kBlock) + g / (fp8::kBlock / G)] = (uint8_t)byte;
+        if (!held_out) return;
+        const uint32_t f = fp8::factor(byte);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fp8::widen(word[i], f, reinterpret_cast<uint32_t*>(held) + 2 * i);
     } else {
 #pragma unroll
         for (int i = 0; i < G; ++i) held[i] = __float2bfloat16_rn(y[i]);
@@ -186,9 +207,10 @@ template <typename T, int kDimOf>
 static cudaError_t launch_rows(const AppendCall& p, int format, cudaStream_t stream, bool pdl) {
     constexpr uint64_t rows = kAppendThreads / (kDimOf / int4::kGroup);
     const dim3 grid((uint32_t)((p.tokens + rows - 1) / rows));
-    if (format == DS_CACHE_INT4)
-        return launch_kernel(append_kernel<T, kDimOf, true>, grid, dim3(kAppendThreads), 0, stream, pdl, p);
-    return launch_kernel(append_kernel<T, kDimOf, false>, grid, dim3(kAppendThreads), 0, stream, pdl, p);
+    auto launch = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kAppendThreads), 0, stream, pdl, p); };
+    if (format == DS_CACHE_INT4) return launch(append_kernel<T, kDimOf, DS_CACHE_INT4>);
+    if (format == DS_CACHE_FP8) return launch(append_kernel<T, kDimOf, DS_CACHE_FP8>);
+    return launch(append_kernel<T, kDimOf, DS_CACHE_BF16>);
 }
 
 template <typename T>

@@ -1,0 +1,151 @@
+// Rows read back from a paged cache: row slot[i] of entry seq[i], widened exactly and rounded
+// once to the output's type.
+//
+// Bound by the bytes read and written (for a few rows: by the launch and three dependent loads, the
+// indices, the page id and the row). A thread has 8 neighbouring elements of kUnroll rows, so that
+// neighbours store 16 bytes (32 for fp32) each without a gap, and the loads of its rows are in
+// flight together.
+
+#include "fp8.cuh"
+#include "int4.cuh"
+#include "kernels.h"
+
+namespace dsrows {
+
+namespace {
+
+constexpr int kFetchThreads = 256;
+constexpr int kFetchUnroll = 4;
+
+// 8 elements from 4 bf16 pairs.
+__device__ __forceinline__ void put8(__nv_bfloat16* out, const uint32_t (&w)[4], bool wide) {
+    if (wide) {
+        *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        reinterpret_cast<uint16_t*>(out)[i] = (uint16_t)(w[i / 2] >> 16 * (i % 2));
+}
+__device__ __forceinline__ float element(const uint32_t (&w)[4], int i) {
+    return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+}
+__device__ __forceinline__ void put8(float* out, const uint32_t (&w)[4], bool wide) {
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            reinterpret_cast<float4*>(out)[i] = make_float4(element(w, 4 * i), element(w, 4 * i + 1),
+                                                            element(w, 4 * i + 2), element(w, 4 * i + 3));
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = element(w, i);
+}
+__device__ __forceinline__ void put8(__half* out, const uint32_t (&w)[4], bool wide) {
+    __align__(16) __half h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = __float2half_rn(element(w, i));
+    if (wide) {
+        *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(h);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = h[i];
+}
+
+}  // namespace
+
+template <typename T, int kDimOf, int kFormat>
+__global__ void __launch_bounds__(kFetchThreads) fetch_kernel(const __grid_constant__ FetchCall p) {
+    constexpr int LANES = kDimOf / 8;  // threads of a row
+    constexpr int ROWS = kFetchThreads / LANES;
+    pdl_trigger();
+    const int r = threadIdx.x / LANES, g = threadIdx.x % LANES;
+    const uint64_t first = (uint64_t)blockIdx.x * (ROWS * kFetchUnroll) + r;
+    const uint32_t shift = p.cache.page_shift;
+    pdl_wait();
+    int32_t seq[kFetchUnroll], slot[kFetchUnroll], id[kFetchUnroll];
+#pragma unroll
+    for (int u = 0; u < kFetchUnroll; ++u) {
+        const uint64_t token = first + u * ROWS;
+        seq[u] = token < p.tokens ? p.seq[token] : -1;
+        slot[u] = seq[u] != -1 ? p.slot[token] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kFetchUnroll; ++u) {
+        const uint32_t page_no = (uint32_t)slot[u] >> shift;
+        const bool in = seq[u] >= 0 && (uint32_t)seq[u] < p.cache.entries && slot[u] >= 0 && page_no < p.cache.table_stride;
+        id[u] = in ? p.cache.table[(uint64_t)seq[u] * p.cache.table_stride + page_no] : -1;
+        if ((uint32_t)id[u] >= p.cache.num_pages) id[u] = -1;
+    }
+    // The row's 8 elements as they are held, and their scale.
+    uint4 d[kFetchUnroll];
+    uint32_t sc[kFetchUnroll];
+#pragma unroll
+    for (int u = 0; u < kFetchUnroll; ++u) {
+        if (id[u] < 0) continue;
+        const uint8_t* page = p.cache.pages + ((size_t)(uint32_t)id[u] << shift) * p.cache.row_bytes;
+        const size_t size = (size_t)1 << shift, at = (uint32_t)slot[u] & ((1u << shift) - 1);
+        if constexpr (kFormat == DS_CACHE_BF16) {
+            d[u] = *reinterpret_cast<const uint4*>(page + (at * kDimOf + 8 * g) * 2);
+        } else if constexpr (kFormat == DS_CACHE_FP8) {
+            const uint2 v = *reinterpret_cast<const uint2*>(
+                kDimOf == kDim ? page + at * kDimOf + 8 * g : page + (size_t)(g / 2) * (16 * size) + at * 16 + (g % 2) * 8);
+            d[u] = make_uint4(v.x, v.y, 0, 0);
+            sc[u] = page[size * kDimOf + at * (kDimOf / fp8::kBlock) + 8 * g / fp8::kBlock];
+        } else if constexpr (kDimOf == kDim) {
+            const uint8_t* row = page + at * p.cache.row_bytes;
+            d[u].x = *reinterpret_cast<const uint32_t*>(row + 4 * g);
+            sc[u] = row[kDimOf / 2 + g / 2];
+        } else {
+            d[u].x = *reinterpret_cast<const uint32_t*>(page + (size_t)(g / 4) * (16 * size) + at * 16 + (g % 4) * 4);
+            sc[u] = page[size * (kDimOf / 2) + at * (kDimOf / int4::kGroup) + g / 2];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kFetchUnroll; ++u) {
+        const uint64_t token = first + u * ROWS;
+        if (token >= p.tokens) break;
+        if (g == 0 && p.invalid) p.invalid[token] = seq[u] != -1 && id[u] < 0 ? 1u : 0u;
+        if (seq[u] == -1) continue;
+        uint32_t w[4] = {0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};  // no row: NaN
+        if (id[u] >= 0) {
+            if constexpr (kFormat == DS_CACHE_BF16) {
+                w[0] = d[u].x, w[1] = d[u].y, w[2] = d[u].z, w[3] = d[u].w;
+            } else if constexpr (kFormat == DS_CACHE_FP8) {
+                const uint32_t f = fp8::factor(sc[u]);
+                fp8::widen(d[u].x, f, w);
+                fp8::widen(d[u].y, f, w + 2);
+            } else {
+                int4::Factors f, unused;
+                int4::factors2<0>(sc[u], f, unused);
+                int4::widen(d[u].x, f, w);
+            }
+        }
+        put8(static_cast<T*>(p.out) + token * p.out_stride + 8 * g, w, p.wide != 0);
+    }
+}
+
+template <typename T, int kDimOf>
+static cudaError_t launch_rows(const FetchCall& p, int format, cudaStream_t stream, bool pdl) {
+    constexpr uint64_t rows = kFetchThreads / (kDimOf / 8) * kFetchUnroll;
+    const dim3 grid((uint32_t)((p.tokens + rows - 1) / rows));
+    auto launch = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kFetchThreads), 0, stream, pdl, p); };
+    if (format == DS_CACHE_INT4) return launch(fetch_kernel<T, kDimOf, DS_CACHE_INT4>);
+    if (format == DS_CACHE_FP8) return launch(fetch_kernel<T, kDimOf, DS_CACHE_FP8>);
+    return launch(fetch_kernel<T, kDimOf, DS_CACHE_BF16>);
+}
+
+template <typename T>
+static cudaError_t launch_type(const FetchCall& p, uint32_t dim, int format, cudaStream_t stream, bool pdl) {
+    return dim == kDim ? launch_rows<T, kDim>(p, format, stream, pdl) : launch_rows<T, kIdxDim>(p, format, stream, pdl);
+}
+
+cudaError_t launch_fetch(const FetchCall& p, int dtype, uint32_t dim, int format, cudaStream_t stream, bool pdl) {
+    if (p.tokens == 0) return cudaSuccess;
+    if (dtype == DS_F32) return launch_type<float>(p, dim, format, stream, pdl);
+    if (dtype == DS_F16) return launch_type<__half>(p, dim, format, stream, pdl);
+    return launch_type<__nv_bfloat16>(p, dim, format, stream, pdl);
+}
+
+}  // namespace dsrows

@@ -176,6 +176,17 @@ struct AppendCall {
     uint32_t wide;  // the rows of x start on 16-byte boundaries
 };
 
+struct FetchCall {
+    PagedCache cache;
+    void* out;
+    uint64_t out_stride;
+    uint64_t tokens;
+    const int32_t* seq;
+    const int32_t* slot;
+    uint32_t* invalid;
+    uint32_t wide;  // the rows of out start on 16-byte boundaries
+};
+
 // Indexer scores over a paged key cache, one query per entry.
 struct PagedIndexerParams {
     CUtensorMap kmap;  // bf16 pages: [num_pages * page_size, 128], box {64, min(page_size, 128)}, 128-B swizzle
@@ -199,6 +210,7 @@ struct PagedTailParams : TailParams {
 
 cudaError_t launch_rope(RopeCall p, int dtype, int layout, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_append(const AppendCall& p, int dtype, uint32_t dim, int format, cudaStream_t stream, bool pdl);
+cudaError_t launch_fetch(const FetchCall& p, int dtype, uint32_t dim, int format, cudaStream_t stream, bool pdl);
 cudaError_t launch_paged_indexer(const PagedIndexerParams& p, int format, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_sparse_attn_paged(const PagedTailParams& p, int format, cudaStream_t stream, bool pdl);
 

@@ -1,5 +1,5 @@
 """Positions and paged caches: the binding of ``ds_rows_rope``, ``ds_rows_append``,
-``ds_rows_indexer_score_paged`` and ``ds_rows_sparse_attn_paged``.
+``ds_rows_fetch``, ``ds_rows_indexer_score_paged`` and ``ds_rows_sparse_attn_paged``.
 
 A ``Rope`` and a ``PagedCache`` are made once and kept: they hold the tensors that
 the library reads and the C structures that describe them. The calls themselves
@@ -20,7 +20,7 @@ from . import DIM, DS_OK, HEADS, INDEX_DIM, INDEX_HEADS, _check, load
 PAGED_WORKSPACE_BYTES = 256  # DS_PAGED_WORKSPACE_BYTES
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # DS_BF16, DS_F16, DS_F32
 _LAYOUTS = {"interleaved": 0, "half": 1}                           # DS_ROPE_*
-_FORMATS = {"bf16": 0, "int4": 1}                                  # DS_CACHE_*
+_FORMATS = {"bf16": 0, "int4": 1, "fp8": 3}                        # DS_CACHE_*
 _U32_MAX = 0xFFFFFFFF
 
 
@@ -45,10 +45,11 @@ def declare(lib) -> None:
     lib.ds_rows_page_bytes.argtypes = [u32, u32, i32]
     lib.ds_rows_page_bytes.restype = sz
     lib.ds_rows_append.argtypes = [cache, vp, u64, i32, u64, vp, vp, rope, vp, vp, vp, vp]
+    lib.ds_rows_fetch.argtypes = [cache, vp, vp, vp, u64, i32, u64, vp, vp]
     lib.ds_rows_indexer_score_paged.argtypes = [i32, vp, cache, vp, vp, vp, sz, vp]
     lib.ds_rows_sparse_attn_paged.argtypes = [i32, vp, cache, vp, vp, sz, vp, f32, vp, vp, vp, sz, vp]
-    for f in (lib.ds_rows_rope_turns, lib.ds_rows_rope, lib.ds_rows_append, lib.ds_rows_indexer_score_paged,
-              lib.ds_rows_sparse_attn_paged):
+    for f in (lib.ds_rows_rope_turns, lib.ds_rows_rope, lib.ds_rows_append, lib.ds_rows_fetch,
+              lib.ds_rows_indexer_score_paged, lib.ds_rows_sparse_attn_paged):
         f.restype = i32
 
 
@@ -223,7 +224,7 @@ def ds_rows_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, out: torc
 # ---------------------------------------------------------------------------
 
 def ds_rows_page_bytes(page_size: int, dim: int, fmt: str) -> int:
-    """Bytes of one page of `page_size` rows of `dim` (128 or 512) elements held as "bf16" or "int4"."""
+    """Bytes of one page of `page_size` rows of `dim` (128 or 512) elements held as "bf16", "fp8" or "int4"."""
     lib = load()
     n = lib.ds_rows_page_bytes(_u32(page_size, "page_size"), _u32(dim, "dim"),
                                _code(_FORMATS, fmt, "the cache's format"))
@@ -296,6 +297,29 @@ def ds_rows_append(cache: PagedCache, x: torch.Tensor, seq: torch.Tensor, slot: 
         return
     _call(dev, lib.ds_rows_append, cache._ref, x.data_ptr(), row if n > 1 else 0, code, n, ps, pl,
           None if rope is None else rope._ref, pp, pv, pi, _stream_of(stream, dev))
+
+
+def ds_rows_fetch(cache: PagedCache, seq: torch.Tensor, slot: torch.Tensor, out: torch.Tensor,
+                  invalid: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Read row slot[i] of entry seq[i] (-1: padding, left as it is) back into row i of out
+    [tokens, dim]: bf16, fp16 or fp32, its rows contiguous. seq, slot: int32 [tokens].
+    invalid (optional, int32 [tokens]) receives 1 where there is no such row; out is NaN there."""
+    lib = load()
+    dev = _cuda(out, "out")
+    if cache.device_index != dev:
+        raise ValueError(f"out is on {out.device}, the cache on {cache.pages.device}")
+    if out.dim() != 2 or out.shape[1] != cache.dim:
+        raise ValueError(f"out must be [tokens, {cache.dim}], got {tuple(out.shape)}")
+    row, element = out.stride()
+    if element != 1:
+        raise ValueError("the elements of a row of out must be contiguous")
+    code = _code(_DTYPES, out.dtype, "the type of out")
+    n = out.shape[0]
+    ps, pl = _tensor(seq, "seq", torch.int32, dev, n), _tensor(slot, "slot", torch.int32, dev, n)
+    pi = None if invalid is None else _tensor(invalid, "invalid", torch.int32, dev, n)
+    if n == 0:
+        return
+    _call(dev, lib.ds_rows_fetch, cache._ref, ps, pl, out.data_ptr(), row, code, n, pi, _stream_of(stream, dev))
 
 
 def ds_rows_indexer_score_paged(rows, q_index: torch.Tensor, w_index: torch.Tensor, keys: PagedCache,

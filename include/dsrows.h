@@ -385,7 +385,7 @@ int ds_rows_compress_kv(int rows, const ds_compressor_row_t* table, const float*
  * `inverse` on the output where the model asks for it.
  * ------------------------------------------------------------------------- */
 
-/* Element types of ds_rows_rope and ds_rows_append. */
+/* Element types of ds_rows_rope, ds_rows_append and ds_rows_fetch. */
 #define DS_BF16 0
 #define DS_F16 1
 #define DS_F32 2
@@ -458,6 +458,7 @@ int ds_rows_rope(const ds_rope_t* rope, const void* x, uint64_t x_token_stride, 
 /* Types of a paged cache. */
 #define DS_CACHE_BF16 0
 #define DS_CACHE_INT4 1
+#define DS_CACHE_FP8 3 /* 2 is not in use */
 
 /*
  * A paged cache of `dim`-wide rows (128: indexer keys, 512: shared K/V rows).
@@ -474,6 +475,13 @@ int ds_rows_rope(const ds_rope_t* rope, const void* x, uint64_t x_token_stride, 
  *                    dim 128: 4 planes [page_size][16 bytes], plane c with values
  *                    32 c .. 32 c + 31 of each row, then [page_size][8 scales]
  *                    (a plane is read by consecutive threads without bank conflicts).
+ *     DS_CACHE_FP8   a row is dim / 128 blocks of 128 values v 2^e: v an e4m3 byte, e =
+ *                    -100 .. 7 held as the byte e + 127 (any other byte makes its block
+ *                    NaN; the e4m3 bytes 0x7F and 0xFF are never written, and read as 480 and
+ *                    -480). Every value is exact in bf16.
+ *                    dim 512: [page_size][512 bytes of values], then [page_size][4 exponents].
+ *                    dim 128: 8 planes [page_size][16 bytes], plane c with values
+ *                    16 c .. 16 c + 15 of each row, then [page_size] exponents.
  *   page_table  device int32 [entries, table_stride] (4-B aligned)
  *   page_size   rows of a page: 16, 32, 64, 128 or 256
  *   num_pages   pages of the pool; num_pages * page_size < 2^31
@@ -512,11 +520,29 @@ size_t ds_rows_page_bytes(uint32_t page_size, uint32_t dim, int format);
  * even. DS_CACHE_INT4, per group of 16 values y: s = e4m3(min(max|y| / 7, 448)) to
  * nearest even, n = y / s to the nearest integer (even on ties) within -7 .. 7
  * (s = 0: n = 0); a group with a non-finite value is stored as NaN. n s is exact
- * in bf16 and in fp16.
+ * in bf16 and in fp16. DS_CACHE_FP8, per block of 128 values y: e = the least of -100 .. 7
+ * with max|y| <= 448 2^e (7 if there is none), v = y 2^-e to the nearest e4m3 (even on
+ * ties, saturating at 448); a block with a non-finite value is stored as NaN.
  */
 int ds_rows_append(const ds_paged_cache_t* cache, const void* x, uint64_t x_stride, int dtype, uint64_t tokens,
                    const int32_t* seq, const int32_t* slot, const ds_rope_t* rope, const int32_t* positions,
                    ds_bf16* values, uint32_t* invalid, void* stream);
+
+/*
+ * Rows read back from a paged cache: row i of out [tokens, dim] becomes row slot[i] of
+ * entry seq[i], as ds_rows_append's `values` gave it: widened exactly, rounded once to
+ * `dtype` (only DS_F16 can round: to nearest even, to infinity past 65504).
+ *   seq, slot  device int32 [tokens]. seq -1 marks padding: the row of out is left as it
+ *              is. The same (seq, slot) may come up again.
+ *   out        device, element type `dtype`, rows out_stride elements apart (the elements of
+ *              a row contiguous; out_stride >= dim, at most 2^31; of a lone row: not looked
+ *              at); must not share memory with the pages. 16-byte aligned rows are fastest.
+ *   tokens     below 2^31; 0 enqueues nothing
+ *   invalid    optional uint32 [tokens]: 1 where seq, slot or its page id is out of range
+ *              (the row of out is NaN), else 0
+ */
+int ds_rows_fetch(const ds_paged_cache_t* cache, const int32_t* seq, const int32_t* slot, void* out,
+                  uint64_t out_stride, int dtype, uint64_t tokens, uint32_t* invalid, void* stream);
 
 /*
  * ds_rows_indexer_score with the keys in a paged cache (dim 128): entry e of the

@@ -3,7 +3,8 @@
 Test infrastructure, as the rest of this package. The rotation follows its formula
 with 64-bit angles; the 4-bit type is spelled out value by value and byte by byte
 (groups of 16 values n * s, s e4m3, n in -7..7 held as n + 8; value i of a word at
-bits 4 (i // 2) + 16 (i mod 2)).
+bits 4 (i // 2) + 16 (i mod 2)), and so is the 8-bit type (blocks of 128 values v * 2^e,
+v e4m3, e in -100..7 held as e + 127).
 """
 
 from __future__ import annotations
@@ -112,8 +113,46 @@ def int4_numbers(data):
 
 
 # ---------------------------------------------------------------------------
+# the 8-bit blocks
+# ---------------------------------------------------------------------------
+
+BLOCK = 128
+
+
+def fp8_quantise(y):
+    """Rows [rows, dim] -> (value bytes [rows, dim], exponent bytes [rows, dim / 128])."""
+    g = np.asarray(y, np.float64).reshape(len(y), -1, BLOCK)
+    bad = ~np.isfinite(g).all(-1)
+    g = np.where(bad[..., None], 0.0, g)
+    top = np.abs(g).max(-1)
+    e = np.full(top.shape, 7)
+    for k in range(6, -101, -1):
+        e = np.where(top <= 448 * 2.0 ** k, k, e)
+    v = g / 2.0 ** e[..., None]
+    byte = e4m3_byte(np.abs(v)) | np.where(np.signbit(v), 0x80, 0).astype(np.uint8)
+    return byte.reshape(np.shape(y)), np.where(bad, 255, e + 127).astype(np.uint8)
+
+
+def fp8_values(byte, exponents):
+    """The numbers of value bytes [rows, dim]; the codes of e4m3's NaN stand for +-480."""
+    b = np.asarray(byte, np.int64)
+    v = np.where((b & 127) == 127, np.where(b & 128, -480.0, 480.0), e4m3_value(b))
+    x = np.asarray(exponents, np.int64)
+    scale = np.where((x >= 27) & (x <= 134), 2.0 ** (np.clip(x, 27, 134) - 127.0), np.nan)
+    return (v.reshape(len(b), -1, BLOCK) * scale[..., None]).reshape(b.shape)
+
+
+# ---------------------------------------------------------------------------
 # pages
 # ---------------------------------------------------------------------------
+
+def fp8_places(dim, page_size):
+    """Byte offsets inside an 8-bit page of each row's values [page_size, dim] and exponents [page_size, dim / 128]."""
+    r = np.arange(page_size)[:, None]
+    v, s = np.arange(dim)[None], np.arange(dim // BLOCK)[None]
+    scales = dim * page_size + dim // BLOCK * r + s
+    return (r * 512 + v if dim == 512 else v // 16 * (16 * page_size) + 16 * r + v % 16), scales
+
 
 def row_places(dim, page_size):
     """Byte offsets inside a 4-bit page of each row's values [page_size, dim / 2] and scales [page_size, dim / 16]."""
