@@ -1120,7 +1120,6 @@ int ds_rows_indexer_score_paged(int rows, const ds_row_t* table, const ds_paged_
     if (rc) return rc;
     rc = check_cache(keys, DS_INDEX_DIM, rows);
     if (rc) return rc;
-    if (keys->format == DS_CACHE_FP8) return fail(DS_EINVAL, "scores over 8-bit pages are not built");
     rc = check_reach(rows, table, keys);
     if (rc) return rc;
     rc = check_indexer_args(q_index, w_index);
@@ -1171,7 +1170,6 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
     if (rc) return rc;
     rc = check_cache(kv, DS_DIM, rows);
     if (rc) return rc;
-    if (kv->format == DS_CACHE_FP8) return fail(DS_EINVAL, "attention over 8-bit pages are not built");
     rc = check_reach(rows, table, kv);
     if (rc) return rc;
     rc = check_attn_args(q_attn, sinks, sinks_row_stride, scale, out);

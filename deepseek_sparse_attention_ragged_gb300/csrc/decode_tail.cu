@@ -43,7 +43,7 @@
 // its own best-first index list.
 //
 // Over a paged cache (sparse_attn_paged_kernel) the rows come from the pages of a pool, in
-// bf16 or widened from 4 bits as they are gathered, and the partials cross the cluster in
+// bf16 or widened from 8 or 4 bits as they are gathered, and the partials cross the cluster in
 // distributed shared memory; every reduction is the same, so the output is bitwise that of
 // the rows that the cache stands for.
 //
@@ -62,6 +62,7 @@
 
 #include "attend.cuh"
 #include "common.cuh"
+#include "fp8.cuh"
 #include "int4.cuh"
 #include "kernels.h"
 #include "select.cuh"
@@ -159,8 +160,9 @@ __device__ __forceinline__ uint32_t sw128_chunk(int r, int ch, int block) {
 
 // Where the KV rows lie: one contiguous bf16 cache per entry, or the pages of a
 // pool in bf16 or 4 bits (the caller's indices only).
-enum class Cache { kContiguous, kPagedBf16, kPagedInt4 };
+enum class Cache { kContiguous, kPagedBf16, kPagedInt4, kPagedFp8 };
 constexpr int kInt4RowBytes = kDim / 2 + kDim / int4::kGroup;
+constexpr int kFp8RowBytes = kDim + kDim / fp8::kBlock;  // of a page: its rows' values, then their exponents
 
 constexpr uint32_t kNoIndex = 0xFFFFFFFFu;
 
@@ -334,9 +336,15 @@ __device__ __forceinline__ void tail_body(const Params& p) {
         g = bitonic512_asc(g, reinterpret_cast<uint32_t*>(gs.h), [&] {
             if (((uint32_t)t >> 6) == rank && mine != kNoIndex) {
                 const int32_t at = place_of(mine);
-                if (at >= 0)
+                if (at >= 0 && kCache == Cache::kPagedFp8) {
+                    const uint32_t page_rows = 1u << shift, in_page = (uint32_t)at & (page_rows - 1);
+                    const uint8_t* page = p.cache.pages + (size_t)((uint32_t)at - in_page) * kFp8RowBytes;
+                    for (uint32_t o = 0; o < (uint32_t)kDim; o += 128) prefetch_l2(page + (size_t)in_page * kDim + o);
+                    prefetch_l2(page + (size_t)page_rows * kDim + in_page * (kDim / fp8::kBlock));
+                } else if (at >= 0) {
                     for (uint32_t o = 0; o < p.cache.row_bytes; o += 128)
                         prefetch_l2(p.cache.pages + (size_t)at * p.cache.row_bytes + o);
+                }
             }
         });
         if ((uint32_t)t - first < (uint32_t)kChunkSlots && g != kNoIndex) {
@@ -421,6 +429,48 @@ __device__ __forceinline__ void tail_body(const Params& p) {
                     int4::widen(w[c], f[c >> 1], o);
                     *reinterpret_cast<uint4*>(g_s + sw128_chunk(r, 4 * u + c, kGBlock)) =
                         make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        }
+    } else if constexpr (kCache == Cache::kPagedFp8) {
+        // The same with units of 16 values (16 bytes), eight steps in two halves: half of a row's
+        // loads are in flight while the other half is widened.
+        constexpr int kUnits = kDim / 16 / 4, kHalf = kUnits / 2;
+        if (has_chunk) {
+            const int r = 8 * warp + (lane & 7);
+            const int i = idx_s[r];
+            const uint32_t shift = p.cache.page_shift, at = (uint32_t)max(i, 0), in_page = at & ((1u << shift) - 1);
+            const uint8_t* page = p.cache.pages + (size_t)(at - in_page) * kFp8RowBytes;
+            const uint8_t* row = page + (size_t)in_page * kDim;
+            // An empty slot is zeros (its exponent any in range).
+            uint32_t ex = 0x7F7F7F7Fu;
+            if (i >= 0) ex = __ldcg(reinterpret_cast<const uint32_t*>(page + ((size_t)kDim << shift)) + in_page);
+            uint4 d[2][kHalf];
+            auto load = [&](int half) {
+#pragma unroll
+                for (int n = 0; n < kHalf; ++n) {
+                    d[half][n] = make_uint4(0, 0, 0, 0);
+                    const int u = 4 * (half * kHalf + n) + (lane >> 3);
+                    if (i >= 0) d[half][n] = __ldcg(reinterpret_cast<const uint4*>(row + 16 * u));
+                }
+            };
+            load(0);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (half == 0) load(1);
+#pragma unroll
+                for (int n = 0; n < kHalf; ++n) {
+                    const int u = 4 * (half * kHalf + n) + (lane >> 3);
+                    const uint32_t f = fp8::factor(ex >> (8 * ((half * kHalf + n) / 2)) & 0xFFu);  // 8 units a block
+                    uint32_t o[8];
+                    fp8::widen(d[half][n].x, f, o);
+                    fp8::widen(d[half][n].y, f, o + 2);
+                    fp8::widen(d[half][n].z, f, o + 4);
+                    fp8::widen(d[half][n].w, f, o + 6);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        *reinterpret_cast<uint4*>(g_s + sw128_chunk(r, 2 * u + c, kGBlock)) =
+                            make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                 }
             }
         }
@@ -719,8 +769,9 @@ static cudaError_t launch_paged(const PagedTailParams& p, cudaStream_t stream, b
 
 cudaError_t launch_sparse_attn_paged(const PagedTailParams& p, int format, cudaStream_t stream, bool pdl) {
     if (p.rows == 0) return cudaSuccess;
-    return format == DS_CACHE_INT4 ? launch_paged<Cache::kPagedInt4>(p, stream, pdl)
-                                   : launch_paged<Cache::kPagedBf16>(p, stream, pdl);
+    if (format == DS_CACHE_INT4) return launch_paged<Cache::kPagedInt4>(p, stream, pdl);
+    if (format == DS_CACHE_FP8) return launch_paged<Cache::kPagedFp8>(p, stream, pdl);
+    return launch_paged<Cache::kPagedBf16>(p, stream, pdl);
 }
 
 }  // namespace dsrows

@@ -31,9 +31,10 @@
 // the polling loads 21.5; shared-space pointers and running indexes 20.8.
 //
 // Warp roles: 0 loads, the next kIssuers issue the MMAs (warp 1 owns TMEM), then
-// kEpiSets epilogue sets of four warps and (4-bit pages) kWideSets widening sets.
+// kEpiSets epilogue sets of four warps and (packed pages) kWideSets widening sets.
 
 #include "common.cuh"
+#include "fp8.cuh"
 #include "head_sum.cuh"
 #include "int4.cuh"
 #include "kernels.h"
@@ -47,23 +48,29 @@ constexpr int kTileKeys = 128;
 constexpr int kHalfBytes = kTileKeys * 64 * 2;     // one 64-column SW128 block of a bf16 tile
 constexpr int kBf16Tile = 2 * kHalfBytes;
 constexpr int kQHalf = kIdxHeads * 64 * 2;         // one 64-column block of the query
-constexpr int kInt4Row = kIdxDim / 2 + kIdxDim / int4::kGroup;  // 72 bytes
-constexpr int kInt4Tile = kTileKeys * kInt4Row;
+// A packed key's planes of 16 bytes, its scale bytes and its bytes in all (4 bits: 72, 8 bits: 129).
+template <int kFormat>
+struct Packed {
+    static constexpr int kPlanes = kFormat == DS_CACHE_FP8 ? kIdxDim / 16 : kIdxDim / 32;
+    static constexpr int kScales = kFormat == DS_CACHE_FP8 ? kIdxDim / fp8::kBlock : kIdxDim / int4::kGroup;
+    static constexpr int kRow = 16 * kPlanes + kScales;
+};
 constexpr int kKeyWords = kIdxDim / 2;             // TMEM columns of a widened key (bf16 pairs)
 constexpr int kIssuers = 2;   // warps that issue MMAs, each every second tile
 constexpr int kEpiSets = 2;   // of four epilogue warps, each every second tile
 constexpr int kWideSets = 4;  // of four widening warps, each every fourth tile
 constexpr int kBufs = 4;      // accumulators, and widened tiles
 
-template <bool kInt4>
+template <int kFormat>
 struct Shape {
-    static constexpr int kStages = kInt4 ? 12 : 4;
+    static constexpr bool kPacked = kFormat != DS_CACHE_BF16;  // widened before the MMAs
+    static constexpr int kStages = kFormat == DS_CACHE_INT4 ? 12 : kFormat == DS_CACHE_FP8 ? 8 : 4;
     static constexpr int kLap = 4;  // tiles whose loads are in the lanes' hands
-    static constexpr int kStageBytes = kInt4 ? kInt4Tile : kBf16Tile;
-    static constexpr int kThreads = 32 * (1 + kIssuers) + 128 * (kEpiSets + (kInt4 ? kWideSets : 0));
+    static constexpr int kStageBytes = kPacked ? kTileKeys * Packed<kFormat>::kRow : kBf16Tile;
+    static constexpr int kThreads = 32 * (1 + kIssuers) + 128 * (kEpiSets + (kPacked ? kWideSets : 0));
     static constexpr uint32_t kAccCols = kIdxHeads;
     static constexpr uint32_t kKeyCol = kBufs * kAccCols;  // widened keys: kBufs * kKeyWords columns
-    static constexpr uint32_t kTmemCols = kInt4 ? 512 : 256;
+    static constexpr uint32_t kTmemCols = kPacked ? 512 : 256;
     static constexpr size_t keys = 0;
     static constexpr size_t q = keys + (size_t)kStages * kStageBytes;
     static constexpr size_t w = q + 2 * (size_t)kQHalf;
@@ -72,31 +79,37 @@ struct Shape {
 // The tiles of a buffer belong to one issuer and one set of each kind, and those of a stage to
 // one lane of the loading warp, one issuer and one widening set: a wait for a parity is then
 // never more than one phase ahead of its barrier.
-static_assert(Shape<true>::kStages % Shape<true>::kLap == 0 && Shape<false>::kStages % Shape<false>::kLap == 0, "phases");
+template <int kFormat>
+constexpr bool phases_hold() {
+    using S = Shape<kFormat>;
+    return S::kStages % S::kLap == 0 && S::kStages % kIssuers == 0 && (!S::kPacked || S::kStages % kWideSets == 0);
+}
 static_assert(kBufs % kIssuers == 0 && kBufs % kEpiSets == 0 && kBufs % kWideSets == 0, "phases");
-static_assert(Shape<true>::kStages % kWideSets == 0 && Shape<true>::kStages % kIssuers == 0 &&
-                  Shape<false>::kStages % kIssuers == 0,
-              "phases");
-static_assert(Shape<true>::kKeyCol + kBufs * kKeyWords <= 512, "TMEM columns");
-static_assert(Shape<true>::q % 1024 == 0 && Shape<false>::q % 1024 == 0, "the swizzled query is 1-KiB aligned");
+static_assert(phases_hold<DS_CACHE_BF16>() && phases_hold<DS_CACHE_INT4>() && phases_hold<DS_CACHE_FP8>(), "phases");
+static_assert(Shape<DS_CACHE_INT4>::kKeyCol + kBufs * kKeyWords <= 512, "TMEM columns");
+static_assert(Shape<DS_CACHE_INT4>::q % 1024 == 0 && Shape<DS_CACHE_FP8>::q % 1024 == 0 &&
+                  Shape<DS_CACHE_BF16>::q % 1024 == 0,
+              "the swizzled query is 1-KiB aligned");
 
-template <bool kInt4>
+template <int kFormat>
 struct __align__(8) Bars {
-    uint64_t full[Shape<kInt4>::kStages];
-    uint64_t empty[Shape<kInt4>::kStages];
+    uint64_t full[Shape<kFormat>::kStages];
+    uint64_t empty[Shape<kFormat>::kStages];
     uint64_t key_full[kBufs];   // a widened tile is in TMEM
     uint64_t key_empty[kBufs];  // its MMAs are done
     uint64_t acc_full[kBufs];
     uint64_t acc_empty[kBufs];
-    uint32_t bad[Shape<kInt4>::kStages];  // sub-pages of the tile without a page
+    uint32_t bad[Shape<kFormat>::kStages];  // sub-pages of the tile without a page
     uint32_t tmem_base;
 };
 
-template <bool kInt4>
+template <int kFormat>
 constexpr size_t smem_bytes() {
-    return Shape<kInt4>::bars + sizeof(Bars<kInt4>) + 1024;
+    return Shape<kFormat>::bars + sizeof(Bars<kFormat>) + 1024;
 }
-static_assert(smem_bytes<true>() <= 227 * 1024 && smem_bytes<false>() <= 227 * 1024, "shared memory");
+static_assert(smem_bytes<DS_CACHE_INT4>() <= 227 * 1024 && smem_bytes<DS_CACHE_FP8>() <= 227 * 1024 &&
+                  smem_bytes<DS_CACHE_BF16>() <= 227 * 1024,
+              "shared memory");
 
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -131,17 +144,20 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
 // A wait that gives up ends its role, so every later wait on its work gives up too, and the
 // epilogue writes -inf for the keys that it has no sums for: the caller's buffer never keeps
 // another call's scores.
-template <bool kInt4>
-__global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
+template <int kFormat>
+__global__ void __launch_bounds__(Shape<kFormat>::kThreads, 1)
     paged_indexer_kernel(const __grid_constant__ PagedIndexerParams p) {
-    using S = Shape<kInt4>;
+    using S = Shape<kFormat>;
+    constexpr bool kPacked = S::kPacked;
+    constexpr int kRow = Packed<kFormat>::kRow, kPlanes = Packed<kFormat>::kPlanes;  // packed keys
+    constexpr int kScales = Packed<kFormat>::kScales;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // Aligned by an offset, so that the pointers stay in the shared address space.
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* keys_s = smem + S::keys;
     uint8_t* q_s = smem + S::q;
     float* w_s = reinterpret_cast<float*>(smem + S::w);
-    Bars<kInt4>* bar = reinterpret_cast<Bars<kInt4>*>(smem + S::bars);
+    Bars<kFormat>* bar = reinterpret_cast<Bars<kFormat>*>(smem + S::bars);
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);  // known to be uniform
     const int lane = threadIdx.x & 31;
 
@@ -162,7 +178,7 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(&bar->full[s], 1);
-            mbar_init(&bar->empty[s], kInt4 ? 4 : 1);
+            mbar_init(&bar->empty[s], kPacked ? 4 : 1);
             bar->bad[s] = 0;
         }
         for (int a = 0; a < kBufs; ++a) {
@@ -172,7 +188,7 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
             mbar_init(&bar->acc_empty[a], 4);
         }
         fence_barrier_init();
-        if (!kInt4) tma_prefetch_map(&p.kmap);
+        if (!kPacked) tma_prefetch_map(&p.kmap);
     }
     if (warp == 1) {
         tmem_alloc(&bar->tmem_base, S::kTmemCols);
@@ -208,7 +224,7 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
         constexpr uint32_t lap = S::kLap;  // tiles of up to 8 sub-pages each: 32 lanes
         const uint32_t my_tile = lane / subs, my_sub = lane % subs;
         const uint32_t group = ((1u << subs) - 1) << (my_tile * subs);  // the tile's lanes; subs <= 8
-        const uint32_t sub_bytes = sub_rows * (kInt4 ? kInt4Row : kIdxDim * 2);
+        const uint32_t sub_bytes = sub_rows * (kPacked ? kRow : kIdxDim * 2);
         const int32_t* table = p.cache.table + (size_t)e * p.cache.table_stride;
         const uint64_t policy = l2_policy_evict_first();
         const uint32_t tiles = my_tile < lap ? mine : 0;  // the other lanes have none
@@ -231,9 +247,9 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
                     mbar_arrive_expect_tx(&bar->full[s], __popc(have_bits) * sub_bytes);
                 }
                 if (have) {
-                    uint8_t* dst = keys_s + s * S::kStageBytes + my_sub * (kInt4 ? sub_bytes : sub_rows * 128);
+                    uint8_t* dst = keys_s + s * S::kStageBytes + my_sub * (kPacked ? sub_bytes : sub_rows * 128);
                     const uint32_t in_page = shift <= 7 ? 0u : first_key(it) & ((1u << shift) - 1);
-                    if (!kInt4) {
+                    if (!kPacked) {
                         const int y = (int)(((uint32_t)id << shift) + in_page);
                         tma_load_2d(dst, &p.kmap, &bar->full[s], 0, y, policy);
                         tma_load_2d(dst + kHalfBytes, &p.kmap, &bar->full[s], 64, y, policy);
@@ -243,10 +259,10 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
                             bulk_copy_g2s(dst, page, sub_bytes, &bar->full[s]);
                         } else {
                             // A 128-row slice of each plane, and its scales.
-                            for (uint32_t c = 0; c < 5; ++c)
+                            for (uint32_t c = 0; c <= kPlanes; ++c)
                                 bulk_copy_g2s(dst + c * kTileKeys * 16,
-                                              page + ((size_t)c << shift) * 16 + (size_t)in_page * (c < 4 ? 16 : 8),
-                                              kTileKeys * (c < 4 ? 16 : 8), &bar->full[s]);
+                                              page + ((size_t)c << shift) * 16 + (size_t)in_page * (c < kPlanes ? 16 : kScales),
+                                              kTileKeys * (c < kPlanes ? 16 : kScales), &bar->full[s]);
                         }
                     }
                 }
@@ -277,7 +293,7 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
         uint32_t it = warp - 1, a = it, s = it, ph = 0, sph = 0;  // tile, buffer, stage, their phases
         for (; it < mine; it += kIssuers) {
             if (!wait_short(&bar->acc_empty[a], ph ^ 1)) break;
-            if (kInt4) {
+            if (kPacked) {
                 if (!wait_short(&bar->key_full[a], ph)) break;
             } else {
                 if (!wait_short(&bar->full[s], sph)) break;
@@ -290,13 +306,13 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
                 for (int kk = 0; kk < kIdxDim / 16; ++kk) {
                     const uint32_t koff = (uint32_t)(kk & 3) * 32;  // 16 bf16 inside the 128-byte row
                     const uint64_t bdesc = smem_desc_sw128_kmajor(b_base + (kk >> 2) * kQHalf + koff);
-                    if (kInt4)
+                    if (kPacked)
                         umma_bf16_ta(d_tmem, tmem + S::kKeyCol + a * kKeyWords + kk * 8, bdesc, idesc, kk > 0);
                     else
                         umma_bf16(d_tmem, smem_desc_sw128_kmajor(a_base + (kk >> 2) * kHalfBytes + koff), bdesc, idesc,
                                   kk > 0);
                 }
-                umma_commit(kInt4 ? &bar->key_empty[a] : &bar->empty[s]);
+                umma_commit(kPacked ? &bar->key_empty[a] : &bar->empty[s]);
                 umma_commit(&bar->acc_full[a]);
             }
             __syncwarp();
@@ -318,7 +334,7 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
         for (uint32_t it = set; it < mine; it += kEpiSets, j += kEpiSets * step * kTileKeys) {
             // A bf16 key without a page is left out here (a widened one is NaN).
             bool have = true;
-            if (!kInt4 && j < kv_len) {
+            if (!kPacked && j < kv_len) {
                 const int32_t id = p.cache.table[(size_t)e * p.cache.table_stride + (j >> shift)];
                 have = id >= 0 && (uint32_t)id < p.cache.num_pages;
             }
@@ -346,36 +362,58 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
         const int quarter = warp & 3;
         const uint32_t key = quarter * 32 + lane;
         const uint32_t sub = key / sub_rows, row = key % sub_rows;
-        const uint8_t* row_s = keys_s + sub * sub_rows * kInt4Row + row * 16;
-        const uint8_t* scale_s = keys_s + (sub * kInt4Row + kIdxDim / 2) * sub_rows + row * 8;
+        const uint8_t* row_s = keys_s + sub * sub_rows * kRow + row * 16;
+        const uint8_t* scale_s = keys_s + (sub * kRow + 16 * kPlanes) * sub_rows + row * kScales;
         const uint32_t tcol = tmem + ((uint32_t)(quarter * 32) << 16) + S::kKeyCol;
         uint32_t a = set, s = set, ph = 0, sph = 0;  // buffer, stage, their phases
         for (uint32_t it = set; it < mine; it += kWideSets) {
             const uint32_t taddr = tcol + a * kKeyWords;
             if (!wait_short(&bar->full[s], sph)) break;
-            uint4 d[4];
+            uint4 d[kPlanes];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < kPlanes; ++c)
                 d[c] = *reinterpret_cast<const uint4*>(row_s + s * S::kStageBytes + c * sub_rows * 16);
-            uint2 sc = *reinterpret_cast<const uint2*>(scale_s + s * S::kStageBytes);
             // A key without a page becomes NaN (its score -inf).
-            if ((bar->bad[s] >> sub) & 1) sc.x = sc.y = 0x7F7F7F7Fu;
+            const bool none = (bar->bad[s] >> sub) & 1;
+            uint2 sc;
+            if constexpr (kFormat == DS_CACHE_FP8) {
+                sc.x = none ? fp8::kNanByte : scale_s[s * S::kStageBytes];
+            } else {
+                sc = *reinterpret_cast<const uint2*>(scale_s + s * S::kStageBytes);
+                if (none) sc.x = sc.y = 0x7F7F7F7Fu;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar->empty[s]);
             if (!wait_short(&bar->key_empty[a], ph ^ 1)) break;
             tc_fence_after();
+            if constexpr (kFormat == DS_CACHE_FP8) {
+                const uint32_t f = fp8::factor(sc.x);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                int4::Factors f0, f1;  // two groups a plane
-                const uint32_t b = c < 2 ? sc.x : sc.y;
-                if (c % 2 == 0) int4::factors2<0>(b, f0, f1);
-                else int4::factors2<2>(b, f0, f1);
-                uint32_t r[16];
-                int4::widen(d[c].x, f0, r);
-                int4::widen(d[c].y, f0, r + 4);
-                int4::widen(d[c].z, f1, r + 8);
-                int4::widen(d[c].w, f1, r + 12);
-                tmem_st_x16(taddr + c * 16, r);
+                for (int c = 0; c < kPlanes; c += 2) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        fp8::widen(d[c + h].x, f, r + 8 * h);
+                        fp8::widen(d[c + h].y, f, r + 8 * h + 2);
+                        fp8::widen(d[c + h].z, f, r + 8 * h + 4);
+                        fp8::widen(d[c + h].w, f, r + 8 * h + 6);
+                    }
+                    tmem_st_x16(taddr + c * 8, r);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < kPlanes; ++c) {
+                    int4::Factors f0, f1;  // two groups a plane
+                    const uint32_t b = c < 2 ? sc.x : sc.y;
+                    if (c % 2 == 0) int4::factors2<0>(b, f0, f1);
+                    else int4::factors2<2>(b, f0, f1);
+                    uint32_t r[16];
+                    int4::widen(d[c].x, f0, r);
+                    int4::widen(d[c].y, f0, r + 4);
+                    int4::widen(d[c].z, f1, r + 8);
+                    int4::widen(d[c].w, f1, r + 12);
+                    tmem_st_x16(taddr + c * 16, r);
+                }
             }
             tmem_st_wait();
             tc_fence_before();
@@ -394,18 +432,20 @@ __global__ void __launch_bounds__(Shape<kInt4>::kThreads, 1)
     }
 }
 
-template <bool kInt4>
+template <int kFormat>
 static cudaError_t launch(const PagedIndexerParams& p, int num_sms, cudaStream_t stream, bool pdl) {
     static std::atomic<uint64_t> smem_set{0};
-    constexpr size_t bytes = smem_bytes<kInt4>();
-    const cudaError_t err = set_smem_limit_once(paged_indexer_kernel<kInt4>, bytes, smem_set);
+    constexpr size_t bytes = smem_bytes<kFormat>();
+    const cudaError_t err = set_smem_limit_once(paged_indexer_kernel<kFormat>, bytes, smem_set);
     if (err != cudaSuccess) return err;
     const uint32_t grid = p.total_tiles < (uint32_t)num_sms ? p.total_tiles : (uint32_t)num_sms;
-    return launch_kernel(paged_indexer_kernel<kInt4>, dim3(grid), dim3(Shape<kInt4>::kThreads), bytes, stream, pdl, p);
+    return launch_kernel(paged_indexer_kernel<kFormat>, dim3(grid), dim3(Shape<kFormat>::kThreads), bytes, stream, pdl, p);
 }
 
 cudaError_t launch_paged_indexer(const PagedIndexerParams& p, int format, int num_sms, cudaStream_t stream, bool pdl) {
-    return format == DS_CACHE_INT4 ? launch<true>(p, num_sms, stream, pdl) : launch<false>(p, num_sms, stream, pdl);
+    if (format == DS_CACHE_INT4) return launch<DS_CACHE_INT4>(p, num_sms, stream, pdl);
+    if (format == DS_CACHE_FP8) return launch<DS_CACHE_FP8>(p, num_sms, stream, pdl);
+    return launch<DS_CACHE_BF16>(p, num_sms, stream, pdl);
 }
 
 }  // namespace dsrows

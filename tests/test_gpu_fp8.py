@@ -4,7 +4,10 @@ Tolerances: a fetched row is what the pages' bytes spell (exact in bf16 and fp32
 rounding in fp16). An appended row without a rotation is exact; with one, the rotation's
 bound (5e-7 of m (|a| + |b|), derived beside its own tests) comes on top of the type's half
 step: 2^-4 of the value, or 2^-10 2^e below e4m3's normal numbers, where e is the
-block's exponent (448 2^(e-1) < max, so 2^e < max / 224).
+block's exponent (448 2^(e-1) < max, so 2^e < max / 224). Scores and attention carry the bits of
+the contiguous calls; the scores' bound is the one derived beside the paged tests, and the
+attention's output is a mean of rows, rounded to bf16: half a step of the largest value, and as
+much again for its weights' and sums' roundings.
 """
 
 import numpy as np
@@ -12,8 +15,11 @@ import pytest
 import torch
 
 import deepseek_sparse_attention_ragged_gb300 as ds
+import oracle
 from oracle import paged as ref
-from test_gpu_paged import BF16, F16, F32, ROPE_RTOL, TYPES, edge_rows, f64, i32, page_table
+from parity import score_bound
+from test_gpu_paged import (BF16, F32, ROPE_RTOL, SCALE, SCORE_RTOL, TYPES, attend, edge_rows, f64, i32, page_table, queries,
+                            row_table)
 from test_gpu_paged import make_cache as make_cache_4
 
 pytestmark = pytest.mark.gpu
@@ -290,3 +296,111 @@ def test_append_and_fetch_in_a_graph_and_on_another_stream():
     with pytest.raises(ValueError, match="out must be"):
         ds.ds_rows_fetch(cache, seq, slot, out[:, :128])
     ds.ds_rows_fetch(cache, seq[:0], slot[:0], out[:0])
+
+
+# ---------------------------------------------------------------------------
+# the readers: the bits of the contiguous calls on the bf16 rows that the pages stand for
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("lens", [[1], [15, 16, 17, 127, 128, 129, 255, 257], [1000, 3, 4097], [60000, 20001]])
+def test_scores(page, lens):
+    rng = np.random.default_rng(page + len(lens))
+    cache, values = make_cache(rng, lens, 128, "fp8", page)
+    q = queries(rng, len(lens), 128)
+    w = torch.from_numpy(rng.standard_normal((len(lens), 64)).astype(np.float32) / 8).cuda()
+    scores, plain = (torch.full((len(lens), max(lens) + 3), 123.0, device="cuda") for _ in range(2))
+    ds.ds_rows_indexer_score_paged(row_table(lens), q, w, cache, scores)
+    ds.ds_rows_indexer_score(row_table(lens), q, w, [torch.from_numpy(v).to(BF16).cuda() for v in values], plain)
+    assert torch.equal(scores, plain)
+    for e, n in enumerate(lens):
+        args = f64(q[e]), f64(w[e]), values[e].astype(np.float64)
+        assert np.all(np.abs(f64(scores[e, :n]) - oracle.indexer_score(*args)) <= SCORE_RTOL * score_bound(*args))
+        assert (scores[e, n:] == 123.0).all()
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_scores_of_bad_pages_and_values(page):
+    rng = np.random.default_rng(2)
+    n = 700
+    cache, values = make_cache(rng, [n], 128, "fp8", page)
+    q, w = queries(rng, 1, 128), torch.ones(1, 64, device="cuda")
+    last = (n - 1) // page
+    cache.page_table[0, 0], cache.page_table[0, last] = -5, cache.num_pages
+    row = page + 3
+    one = torch.zeros(1, 128, device="cuda")
+    one[0, 77] = float("nan")
+    ds.ds_rows_append(cache, one, i32([0]), i32([row]))
+    scores = torch.zeros(1, n, device="cuda")
+    ds.ds_rows_indexer_score_paged(row_table([n]), q, w, cache, scores)
+    gone = (np.arange(n) // page == 0) | (np.arange(n) // page == last) | (np.arange(n) == row)
+    got = f64(scores[0])
+    assert np.all(got[gone] == -np.inf)
+    args = f64(q[0]), f64(w[0]), values[0].astype(np.float64)
+    assert np.all(np.abs(got - oracle.indexer_score(*args))[~gone] <= (SCORE_RTOL * score_bound(*args))[~gone])
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("lens,widths", [([1], [1]), ([37, 130, 600], [37, 100, 512]),
+                                         ([2000, 513, 128, 129, 5, 700, 511, 1024], [512, 512, 128, 129, 1, 384, 511, 3])])
+def test_attention(page, lens, widths):
+    rng = np.random.default_rng(page + len(lens))
+    cache, values = make_cache(rng, lens, 512, "fp8", page)
+    rows = [(n, w, 520 * e + 3, e) for e, (n, w) in enumerate(zip(lens, widths))]
+    idx = np.full(520 * len(lens) + 3, -7, np.int64)
+    for e, (n, w) in enumerate(zip(lens, widths)):
+        pick = rng.permutation(n)[:w]
+        if w > 4:
+            pick[1] = pick[0]   # an index twice
+            pick[3] = -1        # an empty slot
+        idx[520 * e + 3: 520 * e + 3 + w] = pick
+    q = queries(rng, len(lens) + 1, 512)
+    sinks = torch.from_numpy(rng.standard_normal((len(lens) + 1, 70)).astype(np.float32)).cuda()
+    out, plain, bad, bad_plain = attend(rows, q, sinks, 70, i32(idx), cache, values)
+    assert torch.equal(out, plain) and torch.equal(bad, bad_plain) and not bad[:-1].any()
+    assert (out[-1] == 4.0).all()
+    want, _ = oracle.sparse_attention(f64(q[0]), values[0].astype(np.float64), idx[3: 3 + widths[0]], f64(sinks[0, :64]),
+                                      SCALE)
+    np.testing.assert_allclose(f64(out[0]), want, atol=2.0 ** -8 * np.abs(values[0]).max())
+
+
+def test_attention_fails_closed():
+    rng = np.random.default_rng(9)
+    cache, values = make_cache(rng, [300] * 5, 512, "fp8", 32)
+    cache.page_table[1, 4], cache.page_table[2, 4] = cache.num_pages, -1
+    nan = torch.ones(2, 512, device="cuda")
+    nan[:, 500] = float("inf")
+    ds.ds_rows_append(cache, nan, i32([3, 4]), i32([10, 10]))
+    idx = np.stack([np.arange(100)] * 5)
+    idx[0, 7], idx[1, 0], idx[2, 99], idx[4, 10] = 300, 4 * 32 + 1, 5 * 32 - 1, 11
+    rows = [(300, 100, 100 * e, e) for e in range(5)]
+    q = queries(rng, 5, 512)
+    out, bad = torch.full_like(q, 4.0), torch.zeros(5, 64, dtype=torch.int32, device="cuda")
+    ds.ds_rows_sparse_attn_paged(rows, q, torch.zeros(64, device="cuda"), 0, i32(idx).reshape(-1), SCALE, out, cache,
+                                 invalid=bad)
+    assert not out[:4].any() and bad[:4].all() and out[4].any() and not bad[4].any()
+
+
+@pytest.mark.parametrize("dim", [128, 512])
+def test_reads_of_pools_past_32_bits(dim):
+    """A row in the last page of a pool of more than 2^32 bytes reads as the same row in the first page."""
+    rng = np.random.default_rng(dim)
+    page = 256
+    num = (1 << 32) // ds.ds_rows_page_bytes(page, dim, "fp8") + 3
+    cache = ds.PagedCache.empty(num, i32([[0], [num - 1]]), page, dim, "fp8")
+    x = torch.randn(page, dim, device="cuda")
+    at = i32(range(page))
+    for e in range(2):
+        ds.ds_rows_append(cache, x, i32(np.full(page, e)), at)
+    q = queries(rng, 1, dim)
+    both = torch.cat([q, q])
+    if dim == 128:
+        scores = torch.zeros(2, page, device="cuda")
+        ds.ds_rows_indexer_score_paged(row_table([page] * 2), both, torch.ones(2, 64, device="cuda"), cache, scores)
+        assert torch.equal(scores[0], scores[1]) and scores.any()
+    else:
+        out = torch.zeros_like(both)
+        rows = [(page, page, 0, 0), (page, page, page, 1)]
+        idx = i32(np.r_[np.arange(page), np.arange(page)])
+        ds.ds_rows_sparse_attn_paged(rows, both, torch.zeros(64, device="cuda"), 0, idx, SCALE, out, cache)
+        assert torch.equal(out[0], out[1]) and out.any()
