@@ -32,6 +32,7 @@ __all__ = [
     "Rope", "ds_rows_rope", "PagedCache", "ds_rows_page_bytes", "ds_rows_append", "ds_rows_fetch",
     "ds_rows_indexer_score_paged",
     "ds_rows_sparse_attn_paged", "PAGED_WORKSPACE_BYTES",
+    "ds_rows_prefix_attn_workspace_bytes", "prefix_attn_workspace", "ds_rows_prefix_attn", "PREFIX_ROWS_MAX",
     "STATUS_WAIT_TIMEOUT", "STATUS_OVERFLOW", "workspace_status", "ds_rows_selftest_bounded_wait",
     "ROWS_MAX", "INDEX_HEADS", "INDEX_DIM", "TOP_K", "HEADS", "DIM",
 ]
@@ -40,6 +41,7 @@ ROWS_MAX = 8
 INDEX_HEADS = 64
 INDEX_DIM = 128
 TOP_K = 512
+PREFIX_ROWS_MAX = 64
 HEADS = 64
 DIM = 512
 
@@ -549,5 +551,5 @@ def ds_rows_compress_kv(kv_states, score_states, start_pos, kv, score, ape, norm
 
 from . import paged as _paged  # noqa: E402  (uses the names above)
 from .paged import (PAGED_WORKSPACE_BYTES, PagedCache, Rope, ds_rows_append, ds_rows_fetch,  # noqa: E402
-                    ds_rows_indexer_score_paged, ds_rows_page_bytes,
-                    ds_rows_rope, ds_rows_sparse_attn_paged)
+                    ds_rows_indexer_score_paged, ds_rows_page_bytes, ds_rows_prefix_attn,
+                    ds_rows_prefix_attn_workspace_bytes, ds_rows_rope, ds_rows_sparse_attn_paged, prefix_attn_workspace)

@@ -8,6 +8,7 @@
 // and alignment. Everything is checked before anything is enqueued.
 
 #include <cudaTypedefs.h>
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -656,6 +657,48 @@ int check_reach(int rows, const ds_row_t* table, const ds_paged_cache_t* cache) 
     return DS_OK;
 }
 
+// The rows of a shared-prefix attention: kv_len and q_row.
+int check_prefix_rows(int rows, const ds_row_t* table, uint32_t prefix_len) {
+    if (rows < 1 || rows > DS_PREFIX_ROWS_MAX)
+        return fail(DS_EINVAL, "rows must be 1..=%d, got %d", DS_PREFIX_ROWS_MAX, rows);
+    if (!table) return fail(DS_EINVAL, "row table is NULL");
+    for (int e = 0; e < rows; ++e) {
+        const ds_row_t& r = table[e];
+        if (r.kv_len == 0) return fail(DS_EINVAL, "row %d: kv_len must be nonzero", e);
+        if (r.kv_len > 0x7FFFFFFFu)
+            return fail(DS_ESIZE, "row %d: kv_len %u of a paged cache must be below 2^31", e, r.kv_len);
+        if (r.kv_len < prefix_len)
+            return fail(DS_EINVAL, "row %d: kv_len %u is shorter than the prefix of %u", e, r.kv_len, prefix_len);
+        if ((uint64_t)r.q_row * DS_HEADS * DS_DIM > 0xFFFFFFFFFFull)
+            return fail(DS_ESIZE, "row %d: q_row %u is out of range", e, r.q_row);
+        for (int o = 0; o < e; ++o)
+            if (table[o].q_row == r.q_row) return fail(DS_EINVAL, "row %d: q_row %u is used twice", e, r.q_row);
+    }
+    return DS_OK;
+}
+
+// The segments of checked rows: their tiles, and the bytes of the workspace.
+size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t prefix_len, uint32_t most_pairs) {
+    p.rows = (uint32_t)rows;
+    p.groups = (p.rows + 1) / 2;
+    p.prefix_len = prefix_len;
+    uint32_t tiles = 0, segs = 0;
+    auto add = [&](uint32_t slots) {
+        p.tile_begin[segs++] = tiles;
+        tiles += (slots + kPrefixTile - 1) / kPrefixTile;  // at most 96 of 2^24
+    };
+    for (uint32_t g = 0; g < p.groups; ++g) add(prefix_len);
+    for (uint32_t e = 0; e < p.rows; ++e) {
+        p.kv_len[e] = table[e].kv_len;
+        p.q_row[e] = table[e].q_row;
+        add(table[e].kv_len - prefix_len);
+    }
+    p.tile_begin[segs] = tiles;
+    p.total_tiles = tiles;
+    p.pairs = tiles < most_pairs ? tiles : most_pairs;
+    return 256 + align256((size_t)(p.pairs + segs - 1) * 2 * kPrefixPartFloats * 4);
+}
+
 }  // namespace
 
 namespace dsrows {
@@ -1192,6 +1235,47 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
     p.cache = paged_cache(*kv);
     const cudaError_t err = launch_sparse_attn_paged(p, kv->format, (cudaStream_t)stream, true);
     return err == cudaSuccess ? DS_OK : cuda_fail(err, "paged attention launch");
+}
+
+size_t ds_rows_prefix_attn_workspace_bytes(int rows, const ds_row_t* table, uint32_t prefix_len) {
+    if (check_prefix_rows(rows, table, prefix_len)) return 0;
+    PrefixParams p;
+    return lay_out_prefix(p, rows, table, prefix_len, kPrefixPairsMax);
+}
+
+int ds_rows_prefix_attn(int rows, const ds_row_t* table, uint32_t prefix_len, const ds_paged_cache_t* kv,
+                        const ds_bf16* q_attn, const float* sinks, size_t sinks_row_stride, float scale, ds_bf16* out,
+                        uint32_t* invalid, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_prefix_rows(rows, table, prefix_len);
+    if (rc) return rc;
+    rc = check_cache(kv, DS_DIM, rows);
+    if (rc) return rc;
+    rc = check_reach(rows, table, kv);
+    if (rc) return rc;
+    rc = check_attn_args(q_attn, sinks, sinks_row_stride, scale, out);
+    if (rc) return rc;
+    if (!aligned4(sinks) || !aligned4(invalid)) return fail(DS_EALIGN, "sinks and invalid must be 4-B aligned");
+    PrefixParams p;
+    Layout L;
+    L.total = lay_out_prefix(p, rows, table, prefix_len, kPrefixPairsMax);
+    rc = check_workspace(nullptr, workspace, workspace_bytes, L);
+    if (rc) return rc;
+    const int sms = num_sms();
+    if (sms <= 0) return fail(DS_ECUDA, "no CUDA device");
+    (void)lay_out_prefix(p, rows, table, prefix_len,
+                         std::min(kPrefixPairsMax, std::max((uint32_t)sms / 2, 1u)));
+    p.cache = paged_cache(*kv);
+    p.q = reinterpret_cast<const __nv_bfloat16*>(q_attn);
+    p.sinks = sinks;
+    p.sinks_row_stride = sinks_row_stride;
+    p.out = reinterpret_cast<__nv_bfloat16*>(out);
+    p.invalid = invalid;
+    p.status = static_cast<uint32_t*>(workspace);
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    StageRange range("dsrows.prefix_attention");
+    const cudaError_t err = launch_prefix_attn(p, kv->format, (cudaStream_t)stream, true);
+    return err == cudaSuccess ? DS_OK : cuda_fail(err, "prefix attention launch");
 }
 
 int ds_rows_compress_kv(int rows, const ds_compressor_row_t* table, const float* kv, const float* score,

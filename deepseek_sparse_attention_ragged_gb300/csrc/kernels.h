@@ -208,6 +208,38 @@ struct PagedTailParams : TailParams {
     PagedCache cache;
 };
 
+// Attention over every cached row of rows that share a prefix. Segments: the prefix for rows 2 g and
+// 2 g + 1 (g < groups), then each row's own rows. A pair of CTAs takes an equal run of the
+// segments' tiles; its state at the end of each segment it had part of is a part, kept for
+// both CTAs at index pair + segment (which no two parts share).
+constexpr uint32_t kPrefixRowsMax = DS_PREFIX_ROWS_MAX;
+constexpr uint32_t kPrefixSegsMax = kPrefixRowsMax / 2 + kPrefixRowsMax;
+constexpr uint32_t kPrefixPairsMax = 76;  // of this GPU's 152 multiprocessors
+constexpr uint32_t kPrefixTile = 128;
+// m, sum and flag of each TMEM lane (head, half), then O [64 column groups][128 lanes][4].
+constexpr size_t kPrefixPartFloats = 3 * 128 + (size_t)DS_HEADS * DS_DIM;
+
+struct PrefixParams {
+    PagedCache cache;
+    const __nv_bfloat16* q;  // [Q, 64, 512]
+    const float* sinks;
+    uint64_t sinks_row_stride;
+    __nv_bfloat16* out;      // [Q, 64, 512]
+    uint32_t* invalid;       // optional [Q, 64]
+    float* parts;
+    uint32_t* status;
+    float scale_log2;        // scale / ln 2
+    uint32_t rows;
+    uint32_t groups;
+    uint32_t prefix_len;
+    uint32_t pairs;
+    uint32_t total_tiles;
+    uint32_t kv_len[kPrefixRowsMax];
+    uint32_t q_row[kPrefixRowsMax];
+    uint32_t tile_begin[kPrefixSegsMax + 1];
+};
+
+cudaError_t launch_prefix_attn(const PrefixParams& p, int format, cudaStream_t stream, bool pdl);
 cudaError_t launch_rope(RopeCall p, int dtype, int layout, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_append(const AppendCall& p, int dtype, uint32_t dim, int format, cudaStream_t stream, bool pdl);
 cudaError_t launch_fetch(const FetchCall& p, int dtype, uint32_t dim, int format, cudaStream_t stream, bool pdl);

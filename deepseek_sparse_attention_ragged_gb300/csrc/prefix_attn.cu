@@ -1,0 +1,776 @@
+// Sink-softmax attention over every cached row, for rows that share a prefix: per row r and head h,
+// over the slots j < kv_len[r] (the first prefix_len of them the same rows for every r),
+//   l_j = scale * q_h . g_j,  m = max(sink_h, max l_j),
+//   out_h = sum_j exp(l_j - m) g_j / (exp(sink_h - m) + sum_j exp(l_j - m)),
+// with g_j the 512-wide cache row (keys and values are the same).
+//
+// The work is a list of segments: the prefix once for every two rows of the batch, then what each
+// row has behind it. A segment is a run of tiles of 128 slots, and the tiles of all segments are
+// dealt out to pairs of CTAs (2-CTA clusters on neighbouring SMs) in equal runs. A pair's run within one
+// segment is a part: it carries the running maximum and sum of the softmax and the accumulated output
+// through its tiles, and leaves them in the workspace. A second kernel joins each row's
+// parts, in their order, with the sink.
+//
+// A pair works on 2 x 64 query vectors (CTA c holds the 64 heads of the segment's row c) with
+// cta_group::2 MMAs of M = 128:
+//   S[128 heads x 128 slots] = Q . G^T      (K = 512; CTA c brings slots 64 c .. 64 c + 63)
+//   O[128 heads x 512 dims] += P . G        (K = 128 slots; CTA c brings dims 256 j + 128 c .. + 127)
+// O of 64 heads takes 256 TMEM columns in this layout, which leaves room for two S; with one CTA and
+// M = 128 it would fill TMEM alone. Each CTA keeps its own softmax: its 64 heads see every slot of the tile,
+// so nothing but the operands crosses the pair.
+//
+// Warp roles: 0 looks up the tiles' rows, 1 issues the MMAs (in the pair's first CTA), 4 to 7
+// do the softmax (a thread has 64 slots of one head), 8 to 15 bring the operands. The K form (64 slots
+// x 128 dims) and the V form (32 slots x 256 dims) of the rows go through one ring of 16 KB units in
+// the order in which the MMAs take them: S of the next tile comes before P . G of this one.
+// Rows past a segment's end and rows without a page are zeros with probability 0.
+
+#include "common.cuh"
+#include "fp8.cuh"
+#include "int4.cuh"
+#include "kernels.h"
+
+namespace dsrows {
+
+namespace {
+
+constexpr int kTile = kPrefixTile;            // slots of a tile
+constexpr int kUnitBytes = 16384;             // a ring unit: [64 slots][128 dims] or [32 slots][256 dims]
+constexpr int kUnits = 8;                     // of the ring
+constexpr int kQBytes = kHeads * kDim * 2;    // the CTA's query row, 8 blocks [64 heads][64 dims]
+constexpr int kPBytes = kHeads * kTile * 2;   // P: 2 blocks [64 heads][64 slots]
+constexpr int kPlaceBufs = 4;                 // tiles whose rows are looked up
+constexpr int kThreads = 512;
+constexpr int kSoftmaxWarp = 4, kBuildWarp = 8, kBuildWarps = 8;
+constexpr int kBuildThreads = 32 * kBuildWarps;
+constexpr uint32_t kOCol = 128;               // TMEM: two S of 64 columns, then O
+constexpr uint32_t kTmemCols = 512;
+constexpr uint16_t kBoth = 3;                 // the CTAs of a pair
+// The running maximum is raised only when a tile's exceeds it by more than this (in units of ln 2): the
+// accumulated output is then scaled, and the weights stay below 2^8.
+constexpr float kSlack = 8.0f;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kNoRow = -1, kBadRow = -2;
+
+struct Layout {
+    static constexpr size_t ring = 0;
+    static constexpr size_t q = ring + (size_t)kUnits * kUnitBytes;
+    static constexpr size_t p = q + kQBytes;
+    static constexpr size_t place = p + kPBytes;                         // i32 [kPlaceBufs][128]
+    static constexpr size_t red = place + kPlaceBufs * kTile * 4;        // f32 [2][128]
+    static constexpr size_t bars = red + 2 * 128 * 4;
+};
+
+struct __align__(8) Bars {
+    // In the pair's first CTA, from both:
+    uint64_t full[kUnits];
+    uint64_t q_full, p_full, s_free[2];
+    // In each CTA:
+    uint64_t empty[kUnits];
+    uint64_t q_free, s_full[2], pv_done, drained;
+    uint64_t place_full[kPlaceBufs], place_free[kPlaceBufs];
+    uint32_t partial[kPlaceBufs];  // some slot of the tile has no row
+    uint32_t tmem_base;
+};
+
+constexpr size_t kSmem = Layout::bars + sizeof(Bars) + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+// ---- the pair's tcgen05 forms and barriers ---------------------------------------------------
+
+__device__ __forceinline__ void umma2_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on `bar` of both CTAs when the MMAs issued so far complete.
+__device__ __forceinline__ void umma2_commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(kBoth)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_first_cta(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(smem_u32(bar), 0))
+                 : "memory");
+}
+// A bounded wait of a whole warp (its lanes go on or give up together), whose first tries read no timer.
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, uint32_t* status) {
+    bool ok = false;
+    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait_cluster(bar, parity);
+    if (!ok) ok = mbar_wait_cluster(bar, parity, status);
+    return __all_sync(0xFFFFFFFFu, ok);
+}
+
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void cp_async_wait_group() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
+// Byte offset of 16-byte chunk `ch` of row `row` in a 128-byte-swizzled block of 128-byte rows.
+__device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t ch) { return row * 128 + ((ch ^ (row & 7)) << 4); }
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+    return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+    return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+          "l"(*reinterpret_cast<const uint64_t*>(&c)));
+    return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&v)[4]) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// ---- the operands ------------------------------------------------------------------------------
+
+// kDims dims of the rows at places at[0 ..] into a ring unit, by the builder's thread tid: 64 rows for 128
+// dims, 32 for 256. dim_of(d) is the row's dim that dim d of the unit is; dst(row, ch) the shared
+// address of dims 8 ch .. 8 ch + 7. A place below 0 brings zeros.
+template <int kFormat, int kDims, class DimOf, class Dst>
+__device__ __forceinline__ void bring(const PagedCache& cache, const int32_t* at, uint32_t tid, DimOf dim_of, Dst dst) {
+    constexpr uint32_t kRows = kUnitBytes / 2 / kDims;
+    if constexpr (kFormat == DS_CACHE_BF16) {
+        constexpr uint32_t kChunks = kDims / 8;
+#pragma unroll
+        for (uint32_t i = 0; i < kRows * kChunks / kBuildThreads; ++i) {
+            const uint32_t k = tid + i * kBuildThreads, row = k / kChunks, ch = k % kChunks;
+            const int32_t place = at[row];
+            const uint8_t* src = cache.pages + (size_t)max(place, 0) * (2 * kDim) + 2 * dim_of(8 * ch);
+            cp_async16_or_zero(dst(row, ch), src, place >= 0);
+        }
+    } else {
+        // A warp has eight rows and four neighbouring pieces of 16 bytes of each: whole sectors are read, and
+        // eight lanes store into eight rows, which the swizzle puts into different banks.
+        constexpr uint32_t kPiece = kFormat == DS_CACHE_FP8 ? 16 : 32;  // values of 16 bytes
+        constexpr uint32_t kN = kRows * kDims / kPiece / kBuildThreads;
+        const uint32_t warp = tid >> 5, lane = tid & 31;
+        const uint32_t row = 8 * (warp % (kRows / 8)) + (lane & 7);
+        const uint32_t first = 4 * kN * (warp / (kRows / 8)) + (lane >> 3);
+        const int32_t place = at[row];
+        uint4 d[kN];
+        uint32_t sc[kN];
+#pragma unroll
+        for (uint32_t n = 0; n < kN; ++n) {
+            const uint32_t dim = dim_of((first + 4 * n) * kPiece);
+            if constexpr (kFormat == DS_CACHE_FP8) {
+                const uint32_t shift = cache.page_shift, where = (uint32_t)max(place, 0), in_page = where & ((1u << shift) - 1);
+                const uint8_t* page = cache.pages + (size_t)(where - in_page) * (kDim + kDim / fp8::kBlock);
+                d[n] = make_uint4(0, 0, 0, 0);
+                sc[n] = 127;
+                if (place >= 0) {
+                    d[n] = __ldcg(reinterpret_cast<const uint4*>(page + (size_t)in_page * kDim + dim));
+                    sc[n] = __ldcg(page + ((size_t)kDim << shift) + in_page * (kDim / fp8::kBlock) + dim / fp8::kBlock);
+                }
+            } else {
+                const uint8_t* src = cache.pages + (size_t)max(place, 0) * (kDim / 2 + kDim / int4::kGroup);
+                d[n] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                sc[n] = 0;
+                if (place >= 0) {
+                    d[n] = __ldcg(reinterpret_cast<const uint4*>(src + dim / 2));
+                    sc[n] = __ldcg(reinterpret_cast<const uint16_t*>(src + kDim / 2 + dim / int4::kGroup));
+                }
+            }
+        }
+#pragma unroll
+        for (uint32_t n = 0; n < kN; ++n) {
+            const uint32_t words[4] = {d[n].x, d[n].y, d[n].z, d[n].w};
+            const uint32_t ch = (first + 4 * n) * (kPiece / 8);
+            if constexpr (kFormat == DS_CACHE_FP8) {
+                const uint32_t f = fp8::factor(sc[n]);
+#pragma unroll
+                for (uint32_t c = 0; c < 2; ++c) {
+                    uint32_t o[4];
+                    fp8::widen(words[2 * c], f, o);
+                    fp8::widen(words[2 * c + 1], f, o + 2);
+                    st_shared_v4(dst(row, ch + c), o);
+                }
+            } else {
+                int4::Factors f[2];
+                int4::factors2<0>(sc[n], f[0], f[1]);
+#pragma unroll
+                for (uint32_t c = 0; c < 4; ++c) {
+                    uint32_t o[4];
+                    int4::widen(words[c], f[c >> 1], o);
+                    st_shared_v4(dst(row, ch + c), o);
+                }
+            }
+        }
+    }
+}
+
+// ---- the pair's tiles --------------------------------------------------------------------------
+
+// A run of a pair's tiles within one segment.
+struct Part {
+    uint32_t seg;
+    uint32_t start;   // its first tile's first slot
+    uint32_t end;     // the segment's last slot + 1
+    uint32_t tiles;
+};
+
+// The parts of pair k in order: for (Walk w(p, k); w.next(part);)
+struct Walk {
+    const PrefixParams& p;
+    uint32_t t, end, seg;
+    __device__ __forceinline__ Walk(const PrefixParams& params, uint32_t pair, uint32_t pairs) : p(params) {
+        t = (uint32_t)((uint64_t)p.total_tiles * pair / pairs);
+        end = (uint32_t)((uint64_t)p.total_tiles * (pair + 1) / pairs);
+        seg = 0;
+    }
+    __device__ __forceinline__ bool next(Part& part) {
+        if (t >= end) return false;
+        while (p.tile_begin[seg + 1] <= t) ++seg;  // t is below the last bound
+        const uint32_t stop = min(end, p.tile_begin[seg + 1]);
+        const bool shared = seg < p.groups;
+        part.seg = seg;
+        part.start = (shared ? 0u : p.prefix_len) + (t - p.tile_begin[seg]) * kTile;
+        part.end = shared ? p.prefix_len : p.kv_len[seg - p.groups];
+        part.tiles = stop - t;
+        t = stop;
+        return true;
+    }
+};
+
+}  // namespace
+
+template <int kFormat>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    prefix_attn_kernel(const __grid_constant__ PrefixParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    Bars* bar = reinterpret_cast<Bars*>(smem + Layout::bars);
+    int32_t* place_s = reinterpret_cast<int32_t*>(smem + Layout::place);
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const uint32_t ring = smem_u32(smem + Layout::ring);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kUnits; ++i) {
+            mbar_init(&bar->full[i], 2 * kBuildWarps);
+            mbar_init(&bar->empty[i], 1);
+        }
+        mbar_init(&bar->q_full, 2 * kBuildWarps);
+        mbar_init(&bar->p_full, 8);
+        mbar_init(&bar->q_free, 1);
+        mbar_init(&bar->pv_done, 1);
+        mbar_init(&bar->drained, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar->s_free[i], 8);
+            mbar_init(&bar->s_full[i], 1);
+        }
+        for (int i = 0; i < kPlaceBufs; ++i) {
+            mbar_init(&bar->place_full[i], 1);
+            mbar_init(&bar->place_free[i], kBuildWarps + 4);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar->tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive_release();  // both CTAs' barriers are set before either arrives on the other's
+    cluster_wait_acquire();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem_base, 0);
+    pdl_wait();
+    pdl_trigger();
+    // The first block starts first; a wait that gives up reports seconds later.
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+
+    Part part;
+    uint32_t it = 0;  // the pair's tiles so far
+    if (warp == 0) {
+        // ---- the tiles' rows: places in the pool ----------------------------------------------
+        bool ok = true;
+        for (Walk w(p, pair, pairs); ok && w.next(part);) {
+            const uint32_t entry = part.seg < p.groups ? 0 : part.seg - p.groups;
+            const int32_t* table = p.cache.table + (size_t)entry * p.cache.table_stride;
+            const uint32_t shift = p.cache.page_shift;
+            for (uint32_t i = 0; i < part.tiles; ++i, ++it) {
+                const uint32_t buf = it % kPlaceBufs;
+                int32_t id[4], at[4];
+                bool all = true;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t j = part.start + i * kTile + lane + 32 * k;
+                    id[k] = j < part.end ? table[j >> shift] : -1;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t j = part.start + i * kTile + lane + 32 * k;
+                    if (j >= part.end) at[k] = kNoRow;
+                    else if (id[k] < 0 || (uint32_t)id[k] >= p.cache.num_pages) at[k] = kBadRow;
+                    else at[k] = (int32_t)(((uint32_t)id[k] << shift) + (j & ((1u << shift) - 1)));
+                    all = all && at[k] >= 0;
+                }
+                all = __all_sync(0xFFFFFFFFu, all);
+                if (!wait_pair(&bar->place_free[buf], (it / kPlaceBufs & 1) ^ 1, p.status)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) place_s[buf * kTile + lane + 32 * k] = at[k];
+                if (lane == 0) bar->partial[buf] = all ? 0u : 1u;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->place_full[buf]);
+            }
+        }
+    } else if (warp == 1) {
+        // ---- the MMAs, issued in the first CTA for both -----------------------------------------
+        if (rank == 0) {
+            constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(128, 256) | 1u << 16;  // B is MN-major
+            const uint32_t q_base = smem_u32(smem + Layout::q), p_base = smem_u32(smem + Layout::p);
+            uint32_t unit = 0, phase = 0;
+            bool ok = true;
+            auto next_unit = [&] {
+                if (++unit == kUnits) unit = 0, phase ^= 1;
+            };
+            // O += P G of tile `of`; `fresh`: the part's first tile.
+            auto accumulate = [&](uint32_t of, bool fresh) -> bool {
+                if (!wait_pair(&bar->p_full, of & 1, p.status)) return false;
+                tc_fence_after();
+#pragma unroll 1
+                for (uint32_t v = 0; v < 4; ++v) {
+                    if (!wait_pair(&bar->full[unit], phase, p.status)) return false;
+                    const uint32_t b = ring + unit * kUnitBytes;
+                    if (elect_one()) {
+#pragma unroll
+                        for (uint32_t ks = 0; ks < 2; ++ks)
+#pragma unroll
+                            for (uint32_t j = 0; j < 2; ++j)
+                                umma2_bf16(tmem + kOCol + 128 * j,
+                                           smem_desc_sw128_kmajor(p_base + (v >> 1) * 8192 + ((v & 1) * 2 + ks) * 32),
+                                           smem_desc_sw128_mnmajor(b + j * 8192 + ks * 2048, 4096, 1024), idesc_o,
+                                           fresh && v == 0 && ks == 0 ? 0u : 1u);
+                        umma2_commit(&bar->empty[unit]);
+                        if (v == 3) umma2_commit(&bar->pv_done);
+                    }
+                    __syncwarp();
+                    next_unit();
+                }
+                return true;
+            };
+            uint32_t n_part = 0;
+            bool fresh = true;  // of the tile whose P G is due
+            for (Walk w(p, pair, pairs); ok && w.next(part); ++n_part) {
+                for (uint32_t i = 0; ok && i < part.tiles; ++i, ++it) {
+                    const uint32_t buf = it & 1;
+                    ok = i != 0 || wait_pair(&bar->q_full, n_part & 1, p.status);
+                    ok = ok && wait_pair(&bar->s_free[buf], (it >> 1 & 1) ^ 1, p.status);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (uint32_t u = 0; ok && u < 4; ++u) {
+                        ok = wait_pair(&bar->full[unit], phase, p.status);
+                        if (!ok) break;
+                        const uint32_t b = ring + unit * kUnitBytes, a = q_base + u * kUnitBytes;
+                        if (elect_one()) {
+#pragma unroll
+                            for (uint32_t ks = 0; ks < 8; ++ks)
+                                umma2_bf16(tmem + buf * 64, smem_desc_sw128_kmajor(a + (ks >> 2) * 8192 + (ks & 3) * 32),
+                                           smem_desc_sw128_kmajor(b + (ks >> 2) * 8192 + (ks & 3) * 32), idesc_s,
+                                           u == 0 && ks == 0 ? 0u : 1u);
+                            umma2_commit(&bar->empty[unit]);
+                            if (u == 3) {
+                                umma2_commit(&bar->s_full[buf]);
+                                if (i + 1 == part.tiles) umma2_commit(&bar->q_free);
+                            }
+                        }
+                        __syncwarp();
+                        next_unit();
+                    }
+                    if (ok && it > 0) ok = accumulate(it - 1, fresh);
+                    fresh = i == 0;
+                }
+            }
+            if (ok && it > 0) ok = accumulate(it - 1, fresh);
+            // Whatever was issued is done before the CTAs leave.
+            if (elect_one()) umma2_commit(&bar->drained);
+            __syncwarp();
+            (void)wait_pair(&bar->drained, 0, p.status);
+        }
+    } else if (warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4) {
+        // ---- softmax: thread = TMEM lane = (head, half of the tile's slots) ---------------------
+        const uint32_t row = threadIdx.x - 32 * kSoftmaxWarp;  // 0 .. 127
+        const uint32_t head = row & 63, half = row >> 6;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp - kSoftmaxWarp)) << 16);
+        float* red = reinterpret_cast<float*>(smem + Layout::red);
+        uint8_t* p_row = smem + Layout::p + half * 8192;
+        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+        uint32_t met = 0;  // the four warps meet once a tile
+        bool ok = true;
+        for (Walk w(p, pair, pairs); ok && w.next(part);) {
+            float m = 0.0f, sum = 0.0f;
+            uint32_t bad = 0;
+            for (uint32_t i = 0; i < part.tiles; ++i, ++it) {
+                const uint32_t buf = it & 1, pbuf = it % kPlaceBufs;
+                uint32_t lo[32], hi[32];
+                if (!(ok = wait_pair(&bar->s_full[buf], it >> 1 & 1, p.status))) break;
+                tc_fence_after();
+                tmem_ld_x32(lanes + buf * 64, lo);
+                tmem_ld_x32(lanes + buf * 64 + 32, hi);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_first_cta(&bar->s_free[buf]);
+                // 0 * t is NaN exactly where a logit is not finite.
+                float2 t[32], odd = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const uint32_t x = c < 16 ? lo[2 * c] : hi[2 * c - 32], y = c < 16 ? lo[2 * c + 1] : hi[2 * c - 31];
+                    t[c] = mul2(make_float2(__uint_as_float(x), __uint_as_float(y)), scale2);
+                    odd = fma2(t[c], make_float2(0.0f, 0.0f), odd);
+                }
+                if (!(odd.x + odd.y == 0.0f)) bad = 1;
+                if (!(ok = wait_pair(&bar->place_full[pbuf], it / kPlaceBufs & 1, p.status))) break;
+                if (bar->partial[pbuf]) {
+                    const ::int4* at = reinterpret_cast<const ::int4*>(place_s + pbuf * kTile + half * 64);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const ::int4 a = at[c];
+                        if (a.x == kBadRow || a.y == kBadRow || a.z == kBadRow || a.w == kBadRow) bad = 1;
+                        if (a.x < 0) t[2 * c].x = -INFINITY;
+                        if (a.y < 0) t[2 * c].y = -INFINITY;
+                        if (a.z < 0) t[2 * c + 1].x = -INFINITY;
+                        if (a.w < 0) t[2 * c + 1].y = -INFINITY;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->place_free[pbuf]);
+                float top = fmaxf(t[0].x, t[0].y);
+#pragma unroll
+                for (int c = 1; c < 32; ++c) top = fmaxf(top, fmaxf(t[c].x, t[c].y));
+                red[buf * 128 + row] = top;
+                sync_softmax();
+                ++met;
+                top = fmaxf(top, red[buf * 128 + (row ^ 64)]);
+                // The head's two threads decide alike.
+                float f = 1.0f;
+                if (i == 0) {
+                    m = finite_f(top) ? top : 0.0f;
+                } else if (top > m + kSlack && finite_f(top)) {
+                    f = exp2_fast(m - top);
+                    m = top;
+                    sum *= f;
+                }
+                const bool moved = __any_sync(0xFFFFFFFFu, f != 1.0f);
+                const float2 minus = make_float2(-m, -m);
+                float2 s2 = make_float2(0.0f, 0.0f);
+                uint32_t w16[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float2 x = add2(t[c], minus);
+                    const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                    s2 = add2(s2, e);
+                    w16[c] = pack_bf16(e.x, e.y);
+                }
+                sum += s2.x + s2.y;
+                // P G of the tile before is done: P may be overwritten, and O scaled.
+                if (it > 0 && !(ok = wait_pair(&bar->pv_done, (it - 1) & 1, p.status))) break;
+                tc_fence_after();
+                if (moved) {
+#pragma unroll 1
+                    for (uint32_t c = 0; c < 256; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld_x32(lanes + kOCol + c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st_x32(lanes + kOCol + c, o);
+                    }
+                    tmem_st_wait();
+                }
+#pragma unroll
+                for (uint32_t c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(p_row + swizzled(head, c)) =
+                        make_uint4(w16[4 * c], w16[4 * c + 1], w16[4 * c + 2], w16[4 * c + 3]);
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_first_cta(&bar->p_full);
+            }
+            // ---- the part's state: m, sum, flag and O per lane ----------------------------------
+            if (!ok || !(ok = wait_pair(&bar->pv_done, (it - 1) & 1, p.status))) break;
+            tc_fence_after();
+            float* out = p.parts + ((size_t)(pair + part.seg) * 2 + rank) * kPrefixPartFloats;
+            const uint32_t r = part.seg < p.groups ? 2 * part.seg + rank : rank == 0 ? part.seg - p.groups : p.rows;
+            const bool mine = r < p.rows;  // the pair's second CTA may have no row
+            if (mine) {
+                out[row] = m;
+                out[128 + row] = sum;
+                reinterpret_cast<uint32_t*>(out)[256 + row] = bad;
+            }
+#pragma unroll 1
+            for (uint32_t c = 0; c < 256; c += 32) {
+                uint32_t o[32];
+                tmem_ld_x32(lanes + kOCol + c, o);
+                tmem_ld_wait();
+                float4* to = reinterpret_cast<float4*>(out + 3 * 128) + (c / 4) * 128 + row;
+                if (mine)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        to[k * 128] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                  __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+            }
+            tc_fence_before();
+        }
+        // A warp that gave up still meets the others.
+        const Walk whole(p, pair, pairs);
+        for (const uint32_t all = whole.end - whole.t; met < all; ++met) sync_softmax();
+    } else if (warp >= kBuildWarp) {
+        // ---- operands: the query of each part, then its tiles' units ------------------------------
+        const uint32_t tid = threadIdx.x - 32 * kBuildWarp;
+        uint32_t unit = 0, phase = 0, n_part = 0;
+        uint32_t told = 0, brought = 0;  // units whose arrival was signalled, units issued
+        bool ok = true;
+        constexpr uint32_t kLag = 4;     // units in flight (bf16)
+        auto tell = [&](uint32_t until) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            for (; told < until; ++told)
+                if (lane == 0) arrive_first_cta(&bar->full[told % kUnits]);
+        };
+        // One unit is issued; with bf16 the one kLag before it has landed.
+        auto advance = [&] {
+            ++brought;
+            if (kFormat == DS_CACHE_BF16) {
+                cp_async_commit_group();
+                if (brought > kLag) {
+                    cp_async_wait_group<kLag>();
+                    tell(brought - kLag);
+                }
+            } else {
+                tell(brought);
+            }
+            if (++unit == kUnits) unit = 0, phase ^= 1;
+        };
+        auto k_units = [&](uint32_t of) -> bool {
+            const int32_t* at = place_s + of % kPlaceBufs * kTile + 64 * rank;
+#pragma unroll 1
+            for (uint32_t u = 0; u < 4; ++u) {
+                if (!wait_pair(&bar->empty[unit], phase ^ 1, p.status)) return false;
+                const uint32_t dst = ring + unit * kUnitBytes;
+                bring<kFormat, 128>(p.cache, at, tid, [&](uint32_t d) { return 128 * u + d; },
+                                    [&](uint32_t row, uint32_t ch) { return dst + (ch >> 3) * 8192 + swizzled(row, ch & 7); });
+                advance();
+            }
+            return true;
+        };
+        auto v_units = [&](uint32_t of) -> bool {
+#pragma unroll 1
+            for (uint32_t v = 0; v < 4; ++v) {
+                if (!wait_pair(&bar->empty[unit], phase ^ 1, p.status)) return false;
+                const uint32_t dst = ring + unit * kUnitBytes;
+                const int32_t* at = place_s + of % kPlaceBufs * kTile + 32 * v;
+                bring<kFormat, 256>(p.cache, at, tid,
+                                    [&](uint32_t d) { return 256 * (d >> 7) + 128 * rank + (d & 127); },
+                                    [&](uint32_t row, uint32_t ch) { return dst + (ch >> 3) * 4096 + swizzled(row, ch & 7); });
+                advance();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->place_free[of % kPlaceBufs]);
+            return true;
+        };
+        for (Walk w(p, pair, pairs); ok && w.next(part); ++n_part) {
+            // The query, once the MMAs of the part before have read theirs (they need every unit so far).
+            if (kFormat == DS_CACHE_BF16) cp_async_wait_group<0>();
+            tell(brought);
+            if (n_part > 0 && !(ok = wait_pair(&bar->q_free, (n_part - 1) & 1, p.status))) break;
+            const uint32_t r = part.seg < p.groups ? min(2 * part.seg + rank, p.rows - 1) : part.seg - p.groups;
+            const uint4* q = reinterpret_cast<const uint4*>(p.q + (size_t)p.q_row[r] * kHeads * kDim);
+            uint8_t* q_s = smem + Layout::q;
+#pragma unroll 4
+            for (uint32_t k = tid; k < kQBytes / 16; k += kBuildThreads)
+                *reinterpret_cast<uint4*>(q_s + ((k & 63) >> 3) * 8192 + swizzled(k >> 6, k & 7)) = q[k];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_first_cta(&bar->q_full);
+            for (uint32_t i = 0; ok && i < part.tiles; ++i, ++it) {
+                ok = wait_pair(&bar->place_full[it % kPlaceBufs], it / kPlaceBufs & 1, p.status);
+                ok = ok && k_units(it) && (it == 0 || v_units(it - 1));
+            }
+        }
+        if (ok && it > 0) ok = v_units(it - 1);
+        if (kFormat == DS_CACHE_BF16) cp_async_wait_group<0>();
+        if (ok) tell(brought);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive_release();  // neither CTA leaves while the other's MMAs or arrivals may reach it
+    cluster_wait_acquire();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// ---- the join of a row's parts -------------------------------------------------------------------
+
+namespace {
+constexpr int kJoinSlices = 4;  // threads of an output lane, each with every fourth part
+}
+
+// A block joins 4 columns of the O layout (4 dims of each half of 64 heads) of one row: thread = (lane, slice).
+__global__ void __launch_bounds__(128 * kJoinSlices) prefix_join_kernel(const __grid_constant__ PrefixParams p) {
+    __shared__ float4 acc_s[kJoinSlices - 1][128];
+    __shared__ float m_s[kJoinSlices][128], l_s[kJoinSlices][128];
+    __shared__ uint32_t bad_s[kJoinSlices][128];
+    pdl_trigger();
+    const uint32_t r = blockIdx.x, col = blockIdx.y, lane = threadIdx.x & 127, slice = threadIdx.x >> 7;
+    const uint32_t head = lane & 63;
+    pdl_wait();
+    // The row's parts: those of its group's prefix, then its own.
+    struct Run {
+        uint32_t first, count, seg, cta;
+    } runs[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t seg = i == 0 ? r / 2 : p.groups + r;
+        const uint32_t begin = p.tile_begin[seg], end = p.tile_begin[seg + 1];
+        auto pair_of = [&](uint32_t t) {
+            return (uint32_t)(((uint64_t)(t + 1) * p.pairs - 1) / p.total_tiles);
+        };
+        runs[i] = {0, 0, seg, i == 0 ? r & 1 : 0u};
+        if (begin < end) {
+            runs[i].first = pair_of(begin);
+            runs[i].count = pair_of(end - 1) - runs[i].first + 1;
+        }
+    }
+    const uint32_t count = runs[0].count + runs[1].count;
+    auto part_at = [&](uint32_t i) {
+        const Run run = i < runs[0].count ? runs[0] : runs[1];
+        const uint32_t k = run.first + (i < runs[0].count ? i : i - runs[0].count);
+        return p.parts + ((size_t)(k + run.seg) * 2 + run.cta) * kPrefixPartFloats;
+    };
+    float m = -INFINITY;
+    uint32_t bad = 0;
+    for (uint32_t i = slice; i < count; i += kJoinSlices) {
+        const float* part = part_at(i);
+        m = fmaxf(m, __ldcg(part + lane));
+        const uint32_t* flags = reinterpret_cast<const uint32_t*>(part) + 256;
+        bad |= __ldcg(flags + head) | __ldcg(flags + 64 + head);
+    }
+    m_s[slice][lane] = m;
+    bad_s[slice][lane] = bad;
+    __syncthreads();
+    const float sink = p.sinks[(size_t)p.q_row[r] * p.sinks_row_stride + head];
+    float top = sink * kLog2e;
+    bad = *p.status != 0 ? 1u : 0u;
+#pragma unroll
+    for (int s = 0; s < kJoinSlices; ++s) {
+        top = fmaxf(top, m_s[s][lane]);
+        bad |= bad_s[s][lane];
+    }
+    float l = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (uint32_t i = slice; i < count; i += kJoinSlices) {
+        const float* part = part_at(i);
+        const float f = exp2f(__ldcg(part + lane) - top);
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(part + 3 * 128) + col * 128 + lane);
+        l = fmaf(__ldcg(part + 128 + head) + __ldcg(part + 192 + head), f, l);
+        acc.x = fmaf(o.x, f, acc.x);
+        acc.y = fmaf(o.y, f, acc.y);
+        acc.z = fmaf(o.z, f, acc.z);
+        acc.w = fmaf(o.w, f, acc.w);
+    }
+    l_s[slice][lane] = l;
+    if (slice > 0) acc_s[slice - 1][lane] = acc;
+    __syncthreads();
+    if (slice > 0) return;
+    float den = exp2f(sink * kLog2e - top);
+#pragma unroll
+    for (int s = 0; s < kJoinSlices; ++s) den += l_s[s][lane];
+#pragma unroll
+    for (int s = 0; s < kJoinSlices - 1; ++s) {
+        const float4 o = acc_s[s][lane];
+        acc.x += o.x;
+        acc.y += o.y;
+        acc.z += o.z;
+        acc.w += o.w;
+    }
+    const bool zero = bad || !finite_f(sink) || !finite_f(top) || !finite_f(den) || !(den > 0.0f);
+    const float inv = 1.0f / den;
+    const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    __align__(8) __nv_bfloat16 y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = __float2bfloat16_rn(!zero && finite_f(x[k]) ? x[k] : 0.0f);
+    const uint32_t dim = 256 * (col >> 5) + 128 * (lane >> 6) + 4 * (col & 31);
+    const size_t at = (size_t)p.q_row[r] * kHeads + head;
+    *reinterpret_cast<uint2*>(p.out + at * kDim + dim) = *reinterpret_cast<const uint2*>(y);
+    if (p.invalid && col == 0 && lane < 64) p.invalid[at] = zero ? 1u : 0u;
+}
+
+template <int kFormat>
+static cudaError_t launch(const PrefixParams& p, cudaStream_t stream, bool pdl) {
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t err = set_smem_limit_once(prefix_attn_kernel<kFormat>, kSmem, smem_set);
+    if (err != cudaSuccess) return err;
+    err = launch_kernel(prefix_attn_kernel<kFormat>, dim3(2 * p.pairs), dim3(kThreads), kSmem, stream, pdl, p);
+    if (err != cudaSuccess) return err;
+    return launch_kernel(prefix_join_kernel, dim3(p.rows, 64), dim3(128 * kJoinSlices), 0, stream, true, p);
+}
+
+cudaError_t launch_prefix_attn(const PrefixParams& p, int format, cudaStream_t stream, bool pdl) {
+    if (format == DS_CACHE_INT4) return launch<DS_CACHE_INT4>(p, stream, pdl);
+    if (format == DS_CACHE_FP8) return launch<DS_CACHE_FP8>(p, stream, pdl);
+    return launch<DS_CACHE_BF16>(p, stream, pdl);
+}
+
+}  // namespace dsrows

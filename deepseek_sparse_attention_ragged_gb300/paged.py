@@ -1,5 +1,6 @@
 """Positions and paged caches: the binding of ``ds_rows_rope``, ``ds_rows_append``,
-``ds_rows_fetch``, ``ds_rows_indexer_score_paged`` and ``ds_rows_sparse_attn_paged``.
+``ds_rows_fetch``, ``ds_rows_indexer_score_paged``, ``ds_rows_sparse_attn_paged`` and
+``ds_rows_prefix_attn``.
 
 A ``Rope`` and a ``PagedCache`` are made once and kept: they hold the tensors that
 the library reads and the C structures that describe them. The calls themselves
@@ -48,8 +49,11 @@ def declare(lib) -> None:
     lib.ds_rows_fetch.argtypes = [cache, vp, vp, vp, u64, i32, u64, vp, vp]
     lib.ds_rows_indexer_score_paged.argtypes = [i32, vp, cache, vp, vp, vp, sz, vp]
     lib.ds_rows_sparse_attn_paged.argtypes = [i32, vp, cache, vp, vp, sz, vp, f32, vp, vp, vp, sz, vp]
+    lib.ds_rows_prefix_attn_workspace_bytes.argtypes = [i32, vp, u32]
+    lib.ds_rows_prefix_attn_workspace_bytes.restype = sz
+    lib.ds_rows_prefix_attn.argtypes = [i32, vp, u32, cache, vp, vp, sz, f32, vp, vp, vp, sz, vp]
     for f in (lib.ds_rows_rope_turns, lib.ds_rows_rope, lib.ds_rows_append, lib.ds_rows_fetch,
-              lib.ds_rows_indexer_score_paged, lib.ds_rows_sparse_attn_paged):
+              lib.ds_rows_indexer_score_paged, lib.ds_rows_sparse_attn_paged, lib.ds_rows_prefix_attn):
         f.restype = i32
 
 
@@ -110,11 +114,11 @@ def _call(index: int, fn, *args) -> None:
         _check(load(), rc)
 
 
-def _status_word_for(device: torch.device, raw_stream: int) -> torch.Tensor:
+def _workspace_for(device: torch.device, raw_stream: int, size: int = PAGED_WORKSPACE_BYTES) -> torch.Tensor:
     """A workspace for one call on the stream `raw_stream`, taken from that stream's
     memory, so that it is not handed out again while the call still runs."""
     with torch.cuda.stream(torch.cuda.ExternalStream(raw_stream, device=device)):
-        return torch.empty(PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+        return torch.empty(size, dtype=torch.uint8, device=device)
 
 
 def _u32(value, name: str) -> int:
@@ -362,7 +366,57 @@ def ds_rows_sparse_attn_paged(rows, q_attn: torch.Tensor, sinks: torch.Tensor, s
     pi = None if invalid is None else _tensor(invalid, "invalid", torch.int32, dev, q_rows * HEADS)
     raw = _stream_of(stream, dev)
     if workspace_t is None:
-        workspace_t = _status_word_for(kv.pages.device, raw)
+        workspace_t = _workspace_for(kv.pages.device, raw)
     pw = _tensor(workspace_t, "workspace", torch.uint8, dev, 0)
     _call(dev, lib.ds_rows_sparse_attn_paged, n, words.buffer_info()[0], kv._ref, pq, ps, sinks_row_stride, px, scale,
+          po, pi, pw, workspace_t.numel(), raw)
+
+
+# ---------------------------------------------------------------------------
+# attention over a shared prefix
+# ---------------------------------------------------------------------------
+
+def ds_rows_prefix_attn_workspace_bytes(rows, prefix_len: int) -> int:
+    """Workspace bytes that ds_rows_prefix_attn needs for these rows."""
+    return _prefix_bytes(_rows(rows)[0], _u32(prefix_len, "prefix_len"))
+
+
+def _prefix_bytes(words, prefix_len: int) -> int:
+    lib = load()
+    n = lib.ds_rows_prefix_attn_workspace_bytes(len(words) // 4, words.buffer_info()[0], prefix_len)
+    if n == 0:
+        _check(lib, -1)
+    return int(n)
+
+
+def prefix_attn_workspace(rows, prefix_len: int, device=None) -> torch.Tensor:
+    """A workspace tensor for ds_rows_prefix_attn (uint8, 256-byte aligned by the caching allocator)."""
+    return torch.empty(ds_rows_prefix_attn_workspace_bytes(rows, prefix_len), dtype=torch.uint8,
+                       device=device if device is not None else "cuda")
+
+
+def ds_rows_prefix_attn(rows, prefix_len: int, q_attn: torch.Tensor, sinks: torch.Tensor, sinks_row_stride: int,
+                        scale: float, out: torch.Tensor, kv: PagedCache, invalid: Optional[torch.Tensor] = None,
+                        workspace_t: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Sink-softmax attention of up to 64 rows over all their cached rows (dim 512): slots below
+    prefix_len are those of entry 0 for every row, the others entry e's own.
+
+    rows: (kv_len, width, index_offset, q_row) as elsewhere; width and index_offset are not
+    looked at. workspace_t (optional): prefix_attn_workspace(rows, prefix_len) or a larger one."""
+    lib = load()
+    dev = kv.device_index
+    words, kv_len, _, _, q_row = _rows(rows)
+    n, q_rows, prefix_len = len(kv_len), max(q_row) + 1, _u32(prefix_len, "prefix_len")
+    if sinks_row_stride < 0:
+        raise ValueError(f"sinks_row_stride must not be negative, got {sinks_row_stride}")
+    pq = _tensor(q_attn, "q_attn", torch.bfloat16, dev, q_rows * HEADS * DIM)
+    po = _tensor(out, "out", torch.bfloat16, dev, q_rows * HEADS * DIM)
+    ps = _tensor(sinks, "sinks", torch.float32, dev,
+                 HEADS if sinks_row_stride == 0 else (q_rows - 1) * sinks_row_stride + HEADS)
+    pi = None if invalid is None else _tensor(invalid, "invalid", torch.int32, dev, q_rows * HEADS)
+    raw = _stream_of(stream, dev)
+    if workspace_t is None:
+        workspace_t = _workspace_for(kv.pages.device, raw, _prefix_bytes(words, prefix_len))
+    pw = _tensor(workspace_t, "workspace", torch.uint8, dev, 0)
+    _call(dev, lib.ds_rows_prefix_attn, n, words.buffer_info()[0], prefix_len, kv._ref, pq, ps, sinks_row_stride, scale,
           po, pi, pw, workspace_t.numel(), raw)

@@ -26,7 +26,7 @@
  *   the optional `invalid` output.
  * - Row `r` of a joint call is bitwise equal to a call with only row `r`: all
  *   tiling, split counts and reduction orders depend on that row's kv_len and
- *   width alone.
+ *   width alone (except ds_rows_prefix_attn, which says what it keeps).
  * - Calls that share a workspace or an output must not overlap in time
  *   (order them on one stream).
  * - A call's kernels are chained with programmatic dependent launch. Its first
@@ -54,6 +54,7 @@ extern "C" {
 #define DS_TOPK 512       /* most selected KV rows per row */
 #define DS_HEADS 64       /* attention heads */
 #define DS_DIM 512        /* shared-KV row width (K and V) */
+#define DS_PREFIX_ROWS_MAX 64 /* rows of a shared-prefix attention call */
 
 /* Status codes. */
 #define DS_OK 0
@@ -571,6 +572,42 @@ int ds_rows_indexer_score_paged(int rows, const ds_row_t* table, const ds_paged_
 int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_cache_t* kv, const ds_bf16* q_attn,
                               const float* sinks, size_t sinks_row_stride, const int32_t* indices, float scale,
                               ds_bf16* out, uint32_t* invalid, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes for ds_rows_prefix_attn; 0 when the arguments are invalid (see
+ * ds_rows_last_error). 256-byte aligned, scratch between calls. */
+size_t ds_rows_prefix_attn_workspace_bytes(int rows, const ds_row_t* table, uint32_t prefix_len);
+
+/*
+ * Sink-softmax attention over EVERY cached row, for rows that share a prefix (samples of
+ * one prompt; also layers that attend to all their compressed rows): for each entry e and head h,
+ * over the slots j < kv_len of e,
+ *   l_j = scale * q_attn[q_row, h, :] . g_j
+ *   m = max(sink_h, max_j l_j), den = exp(sink_h - m) + sum_j exp(l_j - m)
+ *   out[q_row, h, :] = bf16( sum_j exp(l_j - m) g_j / den )
+ * where g_j is row j of entry 0 of the cache for j < prefix_len, else row j of entry e.
+ * The prefix is read once for every two entries, and its products with the
+ * queries are taken for them together.
+ *   rows        1 .. DS_PREFIX_ROWS_MAX
+ *   table       kv_len (1 .. 2^31 - 1, at least prefix_len) and q_row (unique) of each entry;
+ *               width and index_offset are not looked at
+ *   prefix_len  shared rows: 0 (nothing is shared) to the shortest kv_len. It may end
+ *               inside a page: behind it each entry reads its own page.
+ *   kv          dim 512, any format, with at least `rows` entries that reach kv_len
+ *   q_attn      bf16 [Q, 64, 512], 16-B aligned; sinks, sinks_row_stride, scale, out and invalid
+ *               as for ds_rows_sparse_attn (sinks and invalid 4-B aligned)
+ *   workspace   at least ds_rows_prefix_attn_workspace_bytes(...) bytes, 256-byte aligned
+ * A page id out of range under one of an entry's rows zeroes every head of it (under the prefix:
+ * of every entry). A head is zeroed where a q element, the sink, an element of one of
+ * the entry's rows or a logit (in units of ln 2) is not finite. Memory behind kv_len, and rows of
+ * an entry's own pages before prefix_len, are not read. Weights exp(l_j - m) are rounded to bf16 for
+ * the product with g_j; maxima, sums and outputs are kept in 32 bits. How the slots are split over the GPU
+ * depends on the whole call, and with it the last bits of a row: the same call gives the same bits, a
+ * call with other rows beside it may not. Status bits as DS_STATUS_* in the workspace's
+ * first word; after a wait that gave up every head of the call is zeros.
+ */
+int ds_rows_prefix_attn(int rows, const ds_row_t* table, uint32_t prefix_len, const ds_paged_cache_t* kv,
+                        const ds_bf16* q_attn, const float* sinks, size_t sinks_row_stride, float scale, ds_bf16* out,
+                        uint32_t* invalid, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Self-test of the device-side failure detection, on the current device. One
