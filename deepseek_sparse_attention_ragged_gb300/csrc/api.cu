@@ -109,10 +109,10 @@ int get_encoder() {
     return g_encode ? DS_OK : fail(DS_ECUDA, "cuTensorMapEncodeTiled is unavailable");
 }
 
-// 2D bf16 row-major [rows, 128] with a {64, box_rows} box and 128-byte swizzle.
-int encode_rows128(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows, const char* what) {
-    const cuuint64_t dims[2] = {128, rows};
-    const cuuint64_t strides[1] = {256};
+// 2D bf16 row-major [rows, width] with a {64, box_rows} box and 128-byte swizzle.
+int encode_rows(CUtensorMap* map, const void* base, uint32_t width, uint64_t rows, uint32_t box_rows, const char* what) {
+    const cuuint64_t dims[2] = {width, rows};
+    const cuuint64_t strides[1] = {2 * (cuuint64_t)width};
     const cuuint32_t box[2] = {64, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
@@ -120,6 +120,10 @@ int encode_rows128(CUtensorMap* map, const void* base, uint64_t rows, uint32_t b
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(DS_ECUDA, "tensor map for %s failed (CUresult %d)", what, (int)r);
     return DS_OK;
+}
+
+int encode_rows128(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows, const char* what) {
+    return encode_rows(map, base, DS_INDEX_DIM, rows, box_rows, what);
 }
 
 // ---- validation ----------------------------------------------------------------
@@ -669,7 +673,7 @@ int check_prefix_rows(int rows, const ds_row_t* table, uint32_t prefix_len) {
             return fail(DS_ESIZE, "row %d: kv_len %u of a paged cache must be below 2^31", e, r.kv_len);
         if (r.kv_len < prefix_len)
             return fail(DS_EINVAL, "row %d: kv_len %u is shorter than the prefix of %u", e, r.kv_len, prefix_len);
-        if ((uint64_t)r.q_row * DS_HEADS * DS_DIM > 0xFFFFFFFFFFull)
+        if (((uint64_t)r.q_row + 1) * DS_HEADS > 0x7FFFFFFFull)  // rows of 512 in a tensor map's coordinate
             return fail(DS_ESIZE, "row %d: q_row %u is out of range", e, r.q_row);
         for (int o = 0; o < e; ++o)
             if (table[o].q_row == r.q_row) return fail(DS_EINVAL, "row %d: q_row %u is used twice", e, r.q_row);
@@ -1264,8 +1268,16 @@ int ds_rows_prefix_attn(int rows, const ds_row_t* table, uint32_t prefix_len, co
     if (sms <= 0) return fail(DS_ECUDA, "no CUDA device");
     (void)lay_out_prefix(p, rows, table, prefix_len,
                          std::min(kPrefixPairsMax, std::max((uint32_t)sms / 2, 1u)));
+    rc = get_encoder();
+    if (rc) return rc;
+    uint32_t q_rows = 0;
+    for (int e = 0; e < rows; ++e) q_rows = std::max(q_rows, table[e].q_row);
+    rc = encode_rows(&p.qmap, q_attn, DS_DIM, ((uint64_t)q_rows + 1) * DS_HEADS, DS_HEADS, "queries");
+    if (rc == DS_OK && kv->format == DS_CACHE_BF16)
+        rc = encode_rows(&p.kvmap, kv->pages, DS_DIM, (uint64_t)kv->num_pages * kv->page_size,
+                         std::min(kv->page_size, kPrefixBoxRows), "paged rows");
+    if (rc) return rc;
     p.cache = paged_cache(*kv);
-    p.q = reinterpret_cast<const __nv_bfloat16*>(q_attn);
     p.sinks = sinks;
     p.sinks_row_stride = sinks_row_stride;
     p.out = reinterpret_cast<__nv_bfloat16*>(out);

@@ -216,12 +216,14 @@ constexpr uint32_t kPrefixRowsMax = DS_PREFIX_ROWS_MAX;
 constexpr uint32_t kPrefixSegsMax = kPrefixRowsMax / 2 + kPrefixRowsMax;
 constexpr uint32_t kPrefixPairsMax = 76;  // of this GPU's 152 multiprocessors
 constexpr uint32_t kPrefixTile = 128;
+constexpr uint32_t kPrefixBoxRows = 32;  // a TMA box of rows: this many, or a smaller page
 // m, sum and flag of each TMEM lane (head, half), then O [64 column groups][128 lanes][4].
 constexpr size_t kPrefixPartFloats = 3 * 128 + (size_t)DS_HEADS * DS_DIM;
 
 struct PrefixParams {
+    CUtensorMap qmap;   // bf16 [Q * 64, 512], box {64, 64}, 128-B swizzle
+    CUtensorMap kvmap;  // bf16 pages: [num_pages * page_size, 512], box {64, min(page_size, 32)}, 128-B swizzle
     PagedCache cache;
-    const __nv_bfloat16* q;  // [Q, 64, 512]
     const float* sinks;
     uint64_t sinks_row_stride;
     __nv_bfloat16* out;      // [Q, 64, 512]

@@ -20,7 +20,8 @@
 // so nothing but the operands crosses the pair.
 //
 // Warp roles: 0 looks up the tiles' rows, 1 issues the MMAs (in the pair's first CTA), 4 to 7
-// do the softmax (a thread has 64 slots of one head), 8 to 15 bring the operands. The K form (64 slots
+// do the softmax (a thread has 64 slots of one head); 3 loads the queries by TMA, 2 the rows of bf16 pages by TMA where a
+// tile is whole boxes of rows, and 8 to 15 bring the other tiles and the packed types. The K form (64 slots
 // x 128 dims) and the V form (32 slots x 256 dims) of the rows go through one ring of 16 KB units in
 // the order in which the MMAs take them: S of the next tile comes before P . G of this one.
 // Rows past a segment's end and rows without a page are zeros with probability 0.
@@ -39,6 +40,7 @@ constexpr int kUnitBytes = 16384;             // a ring unit: [64 slots][128 dim
 constexpr int kUnits = 8;                     // of the ring
 constexpr int kQBytes = kHeads * kDim * 2;    // the CTA's query row, 8 blocks [64 heads][64 dims]
 constexpr int kPBytes = kHeads * kTile * 2;   // P: 2 blocks [64 heads][64 slots]
+constexpr int kBoxRows = kPrefixBoxRows;      // most rows of a TMA box
 constexpr int kPlaceBufs = 4;                 // tiles whose rows are looked up
 constexpr int kThreads = 512;
 constexpr int kSoftmaxWarp = 4, kBuildWarp = 8, kBuildWarps = 8;
@@ -52,6 +54,8 @@ constexpr float kSlack = 8.0f;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kNoRow = -1, kBadRow = -2;
+constexpr uint32_t kMasked = 1;     // some slot of the tile has no row
+constexpr uint32_t kByThreads = 2;  // the tile is not whole boxes of rows of one page each
 
 struct Layout {
     static constexpr size_t ring = 0;
@@ -70,7 +74,8 @@ struct __align__(8) Bars {
     uint64_t empty[kUnits];
     uint64_t q_free, s_full[2], pv_done, drained;
     uint64_t place_full[kPlaceBufs], place_free[kPlaceBufs];
-    uint32_t partial[kPlaceBufs];  // some slot of the tile has no row
+    uint64_t grant[kUnits];        // bf16: the unit is free, and the builders' to fill
+    uint32_t form[kPlaceBufs];     // of the tile: kMasked, kByThreads
     uint32_t tmem_base;
 };
 
@@ -102,6 +107,25 @@ __device__ __forceinline__ void umma2_commit(uint64_t* bar) {
 __device__ __forceinline__ void arrive_first_cta(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(smem_u32(bar), 0))
                  : "memory");
+}
+__device__ __forceinline__ void arrive_first_cta(uint64_t* bar, uint32_t count) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr(smem_u32(bar), 0)),
+                 "r"(count)
+                 : "memory");
+}
+__device__ __forceinline__ void arrive_first_cta_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cluster.b64 _, [%0], %1;" ::"r"(
+                     cluster_addr(smem_u32(bar), 0)),
+                 "r"(bytes)
+                 : "memory");
+}
+// A tile of a tensor map into this CTA's shared memory, its bytes counted on the first CTA's barrier.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(dst),
+        "l"(map), "r"(cluster_addr(smem_u32(bar), 0)), "r"(x), "r"(y)
+        : "memory");
 }
 // A bounded wait of a whole warp (its lanes go on or give up together), whose first tries read no timer.
 __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, uint32_t* status) {
@@ -176,37 +200,33 @@ __device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 1, 128;"
 
 // ---- the operands ------------------------------------------------------------------------------
 
-// kDims dims of the rows at places at[0 ..] into a ring unit, by the builder's thread tid: 64 rows for 128
-// dims, 32 for 256. dim_of(d) is the row's dim that dim d of the unit is; dst(row, ch) the shared
-// address of dims 8 ch .. 8 ch + 7. A place below 0 brings zeros.
-template <int kFormat, int kDims, class DimOf, class Dst>
-__device__ __forceinline__ void bring(const PagedCache& cache, const int32_t* at, uint32_t tid, DimOf dim_of, Dst dst) {
-    constexpr uint32_t kRows = kUnitBytes / 2 / kDims;
-    if constexpr (kFormat == DS_CACHE_BF16) {
-        constexpr uint32_t kChunks = kDims / 8;
-#pragma unroll
-        for (uint32_t i = 0; i < kRows * kChunks / kBuildThreads; ++i) {
-            const uint32_t k = tid + i * kBuildThreads, row = k / kChunks, ch = k % kChunks;
-            const int32_t place = at[row];
-            const uint8_t* src = cache.pages + (size_t)max(place, 0) * (2 * kDim) + 2 * dim_of(8 * ch);
-            cp_async16_or_zero(dst(row, ch), src, place >= 0);
-        }
-    } else {
-        // A warp has eight rows and four neighbouring pieces of 16 bytes of each: whole sectors are read, and
-        // eight lanes store into eight rows, which the swizzle puts into different banks.
-        constexpr uint32_t kPiece = kFormat == DS_CACHE_FP8 ? 16 : 32;  // values of 16 bytes
-        constexpr uint32_t kN = kRows * kDims / kPiece / kBuildThreads;
-        const uint32_t warp = tid >> 5, lane = tid & 31;
-        const uint32_t row = 8 * (warp % (kRows / 8)) + (lane & 7);
-        const uint32_t first = 4 * kN * (warp / (kRows / 8)) + (lane >> 3);
-        const int32_t place = at[row];
-        uint4 d[kN];
-        uint32_t sc[kN];
+// The dim of a row that dim d of CTA `rank`'s half of it is (V form).
+__device__ __forceinline__ uint32_t v_dim(uint32_t d, uint32_t rank) { return 256 * (d >> 7) + 128 * rank + (d & 127); }
+
+// A builder thread's share of a unit of packed rows: one row's values from a 16-byte piece (4 bits) or two (8 bits).
+// A warp has eight rows and neighbouring pieces of each: whole sectors are read, and eight lanes store into
+// eight rows, which the swizzle puts into different banks.
+template <int kFormat>
+struct Piece {
+    static constexpr uint32_t kValues = kFormat == DS_CACHE_FP8 ? 16 : 32;  // of 16 bytes
+    static constexpr uint32_t kN = kFormat == DS_CACHE_FP8 ? 2 : 1;
+    uint4 d[kN];
+    uint32_t sc[kN];
+
+    // The first dim of the unit that a lane has, in the warps' quarter `part` of 128 dims each; the
+    // second piece (8 bits) is 64 dims on.
+    static __device__ __forceinline__ uint32_t first(uint32_t part, uint32_t lane) {
+        return 128 * part + kValues * (lane >> 3);
+    }
+    // The values of the pieces at dims dim_of(0) and dim_of(64) of a row; zeros without one.
+    template <class DimOf>
+    __device__ __forceinline__ void load(const PagedCache& cache, int32_t place, DimOf dim_of) {
+        const uint32_t where = (uint32_t)max(place, 0);
 #pragma unroll
         for (uint32_t n = 0; n < kN; ++n) {
-            const uint32_t dim = dim_of((first + 4 * n) * kPiece);
+            const uint32_t dim = dim_of(64 * n);
             if constexpr (kFormat == DS_CACHE_FP8) {
-                const uint32_t shift = cache.page_shift, where = (uint32_t)max(place, 0), in_page = where & ((1u << shift) - 1);
+                const uint32_t shift = cache.page_shift, in_page = where & ((1u << shift) - 1);
                 const uint8_t* page = cache.pages + (size_t)(where - in_page) * (kDim + kDim / fp8::kBlock);
                 d[n] = make_uint4(0, 0, 0, 0);
                 sc[n] = 127;
@@ -215,19 +235,23 @@ __device__ __forceinline__ void bring(const PagedCache& cache, const int32_t* at
                     sc[n] = __ldcg(page + ((size_t)kDim << shift) + in_page * (kDim / fp8::kBlock) + dim / fp8::kBlock);
                 }
             } else {
-                const uint8_t* src = cache.pages + (size_t)max(place, 0) * (kDim / 2 + kDim / int4::kGroup);
+                const uint8_t* row = cache.pages + (size_t)where * (kDim / 2 + kDim / int4::kGroup);
                 d[n] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
                 sc[n] = 0;
                 if (place >= 0) {
-                    d[n] = __ldcg(reinterpret_cast<const uint4*>(src + dim / 2));
-                    sc[n] = __ldcg(reinterpret_cast<const uint16_t*>(src + kDim / 2 + dim / int4::kGroup));
+                    d[n] = __ldcg(reinterpret_cast<const uint4*>(row + dim / 2));
+                    sc[n] = __ldcg(reinterpret_cast<const uint16_t*>(row + kDim / 2 + dim / int4::kGroup));
                 }
             }
         }
+    }
+    // Widened into the unit: dst(ch) is the shared address of its row's dims 8 ch .. 8 ch + 7.
+    template <class Dst>
+    __device__ __forceinline__ void store(uint32_t first_dim, Dst dst) const {
 #pragma unroll
         for (uint32_t n = 0; n < kN; ++n) {
             const uint32_t words[4] = {d[n].x, d[n].y, d[n].z, d[n].w};
-            const uint32_t ch = (first + 4 * n) * (kPiece / 8);
+            const uint32_t ch = (first_dim + 64 * n) / 8;
             if constexpr (kFormat == DS_CACHE_FP8) {
                 const uint32_t f = fp8::factor(sc[n]);
 #pragma unroll
@@ -235,7 +259,7 @@ __device__ __forceinline__ void bring(const PagedCache& cache, const int32_t* at
                     uint32_t o[4];
                     fp8::widen(words[2 * c], f, o);
                     fp8::widen(words[2 * c + 1], f, o + 2);
-                    st_shared_v4(dst(row, ch + c), o);
+                    st_shared_v4(dst(ch + c), o);
                 }
             } else {
                 int4::Factors f[2];
@@ -244,12 +268,12 @@ __device__ __forceinline__ void bring(const PagedCache& cache, const int32_t* at
                 for (uint32_t c = 0; c < 4; ++c) {
                     uint32_t o[4];
                     int4::widen(words[c], f[c >> 1], o);
-                    st_shared_v4(dst(row, ch + c), o);
+                    st_shared_v4(dst(ch + c), o);
                 }
             }
         }
     }
-}
+};
 
 // ---- the pair's tiles --------------------------------------------------------------------------
 
@@ -302,8 +326,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(&bar->full[i], 2 * kBuildWarps);
             mbar_init(&bar->empty[i], 1);
+            mbar_init(&bar->grant[i], 1);
         }
-        mbar_init(&bar->q_full, 2 * kBuildWarps);
+        mbar_init(&bar->q_full, 2);
         mbar_init(&bar->p_full, 8);
         mbar_init(&bar->q_free, 1);
         mbar_init(&bar->pv_done, 1);
@@ -314,7 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kPlaceBufs; ++i) {
             mbar_init(&bar->place_full[i], 1);
-            mbar_init(&bar->place_free[i], kBuildWarps + 4);
+            mbar_init(&bar->place_free[i], kBuildWarps + 4 + (kFormat == DS_CACHE_BF16 ? 1 : 0));
         }
         fence_barrier_init();
     }
@@ -368,7 +393,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) place_s[buf * kTile + lane + 32 * k] = at[k];
-                if (lane == 0) bar->partial[buf] = all ? 0u : 1u;
+                const uint32_t box = min(1u << shift, (uint32_t)kBoxRows);
+                if (lane == 0) bar->form[buf] = (all ? 0u : kMasked) | (all && part.start % box == 0 ? 0u : kByThreads);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->place_full[buf]);
             }
@@ -481,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (!(odd.x + odd.y == 0.0f)) bad = 1;
                 if (!(ok = wait_pair(&bar->place_full[pbuf], it / kPlaceBufs & 1, p.status))) break;
-                if (bar->partial[pbuf]) {
+                if (bar->form[pbuf] & kMasked) {
                     const ::int4* at = reinterpret_cast<const ::int4*>(place_s + pbuf * kTile + half * 64);
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
@@ -575,82 +601,175 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // A warp that gave up still meets the others.
         const Walk whole(p, pair, pairs);
         for (const uint32_t all = whole.end - whole.t; met < all; ++met) sync_softmax();
-    } else if (warp >= kBuildWarp) {
-        // ---- operands: the query of each part, then its tiles' units ------------------------------
-        const uint32_t tid = threadIdx.x - 32 * kBuildWarp;
-        uint32_t unit = 0, phase = 0, n_part = 0;
-        uint32_t told = 0, brought = 0;  // units whose arrival was signalled, units issued
-        bool ok = true;
-        constexpr uint32_t kLag = 4;     // units in flight (bf16)
-        auto tell = [&](uint32_t until) {
-            fence_proxy_async_smem();
+    } else if (warp == 3) {
+        // ---- each part's query, once the MMAs of the part before have read theirs --------------
+        uint32_t n_part = 0;
+        for (Walk w(p, pair, pairs); w.next(part); ++n_part) {
+            if (n_part > 0 && !wait_pair(&bar->q_free, (n_part - 1) & 1, p.status)) break;
+            const uint32_t r = part.seg < p.groups ? min(2 * part.seg + rank, p.rows - 1) : part.seg - p.groups;
+            if (lane == 0) arrive_first_cta_expect(&bar->q_full, kQBytes);
             __syncwarp();
-            for (; told < until; ++told)
-                if (lane == 0) arrive_first_cta(&bar->full[told % kUnits]);
-        };
-        // One unit is issued; with bf16 the one kLag before it has landed.
-        auto advance = [&] {
-            ++brought;
-            if (kFormat == DS_CACHE_BF16) {
-                cp_async_commit_group();
-                if (brought > kLag) {
-                    cp_async_wait_group<kLag>();
-                    tell(brought - kLag);
-                }
-            } else {
-                tell(brought);
-            }
-            if (++unit == kUnits) unit = 0, phase ^= 1;
-        };
-        auto k_units = [&](uint32_t of) -> bool {
-            const int32_t* at = place_s + of % kPlaceBufs * kTile + 64 * rank;
+            if (lane < 8)
+                tma_load_pair(smem_u32(smem + Layout::q) + lane * 8192, &p.qmap, &bar->q_full, 64 * lane,
+                              (int)(p.q_row[r] * kHeads));
+        }
+    } else if (kFormat == DS_CACHE_BF16 && warp == 2) {
+        // ---- bf16 operands: boxes of rows; the tiles that are not whole boxes are left to threads --
+        uint32_t unit = 0, phase = 0;
+        const uint32_t box = min(1u << p.cache.page_shift, (uint32_t)kBoxRows);
+        bool ok = true;
+        auto fill = [&](uint32_t of, bool v_form) -> bool {
+            const int32_t* at = place_s + of % kPlaceBufs * kTile;
+            const bool whole = !(bar->form[of % kPlaceBufs] & kByThreads);
+            const uint32_t groups = (v_form ? 32 : 64) / box;  // of rows; lane = (row group, 64 dims)
+            const uint32_t group = lane % groups, dims = lane / groups;
 #pragma unroll 1
             for (uint32_t u = 0; u < 4; ++u) {
                 if (!wait_pair(&bar->empty[unit], phase ^ 1, p.status)) return false;
-                const uint32_t dst = ring + unit * kUnitBytes;
-                bring<kFormat, 128>(p.cache, at, tid, [&](uint32_t d) { return 128 * u + d; },
-                                    [&](uint32_t row, uint32_t ch) { return dst + (ch >> 3) * 8192 + swizzled(row, ch & 7); });
-                advance();
+                if (!whole) {
+                    if (lane == 0) mbar_arrive(&bar->grant[unit]);
+                } else {
+                    if (lane == 0) {
+                        arrive_first_cta(&bar->full[unit], kBuildWarps - 1);
+                        arrive_first_cta_expect(&bar->full[unit], kUnitBytes);
+                    }
+                    __syncwarp();
+                    if (dims < (v_form ? 4u : 2u)) {
+                        const uint32_t row = group * box;
+                        const int y = at[(v_form ? 32 * u : 64 * rank) + row];
+                        const uint32_t x = v_form ? 256 * (dims >> 1) + 128 * rank + 64 * (dims & 1) : 128 * u + 64 * dims;
+                        tma_load_pair(ring + unit * kUnitBytes + dims * (v_form ? 4096 : 8192) + row * 128, &p.kvmap,
+                                      &bar->full[unit], (int)x, y);
+                    }
+                }
+                __syncwarp();
+                if (++unit == kUnits) unit = 0, phase ^= 1;
             }
+            if (v_form && lane == 0) mbar_arrive(&bar->place_free[of % kPlaceBufs]);
             return true;
         };
-        auto v_units = [&](uint32_t of) -> bool {
-#pragma unroll 1
-            for (uint32_t v = 0; v < 4; ++v) {
-                if (!wait_pair(&bar->empty[unit], phase ^ 1, p.status)) return false;
-                const uint32_t dst = ring + unit * kUnitBytes;
-                const int32_t* at = place_s + of % kPlaceBufs * kTile + 32 * v;
-                bring<kFormat, 256>(p.cache, at, tid,
-                                    [&](uint32_t d) { return 256 * (d >> 7) + 128 * rank + (d & 127); },
-                                    [&](uint32_t row, uint32_t ch) { return dst + (ch >> 3) * 4096 + swizzled(row, ch & 7); });
-                advance();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->place_free[of % kPlaceBufs]);
-            return true;
-        };
-        for (Walk w(p, pair, pairs); ok && w.next(part); ++n_part) {
-            // The query, once the MMAs of the part before have read theirs (they need every unit so far).
-            if (kFormat == DS_CACHE_BF16) cp_async_wait_group<0>();
-            tell(brought);
-            if (n_part > 0 && !(ok = wait_pair(&bar->q_free, (n_part - 1) & 1, p.status))) break;
-            const uint32_t r = part.seg < p.groups ? min(2 * part.seg + rank, p.rows - 1) : part.seg - p.groups;
-            const uint4* q = reinterpret_cast<const uint4*>(p.q + (size_t)p.q_row[r] * kHeads * kDim);
-            uint8_t* q_s = smem + Layout::q;
-#pragma unroll 4
-            for (uint32_t k = tid; k < kQBytes / 16; k += kBuildThreads)
-                *reinterpret_cast<uint4*>(q_s + ((k & 63) >> 3) * 8192 + swizzled(k >> 6, k & 7)) = q[k];
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive_first_cta(&bar->q_full);
+        for (Walk w(p, pair, pairs); ok && w.next(part);)
             for (uint32_t i = 0; ok && i < part.tiles; ++i, ++it) {
                 ok = wait_pair(&bar->place_full[it % kPlaceBufs], it / kPlaceBufs & 1, p.status);
-                ok = ok && k_units(it) && (it == 0 || v_units(it - 1));
+                ok = ok && fill(it, false) && (it == 0 || fill(it - 1, true));
+            }
+        if (ok) (void)fill(it - 1, true);
+    } else if (kFormat == DS_CACHE_BF16 && warp >= kBuildWarp) {
+        // ---- bf16 tiles that are not whole boxes: rows by 16 bytes, zeros for what is missing -----
+        const uint32_t tid = threadIdx.x - 32 * kBuildWarp;
+        uint32_t unit = 0, granted = 0;  // a bit for each unit's barrier: its phase
+        bool ok = true;
+        auto build = [&](uint32_t of, bool v_form) -> bool {
+            const int32_t* at = place_s + of % kPlaceBufs * kTile;
+            const uint32_t first = unit;
+            if (bar->form[of % kPlaceBufs] & kByThreads) {
+#pragma unroll 1
+                for (uint32_t u = 0; u < 4; ++u) {
+                    if (!wait_pair(&bar->grant[unit], granted >> unit & 1, p.status)) return false;
+                    granted ^= 1u << unit;
+                    const uint32_t dst = ring + unit * kUnitBytes;
+#pragma unroll
+                    for (uint32_t i = 0; i < kUnitBytes / 16 / kBuildThreads; ++i) {
+                        const uint32_t k = tid + i * kBuildThreads;
+                        const uint32_t row = v_form ? k >> 5 : k >> 4, ch = v_form ? k & 31 : k & 15;  // 8 dims
+                        const uint32_t dim = v_form ? 256 * (ch >> 4) + 128 * rank + 8 * (ch & 15) : 128 * u + 8 * ch;
+                        const int32_t place = at[(v_form ? 32 * u : 64 * rank) + row];
+                        cp_async16_or_zero(dst + (ch >> 3) * (v_form ? 4096 : 8192) + swizzled(row, ch & 7),
+                                           p.cache.pages + (size_t)max(place, 0) * (2 * kDim) + 2 * dim, place >= 0);
+                    }
+                    cp_async_commit_group();
+                    if (++unit == kUnits) unit = 0;
+                }
+#pragma unroll
+                for (uint32_t u = 0; u < 4; ++u) {
+                    if (u == 0) cp_async_wait_group<3>();
+                    else if (u == 1) cp_async_wait_group<2>();
+                    else if (u == 2) cp_async_wait_group<1>();
+                    else cp_async_wait_group<0>();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive_first_cta(&bar->full[(first + u) % kUnits], 1);
+                }
+            } else {
+                unit = (unit + 4) % kUnits;
+            }
+            __syncwarp();
+            if (v_form && lane == 0) mbar_arrive(&bar->place_free[of % kPlaceBufs]);
+            return true;
+        };
+        for (Walk w(p, pair, pairs); ok && w.next(part);)
+            for (uint32_t i = 0; ok && i < part.tiles; ++i, ++it) {
+                ok = wait_pair(&bar->place_full[it % kPlaceBufs], it / kPlaceBufs & 1, p.status);
+                ok = ok && build(it, false) && (it == 0 || build(it - 1, true));
+            }
+        if (ok) (void)build(it - 1, true);
+        cp_async_wait_group<0>();
+    } else if (kFormat != DS_CACHE_BF16 && warp >= kBuildWarp) {
+        // ---- packed operands: widened by threads. The loads of the next four units (one form of a tile) are
+        // issued as this form's units are stored.
+        const uint32_t w8 = warp - kBuildWarp;
+        uint32_t unit = 0, phase = 0;
+        bool ok = true;
+        Piece<kFormat> held[4];
+        auto fetch = [&](uint32_t of, bool v_form, uint32_t u) {
+            const int32_t* at = place_s + of % kPlaceBufs * kTile;
+            if (v_form) {
+                const uint32_t d = Piece<kFormat>::first(w8 >> 2, lane);
+                held[u].load(p.cache, at[32 * u + 8 * (w8 & 3) + (lane & 7)],
+                             [&](uint32_t n) { return v_dim(d + n, rank); });
+            } else {
+                const uint32_t d = Piece<kFormat>::first(0, lane);
+                held[u].load(p.cache, at[64 * rank + 8 * w8 + (lane & 7)], [&](uint32_t n) { return 128 * u + d + n; });
+            }
+        };
+        // The units of one form, and the loads of the form that follows (`then`; none past the end).
+        auto form = [&](bool v_form, uint32_t next_of, bool next_v, bool then) -> bool {
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u) {
+                if (!wait_pair(&bar->empty[unit], phase ^ 1, p.status)) return false;
+                const uint32_t dst = ring + unit * kUnitBytes;
+                if (v_form)
+                    held[u].store(Piece<kFormat>::first(w8 >> 2, lane), [&](uint32_t ch) {
+                        return dst + (ch >> 3) * 4096 + swizzled(8 * (w8 & 3) + (lane & 7), ch & 7);
+                    });
+                else
+                    held[u].store(Piece<kFormat>::first(0, lane), [&](uint32_t ch) {
+                        return dst + (ch >> 3) * 8192 + swizzled(8 * w8 + (lane & 7), ch & 7);
+                    });
+                if (then) fetch(next_of, next_v, u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_first_cta(&bar->full[unit], 1);
+                if (++unit == kUnits) unit = 0, phase ^= 1;
+            }
+            if (then && next_v) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->place_free[next_of % kPlaceBufs]);
+            }
+            return true;
+        };
+        const Walk whole(p, pair, pairs);
+        const uint32_t n = whole.end - whole.t;  // K(0), K(1), V(0), K(2), V(1), ..., V(n - 1)
+        auto looked_up = [&](uint32_t of) {
+            return wait_pair(&bar->place_full[of % kPlaceBufs], of / kPlaceBufs & 1, p.status);
+        };
+        ok = looked_up(0);
+        if (ok)
+            for (uint32_t u = 0; u < 4; ++u) fetch(0, false, u);
+        for (it = 0; ok && it < n; ++it) {
+            const bool more = it + 1 < n;
+            // K(it): then V(it - 1), or without one K(1) or V(0).
+            if (it == 0) {
+                ok = !more || looked_up(1);
+                ok = ok && form(false, more ? 1 : 0, !more, true);
+            } else {
+                ok = form(false, it - 1, true, true);
+                // V(it - 1): then K(it + 1), or at the end V(it).
+                ok = ok && (!more || looked_up(it + 1));
+                ok = ok && form(true, more ? it + 1 : it, !more, true);
             }
         }
-        if (ok && it > 0) ok = v_units(it - 1);
-        if (kFormat == DS_CACHE_BF16) cp_async_wait_group<0>();
-        if (ok) tell(brought);
+        if (ok) (void)form(true, 0, false, false);  // V(n - 1)
     }
 
     tc_fence_before();
