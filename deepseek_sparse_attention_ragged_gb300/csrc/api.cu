@@ -681,15 +681,24 @@ int check_prefix_rows(int rows, const ds_row_t* table, uint32_t prefix_len) {
     return DS_OK;
 }
 
-// The segments of checked rows: their tiles, and the bytes of the workspace.
+// The segments of checked rows on the line that is dealt out to the pairs of CTAs, and the bytes of
+// the workspace. With a tile for every pair, or less, each pair has one; else a
+// segment's set-up (its query, the first tile's way through the pipeline, what it leaves in the workspace)
+// counts as two tiles, so that the pairs with the rows' short ends do not finish last.
 size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t prefix_len, uint32_t most_pairs) {
     p.rows = (uint32_t)rows;
     p.groups = (p.rows + 1) / 2;
     p.prefix_len = prefix_len;
-    uint32_t tiles = 0, segs = 0;
+    uint32_t tiles = 0;
+    auto tiles_of = [](uint32_t slots) { return (slots + kPrefixTile - 1) / kPrefixTile; };  // at most 2^24
+    tiles += p.groups * tiles_of(prefix_len);
+    for (uint32_t e = 0; e < p.rows; ++e) tiles += tiles_of(table[e].kv_len - prefix_len);
+    p.pairs = tiles < most_pairs ? tiles : most_pairs;
+    p.seg_cost = tiles <= most_pairs ? 0 : 2;
+    uint32_t segs = 0, at = 0;
     auto add = [&](uint32_t slots) {
-        p.tile_begin[segs++] = tiles;
-        tiles += (slots + kPrefixTile - 1) / kPrefixTile;  // at most 96 of 2^24
+        p.begin[segs++] = at;
+        if (slots) at += p.seg_cost + tiles_of(slots);
     };
     for (uint32_t g = 0; g < p.groups; ++g) add(prefix_len);
     for (uint32_t e = 0; e < p.rows; ++e) {
@@ -697,9 +706,7 @@ size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t
         p.q_row[e] = table[e].q_row;
         add(table[e].kv_len - prefix_len);
     }
-    p.tile_begin[segs] = tiles;
-    p.total_tiles = tiles;
-    p.pairs = tiles < most_pairs ? tiles : most_pairs;
+    p.begin[segs] = p.line = at;
     return 256 + align256((size_t)(p.pairs + segs - 1) * 2 * kPrefixPartFloats * 4);
 }
 

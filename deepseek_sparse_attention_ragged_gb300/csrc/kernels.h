@@ -235,10 +235,11 @@ struct PrefixParams {
     uint32_t groups;
     uint32_t prefix_len;
     uint32_t pairs;
-    uint32_t total_tiles;
+    uint32_t seg_cost;  // units of the line for a segment's set-up, before its tiles
+    uint32_t line;      // its length
     uint32_t kv_len[kPrefixRowsMax];
     uint32_t q_row[kPrefixRowsMax];
-    uint32_t tile_begin[kPrefixSegsMax + 1];
+    uint32_t begin[kPrefixSegsMax + 1];  // of each segment on the line (empty ones take nothing)
 };
 
 cudaError_t launch_prefix_attn(const PrefixParams& p, int format, cudaStream_t stream, bool pdl);

@@ -20,8 +20,8 @@
 // so nothing but the operands crosses the pair.
 //
 // Warp roles: 0 looks up the tiles' rows, 1 issues the MMAs (in the pair's first CTA), 4 to 7
-// do the softmax (a thread has 64 slots of one head); 3 loads the queries by TMA, 2 the rows of bf16 pages by TMA where a
-// tile is whole boxes of rows, and 8 to 15 bring the other tiles and the packed types. The K form (64 slots
+// do the softmax (a thread has 64 slots of one head); 3 loads the queries, and 8 to 15
+// bring the operands, each one unit of a ring. The K form (64 slots
 // x 128 dims) and the V form (32 slots x 256 dims) of the rows go through one ring of 16 KB units in
 // the order in which the MMAs take them: S of the next tile comes before P . G of this one.
 // Rows past a segment's end and rows without a page are zeros with probability 0.
@@ -43,8 +43,8 @@ constexpr int kPBytes = kHeads * kTile * 2;   // P: 2 blocks [64 heads][64 slots
 constexpr int kBoxRows = kPrefixBoxRows;      // most rows of a TMA box
 constexpr int kPlaceBufs = 4;                 // tiles whose rows are looked up
 constexpr int kThreads = 512;
-constexpr int kSoftmaxWarp = 4, kBuildWarp = 8, kBuildWarps = 8;
-constexpr int kBuildThreads = 32 * kBuildWarps;
+constexpr int kSoftmaxWarp = 4, kBuildWarp = 8;
+static_assert(kThreads / 32 == kBuildWarp + kUnits, "a warp for each unit");
 constexpr uint32_t kOCol = 128;               // TMEM: two S of 64 columns, then O
 constexpr uint32_t kTmemCols = 512;
 constexpr uint16_t kBoth = 3;                 // the CTAs of a pair
@@ -74,7 +74,6 @@ struct __align__(8) Bars {
     uint64_t empty[kUnits];
     uint64_t q_free, s_full[2], pv_done, drained;
     uint64_t place_full[kPlaceBufs], place_free[kPlaceBufs];
-    uint64_t grant[kUnits];        // bf16: the unit is free, and the builders' to fill
     uint32_t form[kPlaceBufs];     // of the tile: kMasked, kByThreads
     uint32_t tmem_base;
 };
@@ -106,11 +105,6 @@ __device__ __forceinline__ void umma2_commit(uint64_t* bar) {
 // what counts. (With cluster scope an arrival takes 323 cycles instead of 8, and waits for every load in flight.)
 __device__ __forceinline__ void arrive_first_cta(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(smem_u32(bar), 0))
-                 : "memory");
-}
-__device__ __forceinline__ void arrive_first_cta(uint64_t* bar, uint32_t count) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr(smem_u32(bar), 0)),
-                 "r"(count)
                  : "memory");
 }
 __device__ __forceinline__ void arrive_first_cta_expect(uint64_t* bar, uint32_t bytes) {
@@ -203,45 +197,38 @@ __device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 1, 128;"
 // The dim of a row that dim d of CTA `rank`'s half of it is (V form).
 __device__ __forceinline__ uint32_t v_dim(uint32_t d, uint32_t rank) { return 256 * (d >> 7) + 128 * rank + (d & 127); }
 
-// A builder thread's share of a unit of packed rows: one row's values from a 16-byte piece (4 bits) or two (8 bits).
-// A warp has eight rows and neighbouring pieces of each: whole sectors are read, and eight lanes store into
+// A lane's values of a step of a packed unit, eight rows of 128 dims: a 16-byte piece of one row (4 bits) or
+// two (8 bits). Four neighbouring pieces of each row are read together, and eight lanes store into
 // eight rows, which the swizzle puts into different banks.
 template <int kFormat>
 struct Piece {
     static constexpr uint32_t kValues = kFormat == DS_CACHE_FP8 ? 16 : 32;  // of 16 bytes
-    static constexpr uint32_t kN = kFormat == DS_CACHE_FP8 ? 2 : 1;
+    static constexpr uint32_t kN = kFormat == DS_CACHE_FP8 ? 2 : 1;         // the second is 64 dims on
     uint4 d[kN];
-    uint32_t sc[kN];
+    uint32_t sc;
 
-    // The first dim of the unit that a lane has, in the warps' quarter `part` of 128 dims each; the
-    // second piece (8 bits) is 64 dims on.
-    static __device__ __forceinline__ uint32_t first(uint32_t part, uint32_t lane) {
-        return 128 * part + kValues * (lane >> 3);
-    }
-    // The values of the pieces at dims dim_of(0) and dim_of(64) of a row; zeros without one.
-    template <class DimOf>
-    __device__ __forceinline__ void load(const PagedCache& cache, int32_t place, DimOf dim_of) {
+    static __device__ __forceinline__ uint32_t first(uint32_t lane) { return kValues * (lane >> 3); }
+    // The pieces at dims dim and dim + 64 of the row at `place`; zeros without one.
+    __device__ __forceinline__ void load(const PagedCache& cache, int32_t place, uint32_t dim) {
         const uint32_t where = (uint32_t)max(place, 0);
-#pragma unroll
-        for (uint32_t n = 0; n < kN; ++n) {
-            const uint32_t dim = dim_of(64 * n);
-            if constexpr (kFormat == DS_CACHE_FP8) {
-                const uint32_t shift = cache.page_shift, in_page = where & ((1u << shift) - 1);
-                const uint8_t* page = cache.pages + (size_t)(where - in_page) * (kDim + kDim / fp8::kBlock);
-                d[n] = make_uint4(0, 0, 0, 0);
-                sc[n] = 127;
-                if (place >= 0) {
-                    d[n] = __ldcg(reinterpret_cast<const uint4*>(page + (size_t)in_page * kDim + dim));
-                    sc[n] = __ldcg(page + ((size_t)kDim << shift) + in_page * (kDim / fp8::kBlock) + dim / fp8::kBlock);
-                }
-            } else {
-                const uint8_t* row = cache.pages + (size_t)where * (kDim / 2 + kDim / int4::kGroup);
-                d[n] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                sc[n] = 0;
-                if (place >= 0) {
-                    d[n] = __ldcg(reinterpret_cast<const uint4*>(row + dim / 2));
-                    sc[n] = __ldcg(reinterpret_cast<const uint16_t*>(row + kDim / 2 + dim / int4::kGroup));
-                }
+        if constexpr (kFormat == DS_CACHE_FP8) {
+            const uint32_t shift = cache.page_shift, in_page = where & ((1u << shift) - 1);
+            const uint8_t* page = cache.pages + (size_t)(where - in_page) * (kDim + kDim / fp8::kBlock);
+            const uint8_t* row = page + (size_t)in_page * kDim + dim;
+            d[0] = d[1] = make_uint4(0, 0, 0, 0);
+            sc = 127;
+            if (place >= 0) {
+                d[0] = __ldcg(reinterpret_cast<const uint4*>(row));
+                d[1] = __ldcg(reinterpret_cast<const uint4*>(row + 64));
+                sc = __ldcg(page + ((size_t)kDim << shift) + in_page * (kDim / fp8::kBlock) + dim / fp8::kBlock);
+            }
+        } else {
+            const uint8_t* row = cache.pages + (size_t)where * (kDim / 2 + kDim / int4::kGroup);
+            d[0] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+            sc = 0;
+            if (place >= 0) {
+                d[0] = __ldcg(reinterpret_cast<const uint4*>(row + dim / 2));
+                sc = __ldcg(reinterpret_cast<const uint16_t*>(row + kDim / 2 + dim / int4::kGroup));
             }
         }
     }
@@ -253,7 +240,7 @@ struct Piece {
             const uint32_t words[4] = {d[n].x, d[n].y, d[n].z, d[n].w};
             const uint32_t ch = (first_dim + 64 * n) / 8;
             if constexpr (kFormat == DS_CACHE_FP8) {
-                const uint32_t f = fp8::factor(sc[n]);
+                const uint32_t f = fp8::factor(sc);
 #pragma unroll
                 for (uint32_t c = 0; c < 2; ++c) {
                     uint32_t o[4];
@@ -263,7 +250,7 @@ struct Piece {
                 }
             } else {
                 int4::Factors f[2];
-                int4::factors2<0>(sc[n], f[0], f[1]);
+                int4::factors2<0>(sc, f[0], f[1]);
 #pragma unroll
                 for (uint32_t c = 0; c < 4; ++c) {
                     uint32_t o[4];
@@ -285,26 +272,33 @@ struct Part {
     uint32_t tiles;
 };
 
-// The parts of pair k in order: for (Walk w(p, k); w.next(part);)
+// The parts of pair k in order: for (Walk w(p, k, pairs); w.next(part);). What is dealt out in equal runs
+// is a line on which a segment's tiles follow p.seg_cost units for its set-up.
 struct Walk {
     const PrefixParams& p;
     uint32_t t, end, seg;
     __device__ __forceinline__ Walk(const PrefixParams& params, uint32_t pair, uint32_t pairs) : p(params) {
-        t = (uint32_t)((uint64_t)p.total_tiles * pair / pairs);
-        end = (uint32_t)((uint64_t)p.total_tiles * (pair + 1) / pairs);
+        t = (uint32_t)((uint64_t)p.line * pair / pairs);
+        end = (uint32_t)((uint64_t)p.line * (pair + 1) / pairs);
         seg = 0;
     }
     __device__ __forceinline__ bool next(Part& part) {
-        if (t >= end) return false;
-        while (p.tile_begin[seg + 1] <= t) ++seg;  // t is below the last bound
-        const uint32_t stop = min(end, p.tile_begin[seg + 1]);
-        const bool shared = seg < p.groups;
-        part.seg = seg;
-        part.start = (shared ? 0u : p.prefix_len) + (t - p.tile_begin[seg]) * kTile;
-        part.end = shared ? p.prefix_len : p.kv_len[seg - p.groups];
-        part.tiles = stop - t;
-        t = stop;
-        return true;
+        while (t < end) {
+            while (p.begin[seg + 1] <= t) ++seg;  // t is below the last bound
+            const uint32_t first = p.begin[seg] + p.seg_cost, stop = min(end, p.begin[seg + 1]);
+            t = max(t, first);
+            if (t < stop) {
+                const bool shared = seg < p.groups;
+                part.seg = seg;
+                part.start = (shared ? 0u : p.prefix_len) + (t - first) * kTile;
+                part.end = shared ? p.prefix_len : p.kv_len[seg - p.groups];
+                part.tiles = stop - t;
+                t = stop;
+                return true;
+            }
+            t = max(t, stop);
+        }
+        return false;
     }
 };
 
@@ -324,9 +318,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kUnits; ++i) {
-            mbar_init(&bar->full[i], 2 * kBuildWarps);
+            mbar_init(&bar->full[i], 2);
             mbar_init(&bar->empty[i], 1);
-            mbar_init(&bar->grant[i], 1);
         }
         mbar_init(&bar->q_full, 2);
         mbar_init(&bar->p_full, 8);
@@ -339,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kPlaceBufs; ++i) {
             mbar_init(&bar->place_full[i], 1);
-            mbar_init(&bar->place_free[i], kBuildWarps + 4 + (kFormat == DS_CACHE_BF16 ? 1 : 0));
+            mbar_init(&bar->place_free[i], 4 + 4 + 4);  // K form, V form, softmax
         }
         fence_barrier_init();
     }
@@ -599,8 +592,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_before();
         }
         // A warp that gave up still meets the others.
-        const Walk whole(p, pair, pairs);
-        for (const uint32_t all = whole.end - whole.t; met < all; ++met) sync_softmax();
+        uint32_t all = 0;
+        for (Walk w(p, pair, pairs); w.next(part);) all += part.tiles;
+        for (; met < all; ++met) sync_softmax();
     } else if (warp == 3) {
         // ---- each part's query, once the MMAs of the part before have read theirs --------------
         uint32_t n_part = 0;
@@ -613,163 +607,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tma_load_pair(smem_u32(smem + Layout::q) + lane * 8192, &p.qmap, &bar->q_full, 64 * lane,
                               (int)(p.q_row[r] * kHeads));
         }
-    } else if (kFormat == DS_CACHE_BF16 && warp == 2) {
-        // ---- bf16 operands: boxes of rows; the tiles that are not whole boxes are left to threads --
-        uint32_t unit = 0, phase = 0;
-        const uint32_t box = min(1u << p.cache.page_shift, (uint32_t)kBoxRows);
-        bool ok = true;
-        auto fill = [&](uint32_t of, bool v_form) -> bool {
-            const int32_t* at = place_s + of % kPlaceBufs * kTile;
-            const bool whole = !(bar->form[of % kPlaceBufs] & kByThreads);
-            const uint32_t groups = (v_form ? 32 : 64) / box;  // of rows; lane = (row group, 64 dims)
-            const uint32_t group = lane % groups, dims = lane / groups;
-#pragma unroll 1
-            for (uint32_t u = 0; u < 4; ++u) {
-                if (!wait_pair(&bar->empty[unit], phase ^ 1, p.status)) return false;
-                if (!whole) {
-                    if (lane == 0) mbar_arrive(&bar->grant[unit]);
-                } else {
-                    if (lane == 0) {
-                        arrive_first_cta(&bar->full[unit], kBuildWarps - 1);
-                        arrive_first_cta_expect(&bar->full[unit], kUnitBytes);
-                    }
-                    __syncwarp();
-                    if (dims < (v_form ? 4u : 2u)) {
-                        const uint32_t row = group * box;
-                        const int y = at[(v_form ? 32 * u : 64 * rank) + row];
-                        const uint32_t x = v_form ? 256 * (dims >> 1) + 128 * rank + 64 * (dims & 1) : 128 * u + 64 * dims;
-                        tma_load_pair(ring + unit * kUnitBytes + dims * (v_form ? 4096 : 8192) + row * 128, &p.kvmap,
-                                      &bar->full[unit], (int)x, y);
-                    }
-                }
-                __syncwarp();
-                if (++unit == kUnits) unit = 0, phase ^= 1;
-            }
-            if (v_form && lane == 0) mbar_arrive(&bar->place_free[of % kPlaceBufs]);
-            return true;
-        };
-        for (Walk w(p, pair, pairs); ok && w.next(part);)
-            for (uint32_t i = 0; ok && i < part.tiles; ++i, ++it) {
-                ok = wait_pair(&bar->place_full[it % kPlaceBufs], it / kPlaceBufs & 1, p.status);
-                ok = ok && fill(it, false) && (it == 0 || fill(it - 1, true));
-            }
-        if (ok) (void)fill(it - 1, true);
-    } else if (kFormat == DS_CACHE_BF16 && warp >= kBuildWarp) {
-        // ---- bf16 tiles that are not whole boxes: rows by 16 bytes, zeros for what is missing -----
-        const uint32_t tid = threadIdx.x - 32 * kBuildWarp;
-        uint32_t unit = 0, granted = 0;  // a bit for each unit's barrier: its phase
-        bool ok = true;
-        auto build = [&](uint32_t of, bool v_form) -> bool {
-            const int32_t* at = place_s + of % kPlaceBufs * kTile;
-            const uint32_t first = unit;
-            if (bar->form[of % kPlaceBufs] & kByThreads) {
-#pragma unroll 1
-                for (uint32_t u = 0; u < 4; ++u) {
-                    if (!wait_pair(&bar->grant[unit], granted >> unit & 1, p.status)) return false;
-                    granted ^= 1u << unit;
-                    const uint32_t dst = ring + unit * kUnitBytes;
-#pragma unroll
-                    for (uint32_t i = 0; i < kUnitBytes / 16 / kBuildThreads; ++i) {
-                        const uint32_t k = tid + i * kBuildThreads;
-                        const uint32_t row = v_form ? k >> 5 : k >> 4, ch = v_form ? k & 31 : k & 15;  // 8 dims
-                        const uint32_t dim = v_form ? 256 * (ch >> 4) + 128 * rank + 8 * (ch & 15) : 128 * u + 8 * ch;
-                        const int32_t place = at[(v_form ? 32 * u : 64 * rank) + row];
-                        cp_async16_or_zero(dst + (ch >> 3) * (v_form ? 4096 : 8192) + swizzled(row, ch & 7),
-                                           p.cache.pages + (size_t)max(place, 0) * (2 * kDim) + 2 * dim, place >= 0);
-                    }
-                    cp_async_commit_group();
-                    if (++unit == kUnits) unit = 0;
-                }
-#pragma unroll
-                for (uint32_t u = 0; u < 4; ++u) {
-                    if (u == 0) cp_async_wait_group<3>();
-                    else if (u == 1) cp_async_wait_group<2>();
-                    else if (u == 2) cp_async_wait_group<1>();
-                    else cp_async_wait_group<0>();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) arrive_first_cta(&bar->full[(first + u) % kUnits], 1);
-                }
-            } else {
-                unit = (unit + 4) % kUnits;
-            }
-            __syncwarp();
-            if (v_form && lane == 0) mbar_arrive(&bar->place_free[of % kPlaceBufs]);
-            return true;
-        };
-        for (Walk w(p, pair, pairs); ok && w.next(part);)
-            for (uint32_t i = 0; ok && i < part.tiles; ++i, ++it) {
-                ok = wait_pair(&bar->place_full[it % kPlaceBufs], it / kPlaceBufs & 1, p.status);
-                ok = ok && build(it, false) && (it == 0 || build(it - 1, true));
-            }
-        if (ok) (void)build(it - 1, true);
-        cp_async_wait_group<0>();
-    } else if (kFormat != DS_CACHE_BF16 && warp >= kBuildWarp) {
-        // ---- packed operands: widened by threads. The loads of the next four units (one form of a tile) are
-        // issued as this form's units are stored.
-        const uint32_t w8 = warp - kBuildWarp;
-        uint32_t unit = 0, phase = 0;
-        bool ok = true;
-        Piece<kFormat> held[4];
-        auto fetch = [&](uint32_t of, bool v_form, uint32_t u) {
-            const int32_t* at = place_s + of % kPlaceBufs * kTile;
-            if (v_form) {
-                const uint32_t d = Piece<kFormat>::first(w8 >> 2, lane);
-                held[u].load(p.cache, at[32 * u + 8 * (w8 & 3) + (lane & 7)],
-                             [&](uint32_t n) { return v_dim(d + n, rank); });
-            } else {
-                const uint32_t d = Piece<kFormat>::first(0, lane);
-                held[u].load(p.cache, at[64 * rank + 8 * w8 + (lane & 7)], [&](uint32_t n) { return 128 * u + d + n; });
-            }
-        };
-        // The units of one form, and the loads of the form that follows (`then`; none past the end).
-        auto form = [&](bool v_form, uint32_t next_of, bool next_v, bool then) -> bool {
-#pragma unroll
-            for (uint32_t u = 0; u < 4; ++u) {
-                if (!wait_pair(&bar->empty[unit], phase ^ 1, p.status)) return false;
-                const uint32_t dst = ring + unit * kUnitBytes;
-                if (v_form)
-                    held[u].store(Piece<kFormat>::first(w8 >> 2, lane), [&](uint32_t ch) {
-                        return dst + (ch >> 3) * 4096 + swizzled(8 * (w8 & 3) + (lane & 7), ch & 7);
-                    });
-                else
-                    held[u].store(Piece<kFormat>::first(0, lane), [&](uint32_t ch) {
-                        return dst + (ch >> 3) * 8192 + swizzled(8 * w8 + (lane & 7), ch & 7);
-                    });
-                if (then) fetch(next_of, next_v, u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive_first_cta(&bar->full[unit], 1);
-                if (++unit == kUnits) unit = 0, phase ^= 1;
-            }
-            if (then && next_v) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->place_free[next_of % kPlaceBufs]);
-            }
-            return true;
-        };
-        const Walk whole(p, pair, pairs);
-        const uint32_t n = whole.end - whole.t;  // K(0), K(1), V(0), K(2), V(1), ..., V(n - 1)
+    } else if (warp >= kBuildWarp) {
+        // ---- operands: warp b fills unit b of the ring, one lap a tile ----------------------------
+        // With n tiles the ring's order K(0), K(1), V(0), K(2), V(1), .. K(n - 1), V(n - 2), V(n - 1) gives units 0 to
+        // 3 K(0), then V(0 .. n - 2), and units 4 to 7 K(1 .. n - 1), then V(n - 1).
+        const uint32_t unit = warp - kBuildWarp, u = unit & 3;
+        const uint32_t dst = ring + unit * kUnitBytes;
+        uint32_t n = 0;
+        for (Walk w(p, pair, pairs); w.next(part);) n += part.tiles;
+        auto tile_of = [&](uint32_t lap) { return unit < 4 ? (lap ? lap - 1 : 0) : min(lap + 1, n - 1); };
+        auto v_form_of = [&](uint32_t lap) { return unit < 4 ? lap > 0 : lap + 1 >= n; };
         auto looked_up = [&](uint32_t of) {
             return wait_pair(&bar->place_full[of % kPlaceBufs], of / kPlaceBufs & 1, p.status);
         };
-        ok = looked_up(0);
-        if (ok)
-            for (uint32_t u = 0; u < 4; ++u) fetch(0, false, u);
-        for (it = 0; ok && it < n; ++it) {
-            const bool more = it + 1 < n;
-            // K(it): then V(it - 1), or without one K(1) or V(0).
-            if (it == 0) {
-                ok = !more || looked_up(1);
-                ok = ok && form(false, more ? 1 : 0, !more, true);
-            } else {
-                ok = form(false, it - 1, true, true);
-                // V(it - 1): then K(it + 1), or at the end V(it).
-                ok = ok && (!more || looked_up(it + 1));
-                ok = ok && form(true, more ? it + 1 : it, !more, true);
+        auto read = [&](uint32_t of) {  // this warp has read the tile's places
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->place_free[of % kPlaceBufs]);
+        };
+        if constexpr (kFormat == DS_CACHE_BF16) {
+            const uint32_t box = min(1u << p.cache.page_shift, (uint32_t)kBoxRows);
+            for (uint32_t lap = 0; lap < n; ++lap) {
+                const uint32_t of = tile_of(lap);
+                const bool v_form = v_form_of(lap);
+                if (!looked_up(of) || !wait_pair(&bar->empty[unit], (lap & 1) ^ 1, p.status)) break;
+                const int32_t* at = place_s + of % kPlaceBufs * kTile + (v_form ? 32 * u : 64 * rank);
+                if (!(bar->form[of % kPlaceBufs] & kByThreads)) {
+                    // Boxes of rows: lane = (row group, 64 dims).
+                    const uint32_t groups = (v_form ? 32 : 64) / box;
+                    const uint32_t row = lane % groups * box, dims = lane / groups;
+                    if (lane == 0) arrive_first_cta_expect(&bar->full[unit], kUnitBytes);
+                    __syncwarp();
+                    if (dims < (v_form ? 4u : 2u))
+                        tma_load_pair(dst + dims * (v_form ? 4096 : 8192) + row * 128, &p.kvmap, &bar->full[unit],
+                                      (int)(v_form ? v_dim(64 * dims, rank) : 128 * u + 64 * dims), at[row]);
+                    read(of);
+                } else {
+                    // Rows by 16 bytes, zeros for those that are missing.
+#pragma unroll 8
+                    for (uint32_t k = lane; k < kUnitBytes / 16; k += 32) {
+                        const uint32_t row = v_form ? k >> 5 : k >> 4, ch = v_form ? k & 31 : k & 15;  // 8 dims
+                        const int32_t place = at[row];
+                        const uint32_t dim = v_form ? v_dim(8 * ch, rank) : 128 * u + 8 * ch;
+                        cp_async16_or_zero(dst + (ch >> 3) * (v_form ? 4096 : 8192) + swizzled(row, ch & 7),
+                                           p.cache.pages + (size_t)max(place, 0) * (2 * kDim) + 2 * dim, place >= 0);
+                    }
+                    read(of);
+                    cp_async_commit_group();
+                    cp_async_wait_group<0>();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive_first_cta(&bar->full[unit]);
+                }
+            }
+        } else {
+            // Packed rows, widened: a lap's loads are issued when the lap before has been stored. Step s of a unit
+            // has eight rows (K form: 8 s ..; V form: 8 (s / 2) .., 128 dims each).
+            constexpr uint32_t kSteps = 8;
+            Piece<kFormat> held[kSteps];
+            auto fetch = [&](uint32_t lap) -> bool {
+                const uint32_t of = tile_of(lap);
+                const bool v_form = v_form_of(lap);
+                if (!looked_up(of)) return false;
+                const int32_t* at = place_s + of % kPlaceBufs * kTile + (v_form ? 32 * u : 64 * rank);
+                const uint32_t d = Piece<kFormat>::first(lane);
+#pragma unroll
+                for (uint32_t s = 0; s < kSteps; ++s) {
+                    const int32_t place = at[8 * (v_form ? s >> 1 : s) + (lane & 7)];
+                    held[s].load(p.cache, place, v_form ? v_dim(128 * (s & 1), rank) + d : 128 * u + d);
+                }
+                read(of);
+                return true;
+            };
+            if (n > 0 && fetch(0)) {
+                for (uint32_t lap = 0; lap < n; ++lap) {
+                    const bool v_form = v_form_of(lap);
+                    if (!wait_pair(&bar->empty[unit], (lap & 1) ^ 1, p.status)) break;
+#pragma unroll
+                    for (uint32_t s = 0; s < kSteps; ++s) {
+                        const uint32_t row = 8 * (v_form ? s >> 1 : s) + (lane & 7);
+                        const uint32_t block = dst + (v_form ? (s & 1) * 8192 : 0), size = v_form ? 4096 : 8192;
+                        held[s].store(Piece<kFormat>::first(lane),
+                                      [&](uint32_t ch) { return block + (ch >> 3) * size + swizzled(row, ch & 7); });
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive_first_cta(&bar->full[unit]);
+                    if (lap + 1 < n && !fetch(lap + 1)) break;
+                }
             }
         }
-        if (ok) (void)form(true, 0, false, false);  // V(n - 1)
     }
 
     tc_fence_before();
@@ -785,98 +711,128 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ---- the join of a row's parts -------------------------------------------------------------------
 
 namespace {
-constexpr int kJoinSlices = 4;  // threads of an output lane, each with every fourth part
-}
+constexpr int kJoinSlices = 8;
+constexpr int kJoinThreads = 128 * kJoinSlices;
+constexpr uint32_t kJoinSplit = 12;  // from this many parts on, the slices share a column's parts
+constexpr uint32_t kJoinParts = kPrefixPairsMax + 2;  // a row's, at most: its segments lie on one line of runs
 
-// A block joins 4 columns of the O layout (4 dims of each half of 64 heads) of one row: thread = (lane, slice).
-__global__ void __launch_bounds__(128 * kJoinSlices) prefix_join_kernel(const __grid_constant__ PrefixParams p) {
-    __shared__ float4 acc_s[kJoinSlices - 1][128];
-    __shared__ float m_s[kJoinSlices][128], l_s[kJoinSlices][128];
-    __shared__ uint32_t bad_s[kJoinSlices][128];
-    pdl_trigger();
-    const uint32_t r = blockIdx.x, col = blockIdx.y, lane = threadIdx.x & 127, slice = threadIdx.x >> 7;
-    const uint32_t head = lane & 63;
-    pdl_wait();
-    // The row's parts: those of its group's prefix, then its own.
-    struct Run {
-        uint32_t first, count, seg, cta;
-    } runs[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t seg = i == 0 ? r / 2 : p.groups + r;
-        const uint32_t begin = p.tile_begin[seg], end = p.tile_begin[seg + 1];
-        auto pair_of = [&](uint32_t t) {
-            return (uint32_t)(((uint64_t)(t + 1) * p.pairs - 1) / p.total_tiles);
-        };
-        runs[i] = {0, 0, seg, i == 0 ? r & 1 : 0u};
-        if (begin < end) {
-            runs[i].first = pair_of(begin);
-            runs[i].count = pair_of(end - 1) - runs[i].first + 1;
-        }
+// A row's parts in their order: those of its group's prefix, then its own.
+struct RowParts {
+    const float *shared, *own;  // of the first part of each
+    uint32_t n0, count;
+    static constexpr size_t kStep = 2 * kPrefixPartFloats;  // from one pair's to the next pair's
+    static __device__ __forceinline__ uint32_t runs(const PrefixParams& p, uint32_t seg, uint32_t& first) {
+        const uint32_t begin = p.begin[seg], end = p.begin[seg + 1];
+        auto pair_of = [&](uint32_t t) { return (uint32_t)(((uint64_t)(t + 1) * p.pairs - 1) / p.line); };
+        first = begin < end ? pair_of(begin + p.seg_cost) : 0;
+        return begin < end ? pair_of(end - 1) - first + 1 : 0;
     }
-    const uint32_t count = runs[0].count + runs[1].count;
-    auto part_at = [&](uint32_t i) {
-        const Run run = i < runs[0].count ? runs[0] : runs[1];
-        const uint32_t k = run.first + (i < runs[0].count ? i : i - runs[0].count);
-        return p.parts + ((size_t)(k + run.seg) * 2 + run.cta) * kPrefixPartFloats;
-    };
+    __device__ __forceinline__ RowParts(const PrefixParams& p, uint32_t r) {
+        uint32_t a, b;
+        n0 = runs(p, r / 2, a);
+        count = n0 + runs(p, p.groups + r, b);
+        shared = p.parts + (a + r / 2) * kStep + (r & 1) * kPrefixPartFloats;
+        own = p.parts + (b + p.groups + r) * kStep;
+    }
+    __device__ __forceinline__ const float* at(uint32_t i) const { return i < n0 ? shared + i * kStep : own + (i - n0) * kStep; }
+};
+}  // namespace
+
+// A block joins `cols` columns of the O layout (4 dims of each half of 64 heads) of one row. The factors
+// exp(m_i - m) of the parts come first, for every lane; then a thread = (lane, slice) has whole
+// columns (few parts), or a slice of a column's parts.
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ PrefixParams p, uint32_t cols) {
+    __shared__ float fac_s[kJoinParts][kHeads];
+    __shared__ float m_s[kJoinSlices][kHeads], l_s[kJoinSlices][kHeads];
+    __shared__ uint32_t bad_s[kJoinSlices][kHeads];
+    __shared__ float4 acc_s[kJoinSlices][128];
+    pdl_trigger();
+    const uint32_t r = blockIdx.x, lane = threadIdx.x & 127, slice = threadIdx.x >> 7, head = lane & 63;
+    const RowParts parts(p, r);
+    const size_t at = (size_t)p.q_row[r] * kHeads + head;
+    pdl_wait();
+    const float sink = p.sinks[(size_t)p.q_row[r] * p.sinks_row_stride + head];
     float m = -INFINITY;
-    uint32_t bad = 0;
-    for (uint32_t i = slice; i < count; i += kJoinSlices) {
-        const float* part = part_at(i);
-        m = fmaxf(m, __ldcg(part + lane));
+    uint32_t bad = *p.status != 0 ? 1u : 0u;
+#pragma unroll 4
+    for (uint32_t i = slice; i < parts.count; i += kJoinSlices) {
+        const float* part = parts.at(i);
         const uint32_t* flags = reinterpret_cast<const uint32_t*>(part) + 256;
+        m = fmaxf(m, __ldcg(part + head));  // both of a head's lanes have it
         bad |= __ldcg(flags + head) | __ldcg(flags + 64 + head);
     }
-    m_s[slice][lane] = m;
-    bad_s[slice][lane] = bad;
+    m_s[slice][head] = m;
+    bad_s[slice][head] = bad;
     __syncthreads();
-    const float sink = p.sinks[(size_t)p.q_row[r] * p.sinks_row_stride + head];
     float top = sink * kLog2e;
-    bad = *p.status != 0 ? 1u : 0u;
+    bad = 0;
 #pragma unroll
     for (int s = 0; s < kJoinSlices; ++s) {
-        top = fmaxf(top, m_s[s][lane]);
-        bad |= bad_s[s][lane];
+        top = fmaxf(top, m_s[s][head]);
+        bad |= bad_s[s][head];
     }
     float l = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (uint32_t i = slice; i < count; i += kJoinSlices) {
-        const float* part = part_at(i);
-        const float f = exp2f(__ldcg(part + lane) - top);
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(part + 3 * 128) + col * 128 + lane);
+    for (uint32_t i = slice; i < parts.count; i += kJoinSlices) {
+        const float* part = parts.at(i);
+        const float f = exp2f(__ldcg(part + head) - top);
+        fac_s[i][head] = f;
         l = fmaf(__ldcg(part + 128 + head) + __ldcg(part + 192 + head), f, l);
+    }
+    l_s[slice][head] = l;
+    __syncthreads();
+    float den = exp2f(sink * kLog2e - top);
+#pragma unroll
+    for (int s = 0; s < kJoinSlices; ++s) den += l_s[s][head];
+    const bool zero = bad || !finite_f(sink) || !finite_f(top) || !finite_f(den) || !(den > 0.0f);
+    const float inv = 1.0f / den;
+    if (p.invalid && blockIdx.y == 0 && threadIdx.x < 64) p.invalid[at] = zero ? 1u : 0u;
+
+    auto add = [&](float4& acc, uint32_t i, uint32_t col) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(parts.at(i) + 3 * 128) + col * 128 + lane);
+        const float f = fac_s[i][head];
         acc.x = fmaf(o.x, f, acc.x);
         acc.y = fmaf(o.y, f, acc.y);
         acc.z = fmaf(o.z, f, acc.z);
         acc.w = fmaf(o.w, f, acc.w);
+    };
+    auto put = [&](const float4& acc, uint32_t col) {
+        const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+        __align__(8) __nv_bfloat16 y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = __float2bfloat16_rn(!zero && finite_f(x[k]) ? x[k] : 0.0f);
+        const uint32_t dim = 256 * (col >> 5) + 128 * (lane >> 6) + 4 * (col & 31);
+        *reinterpret_cast<uint2*>(p.out + at * kDim + dim) = *reinterpret_cast<const uint2*>(y);
+    };
+    const uint32_t col0 = blockIdx.y * cols;
+    if (parts.count < kJoinSplit) {
+        for (uint32_t c = slice; c < cols; c += kJoinSlices) {
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (uint32_t i = 0; i < parts.count; ++i) add(acc, i, col0 + c);
+            put(acc, col0 + c);
+        }
+        return;
     }
-    l_s[slice][lane] = l;
-    if (slice > 0) acc_s[slice - 1][lane] = acc;
-    __syncthreads();
-    if (slice > 0) return;
-    float den = exp2f(sink * kLog2e - top);
+    for (uint32_t c = 0; c < cols; ++c) {
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (uint32_t i = slice; i < parts.count; i += kJoinSlices) add(acc, i, col0 + c);
+        acc_s[slice][lane] = acc;
+        __syncthreads();
+        if (slice == 0) {
 #pragma unroll
-    for (int s = 0; s < kJoinSlices; ++s) den += l_s[s][lane];
-#pragma unroll
-    for (int s = 0; s < kJoinSlices - 1; ++s) {
-        const float4 o = acc_s[s][lane];
-        acc.x += o.x;
-        acc.y += o.y;
-        acc.z += o.z;
-        acc.w += o.w;
+            for (int s = 1; s < kJoinSlices; ++s) {
+                const float4 o = acc_s[s][lane];
+                acc.x += o.x;
+                acc.y += o.y;
+                acc.z += o.z;
+                acc.w += o.w;
+            }
+            put(acc, col0 + c);
+        }
+        __syncthreads();
     }
-    const bool zero = bad || !finite_f(sink) || !finite_f(top) || !finite_f(den) || !(den > 0.0f);
-    const float inv = 1.0f / den;
-    const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-    __align__(8) __nv_bfloat16 y[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] = __float2bfloat16_rn(!zero && finite_f(x[k]) ? x[k] : 0.0f);
-    const uint32_t dim = 256 * (col >> 5) + 128 * (lane >> 6) + 4 * (col & 31);
-    const size_t at = (size_t)p.q_row[r] * kHeads + head;
-    *reinterpret_cast<uint2*>(p.out + at * kDim + dim) = *reinterpret_cast<const uint2*>(y);
-    if (p.invalid && col == 0 && lane < 64) p.invalid[at] = zero ? 1u : 0u;
 }
 
 template <int kFormat>
@@ -886,7 +842,9 @@ static cudaError_t launch(const PrefixParams& p, cudaStream_t stream, bool pdl) 
     if (err != cudaSuccess) return err;
     err = launch_kernel(prefix_attn_kernel<kFormat>, dim3(2 * p.pairs), dim3(kThreads), kSmem, stream, pdl, p);
     if (err != cudaSuccess) return err;
-    return launch_kernel(prefix_join_kernel, dim3(p.rows, 64), dim3(128 * kJoinSlices), 0, stream, true, p);
+    // Columns a block: enough blocks for the GPU, and at least a column for each slice where the rows are many.
+    const uint32_t cols = p.rows >= 16 ? 16 : p.rows >= 8 ? 8 : p.rows >= 4 ? 4 : p.rows >= 2 ? 2 : 1;
+    return launch_kernel(prefix_join_kernel, dim3(p.rows, 64 / cols), dim3(kJoinThreads), 0, stream, true, p, cols);
 }
 
 cudaError_t launch_prefix_attn(const PrefixParams& p, int format, cudaStream_t stream, bool pdl) {
