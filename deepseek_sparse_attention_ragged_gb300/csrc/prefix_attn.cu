@@ -42,9 +42,12 @@ constexpr int kQBytes = kHeads * kDim * 2;    // the CTA's query row, 8 blocks [
 constexpr int kPBytes = kHeads * kTile * 2;   // P: 2 blocks [64 heads][64 slots]
 constexpr int kBoxRows = kPrefixBoxRows;      // most rows of a TMA box
 constexpr int kPlaceBufs = 4;                 // tiles whose rows are looked up
-constexpr int kThreads = 512;
 constexpr int kSoftmaxWarp = 4, kBuildWarp = 8;
-static_assert(kThreads / 32 == kBuildWarp + kUnits, "a warp for each unit");
+// Warps that fill a ring unit: packed rows are widened by two.
+template <int kFormat>
+constexpr int kFillers = kFormat == DS_CACHE_BF16 ? 1 : 2;
+template <int kFormat>
+constexpr int kThreads = 32 * (kBuildWarp + kUnits * kFillers<kFormat>);
 constexpr uint32_t kOCol = 128;               // TMEM: two S of 64 columns, then O
 constexpr uint32_t kTmemCols = 512;
 constexpr uint16_t kBoth = 3;                 // the CTAs of a pair
@@ -122,10 +125,10 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
         : "memory");
 }
 // A bounded wait of a whole warp (its lanes go on or give up together), whose first tries read no timer.
-__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, uint32_t* status) {
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t* status) {
     bool ok = false;
-    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait_cluster(bar, parity);
-    if (!ok) ok = mbar_wait_cluster(bar, parity, status);
+    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+    if (!ok) ok = mbar_wait(bar, parity, status);
     return __all_sync(0xFFFFFFFFu, ok);
 }
 
@@ -305,7 +308,7 @@ struct Walk {
 }  // namespace
 
 template <int kFormat>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1)
     prefix_attn_kernel(const __grid_constant__ PrefixParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -318,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kUnits; ++i) {
-            mbar_init(&bar->full[i], 2);
+            mbar_init(&bar->full[i], 2 * kFillers<kFormat>);
             mbar_init(&bar->empty[i], 1);
         }
         mbar_init(&bar->q_full, 2);
@@ -332,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kPlaceBufs; ++i) {
             mbar_init(&bar->place_full[i], 1);
-            mbar_init(&bar->place_free[i], 4 + 4 + 4);  // K form, V form, softmax
+            mbar_init(&bar->place_free[i], 2 * 4 * kFillers<kFormat> + 4);  // K form, V form, softmax
         }
         fence_barrier_init();
     }
@@ -380,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     all = all && at[k] >= 0;
                 }
                 all = __all_sync(0xFFFFFFFFu, all);
-                if (!wait_pair(&bar->place_free[buf], (it / kPlaceBufs & 1) ^ 1, p.status)) {
+                if (!wait_warp(&bar->place_free[buf], (it / kPlaceBufs & 1) ^ 1, p.status)) {
                     ok = false;
                     break;
                 }
@@ -399,26 +402,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             constexpr uint32_t idesc_o = idesc_bf16_f32(128, 256) | 1u << 16;  // B is MN-major
             const uint32_t q_base = smem_u32(smem + Layout::q), p_base = smem_u32(smem + Layout::p);
             uint32_t unit = 0, phase = 0;
+            uint32_t ready = 0;  // units from `unit` on that are known to be full
             bool ok = true;
+            // A full unit at `unit`: the lanes look at the next eight together, since a wait for each takes about as
+            // long as its MMAs.
+            auto wait_unit = [&]() -> bool {
+                if (ready > 0) return true;
+                uint64_t start = 0;
+                for (uint32_t tries = 0;; ++tries) {
+                    const uint32_t at = unit + (lane & (kUnits - 1));
+                    const bool full = mbar_try_wait(&bar->full[at & (kUnits - 1)], phase ^ (at >= kUnits ? 1u : 0u));
+                    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, full) & ((1u << kUnits) - 1);
+                    ready = __ffs(~bits) - 1;
+                    if (ready > 0) return true;
+                    if ((tries & 63) == 63) {
+                        const uint64_t now = __shfl_sync(0xFFFFFFFFu, global_timer_ns(), 0);
+                        if (start == 0) start = now;
+                        if (now - start > kWaitBudgetNs) {
+                            if (lane == 0) atomicOr(p.status, kStatusWaitTimeout);
+                            return false;
+                        }
+                    }
+                }
+            };
             auto next_unit = [&] {
+                --ready;
                 if (++unit == kUnits) unit = 0, phase ^= 1;
             };
             // O += P G of tile `of`; `fresh`: the part's first tile.
             auto accumulate = [&](uint32_t of, bool fresh) -> bool {
-                if (!wait_pair(&bar->p_full, of & 1, p.status)) return false;
+                if (!wait_warp(&bar->p_full, of & 1, p.status)) return false;
                 tc_fence_after();
 #pragma unroll 1
                 for (uint32_t v = 0; v < 4; ++v) {
-                    if (!wait_pair(&bar->full[unit], phase, p.status)) return false;
+                    if (!wait_unit()) return false;
                     const uint32_t b = ring + unit * kUnitBytes;
+                    const uint64_t a_desc = smem_desc_sw128_kmajor(p_base + (v >> 1) * 8192 + (v & 1) * 64);
+                    const uint64_t b_desc = smem_desc_sw128_mnmajor(b, 4096, 1024);
                     if (elect_one()) {
 #pragma unroll
                         for (uint32_t ks = 0; ks < 2; ++ks)
 #pragma unroll
                             for (uint32_t j = 0; j < 2; ++j)
-                                umma2_bf16(tmem + kOCol + 128 * j,
-                                           smem_desc_sw128_kmajor(p_base + (v >> 1) * 8192 + ((v & 1) * 2 + ks) * 32),
-                                           smem_desc_sw128_mnmajor(b + j * 8192 + ks * 2048, 4096, 1024), idesc_o,
+                                umma2_bf16(tmem + kOCol + 128 * j, a_desc + ks * (32 >> 4),
+                                           b_desc + ((j * 8192 + ks * 2048) >> 4), idesc_o,
                                            fresh && v == 0 && ks == 0 ? 0u : 1u);
                         umma2_commit(&bar->empty[unit]);
                         if (v == 3) umma2_commit(&bar->pv_done);
@@ -433,19 +460,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (Walk w(p, pair, pairs); ok && w.next(part); ++n_part) {
                 for (uint32_t i = 0; ok && i < part.tiles; ++i, ++it) {
                     const uint32_t buf = it & 1;
-                    ok = i != 0 || wait_pair(&bar->q_full, n_part & 1, p.status);
-                    ok = ok && wait_pair(&bar->s_free[buf], (it >> 1 & 1) ^ 1, p.status);
+                    ok = i != 0 || wait_warp(&bar->q_full, n_part & 1, p.status);
+                    ok = ok && wait_warp(&bar->s_free[buf], (it >> 1 & 1) ^ 1, p.status);
                     tc_fence_after();
 #pragma unroll 1
                     for (uint32_t u = 0; ok && u < 4; ++u) {
-                        ok = wait_pair(&bar->full[unit], phase, p.status);
+                        ok = wait_unit();
                         if (!ok) break;
-                        const uint32_t b = ring + unit * kUnitBytes, a = q_base + u * kUnitBytes;
+                        const uint64_t a_desc = smem_desc_sw128_kmajor(q_base + u * kUnitBytes);
+                        const uint64_t b_desc = smem_desc_sw128_kmajor(ring + unit * kUnitBytes);
                         if (elect_one()) {
 #pragma unroll
                             for (uint32_t ks = 0; ks < 8; ++ks)
-                                umma2_bf16(tmem + buf * 64, smem_desc_sw128_kmajor(a + (ks >> 2) * 8192 + (ks & 3) * 32),
-                                           smem_desc_sw128_kmajor(b + (ks >> 2) * 8192 + (ks & 3) * 32), idesc_s,
+                                umma2_bf16(tmem + buf * 64, a_desc + (((ks >> 2) * 8192 + (ks & 3) * 32) >> 4),
+                                           b_desc + (((ks >> 2) * 8192 + (ks & 3) * 32) >> 4), idesc_s,
                                            u == 0 && ks == 0 ? 0u : 1u);
                             umma2_commit(&bar->empty[unit]);
                             if (u == 3) {
@@ -464,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // Whatever was issued is done before the CTAs leave.
             if (elect_one()) umma2_commit(&bar->drained);
             __syncwarp();
-            (void)wait_pair(&bar->drained, 0, p.status);
+            (void)wait_warp(&bar->drained, 0, p.status);
         }
     } else if (warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4) {
         // ---- softmax: thread = TMEM lane = (head, half of the tile's slots) ---------------------
@@ -481,42 +509,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t bad = 0;
             for (uint32_t i = 0; i < part.tiles; ++i, ++it) {
                 const uint32_t buf = it & 1, pbuf = it % kPlaceBufs;
-                uint32_t lo[32], hi[32];
-                if (!(ok = wait_pair(&bar->s_full[buf], it >> 1 & 1, p.status))) break;
+                if (!(ok = wait_warp(&bar->s_full[buf], it >> 1 & 1, p.status))) break;
                 tc_fence_after();
-                tmem_ld_x32(lanes + buf * 64, lo);
-                tmem_ld_x32(lanes + buf * 64 + 32, hi);
-                tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_first_cta(&bar->s_free[buf]);
-                // 0 * t is NaN exactly where a logit is not finite.
-                float2 t[32], odd = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const uint32_t x = c < 16 ? lo[2 * c] : hi[2 * c - 32], y = c < 16 ? lo[2 * c + 1] : hi[2 * c - 31];
-                    t[c] = mul2(make_float2(__uint_as_float(x), __uint_as_float(y)), scale2);
-                    odd = fma2(t[c], make_float2(0.0f, 0.0f), odd);
-                }
-                if (!(odd.x + odd.y == 0.0f)) bad = 1;
-                if (!(ok = wait_pair(&bar->place_full[pbuf], it / kPlaceBufs & 1, p.status))) break;
-                if (bar->form[pbuf] & kMasked) {
-                    const ::int4* at = reinterpret_cast<const ::int4*>(place_s + pbuf * kTile + half * 64);
+                if (!(ok = wait_warp(&bar->place_full[pbuf], it / kPlaceBufs & 1, p.status))) break;
+                const bool masked = bar->form[pbuf] & kMasked;
+                const ::int4* at = reinterpret_cast<const ::int4*>(place_s + pbuf * kTile + half * 64);
+                // The largest logit. 0 * t is NaN exactly where one is not finite.
+                float top = -INFINITY;
+                float2 odd = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+                for (uint32_t h = 0; h < 2; ++h) {
+                    uint32_t v[32];
+                    tmem_ld_x32(lanes + buf * 64 + 32 * h, v);
+                    tmem_ld_wait();
+                    float2 t[16];
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        const ::int4 a = at[c];
-                        if (a.x == kBadRow || a.y == kBadRow || a.z == kBadRow || a.w == kBadRow) bad = 1;
-                        if (a.x < 0) t[2 * c].x = -INFINITY;
-                        if (a.y < 0) t[2 * c].y = -INFINITY;
-                        if (a.z < 0) t[2 * c + 1].x = -INFINITY;
-                        if (a.w < 0) t[2 * c + 1].y = -INFINITY;
+                        t[c] = mul2(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), scale2);
+                        odd = fma2(t[c], make_float2(0.0f, 0.0f), odd);
                     }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->place_free[pbuf]);
-                float top = fmaxf(t[0].x, t[0].y);
+                    if (masked) {
 #pragma unroll
-                for (int c = 1; c < 32; ++c) top = fmaxf(top, fmaxf(t[c].x, t[c].y));
+                        for (int c = 0; c < 8; ++c) {
+                            const ::int4 a = at[8 * h + c];
+                            if (a.x == kBadRow || a.y == kBadRow || a.z == kBadRow || a.w == kBadRow) bad = 1;
+                            if (a.x < 0) t[2 * c].x = -INFINITY;
+                            if (a.y < 0) t[2 * c].y = -INFINITY;
+                            if (a.z < 0) t[2 * c + 1].x = -INFINITY;
+                            if (a.w < 0) t[2 * c + 1].y = -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) top = fmaxf(top, fmaxf(t[c].x, t[c].y));
+                }
+                if (!(odd.x + odd.y == 0.0f)) bad = 1;
                 red[buf * 128 + row] = top;
                 sync_softmax();
                 ++met;
@@ -531,19 +557,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     sum *= f;
                 }
                 const bool moved = __any_sync(0xFFFFFFFFu, f != 1.0f);
+                // The weights, from S again: 64 logits and 64 weights at once are more registers than there are.
                 const float2 minus = make_float2(-m, -m);
                 float2 s2 = make_float2(0.0f, 0.0f);
                 uint32_t w16[32];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float2 x = add2(t[c], minus);
-                    const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-                    s2 = add2(s2, e);
-                    w16[c] = pack_bf16(e.x, e.y);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[32];
+                    tmem_ld_x32(lanes + buf * 64 + 32 * h, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float2 x = fma2(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), scale2,
+                                              minus);
+                        float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                        if (masked) {
+                            const int2 a = reinterpret_cast<const int2*>(at)[16 * h + c];
+                            e = make_float2(a.x < 0 ? 0.0f : e.x, a.y < 0 ? 0.0f : e.y);
+                        }
+                        s2 = add2(s2, e);
+                        w16[16 * h + c] = pack_bf16(e.x, e.y);
+                    }
                 }
                 sum += s2.x + s2.y;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    arrive_first_cta(&bar->s_free[buf]);
+                    mbar_arrive(&bar->place_free[pbuf]);
+                }
                 // P G of the tile before is done: P may be overwritten, and O scaled.
-                if (it > 0 && !(ok = wait_pair(&bar->pv_done, (it - 1) & 1, p.status))) break;
+                if (it > 0 && !(ok = wait_warp(&bar->pv_done, (it - 1) & 1, p.status))) break;
                 tc_fence_after();
                 if (moved) {
 #pragma unroll 1
@@ -567,7 +611,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) arrive_first_cta(&bar->p_full);
             }
             // ---- the part's state: m, sum, flag and O per lane ----------------------------------
-            if (!ok || !(ok = wait_pair(&bar->pv_done, (it - 1) & 1, p.status))) break;
+            if (!ok || !(ok = wait_warp(&bar->pv_done, (it - 1) & 1, p.status))) break;
             tc_fence_after();
             float* out = p.parts + ((size_t)(pair + part.seg) * 2 + rank) * kPrefixPartFloats;
             const uint32_t r = part.seg < p.groups ? 2 * part.seg + rank : rank == 0 ? part.seg - p.groups : p.rows;
@@ -599,7 +643,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---- each part's query, once the MMAs of the part before have read theirs --------------
         uint32_t n_part = 0;
         for (Walk w(p, pair, pairs); w.next(part); ++n_part) {
-            if (n_part > 0 && !wait_pair(&bar->q_free, (n_part - 1) & 1, p.status)) break;
+            if (n_part > 0 && !wait_warp(&bar->q_free, (n_part - 1) & 1, p.status)) break;
             const uint32_t r = part.seg < p.groups ? min(2 * part.seg + rank, p.rows - 1) : part.seg - p.groups;
             if (lane == 0) arrive_first_cta_expect(&bar->q_full, kQBytes);
             __syncwarp();
@@ -608,17 +652,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                               (int)(p.q_row[r] * kHeads));
         }
     } else if (warp >= kBuildWarp) {
-        // ---- operands: warp b fills unit b of the ring, one lap a tile ----------------------------
+        // ---- operands: warp b fills unit b (mod kUnits) of the ring, one lap a tile ----------------
         // With n tiles the ring's order K(0), K(1), V(0), K(2), V(1), .. K(n - 1), V(n - 2), V(n - 1) gives units 0 to
         // 3 K(0), then V(0 .. n - 2), and units 4 to 7 K(1 .. n - 1), then V(n - 1).
-        const uint32_t unit = warp - kBuildWarp, u = unit & 3;
+        const uint32_t unit = (warp - kBuildWarp) % kUnits, u = unit & 3;
         const uint32_t dst = ring + unit * kUnitBytes;
         uint32_t n = 0;
         for (Walk w(p, pair, pairs); w.next(part);) n += part.tiles;
         auto tile_of = [&](uint32_t lap) { return unit < 4 ? (lap ? lap - 1 : 0) : min(lap + 1, n - 1); };
         auto v_form_of = [&](uint32_t lap) { return unit < 4 ? lap > 0 : lap + 1 >= n; };
         auto looked_up = [&](uint32_t of) {
-            return wait_pair(&bar->place_full[of % kPlaceBufs], of / kPlaceBufs & 1, p.status);
+            return wait_warp(&bar->place_full[of % kPlaceBufs], of / kPlaceBufs & 1, p.status);
         };
         auto read = [&](uint32_t of) {  // this warp has read the tile's places
             __syncwarp();
@@ -629,7 +673,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (uint32_t lap = 0; lap < n; ++lap) {
                 const uint32_t of = tile_of(lap);
                 const bool v_form = v_form_of(lap);
-                if (!looked_up(of) || !wait_pair(&bar->empty[unit], (lap & 1) ^ 1, p.status)) break;
+                if (!looked_up(of) || !wait_warp(&bar->empty[unit], (lap & 1) ^ 1, p.status)) break;
                 const int32_t* at = place_s + of % kPlaceBufs * kTile + (v_form ? 32 * u : 64 * rank);
                 if (!(bar->form[of % kPlaceBufs] & kByThreads)) {
                     // Boxes of rows: lane = (row group, 64 dims).
@@ -660,9 +704,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         } else {
-            // Packed rows, widened: a lap's loads are issued when the lap before has been stored. Step s of a unit
-            // has eight rows (K form: 8 s ..; V form: 8 (s / 2) .., 128 dims each).
-            constexpr uint32_t kSteps = 8;
+            // Packed rows, widened: a lap's loads are issued when the lap before has been stored. Step s of a unit's
+            // eight has eight rows (K form: 8 s ..; V form: 8 (s / 2) .., 128 dims each); each of its warps has four.
+            constexpr uint32_t kSteps = 8 / kFillers<kFormat>;
+            const uint32_t s0 = (warp - kBuildWarp) / kUnits * kSteps;
             Piece<kFormat> held[kSteps];
             auto fetch = [&](uint32_t lap) -> bool {
                 const uint32_t of = tile_of(lap);
@@ -672,7 +717,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t d = Piece<kFormat>::first(lane);
 #pragma unroll
                 for (uint32_t s = 0; s < kSteps; ++s) {
-                    const int32_t place = at[8 * (v_form ? s >> 1 : s) + (lane & 7)];
+                    const int32_t place = at[8 * (v_form ? (s0 + s) >> 1 : s0 + s) + (lane & 7)];
                     held[s].load(p.cache, place, v_form ? v_dim(128 * (s & 1), rank) + d : 128 * u + d);
                 }
                 read(of);
@@ -681,10 +726,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (n > 0 && fetch(0)) {
                 for (uint32_t lap = 0; lap < n; ++lap) {
                     const bool v_form = v_form_of(lap);
-                    if (!wait_pair(&bar->empty[unit], (lap & 1) ^ 1, p.status)) break;
+                    if (!wait_warp(&bar->empty[unit], (lap & 1) ^ 1, p.status)) break;
 #pragma unroll
                     for (uint32_t s = 0; s < kSteps; ++s) {
-                        const uint32_t row = 8 * (v_form ? s >> 1 : s) + (lane & 7);
+                        const uint32_t row = 8 * (v_form ? (s0 + s) >> 1 : s0 + s) + (lane & 7);
                         const uint32_t block = dst + (v_form ? (s & 1) * 8192 : 0), size = v_form ? 4096 : 8192;
                         held[s].store(Piece<kFormat>::first(lane),
                                       [&](uint32_t ch) { return block + (ch >> 3) * size + swizzled(row, ch & 7); });
@@ -712,6 +757,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 namespace {
 constexpr int kJoinSlices = 8;
+constexpr int kJoinCols = 2;
+constexpr size_t kJoinSmem = sizeof(float4) * kJoinCols * kJoinSlices * 128;
 constexpr int kJoinThreads = 128 * kJoinSlices;
 constexpr uint32_t kJoinSplit = 12;  // from this many parts on, the slices share a column's parts
 constexpr uint32_t kJoinParts = kPrefixPairsMax + 2;  // a row's, at most: its segments lie on one line of runs
@@ -745,7 +792,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     __shared__ float fac_s[kJoinParts][kHeads];
     __shared__ float m_s[kJoinSlices][kHeads], l_s[kJoinSlices][kHeads];
     __shared__ uint32_t bad_s[kJoinSlices][kHeads];
-    __shared__ float4 acc_s[kJoinSlices][128];
+    extern __shared__ __align__(16) float4 acc_raw[];  // [kJoinCols][kJoinSlices][128]
+    auto acc_s = reinterpret_cast<float4(*)[kJoinSlices][128]>(acc_raw);
     pdl_trigger();
     const uint32_t r = blockIdx.x, lane = threadIdx.x & 127, slice = threadIdx.x >> 7, head = lane & 63;
     const RowParts parts(p, r);
@@ -814,22 +862,28 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
         }
         return;
     }
-    for (uint32_t c = 0; c < cols; ++c) {
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (uint32_t i = slice; i < parts.count; i += kJoinSlices) add(acc, i, col0 + c);
-        acc_s[slice][lane] = acc;
+    for (uint32_t c = 0; c < cols; c += kJoinCols) {
+        float4 acc[kJoinCols];
+#pragma unroll
+        for (int k = 0; k < kJoinCols; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 5
+        for (uint32_t i = slice; i < parts.count; i += kJoinSlices)
+#pragma unroll
+            for (int k = 0; k < kJoinCols; ++k) add(acc[k], i, col0 + c + k);
+#pragma unroll
+        for (int k = 0; k < kJoinCols; ++k) acc_s[k][slice][lane] = acc[k];
         __syncthreads();
-        if (slice == 0) {
+        if (slice < kJoinCols) {
+            float4 sum = acc_s[slice][0][lane];
 #pragma unroll
             for (int s = 1; s < kJoinSlices; ++s) {
-                const float4 o = acc_s[s][lane];
-                acc.x += o.x;
-                acc.y += o.y;
-                acc.z += o.z;
-                acc.w += o.w;
+                const float4 o = acc_s[slice][s][lane];
+                sum.x += o.x;
+                sum.y += o.y;
+                sum.z += o.z;
+                sum.w += o.w;
             }
-            put(acc, col0 + c);
+            put(sum, col0 + c + slice);
         }
         __syncthreads();
     }
@@ -840,11 +894,15 @@ static cudaError_t launch(const PrefixParams& p, cudaStream_t stream, bool pdl) 
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t err = set_smem_limit_once(prefix_attn_kernel<kFormat>, kSmem, smem_set);
     if (err != cudaSuccess) return err;
-    err = launch_kernel(prefix_attn_kernel<kFormat>, dim3(2 * p.pairs), dim3(kThreads), kSmem, stream, pdl, p);
+    err = launch_kernel(prefix_attn_kernel<kFormat>, dim3(2 * p.pairs), dim3(kThreads<kFormat>), kSmem, stream, pdl, p);
     if (err != cudaSuccess) return err;
-    // Columns a block: enough blocks for the GPU, and at least a column for each slice where the rows are many.
-    const uint32_t cols = p.rows >= 16 ? 16 : p.rows >= 8 ? 8 : p.rows >= 4 ? 4 : p.rows >= 2 ? 2 : 1;
-    return launch_kernel(prefix_join_kernel, dim3(p.rows, 64 / cols), dim3(kJoinThreads), 0, stream, true, p, cols);
+    // Columns a block: about two blocks for each multiprocessor.
+    static std::atomic<uint64_t> join_set{0};
+    err = set_smem_limit_once(prefix_join_kernel, kJoinSmem, join_set);
+    if (err != cudaSuccess) return err;
+    uint32_t cols = kJoinCols;
+    while (p.rows * (64 / cols) > 4 * kPrefixPairsMax) cols *= 2;
+    return launch_kernel(prefix_join_kernel, dim3(p.rows, 64 / cols), dim3(kJoinThreads), kJoinSmem, stream, true, p, cols);
 }
 
 cudaError_t launch_prefix_attn(const PrefixParams& p, int format, cudaStream_t stream, bool pdl) {
