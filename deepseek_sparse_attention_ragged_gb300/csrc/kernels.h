@@ -217,8 +217,10 @@ constexpr uint32_t kPrefixSegsMax = kPrefixRowsMax / 2 + kPrefixRowsMax;
 constexpr uint32_t kPrefixPairsMax = 76;  // of this GPU's 152 multiprocessors
 constexpr uint32_t kPrefixTile = 128;
 constexpr uint32_t kPrefixBoxRows = 32;  // a TMA box of rows: this many, or a smaller page
-// m, sum and flag of each TMEM lane (head, half), then O [64 column groups][128 lanes][4].
-constexpr size_t kPrefixPartFloats = 3 * 128 + (size_t)DS_HEADS * DS_DIM;
+// For each TMEM lane (head, half) the maximum that O refers to, the two softmax sets' sums and their
+// flags; then O [64 column groups][128 lanes][4].
+constexpr size_t kPrefixHeadFloats = 5 * 128;
+constexpr size_t kPrefixPartFloats = kPrefixHeadFloats + (size_t)DS_HEADS * DS_DIM;
 
 struct PrefixParams {
     CUtensorMap qmap;   // bf16 [Q * 64, 512], box {64, 64}, 128-B swizzle

@@ -19,8 +19,8 @@
 // M = 128 it would fill TMEM alone. Each CTA keeps its own softmax: its 64 heads see every slot of the tile,
 // so nothing but the operands crosses the pair.
 //
-// Warp roles: 0 looks up the tiles' rows, 1 issues the MMAs (in the pair's first CTA), 4 to 7
-// do the softmax (a thread has 64 slots of one head); 3 loads the queries, and 8 to 15
+// Warp roles: 0 looks up the tiles' rows, 1 issues the MMAs (in the pair's first CTA), 4 to 11
+// do the softmax (a thread has 64 slots of one head); 3 loads the queries, and the others
 // bring the operands, each one unit of a ring. The K form (64 slots
 // x 128 dims) and the V form (32 slots x 256 dims) of the rows go through one ring of 16 KB units in
 // the order in which the MMAs take them: S of the next tile comes before P . G of this one.
@@ -42,7 +42,7 @@ constexpr int kQBytes = kHeads * kDim * 2;    // the CTA's query row, 8 blocks [
 constexpr int kPBytes = kHeads * kTile * 2;   // P: 2 blocks [64 heads][64 slots]
 constexpr int kBoxRows = kPrefixBoxRows;      // most rows of a TMA box
 constexpr int kPlaceBufs = 4;                 // tiles whose rows are looked up
-constexpr int kSoftmaxWarp = 4, kBuildWarp = 8;
+constexpr int kSoftmaxWarp = 4, kBuildWarp = 12;  // two sets of four softmax warps
 // Warps that fill a ring unit: packed rows are widened by two.
 template <int kFormat>
 constexpr int kFillers = kFormat == DS_CACHE_BF16 ? 1 : 2;
@@ -66,16 +66,17 @@ struct Layout {
     static constexpr size_t p = q + kQBytes;
     static constexpr size_t place = p + kPBytes;                         // i32 [kPlaceBufs][128]
     static constexpr size_t red = place + kPlaceBufs * kTile * 4;        // f32 [2][128]
-    static constexpr size_t bars = red + 2 * 128 * 4;
+    static constexpr size_t maxima = red + 2 * 128 * 4;                  // f32 [2][128]
+    static constexpr size_t bars = maxima + 2 * 128 * 4;
 };
 
 struct __align__(8) Bars {
     // In the pair's first CTA, from both:
     uint64_t full[kUnits];
-    uint64_t q_full, p_full, s_free[2];
+    uint64_t q_full, p_full, s_free[2], o_read;
     // In each CTA:
     uint64_t empty[kUnits];
-    uint64_t q_free, s_full[2], pv_done, drained;
+    uint64_t q_free, s_full[2], pv_done[2], m_ready[2], drained;
     uint64_t place_full[kPlaceBufs], place_free[kPlaceBufs];
     uint32_t form[kPlaceBufs];     // of the tile: kMasked, kByThreads
     uint32_t tmem_base;
@@ -176,9 +177,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
 }
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&v)[4]) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                 : "memory");
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
@@ -193,7 +193,9 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void sync_softmax(uint32_t set) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + set) : "memory");
+}
 
 // ---- the operands ------------------------------------------------------------------------------
 
@@ -249,7 +251,7 @@ struct Piece {
                     uint32_t o[4];
                     fp8::widen(words[2 * c], f, o);
                     fp8::widen(words[2 * c + 1], f, o + 2);
-                    st_shared_v4(dst(ch + c), o);
+                    st_shared_v4(dst(ch + c), o[0], o[1], o[2], o[3]);
                 }
             } else {
                 int4::Factors f[2];
@@ -258,7 +260,7 @@ struct Piece {
                 for (uint32_t c = 0; c < 4; ++c) {
                     uint32_t o[4];
                     int4::widen(words[c], f[c >> 1], o);
-                    st_shared_v4(dst(ch + c), o);
+                    st_shared_v4(dst(ch + c), o[0], o[1], o[2], o[3]);
                 }
             }
         }
@@ -327,11 +329,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
         mbar_init(&bar->q_full, 2);
         mbar_init(&bar->p_full, 8);
         mbar_init(&bar->q_free, 1);
-        mbar_init(&bar->pv_done, 1);
+        mbar_init(&bar->o_read, 8);
         mbar_init(&bar->drained, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar->s_free[i], 8);
             mbar_init(&bar->s_full[i], 1);
+            mbar_init(&bar->pv_done[i], 1);
+            mbar_init(&bar->m_ready[i], 4);
         }
         for (int i = 0; i < kPlaceBufs; ++i) {
             mbar_init(&bar->place_full[i], 1);
@@ -429,9 +433,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 --ready;
                 if (++unit == kUnits) unit = 0, phase ^= 1;
             };
-            // O += P G of tile `of`; `fresh`: the part's first tile.
+            // O += P G of tile `of`; `fresh`: the part's first tile, which begins O anew (the part before has been read).
+            uint32_t begun = 0;
             auto accumulate = [&](uint32_t of, bool fresh) -> bool {
                 if (!wait_warp(&bar->p_full, of & 1, p.status)) return false;
+                if (fresh && begun++ > 0 && !wait_warp(&bar->o_read, begun & 1, p.status)) return false;
                 tc_fence_after();
 #pragma unroll 1
                 for (uint32_t v = 0; v < 4; ++v) {
@@ -448,7 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                                            b_desc + ((j * 8192 + ks * 2048) >> 4), idesc_o,
                                            fresh && v == 0 && ks == 0 ? 0u : 1u);
                         umma2_commit(&bar->empty[unit]);
-                        if (v == 3) umma2_commit(&bar->pv_done);
+                        if (v == 3) umma2_commit(&bar->pv_done[of & 1]);
                     }
                     __syncwarp();
                     next_unit();
@@ -494,22 +500,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             __syncwarp();
             (void)wait_warp(&bar->drained, 0, p.status);
         }
-    } else if (warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4) {
-        // ---- softmax: thread = TMEM lane = (head, half of the tile's slots) ---------------------
-        const uint32_t row = threadIdx.x - 32 * kSoftmaxWarp;  // 0 .. 127
-        const uint32_t head = row & 63, half = row >> 6;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp - kSoftmaxWarp)) << 16);
-        float* red = reinterpret_cast<float*>(smem + Layout::red);
-        uint8_t* p_row = smem + Layout::p + half * 8192;
+    } else if (warp >= kSoftmaxWarp && warp < kBuildWarp) {
+        // ---- softmax: two sets of four warps, each every second tile; thread = TMEM lane = (head, half of the
+        // tile's slots). A set passes the running maxima on before it takes its exponentials.
+        const uint32_t set = (warp - kSoftmaxWarp) >> 2;
+        const uint32_t row = (threadIdx.x - 32 * kSoftmaxWarp) & 127, head = row & 63, half = row >> 6;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t s_cols = lanes + 64 * set;
+        float* red = reinterpret_cast<float*>(smem + Layout::red) + 128 * set;
+        float* m_s = reinterpret_cast<float*>(smem + Layout::maxima);  // [2][128]
+        const uint32_t p_row = smem_u32(smem + Layout::p) + half * 8192;
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
-        uint32_t met = 0;  // the four warps meet once a tile
+        uint32_t met = 0;  // a set's warps meet once a tile
         bool ok = true;
         for (Walk w(p, pair, pairs); ok && w.next(part);) {
-            float m = 0.0f, sum = 0.0f;
+            float m = -INFINITY, sum = 0.0f;  // the maximum that the sum refers to
             uint32_t bad = 0;
-            for (uint32_t i = 0; i < part.tiles; ++i, ++it) {
-                const uint32_t buf = it & 1, pbuf = it % kPlaceBufs;
-                if (!(ok = wait_warp(&bar->s_full[buf], it >> 1 & 1, p.status))) break;
+            const uint32_t begin = it;
+            for (const uint32_t stop = it + part.tiles; it < stop; ++it) {
+                if ((it & 1) != set) continue;
+                const uint32_t pbuf = it % kPlaceBufs;
+                if (!(ok = wait_warp(&bar->s_full[set], it >> 1 & 1, p.status))) break;
                 tc_fence_after();
                 if (!(ok = wait_warp(&bar->place_full[pbuf], it / kPlaceBufs & 1, p.status))) break;
                 const bool masked = bar->form[pbuf] & kMasked;
@@ -520,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
 #pragma unroll 1
                 for (uint32_t h = 0; h < 2; ++h) {
                     uint32_t v[32];
-                    tmem_ld_x32(lanes + buf * 64 + 32 * h, v);
+                    tmem_ld_x32(s_cols + 32 * h, v);
                     tmem_ld_wait();
                     float2 t[16];
 #pragma unroll
@@ -539,32 +550,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                             if (a.w < 0) t[2 * c + 1].y = -INFINITY;
                         }
                     }
+                    float tops[4];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) top = fmaxf(top, fmaxf(t[c].x, t[c].y));
+                    for (int c = 0; c < 4; ++c) tops[c] = fmaxf(t[c].x, t[c].y);
+#pragma unroll
+                    for (int c = 4; c < 16; ++c) tops[c & 3] = fmaxf(tops[c & 3], fmaxf(t[c].x, t[c].y));
+                    top = fmaxf(top, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
                 }
                 if (!(odd.x + odd.y == 0.0f)) bad = 1;
-                red[buf * 128 + row] = top;
-                sync_softmax();
+                red[row] = top;
+                sync_softmax(set);
                 ++met;
-                top = fmaxf(top, red[buf * 128 + (row ^ 64)]);
-                // The head's two threads decide alike.
-                float f = 1.0f;
-                if (i == 0) {
+                top = fmaxf(top, red[row ^ 64]);
+                // The running maximum of the tile before, and this tile's. A head's two threads decide alike.
+                if (it > 0 && !(ok = wait_warp(&bar->m_ready[set ^ 1], (it - 1) >> 1 & 1, p.status))) break;
+                float f = 1.0f;  // of O
+                if (it == begin) {
                     m = finite_f(top) ? top : 0.0f;
-                } else if (top > m + kSlack && finite_f(top)) {
-                    f = exp2_fast(m - top);
-                    m = top;
-                    sum *= f;
+                } else {
+                    const float before = m_s[128 * (set ^ 1) + row];
+                    float now = before;
+                    if (top > before + kSlack && finite_f(top)) {
+                        now = top;
+                        f = exp2_fast(before - now);
+                    }
+                    if (now != m) sum *= exp2_fast(m - now);  // the set's sum, of its own tiles
+                    m = now;
                 }
+                m_s[128 * set + row] = m;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->m_ready[set]);
                 const bool moved = __any_sync(0xFFFFFFFFu, f != 1.0f);
                 // The weights, from S again: 64 logits and 64 weights at once are more registers than there are.
                 const float2 minus = make_float2(-m, -m);
-                float2 s2 = make_float2(0.0f, 0.0f);
-                uint32_t w16[32];
+                float2 s2[2] = {};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[32];
-                    tmem_ld_x32(lanes + buf * 64 + 32 * h, v);
+                for (uint32_t h = 0; h < 2; ++h) {
+                    uint32_t v[32], w16[16];
+                    tmem_ld_x32(s_cols + 32 * h, v);
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
@@ -575,20 +598,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                             const int2 a = reinterpret_cast<const int2*>(at)[16 * h + c];
                             e = make_float2(a.x < 0 ? 0.0f : e.x, a.y < 0 ? 0.0f : e.y);
                         }
-                        s2 = add2(s2, e);
-                        w16[16 * h + c] = pack_bf16(e.x, e.y);
+                        s2[c & 1] = add2(s2[c & 1], e);
+                        w16[c] = pack_bf16(e.x, e.y);
                     }
+                    if (h == 0) {
+                        // P G of the tile before is done: P may be overwritten, and O scaled.
+                        if (it > 0 && !(ok = wait_warp(&bar->pv_done[(it - 1) & 1], (it - 1) >> 1 & 1, p.status))) break;
+                        tc_fence_after();
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            arrive_first_cta(&bar->s_free[set]);
+                            mbar_arrive(&bar->place_free[pbuf]);
+                        }
+                    }
+#pragma unroll
+                    for (uint32_t c = 0; c < 4; ++c)
+                        st_shared_v4(p_row + swizzled(head, 4 * h + c), w16[4 * c], w16[4 * c + 1], w16[4 * c + 2],
+                                     w16[4 * c + 3]);
                 }
-                sum += s2.x + s2.y;
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    arrive_first_cta(&bar->s_free[buf]);
-                    mbar_arrive(&bar->place_free[pbuf]);
-                }
-                // P G of the tile before is done: P may be overwritten, and O scaled.
-                if (it > 0 && !(ok = wait_warp(&bar->pv_done, (it - 1) & 1, p.status))) break;
-                tc_fence_after();
+                if (!ok) break;
+                s2[0] = add2(s2[0], s2[1]);
+                sum += s2[0].x + s2[0].y;
                 if (moved) {
 #pragma unroll 1
                     for (uint32_t c = 0; c < 256; c += 32) {
@@ -601,32 +633,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                     }
                     tmem_st_wait();
                 }
-#pragma unroll
-                for (uint32_t c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint4*>(p_row + swizzled(head, c)) =
-                        make_uint4(w16[4 * c], w16[4 * c + 1], w16[4 * c + 2], w16[4 * c + 3]);
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_first_cta(&bar->p_full);
             }
-            // ---- the part's state: m, sum, flag and O per lane ----------------------------------
-            if (!ok || !(ok = wait_warp(&bar->pv_done, (it - 1) & 1, p.status))) break;
-            tc_fence_after();
-            float* out = p.parts + ((size_t)(pair + part.seg) * 2 + rank) * kPrefixPartFloats;
+            if (!ok) break;
+            // ---- the part's state: the maximum that O refers to, and each set's sum and flag; the set that had
+            // the last tile also leaves O ------------------------------------------------------------
+            const uint32_t last = it - 1;
             const uint32_t r = part.seg < p.groups ? 2 * part.seg + rank : rank == 0 ? part.seg - p.groups : p.rows;
             const bool mine = r < p.rows;  // the pair's second CTA may have no row
-            if (mine) {
-                out[row] = m;
-                out[128 + row] = sum;
-                reinterpret_cast<uint32_t*>(out)[256 + row] = bad;
+            float* out = p.parts + ((size_t)(pair + part.seg) * 2 + rank) * kPrefixPartFloats;
+            if ((last & 1) != set) {
+                if (!(ok = wait_warp(&bar->m_ready[set ^ 1], last >> 1 & 1, p.status))) break;
+                const float now = m_s[128 * (set ^ 1) + row];
+                if (now != m) sum *= exp2_fast(m - now);
             }
+            if (mine) {
+                out[128 + 128 * set + row] = sum;
+                reinterpret_cast<uint32_t*>(out)[384 + 128 * set + row] = bad;
+            }
+            if ((last & 1) != set) continue;
+            if (mine) out[row] = m;
+            if (!(ok = wait_warp(&bar->pv_done[last & 1], last >> 1 & 1, p.status))) break;
+            tc_fence_after();
 #pragma unroll 1
             for (uint32_t c = 0; c < 256; c += 32) {
                 uint32_t o[32];
                 tmem_ld_x32(lanes + kOCol + c, o);
                 tmem_ld_wait();
-                float4* to = reinterpret_cast<float4*>(out + 3 * 128) + (c / 4) * 128 + row;
+                float4* to = reinterpret_cast<float4*>(out + kPrefixHeadFloats) + (c / 4) * 128 + row;
                 if (mine)
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -634,11 +671,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                                                   __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
             }
             tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_first_cta(&bar->o_read);
         }
         // A warp that gave up still meets the others.
         uint32_t all = 0;
         for (Walk w(p, pair, pairs); w.next(part);) all += part.tiles;
-        for (; met < all; ++met) sync_softmax();
+        for (all = (all + 1 - set) / 2; met < all; ++met) sync_softmax(set);
     } else if (warp == 3) {
         // ---- each part's query, once the MMAs of the part before have read theirs --------------
         uint32_t n_part = 0;
@@ -805,9 +844,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
 #pragma unroll 4
     for (uint32_t i = slice; i < parts.count; i += kJoinSlices) {
         const float* part = parts.at(i);
-        const uint32_t* flags = reinterpret_cast<const uint32_t*>(part) + 256;
+        const uint32_t* flags = reinterpret_cast<const uint32_t*>(part) + 384 + head;
         m = fmaxf(m, __ldcg(part + head));  // both of a head's lanes have it
-        bad |= __ldcg(flags + head) | __ldcg(flags + 64 + head);
+        bad |= __ldcg(flags) | __ldcg(flags + 64) | __ldcg(flags + 128) | __ldcg(flags + 192);
     }
     m_s[slice][head] = m;
     bad_s[slice][head] = bad;
@@ -825,7 +864,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
         const float* part = parts.at(i);
         const float f = exp2f(__ldcg(part + head) - top);
         fac_s[i][head] = f;
-        l = fmaf(__ldcg(part + 128 + head) + __ldcg(part + 192 + head), f, l);
+        const float* sums = part + 128 + head;
+        l = fmaf((__ldcg(sums) + __ldcg(sums + 64)) + (__ldcg(sums + 128) + __ldcg(sums + 192)), f, l);
     }
     l_s[slice][head] = l;
     __syncthreads();
@@ -837,7 +877,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     if (p.invalid && blockIdx.y == 0 && threadIdx.x < 64) p.invalid[at] = zero ? 1u : 0u;
 
     auto add = [&](float4& acc, uint32_t i, uint32_t col) {
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(parts.at(i) + 3 * 128) + col * 128 + lane);
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(parts.at(i) + kPrefixHeadFloats) + col * 128 + lane);
         const float f = fac_s[i][head];
         acc.x = fmaf(o.x, f, acc.x);
         acc.y = fmaf(o.y, f, acc.y);
