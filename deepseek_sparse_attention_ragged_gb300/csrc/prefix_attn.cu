@@ -19,7 +19,7 @@
 // M = 128 it would fill TMEM alone. Each CTA keeps its own softmax: its 64 heads see every slot of the tile,
 // so nothing but the operands crosses the pair.
 //
-// Warp roles: 0 looks up the tiles' rows, 1 issues the MMAs (in the pair's first CTA), 4 to 11
+// Warp roles: 0 looks up the tiles' rows, 1 and 2 issue the MMAs (in the pair's first CTA), 4 to 11
 // do the softmax (a thread has 64 slots of one head); 3 loads the queries, and the others
 // bring the operands, each one unit of a ring. The K form (64 slots
 // x 128 dims) and the V form (32 slots x 256 dims) of the rows go through one ring of 16 KB units in
@@ -330,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
         mbar_init(&bar->p_full, 8);
         mbar_init(&bar->q_free, 1);
         mbar_init(&bar->o_read, 8);
-        mbar_init(&bar->drained, 1);
+        mbar_init(&bar->drained, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar->s_free[i], 8);
             mbar_init(&bar->s_full[i], 1);
@@ -399,27 +399,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 if (lane == 0) mbar_arrive(&bar->place_full[buf]);
             }
         }
-    } else if (warp == 1) {
-        // ---- the MMAs, issued in the first CTA for both -----------------------------------------
+    } else if (warp <= 2) {
+        // ---- the MMAs, issued in the first CTA for both: warp 1 S = Q G^T, warp 2 O += P G. (One warp for both took
+        // 3,900 cycles a tile, twice the MMAs' time: waits of 100 to 200 cycles and 20 or so an MMA, one after another.)
+        // A form's four units are waited for together.
         if (rank == 0) {
-            constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128);
-            constexpr uint32_t idesc_o = idesc_bf16_f32(128, 256) | 1u << 16;  // B is MN-major
-            const uint32_t q_base = smem_u32(smem + Layout::q), p_base = smem_u32(smem + Layout::p);
-            uint32_t unit = 0, phase = 0;
-            uint32_t ready = 0;  // units from `unit` on that are known to be full
-            bool ok = true;
-            // A full unit at `unit`: the lanes look at the next eight together, since a wait for each takes about as
-            // long as its MMAs.
-            auto wait_unit = [&]() -> bool {
-                if (ready > 0) return true;
+            auto units_full = [&](uint32_t slot, uint32_t lap) -> bool {
                 uint64_t start = 0;
-                for (uint32_t tries = 0;; ++tries) {
-                    const uint32_t at = unit + (lane & (kUnits - 1));
-                    const bool full = mbar_try_wait(&bar->full[at & (kUnits - 1)], phase ^ (at >= kUnits ? 1u : 0u));
-                    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, full) & ((1u << kUnits) - 1);
-                    ready = __ffs(~bits) - 1;
-                    if (ready > 0) return true;
-                    if ((tries & 63) == 63) {
+                for (uint32_t tries = 1;; ++tries) {
+                    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(&bar->full[slot + (lane & 3)], lap & 1))) return true;
+                    if (tries % 64 == 0) {
                         const uint64_t now = __shfl_sync(0xFFFFFFFFu, global_timer_ns(), 0);
                         if (start == 0) start = now;
                         if (now - start > kWaitBudgetNs) {
@@ -429,72 +418,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                     }
                 }
             };
-            auto next_unit = [&] {
-                --ready;
-                if (++unit == kUnits) unit = 0, phase ^= 1;
-            };
-            // O += P G of tile `of`; `fresh`: the part's first tile, which begins O anew (the part before has been read).
-            uint32_t begun = 0;
-            auto accumulate = [&](uint32_t of, bool fresh) -> bool {
-                if (!wait_warp(&bar->p_full, of & 1, p.status)) return false;
-                if (fresh && begun++ > 0 && !wait_warp(&bar->o_read, begun & 1, p.status)) return false;
-                tc_fence_after();
-#pragma unroll 1
-                for (uint32_t v = 0; v < 4; ++v) {
-                    if (!wait_unit()) return false;
-                    const uint32_t b = ring + unit * kUnitBytes;
-                    const uint64_t a_desc = smem_desc_sw128_kmajor(p_base + (v >> 1) * 8192 + (v & 1) * 64);
-                    const uint64_t b_desc = smem_desc_sw128_mnmajor(b, 4096, 1024);
-                    if (elect_one()) {
-#pragma unroll
-                        for (uint32_t ks = 0; ks < 2; ++ks)
-#pragma unroll
-                            for (uint32_t j = 0; j < 2; ++j)
-                                umma2_bf16(tmem + kOCol + 128 * j, a_desc + ks * (32 >> 4),
-                                           b_desc + ((j * 8192 + ks * 2048) >> 4), idesc_o,
-                                           fresh && v == 0 && ks == 0 ? 0u : 1u);
-                        umma2_commit(&bar->empty[unit]);
-                        if (v == 3) umma2_commit(&bar->pv_done[of & 1]);
-                    }
-                    __syncwarp();
-                    next_unit();
-                }
-                return true;
-            };
             uint32_t n_part = 0;
-            bool fresh = true;  // of the tile whose P G is due
-            for (Walk w(p, pair, pairs); ok && w.next(part); ++n_part) {
-                for (uint32_t i = 0; ok && i < part.tiles; ++i, ++it) {
-                    const uint32_t buf = it & 1;
-                    ok = i != 0 || wait_warp(&bar->q_full, n_part & 1, p.status);
-                    ok = ok && wait_warp(&bar->s_free[buf], (it >> 1 & 1) ^ 1, p.status);
-                    tc_fence_after();
-#pragma unroll 1
-                    for (uint32_t u = 0; ok && u < 4; ++u) {
-                        ok = wait_unit();
+            bool ok = true;
+            if (warp == 1) {
+                constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
+                const uint64_t a_desc = smem_desc_sw128_kmajor(smem_u32(smem + Layout::q));
+                for (Walk w(p, pair, pairs); ok && w.next(part); ++n_part)
+                    for (uint32_t i = 0; i < part.tiles; ++i, ++it) {
+                        const uint32_t buf = it & 1, slot = it == 0 ? 0 : 4;
+                        ok = i != 0 || wait_warp(&bar->q_full, n_part & 1, p.status);
+                        ok = ok && wait_warp(&bar->s_free[buf], (it >> 1 & 1) ^ 1, p.status);
+                        ok = ok && units_full(slot, it == 0 ? 0 : it - 1);
                         if (!ok) break;
-                        const uint64_t a_desc = smem_desc_sw128_kmajor(q_base + u * kUnitBytes);
-                        const uint64_t b_desc = smem_desc_sw128_kmajor(ring + unit * kUnitBytes);
+                        tc_fence_after();
+                        const uint64_t b_desc = smem_desc_sw128_kmajor(ring + slot * kUnitBytes);
+                        const uint32_t d = tmem + buf * 64;
                         if (elect_one()) {
 #pragma unroll
-                            for (uint32_t ks = 0; ks < 8; ++ks)
-                                umma2_bf16(tmem + buf * 64, a_desc + (((ks >> 2) * 8192 + (ks & 3) * 32) >> 4),
-                                           b_desc + (((ks >> 2) * 8192 + (ks & 3) * 32) >> 4), idesc_s,
-                                           u == 0 && ks == 0 ? 0u : 1u);
-                            umma2_commit(&bar->empty[unit]);
-                            if (u == 3) {
-                                umma2_commit(&bar->s_full[buf]);
-                                if (i + 1 == part.tiles) umma2_commit(&bar->q_free);
+                            for (uint32_t u = 0; u < 4; ++u) {
+#pragma unroll
+                                for (uint32_t ks = 0; ks < 8; ++ks) {
+                                    const uint32_t at = (u * kUnitBytes + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4;
+                                    umma2_bf16(d, a_desc + at, b_desc + at, idesc, u == 0 && ks == 0 ? 0u : 1u);
+                                }
+                                umma2_commit(&bar->empty[slot + u]);
                             }
+                            umma2_commit(&bar->s_full[buf]);
+                            if (i + 1 == part.tiles) umma2_commit(&bar->q_free);
                         }
                         __syncwarp();
-                        next_unit();
                     }
-                    if (ok && it > 0) ok = accumulate(it - 1, fresh);
-                    fresh = i == 0;
-                }
+            } else {
+                constexpr uint32_t idesc = idesc_bf16_f32(128, 256) | 1u << 16;  // B is MN-major
+                const uint64_t a_desc = smem_desc_sw128_kmajor(smem_u32(smem + Layout::p));
+                uint32_t n = 0;
+                for (Walk w(p, pair, pairs); w.next(part);) n += part.tiles;
+                for (Walk w(p, pair, pairs); ok && w.next(part); ++n_part)
+                    for (uint32_t i = 0; i < part.tiles; ++i, ++it) {
+                        const uint32_t slot = it + 1 < n ? 0 : 4, lap = it + 1 < n ? it + 1 : it;
+                        ok = wait_warp(&bar->p_full, it & 1, p.status);
+                        // A part begins O anew, once the part before has been read.
+                        ok = ok && (i != 0 || n_part == 0 || wait_warp(&bar->o_read, (n_part - 1) & 1, p.status));
+                        ok = ok && units_full(slot, lap);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t b_desc = smem_desc_sw128_mnmajor(ring + slot * kUnitBytes, 4096, 1024);
+                        if (elect_one()) {
+#pragma unroll
+                            for (uint32_t v = 0; v < 4; ++v) {
+#pragma unroll
+                                for (uint32_t ks = 0; ks < 2; ++ks)
+#pragma unroll
+                                    for (uint32_t j = 0; j < 2; ++j)
+                                        umma2_bf16(tmem + kOCol + 128 * j,
+                                                   a_desc + (((v >> 1) * 8192 + (v & 1) * 64 + ks * 32) >> 4),
+                                                   b_desc + ((v * kUnitBytes + j * 8192 + ks * 2048) >> 4), idesc,
+                                                   i == 0 && v == 0 && ks == 0 ? 0u : 1u);
+                                umma2_commit(&bar->empty[slot + v]);
+                            }
+                            umma2_commit(&bar->pv_done[it & 1]);
+                        }
+                        __syncwarp();
+                    }
             }
-            if (ok && it > 0) ok = accumulate(it - 1, fresh);
             // Whatever was issued is done before the CTAs leave.
             if (elect_one()) umma2_commit(&bar->drained);
             __syncwarp();
