@@ -43,11 +43,15 @@ constexpr int kPBytes = kHeads * kTile * 2;   // P: 2 blocks [64 heads][64 slots
 constexpr int kBoxRows = kPrefixBoxRows;      // most rows of a TMA box
 constexpr int kPlaceBufs = 4;                 // tiles whose rows are looked up
 constexpr int kSoftmaxWarp = 4, kBuildWarp = 12;  // two sets of four softmax warps
-// Warps that fill a ring unit: packed rows are widened by two.
+// Warps that bring operands, those of them that fill a ring unit, and those that read a tile's places for a form.
 template <int kFormat>
-constexpr int kFillers = kFormat == DS_CACHE_BF16 ? 1 : 2;
+constexpr int kBuildWarps = kFormat == DS_CACHE_BF16 ? kUnits : 16;
 template <int kFormat>
-constexpr int kThreads = 32 * (kBuildWarp + kUnits * kFillers<kFormat>);
+constexpr int kFillers = kFormat == DS_CACHE_BF16 ? 1 : 8;
+template <int kFormat>
+constexpr int kReaders = kFormat == DS_CACHE_BF16 ? 4 : 16;
+template <int kFormat>
+constexpr int kThreads = 32 * (kBuildWarp + kBuildWarps<kFormat>);
 constexpr uint32_t kOCol = 128;               // TMEM: two S of 64 columns, then O
 constexpr uint32_t kTmemCols = 512;
 constexpr uint16_t kBoth = 3;                 // the CTAs of a pair
@@ -339,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
         }
         for (int i = 0; i < kPlaceBufs; ++i) {
             mbar_init(&bar->place_full[i], 1);
-            mbar_init(&bar->place_free[i], 2 * 4 * kFillers<kFormat> + 4);  // K form, V form, softmax
+            mbar_init(&bar->place_free[i], 2 * kReaders<kFormat> + 4);  // K form, V form, softmax
         }
         fence_barrier_init();
     }
@@ -402,12 +406,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
     } else if (warp <= 2) {
         // ---- the MMAs, issued in the first CTA for both: warp 1 S = Q G^T, warp 2 O += P G. (One warp for both took
         // 3,900 cycles a tile, twice the MMAs' time: waits of 100 to 200 cycles and 20 or so an MMA, one after another.)
-        // A form's four units are waited for together.
         if (rank == 0) {
-            auto units_full = [&](uint32_t slot, uint32_t lap) -> bool {
+            // Units slot .. slot + 3, one form of a tile: those that are full among the first u + 1 (bits), once unit u is.
+            auto unit_full = [&](uint32_t slot, uint32_t lap, uint32_t u, uint32_t& bits) -> bool {
                 uint64_t start = 0;
-                for (uint32_t tries = 1;; ++tries) {
-                    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(&bar->full[slot + (lane & 3)], lap & 1))) return true;
+                for (uint32_t tries = 1; !(bits >> u & 1); ++tries) {
+                    bits = __ballot_sync(0xFFFFFFFFu, mbar_try_wait(&bar->full[slot + (lane & 3)], lap & 1)) & 15;
                     if (tries % 64 == 0) {
                         const uint64_t now = __shfl_sync(0xFFFFFFFFu, global_timer_ns(), 0);
                         if (start == 0) start = now;
@@ -417,6 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                         }
                     }
                 }
+                return true;
             };
             uint32_t n_part = 0;
             bool ok = true;
@@ -428,25 +433,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                         const uint32_t buf = it & 1, slot = it == 0 ? 0 : 4;
                         ok = i != 0 || wait_warp(&bar->q_full, n_part & 1, p.status);
                         ok = ok && wait_warp(&bar->s_free[buf], (it >> 1 & 1) ^ 1, p.status);
-                        ok = ok && units_full(slot, it == 0 ? 0 : it - 1);
-                        if (!ok) break;
-                        tc_fence_after();
                         const uint64_t b_desc = smem_desc_sw128_kmajor(ring + slot * kUnitBytes);
                         const uint32_t d = tmem + buf * 64;
-                        if (elect_one()) {
+                        uint32_t full = 0;
 #pragma unroll
-                            for (uint32_t u = 0; u < 4; ++u) {
+                        for (uint32_t u = 0; u < 4; ++u) {
+                            ok = ok && unit_full(slot, it == 0 ? 0 : it - 1, u, full);
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (elect_one()) {
 #pragma unroll
                                 for (uint32_t ks = 0; ks < 8; ++ks) {
                                     const uint32_t at = (u * kUnitBytes + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4;
                                     umma2_bf16(d, a_desc + at, b_desc + at, idesc, u == 0 && ks == 0 ? 0u : 1u);
                                 }
                                 umma2_commit(&bar->empty[slot + u]);
+                                if (u == 3) {
+                                    umma2_commit(&bar->s_full[buf]);
+                                    if (i + 1 == part.tiles) umma2_commit(&bar->q_free);
+                                }
                             }
-                            umma2_commit(&bar->s_full[buf]);
-                            if (i + 1 == part.tiles) umma2_commit(&bar->q_free);
+                            __syncwarp();
                         }
-                        __syncwarp();
+                        if (!ok) break;
                     }
             } else {
                 constexpr uint32_t idesc = idesc_bf16_f32(128, 256) | 1u << 16;  // B is MN-major
@@ -459,13 +468,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                         ok = wait_warp(&bar->p_full, it & 1, p.status);
                         // A part begins O anew, once the part before has been read.
                         ok = ok && (i != 0 || n_part == 0 || wait_warp(&bar->o_read, (n_part - 1) & 1, p.status));
-                        ok = ok && units_full(slot, lap);
-                        if (!ok) break;
-                        tc_fence_after();
                         const uint64_t b_desc = smem_desc_sw128_mnmajor(ring + slot * kUnitBytes, 4096, 1024);
-                        if (elect_one()) {
+                        uint32_t full = 0;
 #pragma unroll
-                            for (uint32_t v = 0; v < 4; ++v) {
+                        for (uint32_t v = 0; v < 4; ++v) {
+                            ok = ok && unit_full(slot, lap, v, full);
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (elect_one()) {
 #pragma unroll
                                 for (uint32_t ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -475,10 +485,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                                                    b_desc + ((v * kUnitBytes + j * 8192 + ks * 2048) >> 4), idesc,
                                                    i == 0 && v == 0 && ks == 0 ? 0u : 1u);
                                 umma2_commit(&bar->empty[slot + v]);
+                                if (v == 3) umma2_commit(&bar->pv_done[it & 1]);
                             }
-                            umma2_commit(&bar->pv_done[it & 1]);
+                            __syncwarp();
                         }
-                        __syncwarp();
+                        if (!ok) break;
                     }
             }
             // Whatever was issued is done before the CTAs leave.
@@ -677,15 +688,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                               (int)(p.q_row[r] * kHeads));
         }
     } else if (warp >= kBuildWarp) {
-        // ---- operands: warp b fills unit b (mod kUnits) of the ring, one lap a tile ----------------
+        // ---- operands -----------------------------------------------------------------------------
         // With n tiles the ring's order K(0), K(1), V(0), K(2), V(1), .. K(n - 1), V(n - 2), V(n - 1) gives units 0 to
         // 3 K(0), then V(0 .. n - 2), and units 4 to 7 K(1 .. n - 1), then V(n - 1).
-        const uint32_t unit = (warp - kBuildWarp) % kUnits, u = unit & 3;
-        const uint32_t dst = ring + unit * kUnitBytes;
         uint32_t n = 0;
         for (Walk w(p, pair, pairs); w.next(part);) n += part.tiles;
-        auto tile_of = [&](uint32_t lap) { return unit < 4 ? (lap ? lap - 1 : 0) : min(lap + 1, n - 1); };
-        auto v_form_of = [&](uint32_t lap) { return unit < 4 ? lap > 0 : lap + 1 >= n; };
         auto looked_up = [&](uint32_t of) {
             return wait_warp(&bar->place_full[of % kPlaceBufs], of / kPlaceBufs & 1, p.status);
         };
@@ -694,10 +701,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             if (lane == 0) mbar_arrive(&bar->place_free[of % kPlaceBufs]);
         };
         if constexpr (kFormat == DS_CACHE_BF16) {
+            // Warp b fills unit b, one lap a tile.
+            const uint32_t unit = warp - kBuildWarp, u = unit & 3;
+            const uint32_t dst = ring + unit * kUnitBytes;
             const uint32_t box = min(1u << p.cache.page_shift, (uint32_t)kBoxRows);
             for (uint32_t lap = 0; lap < n; ++lap) {
-                const uint32_t of = tile_of(lap);
-                const bool v_form = v_form_of(lap);
+                const uint32_t of = unit < 4 ? (lap ? lap - 1 : 0) : min(lap + 1, n - 1);
+                const bool v_form = unit < 4 ? lap > 0 : lap + 1 >= n;
                 if (!looked_up(of) || !wait_warp(&bar->empty[unit], (lap & 1) ^ 1, p.status)) break;
                 const int32_t* at = place_s + of % kPlaceBufs * kTile + (v_form ? 32 * u : 64 * rank);
                 if (!(bar->form[of % kPlaceBufs] & kByThreads)) {
@@ -729,41 +739,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 }
             }
         } else {
-            // Packed rows, widened: a lap's loads are issued when the lap before has been stored. Step s of a unit's
-            // eight has eight rows (K form: 8 s ..; V form: 8 (s / 2) .., 128 dims each); each of its warps has four.
-            constexpr uint32_t kSteps = 8 / kFillers<kFormat>;
-            const uint32_t s0 = (warp - kBuildWarp) / kUnits * kSteps;
-            Piece<kFormat> held[kSteps];
-            auto fetch = [&](uint32_t lap) -> bool {
-                const uint32_t of = tile_of(lap);
-                const bool v_form = v_form_of(lap);
-                if (!looked_up(of)) return false;
-                const int32_t* at = place_s + of % kPlaceBufs * kTile + (v_form ? 32 * u : 64 * rank);
-                const uint32_t d = Piece<kFormat>::first(lane);
-#pragma unroll
-                for (uint32_t s = 0; s < kSteps; ++s) {
-                    const int32_t place = at[8 * (v_form ? (s0 + s) >> 1 : s0 + s) + (lane & 7)];
-                    held[s].load(p.cache, place, v_form ? v_dim(128 * (s & 1), rank) + d : 128 * u + d);
-                }
-                read(of);
-                return true;
+            // Packed rows are widened by two teams of eight warps: team t fills units t and t + 2 of each form, warp s
+            // of it the unit's step s, eight rows of 128 dims (K form: rows 8 s ..; V form: 8 (s / 2) .., 128 dims
+            // each). The loads of a form are issued as the form before it is stored. (Two warps to a unit, four
+            // steps each, took 4000 cycles from a free unit to a full one, and the ring holds no more than a tile.)
+            const uint32_t team = (warp - kBuildWarp) >> 3, s = warp - kBuildWarp & 7;
+            Piece<kFormat> held[2];
+            // Form f of the order above: its tile and kind.
+            auto tile_of = [&](uint32_t f) { return f == 0 ? 0 : f == 2 * n - 1 ? n - 1 : f & 1 ? (f + 1) / 2 : f / 2 - 1; };
+            auto v_form_of = [&](uint32_t f) { return f == 2 * n - 1 || (f > 0 && !(f & 1)); };
+            auto fetch = [&](uint32_t f, uint32_t k) {
+                const uint32_t of = tile_of(f), u = team + 2 * k, d = Piece<kFormat>::first(lane);
+                const int32_t* at = place_s + of % kPlaceBufs * kTile + (lane & 7);
+                if (v_form_of(f)) held[k].load(p.cache, at[32 * u + 8 * (s >> 1)], v_dim(128 * (s & 1), rank) + d);
+                else held[k].load(p.cache, at[64 * rank + 8 * s], 128 * u + d);
             };
-            if (n > 0 && fetch(0)) {
-                for (uint32_t lap = 0; lap < n; ++lap) {
-                    const bool v_form = v_form_of(lap);
-                    if (!wait_warp(&bar->empty[unit], (lap & 1) ^ 1, p.status)) break;
+            bool ok = n > 0 && looked_up(0);
+            if (ok) {
+                fetch(0, 0);
+                fetch(0, 1);
+                read(0);
+            }
+            for (uint32_t f = 0; ok && f < 2 * n; ++f) {
+                const bool v_form = v_form_of(f), then = f + 1 < 2 * n;
+                // Form f lies in units 0 to 3 (f even) or 4 to 7, lap f / 2.
+                const uint32_t row = 8 * (v_form ? s >> 1 : s) + (lane & 7), size = v_form ? 4096 : 8192;
+                ok = !then || looked_up(tile_of(f + 1));
 #pragma unroll
-                    for (uint32_t s = 0; s < kSteps; ++s) {
-                        const uint32_t row = 8 * (v_form ? (s0 + s) >> 1 : s0 + s) + (lane & 7);
-                        const uint32_t block = dst + (v_form ? (s & 1) * 8192 : 0), size = v_form ? 4096 : 8192;
-                        held[s].store(Piece<kFormat>::first(lane),
-                                      [&](uint32_t ch) { return block + (ch >> 3) * size + swizzled(row, ch & 7); });
-                    }
+                for (uint32_t k = 0; k < 2; ++k) {
+                    const uint32_t unit = 4 * (f & 1) + team + 2 * k;
+                    ok = ok && wait_warp(&bar->empty[unit], (f / 2 & 1) ^ 1, p.status);
+                    if (!ok) break;
+                    const uint32_t block = ring + unit * kUnitBytes + (v_form ? (s & 1) * 8192 : 0);
+                    held[k].store(Piece<kFormat>::first(lane),
+                                  [&](uint32_t ch) { return block + (ch >> 3) * size + swizzled(row, ch & 7); });
+                    if (then) fetch(f + 1, k);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) arrive_first_cta(&bar->full[unit]);
-                    if (lap + 1 < n && !fetch(lap + 1)) break;
                 }
+                if (ok && then) read(tile_of(f + 1));
             }
         }
     }
