@@ -685,7 +685,8 @@ int check_prefix_rows(int rows, const ds_row_t* table, uint32_t prefix_len) {
 // the workspace. With a tile for every pair, or less, each pair has one; else a
 // segment's set-up (its query, the first tile's way through the pipeline, what it leaves in the workspace)
 // counts as two tiles, so that the pairs with the rows' short ends do not finish last.
-size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t prefix_len, uint32_t most_pairs) {
+size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t prefix_len, uint32_t most_pairs,
+                      bool& widen) {
     p.rows = (uint32_t)rows;
     p.groups = (p.rows + 1) / 2;
     p.prefix_len = prefix_len;
@@ -707,8 +708,17 @@ size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t
         add(table[e].kv_len - prefix_len);
     }
     p.begin[segs] = p.line = at;
+    uint32_t wide = tiles_of(prefix_len);
+    for (uint32_t e = 0; e < p.rows; ++e) {
+        p.wide_begin[e] = wide;
+        wide += tiles_of(table[e].kv_len - prefix_len);
+    }
+    p.wide_tiles = wide;
+    // Packed rows are widened once, beforehand, where each is attended to by two pairs of entries or more on the average.
+    widen = tiles >= 2 * wide && wide <= 0x7FFFFFFFu / kPrefixTile;
     return 256 + align256((size_t)(p.pairs + segs - 1) * 2 * kPrefixPartFloats * 4);
 }
+constexpr size_t kWideTileBytes = (size_t)kPrefixTile * kDim * 2;
 
 }  // namespace
 
@@ -1248,10 +1258,13 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
     return err == cudaSuccess ? DS_OK : cuda_fail(err, "paged attention launch");
 }
 
-size_t ds_rows_prefix_attn_workspace_bytes(int rows, const ds_row_t* table, uint32_t prefix_len) {
+size_t ds_rows_prefix_attn_workspace_bytes(int rows, const ds_row_t* table, uint32_t prefix_len, int format) {
     if (check_prefix_rows(rows, table, prefix_len)) return 0;
+    if (format != -1 && !ds_rows_page_bytes(16, DS_DIM, format)) return 0;
     PrefixParams p;
-    return lay_out_prefix(p, rows, table, prefix_len, kPrefixPairsMax);
+    bool widen;
+    const size_t parts = lay_out_prefix(p, rows, table, prefix_len, kPrefixPairsMax, widen);
+    return parts + (widen && format != DS_CACHE_BF16 ? p.wide_tiles * kWideTileBytes : 0);
 }
 
 int ds_rows_prefix_attn(int rows, const ds_row_t* table, uint32_t prefix_len, const ds_paged_cache_t* kv,
@@ -1268,19 +1281,23 @@ int ds_rows_prefix_attn(int rows, const ds_row_t* table, uint32_t prefix_len, co
     if (!aligned4(sinks) || !aligned4(invalid)) return fail(DS_EALIGN, "sinks and invalid must be 4-B aligned");
     PrefixParams p;
     Layout L;
-    L.total = lay_out_prefix(p, rows, table, prefix_len, kPrefixPairsMax);
+    bool widen;
+    L.total = lay_out_prefix(p, rows, table, prefix_len, kPrefixPairsMax, widen);
     rc = check_workspace(nullptr, workspace, workspace_bytes, L);
     if (rc) return rc;
     const int sms = num_sms();
     if (sms <= 0) return fail(DS_ECUDA, "no CUDA device");
-    (void)lay_out_prefix(p, rows, table, prefix_len,
-                         std::min(kPrefixPairsMax, std::max((uint32_t)sms / 2, 1u)));
+    (void)lay_out_prefix(p, rows, table, prefix_len, std::min(kPrefixPairsMax, std::max((uint32_t)sms / 2, 1u)), widen);
+    widen = widen && kv->format != DS_CACHE_BF16 && workspace_bytes - L.total >= p.wide_tiles * kWideTileBytes;
+    p.wide = widen ? reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + L.total) : nullptr;
     rc = get_encoder();
     if (rc) return rc;
     uint32_t q_rows = 0;
     for (int e = 0; e < rows; ++e) q_rows = std::max(q_rows, table[e].q_row);
     rc = encode_rows(&p.qmap, q_attn, DS_DIM, ((uint64_t)q_rows + 1) * DS_HEADS, DS_HEADS, "queries");
-    if (rc == DS_OK && kv->format == DS_CACHE_BF16)
+    if (rc == DS_OK && widen)
+        rc = encode_rows(&p.kvmap, p.wide, DS_DIM, (uint64_t)p.wide_tiles * kPrefixTile, kPrefixBoxRows, "widened rows");
+    else if (rc == DS_OK && kv->format == DS_CACHE_BF16)
         rc = encode_rows(&p.kvmap, kv->pages, DS_DIM, (uint64_t)kv->num_pages * kv->page_size,
                          std::min(kv->page_size, kPrefixBoxRows), "paged rows");
     if (rc) return rc;

@@ -6,8 +6,7 @@
 // neighbours store 16 bytes (32 for fp32) each without a gap, and the loads of its rows are in
 // flight together.
 
-#include "fp8.cuh"
-#include "int4.cuh"
+#include "cache_rows.cuh"
 #include "kernels.h"
 
 namespace dsrows {
@@ -78,30 +77,10 @@ __global__ void __launch_bounds__(kFetchThreads) fetch_kernel(const __grid_const
         id[u] = in ? p.cache.table[(uint64_t)seq[u] * p.cache.table_stride + page_no] : -1;
         if ((uint32_t)id[u] >= p.cache.num_pages) id[u] = -1;
     }
-    // The row's 8 elements as they are held, and their scale.
-    uint4 d[kFetchUnroll];
-    uint32_t sc[kFetchUnroll];
+    Held8 held[kFetchUnroll];
 #pragma unroll
-    for (int u = 0; u < kFetchUnroll; ++u) {
-        if (id[u] < 0) continue;
-        const uint8_t* page = p.cache.pages + ((size_t)(uint32_t)id[u] << shift) * p.cache.row_bytes;
-        const size_t size = (size_t)1 << shift, at = (uint32_t)slot[u] & ((1u << shift) - 1);
-        if constexpr (kFormat == DS_CACHE_BF16) {
-            d[u] = *reinterpret_cast<const uint4*>(page + (at * kDimOf + 8 * g) * 2);
-        } else if constexpr (kFormat == DS_CACHE_FP8) {
-            const uint2 v = *reinterpret_cast<const uint2*>(
-                kDimOf == kDim ? page + at * kDimOf + 8 * g : page + (size_t)(g / 2) * (16 * size) + at * 16 + (g % 2) * 8);
-            d[u] = make_uint4(v.x, v.y, 0, 0);
-            sc[u] = page[size * kDimOf + at * (kDimOf / fp8::kBlock) + 8 * g / fp8::kBlock];
-        } else if constexpr (kDimOf == kDim) {
-            const uint8_t* row = page + at * p.cache.row_bytes;
-            d[u].x = *reinterpret_cast<const uint32_t*>(row + 4 * g);
-            sc[u] = row[kDimOf / 2 + g / 2];
-        } else {
-            d[u].x = *reinterpret_cast<const uint32_t*>(page + (size_t)(g / 4) * (16 * size) + at * 16 + (g % 4) * 4);
-            sc[u] = page[size * (kDimOf / 2) + at * (kDimOf / int4::kGroup) + g / 2];
-        }
-    }
+    for (int u = 0; u < kFetchUnroll; ++u)
+        if (id[u] >= 0) held[u] = load8<kDimOf, kFormat>(p.cache, (uint32_t)id[u], (uint32_t)slot[u] & ((1u << shift) - 1), g);
 #pragma unroll
     for (int u = 0; u < kFetchUnroll; ++u) {
         const uint64_t token = first + u * ROWS;
@@ -109,19 +88,7 @@ __global__ void __launch_bounds__(kFetchThreads) fetch_kernel(const __grid_const
         if (g == 0 && p.invalid) p.invalid[token] = seq[u] != -1 && id[u] < 0 ? 1u : 0u;
         if (seq[u] == -1) continue;
         uint32_t w[4] = {0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};  // no row: NaN
-        if (id[u] >= 0) {
-            if constexpr (kFormat == DS_CACHE_BF16) {
-                w[0] = d[u].x, w[1] = d[u].y, w[2] = d[u].z, w[3] = d[u].w;
-            } else if constexpr (kFormat == DS_CACHE_FP8) {
-                const uint32_t f = fp8::factor(sc[u]);
-                fp8::widen(d[u].x, f, w);
-                fp8::widen(d[u].y, f, w + 2);
-            } else {
-                int4::Factors f, unused;
-                int4::factors2<0>(sc[u], f, unused);
-                int4::widen(d[u].x, f, w);
-            }
-        }
+        if (id[u] >= 0) widen8<kFormat>(held[u], w);
         put8(static_cast<T*>(p.out) + token * p.out_stride + 8 * g, w, p.wide != 0);
     }
 }

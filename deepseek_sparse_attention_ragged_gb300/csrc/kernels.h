@@ -224,8 +224,13 @@ constexpr size_t kPrefixPartFloats = kPrefixHeadFloats + (size_t)DS_HEADS * DS_D
 
 struct PrefixParams {
     CUtensorMap qmap;   // bf16 [Q * 64, 512], box {64, 64}, 128-B swizzle
-    CUtensorMap kvmap;  // bf16 pages: [num_pages * page_size, 512], box {64, min(page_size, 32)}, 128-B swizzle
+    // bf16 pages: [num_pages * page_size, 512], box {64, min(page_size, 32)}, 128-B swizzle; or the
+    // widened rows, box {64, 32}
+    CUtensorMap kvmap;
     PagedCache cache;
+    __nv_bfloat16* wide;    // packed pages: their rows widened before the attention, or null
+    uint32_t wide_tiles;
+    uint32_t wide_begin[kPrefixRowsMax];  // first tile of each entry's own rows (the prefix comes first)
     const float* sinks;
     uint64_t sinks_row_stride;
     __nv_bfloat16* out;      // [Q, 64, 512]

@@ -26,6 +26,7 @@
 // the order in which the MMAs take them: S of the next tile comes before P . G of this one.
 // Rows past a segment's end and rows without a page are zeros with probability 0.
 
+#include "cache_rows.cuh"
 #include "common.cuh"
 #include "fp8.cuh"
 #include "int4.cuh"
@@ -42,14 +43,18 @@ constexpr int kQBytes = kHeads * kDim * 2;    // the CTA's query row, 8 blocks [
 constexpr int kPBytes = kHeads * kTile * 2;   // P: 2 blocks [64 heads][64 slots]
 constexpr int kBoxRows = kPrefixBoxRows;      // most rows of a TMA box
 constexpr int kPlaceBufs = 4;                 // tiles whose rows are looked up
+// A kernel's source of rows: the pages of a format, or bf16 rows widened beforehand.
+constexpr int kWidened = -1;
+template <int kFormat>
+constexpr bool kByTma = kFormat == DS_CACHE_BF16 || kFormat == kWidened;
 constexpr int kSoftmaxWarp = 4, kBuildWarp = 12;  // two sets of four softmax warps
 // Warps that bring operands, those of them that fill a ring unit, and those that read a tile's places for a form.
 template <int kFormat>
-constexpr int kBuildWarps = kFormat == DS_CACHE_BF16 ? kUnits : 16;
+constexpr int kBuildWarps = kByTma<kFormat> ? kUnits : 16;
 template <int kFormat>
-constexpr int kFillers = kFormat == DS_CACHE_BF16 ? 1 : 8;
+constexpr int kFillers = kByTma<kFormat> ? 1 : 8;
 template <int kFormat>
-constexpr int kReaders = kFormat == DS_CACHE_BF16 ? 4 : 16;
+constexpr int kReaders = kByTma<kFormat> ? 4 : 16;
 template <int kFormat>
 constexpr int kThreads = 32 * (kBuildWarp + kBuildWarps<kFormat>);
 constexpr uint32_t kOCol = 128;               // TMEM: two S of 64 columns, then O
@@ -373,6 +378,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             const uint32_t entry = part.seg < p.groups ? 0 : part.seg - p.groups;
             const int32_t* table = p.cache.table + (size_t)entry * p.cache.table_stride;
             const uint32_t shift = p.cache.page_shift;
+            // Widened rows: the part's first one.
+            const uint32_t wide = part.seg < p.groups ? part.start : p.wide_begin[entry] * kTile + part.start - p.prefix_len;
             for (uint32_t i = 0; i < part.tiles; ++i, ++it) {
                 const uint32_t buf = it % kPlaceBufs;
                 int32_t id[4], at[4];
@@ -380,12 +387,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t j = part.start + i * kTile + lane + 32 * k;
-                    id[k] = j < part.end ? table[j >> shift] : -1;
+                    id[k] = kFormat != kWidened && j < part.end ? table[j >> shift] : -1;
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t j = part.start + i * kTile + lane + 32 * k;
                     if (j >= part.end) at[k] = kNoRow;
+                    else if (kFormat == kWidened) at[k] = (int32_t)(wide + i * kTile + lane + 32 * k);
                     else if (id[k] < 0 || (uint32_t)id[k] >= p.cache.num_pages) at[k] = kBadRow;
                     else at[k] = (int32_t)(((uint32_t)id[k] << shift) + (j & ((1u << shift) - 1)));
                     all = all && at[k] >= 0;
@@ -700,25 +708,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar->place_free[of % kPlaceBufs]);
         };
-        if constexpr (kFormat == DS_CACHE_BF16) {
+        if constexpr (kByTma<kFormat>) {
             // Warp b fills unit b, one lap a tile.
             const uint32_t unit = warp - kBuildWarp, u = unit & 3;
             const uint32_t dst = ring + unit * kUnitBytes;
-            const uint32_t box = min(1u << p.cache.page_shift, (uint32_t)kBoxRows);
+            const uint32_t box = kFormat == kWidened ? kBoxRows : min(1u << p.cache.page_shift, (uint32_t)kBoxRows);
             for (uint32_t lap = 0; lap < n; ++lap) {
                 const uint32_t of = unit < 4 ? (lap ? lap - 1 : 0) : min(lap + 1, n - 1);
                 const bool v_form = unit < 4 ? lap > 0 : lap + 1 >= n;
                 if (!looked_up(of) || !wait_warp(&bar->empty[unit], (lap & 1) ^ 1, p.status)) break;
                 const int32_t* at = place_s + of % kPlaceBufs * kTile + (v_form ? 32 * u : 64 * rank);
-                if (!(bar->form[of % kPlaceBufs] & kByThreads)) {
+                if (kFormat == kWidened || !(bar->form[of % kPlaceBufs] & kByThreads)) {
                     // Boxes of rows: lane = (row group, 64 dims).
                     const uint32_t groups = (v_form ? 32 : 64) / box;
                     const uint32_t row = lane % groups * box, dims = lane / groups;
+                    // Widened runs end with zeros up to a whole tile.
+                    const int32_t y = kFormat == kWidened
+                                          ? place_s[of % kPlaceBufs * kTile] + (int32_t)((v_form ? 32 * u : 64 * rank) + row)
+                                          : at[row];
                     if (lane == 0) arrive_first_cta_expect(&bar->full[unit], kUnitBytes);
                     __syncwarp();
                     if (dims < (v_form ? 4u : 2u))
                         tma_load_pair(dst + dims * (v_form ? 4096 : 8192) + row * 128, &p.kvmap, &bar->full[unit],
-                                      (int)(v_form ? v_dim(64 * dims, rank) : 128 * u + 64 * dims), at[row]);
+                                      (int)(v_form ? v_dim(64 * dims, rank) : 128 * u + 64 * dims), y);
                     read(of);
                 } else {
                     // Rows by 16 bytes, zeros for those that are missing.
@@ -790,6 +802,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// ---- rows widened beforehand ---------------------------------------------------------------------
+
+namespace {
+constexpr int kWidenThreads = 256;
+constexpr int kWidenRows = 16;  // of a block: four a thread, in flight together
+}  // namespace
+
+// The rows that a call attends to as bf16, each once: the prefix, then each entry's own, every run filled up with
+// zeros to a whole tile. A row without a page is NaN, which zeroes the heads that see it. Bound by the
+// bytes (1 KB written a row); an attention over many rows then reads them as it reads bf16 pages.
+template <int kFormat>
+__global__ void __launch_bounds__(kWidenThreads) prefix_widen_kernel(const __grid_constant__ PrefixParams p) {
+    pdl_trigger();
+    const uint32_t g = threadIdx.x % (kDim / 8), shift = p.cache.page_shift;
+    const uint32_t tile = blockIdx.x / (kTile / kWidenRows);
+    const uint32_t in_tile = blockIdx.x % (kTile / kWidenRows) * kWidenRows + threadIdx.x / (kDim / 8);
+    // The run: its entry, first slot, first tile and end.
+    uint32_t entry = 0, first = 0, begin = 0, end = p.prefix_len;
+    if (tile >= p.wide_begin[0]) {
+        while (entry + 1 < p.rows && tile >= p.wide_begin[entry + 1]) ++entry;
+        first = p.prefix_len;
+        begin = p.wide_begin[entry];
+        end = p.kv_len[entry];
+    }
+    const int32_t* table = p.cache.table + (size_t)entry * p.cache.table_stride;
+    pdl_wait();
+    Held8 held[4];
+    int32_t id[4];
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+        const uint32_t j = first + (tile - begin) * kTile + in_tile + 4 * k;
+        id[k] = j < end ? table[j >> shift] : kNoRow;
+        if (j < end && (uint32_t)id[k] >= p.cache.num_pages) id[k] = kBadRow;
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+        const uint32_t j = first + (tile - begin) * kTile + in_tile + 4 * k;
+        if (id[k] >= 0) held[k] = load8<kDim, kFormat>(p.cache, (uint32_t)id[k], j & ((1u << shift) - 1), g);
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+        const uint32_t empty = id[k] == kBadRow ? 0x7FC07FC0u : 0u;
+        uint32_t w[4] = {empty, empty, empty, empty};
+        if (id[k] >= 0) widen8<kFormat>(held[k], w);
+        *reinterpret_cast<uint4*>(p.wide + ((size_t)tile * kTile + in_tile + 4 * k) * kDim + 8 * g) =
+            make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -946,9 +1007,17 @@ static cudaError_t launch(const PrefixParams& p, cudaStream_t stream, bool pdl) 
     return launch_kernel(prefix_join_kernel, dim3(p.rows, 64 / cols), dim3(kJoinThreads), kJoinSmem, stream, true, p, cols);
 }
 
+template <int kFormat>
+static cudaError_t launch_packed(const PrefixParams& p, cudaStream_t stream, bool pdl) {
+    if (!p.wide) return launch<kFormat>(p, stream, pdl);
+    const cudaError_t err = launch_kernel(prefix_widen_kernel<kFormat>, dim3(p.wide_tiles * (kTile / kWidenRows)),
+                                          dim3(kWidenThreads), 0, stream, pdl, p);
+    return err == cudaSuccess ? launch<kWidened>(p, stream, true) : err;
+}
+
 cudaError_t launch_prefix_attn(const PrefixParams& p, int format, cudaStream_t stream, bool pdl) {
-    if (format == DS_CACHE_INT4) return launch<DS_CACHE_INT4>(p, stream, pdl);
-    if (format == DS_CACHE_FP8) return launch<DS_CACHE_FP8>(p, stream, pdl);
+    if (format == DS_CACHE_INT4) return launch_packed<DS_CACHE_INT4>(p, stream, pdl);
+    if (format == DS_CACHE_FP8) return launch_packed<DS_CACHE_FP8>(p, stream, pdl);
     return launch<DS_CACHE_BF16>(p, stream, pdl);
 }
 

@@ -49,7 +49,7 @@ def declare(lib) -> None:
     lib.ds_rows_fetch.argtypes = [cache, vp, vp, vp, u64, i32, u64, vp, vp]
     lib.ds_rows_indexer_score_paged.argtypes = [i32, vp, cache, vp, vp, vp, sz, vp]
     lib.ds_rows_sparse_attn_paged.argtypes = [i32, vp, cache, vp, vp, sz, vp, f32, vp, vp, vp, sz, vp]
-    lib.ds_rows_prefix_attn_workspace_bytes.argtypes = [i32, vp, u32]
+    lib.ds_rows_prefix_attn_workspace_bytes.argtypes = [i32, vp, u32, i32]
     lib.ds_rows_prefix_attn_workspace_bytes.restype = sz
     lib.ds_rows_prefix_attn.argtypes = [i32, vp, u32, cache, vp, vp, sz, f32, vp, vp, vp, sz, vp]
     for f in (lib.ds_rows_rope_turns, lib.ds_rows_rope, lib.ds_rows_append, lib.ds_rows_fetch,
@@ -376,22 +376,24 @@ def ds_rows_sparse_attn_paged(rows, q_attn: torch.Tensor, sinks: torch.Tensor, s
 # attention over a shared prefix
 # ---------------------------------------------------------------------------
 
-def ds_rows_prefix_attn_workspace_bytes(rows, prefix_len: int) -> int:
-    """Workspace bytes that ds_rows_prefix_attn needs for these rows."""
-    return _prefix_bytes(_rows(rows)[0], _u32(prefix_len, "prefix_len"))
+def ds_rows_prefix_attn_workspace_bytes(rows, prefix_len: int, fmt: Optional[str] = None) -> int:
+    """Workspace bytes that ds_rows_prefix_attn uses for these rows over a cache of `fmt` (None: of any)."""
+    return _prefix_bytes(_rows(rows)[0], _u32(prefix_len, "prefix_len"),
+                         -1 if fmt is None else _code(_FORMATS, fmt, "the cache's format"))
 
 
-def _prefix_bytes(words, prefix_len: int) -> int:
+def _prefix_bytes(words, prefix_len: int, code: int) -> int:
     lib = load()
-    n = lib.ds_rows_prefix_attn_workspace_bytes(len(words) // 4, words.buffer_info()[0], prefix_len)
+    n = lib.ds_rows_prefix_attn_workspace_bytes(len(words) // 4, words.buffer_info()[0], prefix_len, code)
     if n == 0:
         _check(lib, -1)
     return int(n)
 
 
-def prefix_attn_workspace(rows, prefix_len: int, device=None) -> torch.Tensor:
-    """A workspace tensor for ds_rows_prefix_attn (uint8, 256-byte aligned by the caching allocator)."""
-    return torch.empty(ds_rows_prefix_attn_workspace_bytes(rows, prefix_len), dtype=torch.uint8,
+def prefix_attn_workspace(rows, prefix_len: int, fmt: Optional[str] = None, device=None) -> torch.Tensor:
+    """A workspace tensor for ds_rows_prefix_attn over a cache of `fmt`, or of any (uint8, 256-byte aligned by
+    the caching allocator)."""
+    return torch.empty(ds_rows_prefix_attn_workspace_bytes(rows, prefix_len, fmt), dtype=torch.uint8,
                        device=device if device is not None else "cuda")
 
 
@@ -402,7 +404,7 @@ def ds_rows_prefix_attn(rows, prefix_len: int, q_attn: torch.Tensor, sinks: torc
     prefix_len are those of entry 0 for every row, the others entry e's own.
 
     rows: (kv_len, width, index_offset, q_row) as elsewhere; width and index_offset are not
-    looked at. workspace_t (optional): prefix_attn_workspace(rows, prefix_len) or a larger one."""
+    looked at. workspace_t (optional): prefix_attn_workspace(rows, prefix_len, kv.format) or a larger one."""
     lib = load()
     dev = kv.device_index
     words, kv_len, _, _, q_row = _rows(rows)
@@ -416,7 +418,7 @@ def ds_rows_prefix_attn(rows, prefix_len: int, q_attn: torch.Tensor, sinks: torc
     pi = None if invalid is None else _tensor(invalid, "invalid", torch.int32, dev, q_rows * HEADS)
     raw = _stream_of(stream, dev)
     if workspace_t is None:
-        workspace_t = _workspace_for(kv.pages.device, raw, _prefix_bytes(words, prefix_len))
+        workspace_t = _workspace_for(kv.pages.device, raw, _prefix_bytes(words, prefix_len, kv._c.format))
     pw = _tensor(workspace_t, "workspace", torch.uint8, dev, 0)
     _call(dev, lib.ds_rows_prefix_attn, n, words.buffer_info()[0], prefix_len, kv._ref, pq, ps, sinks_row_stride, scale,
           po, pi, pw, workspace_t.numel(), raw)

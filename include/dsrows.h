@@ -573,9 +573,12 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
                               const float* sinks, size_t sinks_row_stride, const int32_t* indices, float scale,
                               ds_bf16* out, uint32_t* invalid, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes for ds_rows_prefix_attn; 0 when the arguments are invalid (see
- * ds_rows_last_error). 256-byte aligned, scratch between calls. */
-size_t ds_rows_prefix_attn_workspace_bytes(int rows, const ds_row_t* table, uint32_t prefix_len);
+/* Workspace bytes for ds_rows_prefix_attn over a cache of `format` (-1: of any); 0 when the
+ * arguments are invalid (see ds_rows_last_error). 256-byte aligned, scratch between calls.
+ * For DS_CACHE_FP8 and DS_CACHE_INT4 it holds the attended rows as bf16 (1 KB each) where
+ * enough entries share them to widen them once beforehand; with DS_CACHE_BF16's
+ * bytes the call works as well, and widens them as they are used (the same bits). */
+size_t ds_rows_prefix_attn_workspace_bytes(int rows, const ds_row_t* table, uint32_t prefix_len, int format);
 
 /*
  * Sink-softmax attention over EVERY cached row, for rows that share a prefix (samples of
@@ -595,7 +598,8 @@ size_t ds_rows_prefix_attn_workspace_bytes(int rows, const ds_row_t* table, uint
  *   kv          dim 512, any format, with at least `rows` entries that reach kv_len
  *   q_attn      bf16 [Q, 64, 512], 16-B aligned; sinks, sinks_row_stride, scale, out and invalid
  *               as for ds_rows_sparse_attn (sinks and invalid 4-B aligned)
- *   workspace   at least ds_rows_prefix_attn_workspace_bytes(...) bytes, 256-byte aligned
+ *   workspace   at least ds_rows_prefix_attn_workspace_bytes(..., DS_CACHE_BF16) bytes, 256-byte
+ *               aligned
  * A page id out of range under one of an entry's rows zeroes every head of it (under the prefix:
  * of every entry). A head is zeroed where a q element, the sink, an element of one of
  * the entry's rows or a logit (in units of ln 2) is not finite. Memory behind kv_len, and rows of

@@ -60,8 +60,17 @@ def test_workspace_bytes(lib):
     size = ds.ds_rows_prefix_attn_workspace_bytes
     assert size([(1, 1, 0, 0)], 0) >= 256 + part
     # The longest and most rows need no more than a part for every pair of processors and every segment.
-    most = size([((1 << 31) - 1, 1, 0, i) for i in range(64)], (1 << 31) - 200)
-    assert most <= 512 + (76 + 96) * part
+    long = [((1 << 31) - 1, 1, 0, i) for i in range(64)], (1 << 31) - 200
+    assert size(*long, "bf16") <= 512 + (76 + 96) * part
+    # Packed rows that many entries share are also held as bf16, a kilobyte each, in whole tiles.
+    shared = [(1000 + i, 1, 0, i) for i in range(6)], 1000
+    for fmt in ("fp8", "int4", None):
+        assert size(*shared, fmt) == size(*shared, "bf16") + (8 + 5) * 128 * 1024
+        assert size([(1000, 1, 0, 0), (1001, 1, 0, 1)], 1000, fmt) == size([(1000, 1, 0, 0), (1001, 1, 0, 1)], 1000, "bf16")
+    with pytest.raises(ValueError, match="one of"):
+        size(*shared, "fp4")
+    tab, n = ds._table([(5, 1, 0, 0)])
+    assert lib.ds_rows_prefix_attn_workspace_bytes(n, tab, 5, 2) == 0 and "format" in _err(lib)
     assert size(iter([(9, 1, 0, 0)]), np.int64(9)) == size([(9, 1, 0, 0)], 9)
     for rows, prefix in (([], 0), ([(5, 1, 0, 0)], 6), ([(5, 1, 0, 0)] * 2, 0)):
         with pytest.raises((ValueError, ds.DsRowsError)):
@@ -70,7 +79,7 @@ def test_workspace_bytes(lib):
         with pytest.raises(ValueError, match="whole number"):
             size([(5, 1, 0, 0)], prefix)
     tab, n = ds._table([(600, 1, 0, 0)])
-    need = lib.ds_rows_prefix_attn_workspace_bytes(n, tab, 500)
+    need = lib.ds_rows_prefix_attn_workspace_bytes(n, tab, 500, 1)
     assert _attn(lib, prefix=500, ws_bytes=need - 1) == -2 and f"needs {need}" in _err(lib)
 
 
