@@ -217,9 +217,9 @@ constexpr uint32_t kPrefixSegsMax = kPrefixRowsMax / 2 + kPrefixRowsMax;
 constexpr uint32_t kPrefixPairsMax = 76;  // of this GPU's 152 multiprocessors
 constexpr uint32_t kPrefixTile = 128;
 constexpr uint32_t kPrefixBoxRows = 32;  // a TMA box of rows: this many, or a smaller page
-// For each TMEM lane (head, half) the maximum that O refers to, the two softmax sets' sums and their
-// flags; then O [64 column groups][128 lanes][4].
-constexpr size_t kPrefixHeadFloats = 5 * 128;
+// For each head the maximum that O refers to; the sums of its slots in four shares (softmax set, half
+// of a tile), NaN where one is flagged; then O [64 column groups][128 TMEM lanes (half, head)][4].
+constexpr size_t kPrefixHeadFloats = 5 * DS_HEADS;
 constexpr size_t kPrefixPartFloats = kPrefixHeadFloats + (size_t)DS_HEADS * DS_DIM;
 
 struct PrefixParams {

@@ -655,12 +655,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 const float now = m_s[128 * (set ^ 1) + row];
                 if (now != m) sum *= exp2_fast(m - now);
             }
-            if (mine) {
-                out[128 + 128 * set + row] = sum;
-                reinterpret_cast<uint32_t*>(out)[384 + 128 * set + row] = bad;
-            }
+            if (mine) out[kHeads + 4 * head + 2 * set + half] = bad ? __int_as_float(0x7FC00000) : sum;  // a flag is NaN
             if ((last & 1) != set) continue;
-            if (mine) out[row] = m;
+            if (mine && half == 0) out[head] = m;
             if (!(ok = wait_warp(&bar->pv_done[last & 1], last >> 1 & 1, p.status))) break;
             tc_fence_after();
 #pragma unroll 1
@@ -857,12 +854,10 @@ __global__ void __launch_bounds__(kWidenThreads) prefix_widen_kernel(const __gri
 // ---- the join of a row's parts -------------------------------------------------------------------
 
 namespace {
-constexpr int kJoinSlices = 8;
-constexpr int kJoinCols = 2;
-constexpr size_t kJoinSmem = sizeof(float4) * kJoinCols * kJoinSlices * 128;
-constexpr int kJoinThreads = 128 * kJoinSlices;
-constexpr uint32_t kJoinSplit = 12;  // from this many parts on, the slices share a column's parts
+constexpr int kJoinThreads = 512;
+constexpr int kJoinWays = kJoinThreads / kHeads;
 constexpr uint32_t kJoinParts = kPrefixPairsMax + 2;  // a row's, at most: its segments lie on one line of runs
+constexpr int kJoinAhead = 8;                         // parts whose O is fetched before the factors are known
 
 // A row's parts in their order: those of its group's prefix, then its own.
 struct RowParts {
@@ -886,108 +881,93 @@ struct RowParts {
 };
 }  // namespace
 
-// A block joins `cols` columns of the O layout (4 dims of each half of 64 heads) of one row. The factors
-// exp(m_i - m) of the parts come first, for every lane; then a thread = (lane, slice) has whole
-// columns (few parts), or a slice of a column's parts.
-__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ PrefixParams p, uint32_t cols) {
+// A block joins columns of the O layout (4 dims of each half of 64 heads) of one row. The factors exp(m_i - m) of the
+// parts come first, for every head; then a thread = (lane, way): with kSplit the four ways have a column's
+// parts i = way mod 4 each (few rows: one column a block), else a column each (`cols` columns a block).
+// Bound by the parts' bytes in L2, and for few rows by its chain of loads.
+template <bool kSplit>
+__global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(const __grid_constant__ PrefixParams p, uint32_t cols) {
+    constexpr uint32_t kWays = kJoinThreads / 128, kStep = kSplit ? kWays : 1;
     __shared__ float fac_s[kJoinParts][kHeads];
-    __shared__ float m_s[kJoinSlices][kHeads], l_s[kJoinSlices][kHeads];
-    __shared__ uint32_t bad_s[kJoinSlices][kHeads];
-    extern __shared__ __align__(16) float4 acc_raw[];  // [kJoinCols][kJoinSlices][128]
-    auto acc_s = reinterpret_cast<float4(*)[kJoinSlices][128]>(acc_raw);
+    __shared__ float m_s[kJoinWays][kHeads], l_s[kJoinWays][kHeads];
+    __shared__ float4 acc_s[kSplit ? kWays - 1 : 1][128];
     pdl_trigger();
-    const uint32_t r = blockIdx.x, lane = threadIdx.x & 127, slice = threadIdx.x >> 7, head = lane & 63;
+    const uint32_t r = blockIdx.x, lane = threadIdx.x & 127, way = threadIdx.x >> 7;
+    const uint32_t head = threadIdx.x & 63, head_way = threadIdx.x >> 6;  // head: the lane's as well
     const RowParts parts(p, r);
     const size_t at = (size_t)p.q_row[r] * kHeads + head;
     pdl_wait();
     const float sink = p.sinks[(size_t)p.q_row[r] * p.sinks_row_stride + head];
+    const uint32_t stopped = *p.status;
+    const uint32_t i0 = kSplit ? way : 0;
+    uint32_t col = blockIdx.y * cols + (kSplit ? 0 : way);
+    auto o_at = [&](uint32_t i) {
+        return __ldcg(reinterpret_cast<const float4*>(parts.at(i) + kPrefixHeadFloats) + col * 128 + lane);
+    };
+    float4 ahead[kJoinAhead];
+    auto fetch_ahead = [&] {
+#pragma unroll
+        for (uint32_t k = 0; k < kJoinAhead; ++k)
+            if (i0 + k * kStep < parts.count) ahead[k] = o_at(i0 + k * kStep);
+    };
+    fetch_ahead();
     float m = -INFINITY;
-    uint32_t bad = *p.status != 0 ? 1u : 0u;
 #pragma unroll 4
-    for (uint32_t i = slice; i < parts.count; i += kJoinSlices) {
-        const float* part = parts.at(i);
-        const uint32_t* flags = reinterpret_cast<const uint32_t*>(part) + 384 + head;
-        m = fmaxf(m, __ldcg(part + head));  // both of a head's lanes have it
-        bad |= __ldcg(flags) | __ldcg(flags + 64) | __ldcg(flags + 128) | __ldcg(flags + 192);
+    for (uint32_t i = head_way; i < parts.count; i += kJoinWays) {
+        const float x = __ldcg(parts.at(i) + head);
+        fac_s[i][head] = x;
+        m = fmaxf(m, x);
     }
-    m_s[slice][head] = m;
-    bad_s[slice][head] = bad;
+    m_s[head_way][head] = m;
     __syncthreads();
     float top = sink * kLog2e;
-    bad = 0;
 #pragma unroll
-    for (int s = 0; s < kJoinSlices; ++s) {
-        top = fmaxf(top, m_s[s][head]);
-        bad |= bad_s[s][head];
-    }
+    for (int k = 0; k < kJoinWays; ++k) top = fmaxf(top, m_s[k][head]);
     float l = 0.0f;
 #pragma unroll 4
-    for (uint32_t i = slice; i < parts.count; i += kJoinSlices) {
-        const float* part = parts.at(i);
-        const float f = exp2f(__ldcg(part + head) - top);
+    for (uint32_t i = head_way; i < parts.count; i += kJoinWays) {
+        const float f = exp2f(fac_s[i][head] - top);
+        const float4 sums = __ldcg(reinterpret_cast<const float4*>(parts.at(i) + kHeads) + head);
         fac_s[i][head] = f;
-        const float* sums = part + 128 + head;
-        l = fmaf((__ldcg(sums) + __ldcg(sums + 64)) + (__ldcg(sums + 128) + __ldcg(sums + 192)), f, l);
+        l = fmaf((sums.x + sums.y) + (sums.z + sums.w), f, l);
     }
-    l_s[slice][head] = l;
+    l_s[head_way][head] = l;
     __syncthreads();
     float den = exp2f(sink * kLog2e - top);
 #pragma unroll
-    for (int s = 0; s < kJoinSlices; ++s) den += l_s[s][head];
-    const bool zero = bad || !finite_f(sink) || !finite_f(top) || !finite_f(den) || !(den > 0.0f);
+    for (int k = 0; k < kJoinWays; ++k) den += l_s[k][head];
+    // A flagged part's sum is NaN.
+    const bool zero = stopped || !finite_f(sink) || !finite_f(top) || !finite_f(den) || !(den > 0.0f);
     const float inv = 1.0f / den;
     if (p.invalid && blockIdx.y == 0 && threadIdx.x < 64) p.invalid[at] = zero ? 1u : 0u;
-
-    auto add = [&](float4& acc, uint32_t i, uint32_t col) {
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(parts.at(i) + kPrefixHeadFloats) + col * 128 + lane);
-        const float f = fac_s[i][head];
+    auto add = [&](float4& acc, const float4& o, float f) {
         acc.x = fmaf(o.x, f, acc.x);
         acc.y = fmaf(o.y, f, acc.y);
         acc.z = fmaf(o.z, f, acc.z);
         acc.w = fmaf(o.w, f, acc.w);
     };
-    auto put = [&](const float4& acc, uint32_t col) {
+    for (const uint32_t stop = (blockIdx.y + 1) * cols;;) {
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (uint32_t k = 0; k < kJoinAhead; ++k)
+            if (i0 + k * kStep < parts.count) add(acc, ahead[k], fac_s[i0 + k * kStep][head]);
+#pragma unroll 8
+        for (uint32_t i = i0 + kJoinAhead * kStep; i < parts.count; i += kStep) add(acc, o_at(i), fac_s[i][head]);
+        if (kSplit) {
+            if (way > 0) acc_s[way - 1][lane] = acc;
+            __syncthreads();
+            if (way > 0) return;
+#pragma unroll
+            for (uint32_t k = 0; k < kWays - 1; ++k) add(acc, acc_s[k][lane], 1.0f);
+        }
         const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
         __align__(8) __nv_bfloat16 y[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = __float2bfloat16_rn(!zero && finite_f(x[k]) ? x[k] : 0.0f);
         const uint32_t dim = 256 * (col >> 5) + 128 * (lane >> 6) + 4 * (col & 31);
         *reinterpret_cast<uint2*>(p.out + at * kDim + dim) = *reinterpret_cast<const uint2*>(y);
-    };
-    const uint32_t col0 = blockIdx.y * cols;
-    if (parts.count < kJoinSplit) {
-        for (uint32_t c = slice; c < cols; c += kJoinSlices) {
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (uint32_t i = 0; i < parts.count; ++i) add(acc, i, col0 + c);
-            put(acc, col0 + c);
-        }
-        return;
-    }
-    for (uint32_t c = 0; c < cols; c += kJoinCols) {
-        float4 acc[kJoinCols];
-#pragma unroll
-        for (int k = 0; k < kJoinCols; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 5
-        for (uint32_t i = slice; i < parts.count; i += kJoinSlices)
-#pragma unroll
-            for (int k = 0; k < kJoinCols; ++k) add(acc[k], i, col0 + c + k);
-#pragma unroll
-        for (int k = 0; k < kJoinCols; ++k) acc_s[k][slice][lane] = acc[k];
-        __syncthreads();
-        if (slice < kJoinCols) {
-            float4 sum = acc_s[slice][0][lane];
-#pragma unroll
-            for (int s = 1; s < kJoinSlices; ++s) {
-                const float4 o = acc_s[slice][s][lane];
-                sum.x += o.x;
-                sum.y += o.y;
-                sum.z += o.z;
-                sum.w += o.w;
-            }
-            put(sum, col0 + c + slice);
-        }
-        __syncthreads();
+        if (kSplit || (col += kWays) >= stop) return;
+        fetch_ahead();
     }
 }
 
@@ -998,13 +978,12 @@ static cudaError_t launch(const PrefixParams& p, cudaStream_t stream, bool pdl) 
     if (err != cudaSuccess) return err;
     err = launch_kernel(prefix_attn_kernel<kFormat>, dim3(2 * p.pairs), dim3(kThreads<kFormat>), kSmem, stream, pdl, p);
     if (err != cudaSuccess) return err;
-    // Columns a block: about two blocks for each multiprocessor.
-    static std::atomic<uint64_t> join_set{0};
-    err = set_smem_limit_once(prefix_join_kernel, kJoinSmem, join_set);
-    if (err != cudaSuccess) return err;
-    uint32_t cols = kJoinCols;
+    // About two blocks for each multiprocessor: a column a block for up to four rows, else four columns or more.
+    if (p.rows <= 4)
+        return launch_kernel(prefix_join_kernel<true>, dim3(p.rows, 64), dim3(kJoinThreads), 0, stream, true, p, 1u);
+    uint32_t cols = 4;
     while (p.rows * (64 / cols) > 4 * kPrefixPairsMax) cols *= 2;
-    return launch_kernel(prefix_join_kernel, dim3(p.rows, 64 / cols), dim3(kJoinThreads), kJoinSmem, stream, true, p, cols);
+    return launch_kernel(prefix_join_kernel<false>, dim3(p.rows, 64 / cols), dim3(kJoinThreads), 0, stream, true, p, cols);
 }
 
 template <int kFormat>

@@ -56,7 +56,7 @@ def test_width_and_index_offset_are_not_looked_at(lib):
 
 
 def test_workspace_bytes(lib):
-    part = 2 * 4 * (5 * 128 + 64 * 512)
+    part = 2 * 4 * (5 * 64 + 64 * 512)
     size = ds.ds_rows_prefix_attn_workspace_bytes
     assert size([(1, 1, 0, 0)], 0) >= 256 + part
     # The longest and most rows need no more than a part for every pair of processors and every segment.
