@@ -338,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
         mbar_init(&bar->q_full, 2);
         mbar_init(&bar->p_full, 8);
         mbar_init(&bar->q_free, 1);
-        mbar_init(&bar->o_read, 8);
+        mbar_init(&bar->o_read, 16);
         mbar_init(&bar->drained, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar->s_free[i], 8);
@@ -364,13 +364,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
     cluster_wait_acquire();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem_base, 0);
+    // The pair's tiles. (What depends on the parameters alone comes before the wait for the kernel before this one.)
+    Part part;
+    uint32_t n = 0;
+    for (Walk w(p, pair, pairs); w.next(part);) n += part.tiles;
+    if (threadIdx.x == 32 * 3) {
+        tma_prefetch_map(&p.qmap);
+        if (kByTma<kFormat>) tma_prefetch_map(&p.kvmap);
+    }
     pdl_wait();
     pdl_trigger();
     // The first block starts first; a wait that gives up reports seconds later.
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
-    Part part;
-    uint32_t it = 0;  // the pair's tiles so far
+    uint32_t it = 0;  // the tiles so far
     if (warp == 0) {
         // ---- the tiles' rows: places in the pool ----------------------------------------------
         bool ok = true;
@@ -468,8 +475,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             } else {
                 constexpr uint32_t idesc = idesc_bf16_f32(128, 256) | 1u << 16;  // B is MN-major
                 const uint64_t a_desc = smem_desc_sw128_kmajor(smem_u32(smem + Layout::p));
-                uint32_t n = 0;
-                for (Walk w(p, pair, pairs); w.next(part);) n += part.tiles;
                 for (Walk w(p, pair, pairs); ok && w.next(part); ++n_part)
                     for (uint32_t i = 0; i < part.tiles; ++i, ++it) {
                         const uint32_t slot = it + 1 < n ? 0 : 4, lap = it + 1 < n ? it + 1 : it;
@@ -644,8 +649,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 if (lane == 0) arrive_first_cta(&bar->p_full);
             }
             if (!ok) break;
-            // ---- the part's state: the maximum that O refers to, and each set's sum and flag; the set that had
-            // the last tile also leaves O ------------------------------------------------------------
+            // ---- the part's state: the maximum that O refers to, each set's sum, and O -------------------
             const uint32_t last = it - 1;
             const uint32_t r = part.seg < p.groups ? 2 * part.seg + rank : rank == 0 ? part.seg - p.groups : p.rows;
             const bool mine = r < p.rows;  // the pair's second CTA may have no row
@@ -656,30 +660,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 if (now != m) sum *= exp2_fast(m - now);
             }
             if (mine) out[kHeads + 4 * head + 2 * set + half] = bad ? __int_as_float(0x7FC00000) : sum;  // a flag is NaN
-            if ((last & 1) != set) continue;
-            if (mine && half == 0) out[head] = m;
+            if (mine && half == 0 && (last & 1) == set) out[head] = m;
             if (!(ok = wait_warp(&bar->pv_done[last & 1], last >> 1 & 1, p.status))) break;
             tc_fence_after();
-#pragma unroll 1
-            for (uint32_t c = 0; c < 256; c += 32) {
+            float4* to = reinterpret_cast<float4*>(out + kPrefixHeadFloats) + 32 * set * 128 + row;
+#pragma unroll
+            for (uint32_t c = 0; c < 128; c += 32) {  // each set a half of the columns
                 uint32_t o[32];
-                tmem_ld_x32(lanes + kOCol + c, o);
+                tmem_ld_x32(lanes + kOCol + 128 * set + c, o);
                 tmem_ld_wait();
-                float4* to = reinterpret_cast<float4*>(out + kPrefixHeadFloats) + (c / 4) * 128 + row;
                 if (mine)
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        to[k * 128] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                  __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                        to[(c / 4 + k) * 128] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                            __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_first_cta(&bar->o_read);
         }
         // A warp that gave up still meets the others.
-        uint32_t all = 0;
-        for (Walk w(p, pair, pairs); w.next(part);) all += part.tiles;
-        for (all = (all + 1 - set) / 2; met < all; ++met) sync_softmax(set);
+        for (; met < (n + 1 - set) / 2; ++met) sync_softmax(set);
     } else if (warp == 3) {
         // ---- each part's query, once the MMAs of the part before have read theirs --------------
         uint32_t n_part = 0;
@@ -696,8 +697,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
         // ---- operands -----------------------------------------------------------------------------
         // With n tiles the ring's order K(0), K(1), V(0), K(2), V(1), .. K(n - 1), V(n - 2), V(n - 1) gives units 0 to
         // 3 K(0), then V(0 .. n - 2), and units 4 to 7 K(1 .. n - 1), then V(n - 1).
-        uint32_t n = 0;
-        for (Walk w(p, pair, pairs); w.next(part);) n += part.tiles;
         auto looked_up = [&](uint32_t of) {
             return wait_warp(&bar->place_full[of % kPlaceBufs], of / kPlaceBufs & 1, p.status);
         };
@@ -794,7 +793,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
 
     tc_fence_before();
     __syncthreads();
-    cluster_arrive_release();  // neither CTA leaves while the other's MMAs or arrivals may reach it
+    cluster_arrive_relaxed();  // neither CTA leaves while the other's MMAs or arrivals may reach it
     cluster_wait_acquire();
     if (warp == 1) {
         tc_fence_after();
