@@ -38,9 +38,8 @@ namespace {
 
 constexpr int kTile = kPrefixTile;            // slots of a tile
 constexpr int kUnitBytes = 16384;             // a ring unit: [64 slots][128 dims] or [32 slots][256 dims]
-constexpr int kUnits = 8;                     // of the ring
 constexpr int kQBytes = kHeads * kDim * 2;    // the CTA's query row, 8 blocks [64 heads][64 dims]
-constexpr int kPBytes = kHeads * kTile * 2;   // P: 2 blocks [64 heads][64 slots]
+constexpr int kPBytes = kHeads * kTile * 2;   // P of a tile: 2 blocks [64 heads][64 slots]
 constexpr int kBoxRows = kPrefixBoxRows;      // most rows of a TMA box
 constexpr int kPlaceBufs = 4;                 // tiles whose rows are looked up
 // A kernel's source of rows: the pages of a format, or bf16 rows widened beforehand.
@@ -48,16 +47,26 @@ constexpr int kWidened = -1;
 template <int kFormat>
 constexpr bool kByTma = kFormat == DS_CACHE_BF16 || kFormat == kWidened;
 constexpr int kSoftmaxWarp = 4, kBuildWarp = 12;  // two sets of four softmax warps
-// Warps that bring operands, those of them that fill a ring unit, and those that read a tile's places for a form.
+// Units of the K form, which hold a tile, and of the V form. Where the rows come by TMA, three units of the V form are
+// enough, and P is held for two tiles (P of the next tile is written while P G of this one runs); widening
+// sets another pace, and has four, and one P.
+constexpr uint32_t kKUnits = 4;
 template <int kFormat>
-constexpr int kBuildWarps = kByTma<kFormat> ? kUnits : 16;
+constexpr uint32_t kVUnits = kByTma<kFormat> ? 3 : 4;
+template <int kFormat>
+constexpr uint32_t kPBufs = kByTma<kFormat> ? 2 : 1;
+constexpr uint32_t kUnitsMax = 8;
+// Warps that bring operands, those of them that fill a unit, and those that read a tile's places for a form.
+template <int kFormat>
+constexpr int kBuildWarps = kByTma<kFormat> ? kKUnits + kVUnits<kFormat> : 16;
 template <int kFormat>
 constexpr int kFillers = kByTma<kFormat> ? 1 : 8;
 template <int kFormat>
 constexpr int kReaders = kByTma<kFormat> ? 4 : 16;
 template <int kFormat>
 constexpr int kThreads = 32 * (kBuildWarp + kBuildWarps<kFormat>);
-constexpr uint32_t kOCol = 128;               // TMEM: two S of 64 columns, then O
+constexpr uint32_t kOCol = 128;               // TMEM: two S of 64 columns, O, two more S
+constexpr uint32_t kSBufs = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint16_t kBoth = 3;                 // the CTAs of a pair
 // The running maximum is raised only when a tile's exceeds it by more than this (in units of ln 2): the
@@ -69,30 +78,32 @@ constexpr int kNoRow = -1, kBadRow = -2;
 constexpr uint32_t kMasked = 1;     // some slot of the tile has no row
 constexpr uint32_t kByThreads = 2;  // the tile is not whole boxes of rows of one page each
 
+template <int kFormat>
 struct Layout {
-    static constexpr size_t ring = 0;
-    static constexpr size_t q = ring + (size_t)kUnits * kUnitBytes;
+    static constexpr size_t ring = 0;  // K units, then V units
+    static constexpr size_t q = ring + (size_t)(kKUnits + kVUnits<kFormat>) * kUnitBytes;
     static constexpr size_t p = q + kQBytes;
-    static constexpr size_t place = p + kPBytes;                         // i32 [kPlaceBufs][128]
-    static constexpr size_t red = place + kPlaceBufs * kTile * 4;        // f32 [2][128]
-    static constexpr size_t maxima = red + 2 * 128 * 4;                  // f32 [2][128]
+    static constexpr size_t place = p + kPBufs<kFormat> * (size_t)kPBytes;  // i32 [kPlaceBufs][128]
+    static constexpr size_t red = place + kPlaceBufs * kTile * 4;          // f32 [2][128]
+    static constexpr size_t maxima = red + 2 * 128 * 4;                    // f32 [2][128]
     static constexpr size_t bars = maxima + 2 * 128 * 4;
 };
 
 struct __align__(8) Bars {
     // In the pair's first CTA, from both:
-    uint64_t full[kUnits];
-    uint64_t q_full, p_full, s_free[2], o_read;
+    uint64_t full[kUnitsMax];
+    uint64_t q_full, p_full[2], s_free[kSBufs], o_read;
     // In each CTA:
-    uint64_t empty[kUnits];
-    uint64_t q_free, s_full[2], pv_done[2], m_ready[2], drained;
+    uint64_t empty[kUnitsMax];
+    uint64_t q_free, s_full[kSBufs], pv_done[2], m_ready[2], drained;
     uint64_t place_full[kPlaceBufs], place_free[kPlaceBufs];
     uint32_t form[kPlaceBufs];     // of the tile: kMasked, kByThreads
     uint32_t tmem_base;
 };
 
-constexpr size_t kSmem = Layout::bars + sizeof(Bars) + 1024;
-static_assert(kSmem <= 227 * 1024, "shared memory");
+template <int kFormat>
+constexpr size_t kSmem = Layout<kFormat>::bars + sizeof(Bars) + 1024;
+static_assert(kSmem<DS_CACHE_BF16> <= 227 * 1024 && kSmem<DS_CACHE_INT4> <= 227 * 1024, "shared memory");
 
 // ---- the pair's tcgen05 forms and barriers ---------------------------------------------------
 
@@ -276,6 +287,9 @@ struct Piece {
     }
 };
 
+// The TMEM columns of S of tile `it`.
+__device__ __forceinline__ uint32_t s_col(uint32_t it) { return (it & 1) * 64 + (it & 2) * 192; }
+
 // ---- the pair's tiles --------------------------------------------------------------------------
 
 // A run of a pair's tiles within one segment.
@@ -321,30 +335,34 @@ struct Walk {
 template <int kFormat>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1)
     prefix_attn_kernel(const __grid_constant__ PrefixParams p) {
+    using L = Layout<kFormat>;
+    constexpr uint32_t kV = kVUnits<kFormat>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    Bars* bar = reinterpret_cast<Bars*>(smem + Layout::bars);
-    int32_t* place_s = reinterpret_cast<int32_t*>(smem + Layout::place);
+    Bars* bar = reinterpret_cast<Bars*>(smem + L::bars);
+    int32_t* place_s = reinterpret_cast<int32_t*>(smem + L::place);
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
     const int lane = threadIdx.x & 31;
     const uint32_t rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const uint32_t ring = smem_u32(smem + Layout::ring);
+    const uint32_t ring = smem_u32(smem + L::ring);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kUnits; ++i) {
+        for (uint32_t i = 0; i < kKUnits + kV; ++i) {
             mbar_init(&bar->full[i], 2 * kFillers<kFormat>);
             mbar_init(&bar->empty[i], 1);
         }
         mbar_init(&bar->q_full, 2);
-        mbar_init(&bar->p_full, 8);
-        mbar_init(&bar->q_free, 1);
         mbar_init(&bar->o_read, 16);
+        mbar_init(&bar->q_free, 1);
         mbar_init(&bar->drained, 2);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar->s_free[i], 8);
-            mbar_init(&bar->s_full[i], 1);
+            mbar_init(&bar->p_full[i], 8);
             mbar_init(&bar->pv_done[i], 1);
             mbar_init(&bar->m_ready[i], 4);
+        }
+        for (uint32_t i = 0; i < kSBufs; ++i) {
+            mbar_init(&bar->s_free[i], 8);
+            mbar_init(&bar->s_full[i], 1);
         }
         for (int i = 0; i < kPlaceBufs; ++i) {
             mbar_init(&bar->place_full[i], 1);
@@ -422,11 +440,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
         // ---- the MMAs, issued in the first CTA for both: warp 1 S = Q G^T, warp 2 O += P G. (One warp for both took
         // 3,900 cycles a tile, twice the MMAs' time: waits of 100 to 200 cycles and 20 or so an MMA, one after another.)
         if (rank == 0) {
-            // Units slot .. slot + 3, one form of a tile: those that are full among the first u + 1 (bits), once unit u is.
-            auto unit_full = [&](uint32_t slot, uint32_t lap, uint32_t u, uint32_t& bits) -> bool {
+            // Unit u of a form, the lanes looking at all the form's units together: lane i at `full` in phase `parity`. Bits
+            // are the units known to be full; lane u + units and later ones look at a barrier before its time.
+            auto unit_full = [&](uint64_t* full, uint32_t parity, uint32_t u, uint32_t units, uint32_t& bits) -> bool {
                 uint64_t start = 0;
                 for (uint32_t tries = 1; !(bits >> u & 1); ++tries) {
-                    bits = __ballot_sync(0xFFFFFFFFu, mbar_try_wait(&bar->full[slot + (lane & 3)], lap & 1)) & 15;
+                    bits = __ballot_sync(0xFFFFFFFFu, mbar_try_wait(full, parity)) & 15 & ((1u << (u + units)) - 1);
                     if (tries % 64 == 0) {
                         const uint64_t now = __shfl_sync(0xFFFFFFFFu, global_timer_ns(), 0);
                         if (start == 0) start = now;
@@ -442,29 +461,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             bool ok = true;
             if (warp == 1) {
                 constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
-                const uint64_t a_desc = smem_desc_sw128_kmajor(smem_u32(smem + Layout::q));
+                const uint64_t a_desc = smem_desc_sw128_kmajor(smem_u32(smem + L::q));
                 for (Walk w(p, pair, pairs); ok && w.next(part); ++n_part)
                     for (uint32_t i = 0; i < part.tiles; ++i, ++it) {
-                        const uint32_t buf = it & 1, slot = it == 0 ? 0 : 4;
                         ok = i != 0 || wait_warp(&bar->q_full, n_part & 1, p.status);
-                        ok = ok && wait_warp(&bar->s_free[buf], (it >> 1 & 1) ^ 1, p.status);
-                        const uint64_t b_desc = smem_desc_sw128_kmajor(ring + slot * kUnitBytes);
-                        const uint32_t d = tmem + buf * 64;
+                        ok = ok && wait_warp(&bar->s_free[it % kSBufs], (it / kSBufs & 1) ^ 1, p.status);
+                        const uint32_t d = tmem + s_col(it);
                         uint32_t full = 0;
 #pragma unroll
                         for (uint32_t u = 0; u < 4; ++u) {
-                            ok = ok && unit_full(slot, it == 0 ? 0 : it - 1, u, full);
+                            ok = ok && unit_full(&bar->full[lane & 3], it & 1, u, kKUnits, full);
                             if (!ok) break;
                             tc_fence_after();
+                            const uint64_t b_desc = smem_desc_sw128_kmajor(ring + u * kUnitBytes);
                             if (elect_one()) {
 #pragma unroll
                                 for (uint32_t ks = 0; ks < 8; ++ks) {
-                                    const uint32_t at = (u * kUnitBytes + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4;
-                                    umma2_bf16(d, a_desc + at, b_desc + at, idesc, u == 0 && ks == 0 ? 0u : 1u);
+                                    const uint32_t at = ((ks >> 2) * 8192 + (ks & 3) * 32) >> 4;
+                                    umma2_bf16(d, a_desc + (u * kUnitBytes >> 4) + at, b_desc + at, idesc,
+                                               u == 0 && ks == 0 ? 0u : 1u);
                                 }
-                                umma2_commit(&bar->empty[slot + u]);
+                                umma2_commit(&bar->empty[u]);
                                 if (u == 3) {
-                                    umma2_commit(&bar->s_full[buf]);
+                                    umma2_commit(&bar->s_full[it % kSBufs]);
                                     if (i + 1 == part.tiles) umma2_commit(&bar->q_free);
                                 }
                             }
@@ -474,20 +493,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                     }
             } else {
                 constexpr uint32_t idesc = idesc_bf16_f32(128, 256) | 1u << 16;  // B is MN-major
-                const uint64_t a_desc = smem_desc_sw128_kmajor(smem_u32(smem + Layout::p));
                 for (Walk w(p, pair, pairs); ok && w.next(part); ++n_part)
                     for (uint32_t i = 0; i < part.tiles; ++i, ++it) {
-                        const uint32_t slot = it + 1 < n ? 0 : 4, lap = it + 1 < n ? it + 1 : it;
-                        ok = wait_warp(&bar->p_full, it & 1, p.status);
+                        ok = wait_warp(&bar->p_full[it & 1], it >> 1 & 1, p.status);
                         // A part begins O anew, once the part before has been read.
                         ok = ok && (i != 0 || n_part == 0 || wait_warp(&bar->o_read, (n_part - 1) & 1, p.status));
-                        const uint64_t b_desc = smem_desc_sw128_mnmajor(ring + slot * kUnitBytes, 4096, 1024);
+                        const uint64_t a_desc = smem_desc_sw128_kmajor(smem_u32(smem + L::p) + it % kPBufs<kFormat> * kPBytes);
+                        const uint32_t mine = 4 * it + (lane & 3);  // the lane's unit of all
                         uint32_t full = 0;
 #pragma unroll
                         for (uint32_t v = 0; v < 4; ++v) {
-                            ok = ok && unit_full(slot, lap, v, full);
+                            ok = ok && unit_full(&bar->full[kKUnits + mine % kV], mine / kV & 1, v, kV, full);
                             if (!ok) break;
                             tc_fence_after();
+                            const uint32_t slot = kKUnits + (4 * it + v) % kV;
+                            const uint64_t b_desc = smem_desc_sw128_mnmajor(ring + slot * kUnitBytes, 4096, 1024);
                             if (elect_one()) {
 #pragma unroll
                                 for (uint32_t ks = 0; ks < 2; ++ks)
@@ -495,9 +515,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                                     for (uint32_t j = 0; j < 2; ++j)
                                         umma2_bf16(tmem + kOCol + 128 * j,
                                                    a_desc + (((v >> 1) * 8192 + (v & 1) * 64 + ks * 32) >> 4),
-                                                   b_desc + ((v * kUnitBytes + j * 8192 + ks * 2048) >> 4), idesc,
+                                                   b_desc + ((j * 8192 + ks * 2048) >> 4), idesc,
                                                    i == 0 && v == 0 && ks == 0 ? 0u : 1u);
-                                umma2_commit(&bar->empty[slot + v]);
+                                umma2_commit(&bar->empty[slot]);
                                 if (v == 3) umma2_commit(&bar->pv_done[it & 1]);
                             }
                             __syncwarp();
@@ -516,10 +536,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
         const uint32_t set = (warp - kSoftmaxWarp) >> 2;
         const uint32_t row = (threadIdx.x - 32 * kSoftmaxWarp) & 127, head = row & 63, half = row >> 6;
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint32_t s_cols = lanes + 64 * set;
-        float* red = reinterpret_cast<float*>(smem + Layout::red) + 128 * set;
-        float* m_s = reinterpret_cast<float*>(smem + Layout::maxima);  // [2][128]
-        const uint32_t p_row = smem_u32(smem + Layout::p) + half * 8192;
+        float* red = reinterpret_cast<float*>(smem + L::red) + 128 * set;
+        float* m_s = reinterpret_cast<float*>(smem + L::maxima);  // [2][128]
+        const uint32_t p_row = smem_u32(smem + L::p) + set % kPBufs<kFormat> * kPBytes + half * 8192;
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
         uint32_t met = 0;  // a set's warps meet once a tile
         bool ok = true;
@@ -530,7 +549,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             for (const uint32_t stop = it + part.tiles; it < stop; ++it) {
                 if ((it & 1) != set) continue;
                 const uint32_t pbuf = it % kPlaceBufs;
-                if (!(ok = wait_warp(&bar->s_full[set], it >> 1 & 1, p.status))) break;
+                const uint32_t sbuf = it % kSBufs, s_cols = lanes + s_col(it);
+                if (!(ok = wait_warp(&bar->s_full[sbuf], it / kSBufs & 1, p.status))) break;
                 tc_fence_after();
                 if (!(ok = wait_warp(&bar->place_full[pbuf], it / kPlaceBufs & 1, p.status))) break;
                 const bool masked = bar->form[pbuf] & kMasked;
@@ -612,14 +632,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                         w16[c] = pack_bf16(e.x, e.y);
                     }
                     if (h == 0) {
-                        // P G of the tile before is done: P may be overwritten, and O scaled.
-                        if (it > 0 && !(ok = wait_warp(&bar->pv_done[(it - 1) & 1], (it - 1) >> 1 & 1, p.status))) break;
-                        tc_fence_after();
+                        // P G of the tile that had this P is done.
+                        const uint32_t had = it - kPBufs<kFormat>;
+                        if (it >= kPBufs<kFormat> && !(ok = wait_warp(&bar->pv_done[had & 1], had >> 1 & 1, p.status))) break;
                     } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            arrive_first_cta(&bar->s_free[set]);
+                            arrive_first_cta(&bar->s_free[sbuf]);
                             mbar_arrive(&bar->place_free[pbuf]);
                         }
                     }
@@ -632,6 +652,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 s2[0] = add2(s2[0], s2[1]);
                 sum += s2[0].x + s2[0].y;
                 if (moved) {
+                    // So is that of the tile before this one: O may be scaled. (Its barrier's phase before this one is
+                    // known to be over: P G of the tiles is done in their order.)
+                    if (!(ok = wait_warp(&bar->pv_done[set ^ 1], (it - 1) >> 1 & 1, p.status))) break;
+                    tc_fence_after();
 #pragma unroll 1
                     for (uint32_t c = 0; c < 256; c += 32) {
                         uint32_t o[32];
@@ -646,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_first_cta(&bar->p_full);
+                if (lane == 0) arrive_first_cta(&bar->p_full[set]);
             }
             if (!ok) break;
             // ---- the part's state: the maximum that O refers to, each set's sum, and O -------------------
@@ -661,10 +685,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             }
             if (mine) out[kHeads + 4 * head + 2 * set + half] = bad ? __int_as_float(0x7FC00000) : sum;  // a flag is NaN
             if (mine && half == 0 && (last & 1) == set) out[head] = m;
+            // The set that did not have the last tile waits for its own first, so that the other barrier is in that phase.
+            if (kPBufs<kFormat> == 2 && (last & 1) != set && last > 0 &&
+                !(ok = wait_warp(&bar->pv_done[set], (last - 1) >> 1 & 1, p.status)))
+                break;
             if (!(ok = wait_warp(&bar->pv_done[last & 1], last >> 1 & 1, p.status))) break;
             tc_fence_after();
             float4* to = reinterpret_cast<float4*>(out + kPrefixHeadFloats) + 32 * set * 128 + row;
-#pragma unroll
+#pragma unroll 1
             for (uint32_t c = 0; c < 128; c += 32) {  // each set a half of the columns
                 uint32_t o[32];
                 tmem_ld_x32(lanes + kOCol + 128 * set + c, o);
@@ -690,13 +718,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             if (lane == 0) arrive_first_cta_expect(&bar->q_full, kQBytes);
             __syncwarp();
             if (lane < 8)
-                tma_load_pair(smem_u32(smem + Layout::q) + lane * 8192, &p.qmap, &bar->q_full, 64 * lane,
+                tma_load_pair(smem_u32(smem + L::q) + lane * 8192, &p.qmap, &bar->q_full, 64 * lane,
                               (int)(p.q_row[r] * kHeads));
         }
     } else if (warp >= kBuildWarp) {
         // ---- operands -----------------------------------------------------------------------------
-        // With n tiles the ring's order K(0), K(1), V(0), K(2), V(1), .. K(n - 1), V(n - 2), V(n - 1) gives units 0 to
-        // 3 K(0), then V(0 .. n - 2), and units 4 to 7 K(1 .. n - 1), then V(n - 1).
         auto looked_up = [&](uint32_t of) {
             return wait_warp(&bar->place_full[of % kPlaceBufs], of / kPlaceBufs & 1, p.status);
         };
@@ -705,14 +731,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             if (lane == 0) mbar_arrive(&bar->place_free[of % kPlaceBufs]);
         };
         if constexpr (kByTma<kFormat>) {
-            // Warp b fills unit b, one lap a tile.
-            const uint32_t unit = warp - kBuildWarp, u = unit & 3;
-            const uint32_t dst = ring + unit * kUnitBytes;
+            // Warp b fills unit b: of the K form one of every tile, of the V form every kV-th.
+            const uint32_t slot = warp - kBuildWarp, dst = ring + slot * kUnitBytes;
+            const bool v_form = slot >= kKUnits;
             const uint32_t box = kFormat == kWidened ? kBoxRows : min(1u << p.cache.page_shift, (uint32_t)kBoxRows);
-            for (uint32_t lap = 0; lap < n; ++lap) {
-                const uint32_t of = unit < 4 ? (lap ? lap - 1 : 0) : min(lap + 1, n - 1);
-                const bool v_form = unit < 4 ? lap > 0 : lap + 1 >= n;
-                if (!looked_up(of) || !wait_warp(&bar->empty[unit], (lap & 1) ^ 1, p.status)) break;
+            for (uint32_t lap = 0;; ++lap) {
+                const uint32_t g = v_form ? slot - kKUnits + lap * kV : 4 * lap + slot, of = g / 4, u = g % 4;
+                if (of >= n) break;
+                if (!looked_up(of) || !wait_warp(&bar->empty[slot], (lap & 1) ^ 1, p.status)) break;
                 const int32_t* at = place_s + of % kPlaceBufs * kTile + (v_form ? 32 * u : 64 * rank);
                 if (kFormat == kWidened || !(bar->form[of % kPlaceBufs] & kByThreads)) {
                     // Boxes of rows: lane = (row group, 64 dims).
@@ -722,10 +748,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                     const int32_t y = kFormat == kWidened
                                           ? place_s[of % kPlaceBufs * kTile] + (int32_t)((v_form ? 32 * u : 64 * rank) + row)
                                           : at[row];
-                    if (lane == 0) arrive_first_cta_expect(&bar->full[unit], kUnitBytes);
+                    if (lane == 0) arrive_first_cta_expect(&bar->full[slot], kUnitBytes);
                     __syncwarp();
                     if (dims < (v_form ? 4u : 2u))
-                        tma_load_pair(dst + dims * (v_form ? 4096 : 8192) + row * 128, &p.kvmap, &bar->full[unit],
+                        tma_load_pair(dst + dims * (v_form ? 4096 : 8192) + row * 128, &p.kvmap, &bar->full[slot],
                                       (int)(v_form ? v_dim(64 * dims, rank) : 128 * u + 64 * dims), y);
                     read(of);
                 } else {
@@ -743,7 +769,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                     cp_async_wait_group<0>();
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) arrive_first_cta(&bar->full[unit]);
+                    if (lane == 0) arrive_first_cta(&bar->full[slot]);
                 }
             }
         } else {
@@ -753,7 +779,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             // steps each, took 4000 cycles from a free unit to a full one, and the ring holds no more than a tile.)
             const uint32_t team = (warp - kBuildWarp) >> 3, s = warp - kBuildWarp & 7;
             Piece<kFormat> held[2];
-            // Form f of the order above: its tile and kind.
+            // The forms in the order in which the MMAs take them: K(0), K(1), V(0), K(2), V(1), .., K(n - 1), V(n - 2),
+            // V(n - 1). Form f's tile and kind.
             auto tile_of = [&](uint32_t f) { return f == 0 ? 0 : f == 2 * n - 1 ? n - 1 : f & 1 ? (f + 1) / 2 : f / 2 - 1; };
             auto v_form_of = [&](uint32_t f) { return f == 2 * n - 1 || (f > 0 && !(f & 1)); };
             auto fetch = [&](uint32_t f, uint32_t k) {
@@ -770,21 +797,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             }
             for (uint32_t f = 0; ok && f < 2 * n; ++f) {
                 const bool v_form = v_form_of(f), then = f + 1 < 2 * n;
-                // Form f lies in units 0 to 3 (f even) or 4 to 7, lap f / 2.
                 const uint32_t row = 8 * (v_form ? s >> 1 : s) + (lane & 7), size = v_form ? 4096 : 8192;
                 ok = !then || looked_up(tile_of(f + 1));
 #pragma unroll
                 for (uint32_t k = 0; k < 2; ++k) {
-                    const uint32_t unit = 4 * (f & 1) + team + 2 * k;
-                    ok = ok && wait_warp(&bar->empty[unit], (f / 2 & 1) ^ 1, p.status);
+                    const uint32_t slot = (v_form ? kKUnits : 0) + team + 2 * k;
+                    ok = ok && wait_warp(&bar->empty[slot], (tile_of(f) & 1) ^ 1, p.status);
                     if (!ok) break;
-                    const uint32_t block = ring + unit * kUnitBytes + (v_form ? (s & 1) * 8192 : 0);
+                    const uint32_t block = ring + slot * kUnitBytes + (v_form ? (s & 1) * 8192 : 0);
                     held[k].store(Piece<kFormat>::first(lane),
                                   [&](uint32_t ch) { return block + (ch >> 3) * size + swizzled(row, ch & 7); });
                     if (then) fetch(f + 1, k);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) arrive_first_cta(&bar->full[unit]);
+                    if (lane == 0) arrive_first_cta(&bar->full[slot]);
                 }
                 if (ok && then) read(tile_of(f + 1));
             }
@@ -856,7 +882,6 @@ namespace {
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWays = kJoinThreads / kHeads;
 constexpr uint32_t kJoinParts = kPrefixPairsMax + 2;  // a row's, at most: its segments lie on one line of runs
-constexpr int kJoinAhead = 8;                         // parts whose O is fetched before the factors are known
 
 // A row's parts in their order: those of its group's prefix, then its own.
 struct RowParts {
@@ -880,36 +905,25 @@ struct RowParts {
 };
 }  // namespace
 
-// A block joins columns of the O layout (4 dims of each half of 64 heads) of one row. The factors exp(m_i - m) of the
-// parts come first, for every head; then a thread = (lane, way): with kSplit the four ways have a column's
-// parts i = way mod 4 each (few rows: one column a block), else a column each (`cols` columns a block).
+// A block joins `units` units of one row. The factors exp(m_i - m) of the parts come first, for every head. Up to eight
+// rows (kSplit) have many parts each: a unit is half a column of the O layout (4 dims of 64 heads), and eight threads have
+// every eighth part each. More rows have few: a unit is four columns, a thread to a lane of each.
 // Bound by the parts' bytes in L2, and for few rows by its chain of loads.
 template <bool kSplit>
-__global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(const __grid_constant__ PrefixParams p, uint32_t cols) {
-    constexpr uint32_t kWays = kJoinThreads / 128, kStep = kSplit ? kWays : 1;
+__global__ void __launch_bounds__(kJoinThreads, 3) prefix_join_kernel(const __grid_constant__ PrefixParams p, uint32_t units) {
+    constexpr uint32_t kLanes = kSplit ? 64 : 128, kWays = kJoinThreads / kLanes, kStep = kSplit ? kWays : 1;
     __shared__ float fac_s[kJoinParts][kHeads];
     __shared__ float m_s[kJoinWays][kHeads], l_s[kJoinWays][kHeads];
-    __shared__ float4 acc_s[kSplit ? kWays - 1 : 1][128];
+    __shared__ float4 acc_s[kSplit ? kWays - 1 : 1][kLanes];
     pdl_trigger();
-    const uint32_t r = blockIdx.x, lane = threadIdx.x & 127, way = threadIdx.x >> 7;
-    const uint32_t head = threadIdx.x & 63, head_way = threadIdx.x >> 6;  // head: the lane's as well
+    const uint32_t r = blockIdx.x, way = threadIdx.x / kLanes;
+    const uint32_t head = threadIdx.x & 63, head_way = threadIdx.x >> 6;
     const RowParts parts(p, r);
     const size_t at = (size_t)p.q_row[r] * kHeads + head;
     pdl_wait();
     const float sink = p.sinks[(size_t)p.q_row[r] * p.sinks_row_stride + head];
     const uint32_t stopped = *p.status;
     const uint32_t i0 = kSplit ? way : 0;
-    uint32_t col = blockIdx.y * cols + (kSplit ? 0 : way);
-    auto o_at = [&](uint32_t i) {
-        return __ldcg(reinterpret_cast<const float4*>(parts.at(i) + kPrefixHeadFloats) + col * 128 + lane);
-    };
-    float4 ahead[kJoinAhead];
-    auto fetch_ahead = [&] {
-#pragma unroll
-        for (uint32_t k = 0; k < kJoinAhead; ++k)
-            if (i0 + k * kStep < parts.count) ahead[k] = o_at(i0 + k * kStep);
-    };
-    fetch_ahead();
     float m = -INFINITY;
 #pragma unroll 4
     for (uint32_t i = head_way; i < parts.count; i += kJoinWays) {
@@ -945,44 +959,45 @@ __global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(const __gr
         acc.z = fmaf(o.z, f, acc.z);
         acc.w = fmaf(o.w, f, acc.w);
     };
-    for (const uint32_t stop = (blockIdx.y + 1) * cols;;) {
+#pragma unroll 1
+    for (uint32_t unit = blockIdx.y * units; unit < (blockIdx.y + 1) * units; ++unit) {
+        const uint32_t col = kSplit ? unit >> 1 : 4 * unit + way;
+        const uint32_t lane = kSplit ? (unit & 1) * 64 + head : threadIdx.x & 127;
+        const size_t o_at = kPrefixHeadFloats + (col * 128 + lane) * 4;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (uint32_t k = 0; k < kJoinAhead; ++k)
-            if (i0 + k * kStep < parts.count) add(acc, ahead[k], fac_s[i0 + k * kStep][head]);
-#pragma unroll 8
-        for (uint32_t i = i0 + kJoinAhead * kStep; i < parts.count; i += kStep) add(acc, o_at(i), fac_s[i][head]);
-        if (kSplit) {
-            if (way > 0) acc_s[way - 1][lane] = acc;
-            __syncthreads();
-            if (way > 0) return;
-#pragma unroll
-            for (uint32_t k = 0; k < kWays - 1; ++k) add(acc, acc_s[k][lane], 1.0f);
-        }
-        const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-        __align__(8) __nv_bfloat16 y[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = __float2bfloat16_rn(!zero && finite_f(x[k]) ? x[k] : 0.0f);
+#pragma unroll 2
+        for (uint32_t i = i0; i < parts.count; i += kStep)
+            add(acc, __ldcg(reinterpret_cast<const float4*>(parts.at(i) + o_at)), fac_s[i][head]);
         const uint32_t dim = 256 * (col >> 5) + 128 * (lane >> 6) + 4 * (col & 31);
-        *reinterpret_cast<uint2*>(p.out + at * kDim + dim) = *reinterpret_cast<const uint2*>(y);
-        if (kSplit || (col += kWays) >= stop) return;
-        fetch_ahead();
+        if (kSplit && way > 0) acc_s[way - 1][head] = acc;
+        if (kSplit) __syncthreads();
+        if (!kSplit || way == 0) {
+            if (kSplit)
+                for (uint32_t k = 0; k < kWays - 1; ++k) add(acc, acc_s[k][head], 1.0f);
+            const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+            __align__(8) __nv_bfloat16 y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = __float2bfloat16_rn(!zero && finite_f(x[k]) ? x[k] : 0.0f);
+            *reinterpret_cast<uint2*>(p.out + at * kDim + dim) = *reinterpret_cast<const uint2*>(y);
+        }
+        if (kSplit) __syncthreads();
     }
 }
 
 template <int kFormat>
 static cudaError_t launch(const PrefixParams& p, cudaStream_t stream, bool pdl) {
     static std::atomic<uint64_t> smem_set{0};
-    cudaError_t err = set_smem_limit_once(prefix_attn_kernel<kFormat>, kSmem, smem_set);
+    cudaError_t err = set_smem_limit_once(prefix_attn_kernel<kFormat>, kSmem<kFormat>, smem_set);
     if (err != cudaSuccess) return err;
-    err = launch_kernel(prefix_attn_kernel<kFormat>, dim3(2 * p.pairs), dim3(kThreads<kFormat>), kSmem, stream, pdl, p);
+    err = launch_kernel(prefix_attn_kernel<kFormat>, dim3(2 * p.pairs), dim3(kThreads<kFormat>), kSmem<kFormat>, stream, pdl, p);
     if (err != cudaSuccess) return err;
-    // About two blocks for each multiprocessor: a column a block for up to four rows, else four columns or more.
-    if (p.rows <= 4)
-        return launch_kernel(prefix_join_kernel<true>, dim3(p.rows, 64), dim3(kJoinThreads), 0, stream, true, p, 1u);
-    uint32_t cols = 4;
-    while (p.rows * (64 / cols) > 4 * kPrefixPairsMax) cols *= 2;
-    return launch_kernel(prefix_join_kernel<false>, dim3(p.rows, 64 / cols), dim3(kJoinThreads), 0, stream, true, p, cols);
+    // About four blocks for each multiprocessor (two, and a column of 64 threads a block, were up to 8 us slower).
+    uint32_t units = 1;
+    const uint32_t all = p.rows <= 8 ? 128 : 16;
+    while (p.rows * (all / units) > 8 * kPrefixPairsMax) units *= 2;
+    const dim3 grid(p.rows, all / units), block(kJoinThreads);
+    if (p.rows <= 8) return launch_kernel(prefix_join_kernel<true>, grid, block, 0, stream, true, p, units);
+    return launch_kernel(prefix_join_kernel<false>, grid, block, 0, stream, true, p, units);
 }
 
 template <int kFormat>

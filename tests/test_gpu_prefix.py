@@ -325,3 +325,43 @@ def test_a_decode_step_of_samples_of_one_prompt():
         assert (got.norm(dim=1) - raw.norm(dim=1)).abs().max() <= 2.0 ** -4 * raw.norm(dim=1).max()
     check(out, q, held, sinks)
     assert torch.isfinite(back).all() and back.any()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int4"])
+@pytest.mark.parametrize("prefix,tails", [(1000, [0, 1, 127, 128, 129, 300]), (1280, [5] * 9), (2049, [3] * 64)])
+def test_rows_widened_beforehand_give_the_same_bits(fmt, prefix, tails):
+    """With the smaller workspace the packed rows are widened as they are used; a page id out of range zeroes the same
+    heads both ways."""
+    rng = np.random.default_rng(prefix)
+    n, page = len(tails), 64
+    cache, held = shared_cache(rng, prefix, tails, fmt, page)
+    q, sinks = queries(rng, n, 512), torch.zeros(64, device="cuda")
+    rows = table(prefix, tails)
+    small, large = (ds.prefix_attn_workspace(rows, prefix, f) for f in ("bf16", fmt))
+    assert large.numel() > small.numel()
+    for change in (lambda: None, lambda: cache.page_table[n - 1, prefix // page].fill_(-1),
+                   lambda: cache.page_table[0, 0].fill_(cache.num_pages)):
+        change()
+        got = []
+        for ws in (small, large):
+            out, bad = torch.full_like(q, 4.0), torch.full((n, 64), 9, dtype=torch.int32, device="cuda")
+            ds.ds_rows_prefix_attn(rows, prefix, q, sinks, 0, SCALE, out, cache, invalid=bad, workspace_t=ws)
+            assert ds.workspace_status(ws) == 0
+            got.append((out, bad))
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+        if change is not None and not got[0][1].any():
+            check(got[0][0], q, held, sinks)
+    assert got[0][1].all() and not got[0][0].any()
+
+
+def test_the_workspace_has_to_be_large_enough():
+    cache, _ = shared_cache(np.random.default_rng(1), 300, [1, 2], "fp8", 16)
+    q = queries(np.random.default_rng(2), 2, 512)
+    ws = ds.prefix_attn_workspace(table(300, [1, 2]), 300, "bf16")
+    with pytest.raises(ds.DsRowsError, match="workspace holds"):
+        ds.ds_rows_prefix_attn(table(300, [1, 2]), 300, q, torch.zeros(64, device="cuda"), 0, SCALE, torch.zeros_like(q),
+                               cache, workspace_t=ws[:-256])
+    for wrong in (q.half(), q.cpu(), q[:1], q.transpose(1, 2)):
+        with pytest.raises((TypeError, ValueError)):
+            ds.ds_rows_prefix_attn(table(300, [1, 2]), 300, wrong, torch.zeros(64, device="cuda"), 0, SCALE,
+                                   torch.zeros_like(q), cache, workspace_t=ws)
