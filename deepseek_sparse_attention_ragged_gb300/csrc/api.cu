@@ -1122,8 +1122,10 @@ int ds_rows_fetch(const ds_paged_cache_t* cache, const int32_t* seq, const int32
     p.slot = slot;
     p.invalid = invalid;
     p.wide = aligned16(out) && (out_stride * elem) % 16 == 0 ? 1u : 0u;
+    const int sms = num_sms();
+    if (sms <= 0) return fail(DS_ECUDA, "no CUDA device");
     StageRange range("dsrows.fetch");
-    const cudaError_t err = launch_fetch(p, dtype, cache->dim, cache->format, (cudaStream_t)stream, true);
+    const cudaError_t err = launch_fetch(p, dtype, cache->dim, cache->format, sms, (cudaStream_t)stream, true);
     return err == cudaSuccess ? DS_OK : cuda_fail(err, "fetch launch");
 }
 

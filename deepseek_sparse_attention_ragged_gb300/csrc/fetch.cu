@@ -14,7 +14,8 @@ namespace dsrows {
 namespace {
 
 constexpr int kFetchThreads = 256;
-constexpr int kFetchUnroll = 4;
+constexpr int kFetchUnroll = 2;
+constexpr int kFetchBlocks = 6;  // of a multiprocessor
 
 // 8 elements from 4 bf16 pairs.
 __device__ __forceinline__ void put8(__nv_bfloat16* out, const uint32_t (&w)[4], bool wide) {
@@ -60,43 +61,73 @@ __global__ void __launch_bounds__(kFetchThreads) fetch_kernel(const __grid_const
     constexpr int ROWS = kFetchThreads / LANES;
     pdl_trigger();
     const int r = threadIdx.x / LANES, g = threadIdx.x % LANES;
-    const uint64_t first = (uint64_t)blockIdx.x * (ROWS * kFetchUnroll) + r;
     const uint32_t shift = p.cache.page_shift;
+    const uint64_t step = (uint64_t)gridDim.x * (ROWS * kFetchUnroll);
+    struct Place {
+        int32_t seq[kFetchUnroll], slot[kFetchUnroll];
+    };
+    auto look = [&](uint64_t first, Place& at) {
+#pragma unroll
+        for (int u = 0; u < kFetchUnroll; ++u) {
+            const uint64_t token = first + u * ROWS;
+            at.seq[u] = token < p.tokens ? p.seq[token] : -1;
+            at.slot[u] = token < p.tokens ? p.slot[token] : 0;
+        }
+    };
+    auto page_of = [&](const Place& at, int32_t (&id)[kFetchUnroll]) {
+#pragma unroll
+        for (int u = 0; u < kFetchUnroll; ++u) {
+            const uint32_t page_no = (uint32_t)at.slot[u] >> shift;
+            const bool in = at.seq[u] >= 0 && (uint32_t)at.seq[u] < p.cache.entries && at.slot[u] >= 0 &&
+                            page_no < p.cache.table_stride;
+            id[u] = in ? p.cache.table[(uint64_t)at.seq[u] * p.cache.table_stride + page_no] : -1;
+        }
+    };
     pdl_wait();
-    int32_t seq[kFetchUnroll], slot[kFetchUnroll], id[kFetchUnroll];
+    // The indices are looked up two steps ahead, the page ids one.
+    uint64_t first = (uint64_t)blockIdx.x * (ROWS * kFetchUnroll) + r;
+    Place now, next;
+    int32_t id[kFetchUnroll];
+    look(first, now);
+    look(first + step, next);
+    page_of(now, id);
+#pragma unroll 1
+    for (; first < p.tokens; first += step) {
+        Held8 held[kFetchUnroll];
 #pragma unroll
-    for (int u = 0; u < kFetchUnroll; ++u) {
-        const uint64_t token = first + u * ROWS;
-        seq[u] = token < p.tokens ? p.seq[token] : -1;
-        slot[u] = seq[u] != -1 ? p.slot[token] : 0;
-    }
+        for (int u = 0; u < kFetchUnroll; ++u) {
+            if ((uint32_t)id[u] >= p.cache.num_pages) id[u] = -1;
+            if (id[u] >= 0)
+                held[u] = load8<kDimOf, kFormat>(p.cache, (uint32_t)id[u], (uint32_t)now.slot[u] & ((1u << shift) - 1), g);
+        }
+        int32_t next_id[kFetchUnroll];
+        Place then;
+        page_of(next, next_id);
+        look(first + 2 * step, then);
 #pragma unroll
-    for (int u = 0; u < kFetchUnroll; ++u) {
-        const uint32_t page_no = (uint32_t)slot[u] >> shift;
-        const bool in = seq[u] >= 0 && (uint32_t)seq[u] < p.cache.entries && slot[u] >= 0 && page_no < p.cache.table_stride;
-        id[u] = in ? p.cache.table[(uint64_t)seq[u] * p.cache.table_stride + page_no] : -1;
-        if ((uint32_t)id[u] >= p.cache.num_pages) id[u] = -1;
-    }
-    Held8 held[kFetchUnroll];
-#pragma unroll
-    for (int u = 0; u < kFetchUnroll; ++u)
-        if (id[u] >= 0) held[u] = load8<kDimOf, kFormat>(p.cache, (uint32_t)id[u], (uint32_t)slot[u] & ((1u << shift) - 1), g);
-#pragma unroll
-    for (int u = 0; u < kFetchUnroll; ++u) {
-        const uint64_t token = first + u * ROWS;
-        if (token >= p.tokens) break;
-        if (g == 0 && p.invalid) p.invalid[token] = seq[u] != -1 && id[u] < 0 ? 1u : 0u;
-        if (seq[u] == -1) continue;
-        uint32_t w[4] = {0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};  // no row: NaN
-        if (id[u] >= 0) widen8<kFormat>(held[u], w);
-        put8(static_cast<T*>(p.out) + token * p.out_stride + 8 * g, w, p.wide != 0);
+        for (int u = 0; u < kFetchUnroll; ++u) {
+            const uint64_t token = first + u * ROWS;
+            const bool row = now.seq[u] != -1;  // also false past the last token
+            if (g == 0 && p.invalid && token < p.tokens) p.invalid[token] = row && id[u] < 0 ? 1u : 0u;
+            if (row) {
+                uint32_t w[4] = {0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};  // no page: NaN
+                if (id[u] >= 0) widen8<kFormat>(held[u], w);
+                put8(static_cast<T*>(p.out) + token * p.out_stride + 8 * g, w, p.wide != 0);
+            }
+            id[u] = next_id[u];
+        }
+        now = next;
+        next = then;
     }
 }
 
 template <typename T, int kDimOf>
-static cudaError_t launch_rows(const FetchCall& p, int format, cudaStream_t stream, bool pdl) {
+static cudaError_t launch_rows(const FetchCall& p, int format, int num_sms, cudaStream_t stream, bool pdl) {
     constexpr uint64_t rows = kFetchThreads / (kDimOf / 8) * kFetchUnroll;
-    const dim3 grid((uint32_t)((p.tokens + rows - 1) / rows));
+    // Blocks with the same number of steps each.
+    const uint64_t work = (p.tokens + rows - 1) / rows, most = (uint64_t)num_sms * kFetchBlocks;
+    const uint64_t steps = (work + most - 1) / most;
+    const dim3 grid((uint32_t)((work + steps - 1) / steps));
     auto launch = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kFetchThreads), 0, stream, pdl, p); };
     if (format == DS_CACHE_INT4) return launch(fetch_kernel<T, kDimOf, DS_CACHE_INT4>);
     if (format == DS_CACHE_FP8) return launch(fetch_kernel<T, kDimOf, DS_CACHE_FP8>);
@@ -104,15 +135,17 @@ static cudaError_t launch_rows(const FetchCall& p, int format, cudaStream_t stre
 }
 
 template <typename T>
-static cudaError_t launch_type(const FetchCall& p, uint32_t dim, int format, cudaStream_t stream, bool pdl) {
-    return dim == kDim ? launch_rows<T, kDim>(p, format, stream, pdl) : launch_rows<T, kIdxDim>(p, format, stream, pdl);
+static cudaError_t launch_type(const FetchCall& p, uint32_t dim, int format, int num_sms, cudaStream_t stream, bool pdl) {
+    return dim == kDim ? launch_rows<T, kDim>(p, format, num_sms, stream, pdl)
+                       : launch_rows<T, kIdxDim>(p, format, num_sms, stream, pdl);
 }
 
-cudaError_t launch_fetch(const FetchCall& p, int dtype, uint32_t dim, int format, cudaStream_t stream, bool pdl) {
+cudaError_t launch_fetch(const FetchCall& p, int dtype, uint32_t dim, int format, int num_sms, cudaStream_t stream,
+                         bool pdl) {
     if (p.tokens == 0) return cudaSuccess;
-    if (dtype == DS_F32) return launch_type<float>(p, dim, format, stream, pdl);
-    if (dtype == DS_F16) return launch_type<__half>(p, dim, format, stream, pdl);
-    return launch_type<__nv_bfloat16>(p, dim, format, stream, pdl);
+    if (dtype == DS_F32) return launch_type<float>(p, dim, format, num_sms, stream, pdl);
+    if (dtype == DS_F16) return launch_type<__half>(p, dim, format, num_sms, stream, pdl);
+    return launch_type<__nv_bfloat16>(p, dim, format, num_sms, stream, pdl);
 }
 
 }  // namespace dsrows

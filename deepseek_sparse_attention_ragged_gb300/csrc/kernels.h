@@ -252,7 +252,8 @@ struct PrefixParams {
 cudaError_t launch_prefix_attn(const PrefixParams& p, int format, cudaStream_t stream, bool pdl);
 cudaError_t launch_rope(RopeCall p, int dtype, int layout, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_append(const AppendCall& p, int dtype, uint32_t dim, int format, cudaStream_t stream, bool pdl);
-cudaError_t launch_fetch(const FetchCall& p, int dtype, uint32_t dim, int format, cudaStream_t stream, bool pdl);
+cudaError_t launch_fetch(const FetchCall& p, int dtype, uint32_t dim, int format, int num_sms, cudaStream_t stream,
+                         bool pdl);
 cudaError_t launch_paged_indexer(const PagedIndexerParams& p, int format, int num_sms, cudaStream_t stream, bool pdl);
 cudaError_t launch_sparse_attn_paged(const PagedTailParams& p, int format, cudaStream_t stream, bool pdl);
 
