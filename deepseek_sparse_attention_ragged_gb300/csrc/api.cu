@@ -1305,6 +1305,7 @@ int ds_rows_prefix_attn(int rows, const ds_row_t* table, uint32_t prefix_len, co
                          std::min(kv->page_size, kPrefixBoxRows), "paged rows");
     if (rc) return rc;
     p.cache = paged_cache(*kv);
+    p.q = reinterpret_cast<const __nv_bfloat16*>(q_attn);
     p.sinks = sinks;
     p.sinks_row_stride = sinks_row_stride;
     p.out = reinterpret_cast<__nv_bfloat16*>(out);

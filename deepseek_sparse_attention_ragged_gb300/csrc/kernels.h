@@ -231,6 +231,7 @@ struct PrefixParams {
     __nv_bfloat16* wide;    // packed pages: their rows widened before the attention, or null
     uint32_t wide_tiles;
     uint32_t wide_begin[kPrefixRowsMax];  // first tile of each entry's own rows (the prefix comes first)
+    const __nv_bfloat16* q;  // [Q, 64, 512]
     const float* sinks;
     uint64_t sinks_row_stride;
     __nv_bfloat16* out;      // [Q, 64, 512]

@@ -26,6 +26,8 @@
 // the order in which the MMAs take them: S of the next tile comes before P . G of this one.
 // Rows past a segment's end and rows without a page are zeros with probability 0.
 
+#include <float.h>
+
 #include "cache_rows.cuh"
 #include "common.cuh"
 #include "fp8.cuh"
@@ -287,6 +289,8 @@ struct Piece {
     }
 };
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // The TMEM columns of S of tile `it`.
 __device__ __forceinline__ uint32_t s_col(uint32_t it) { return (it & 1) * 64 + (it & 2) * 192; }
 
@@ -389,6 +393,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
     if (threadIdx.x == 32 * 3) {
         tma_prefetch_map(&p.qmap);
         if (kByTma<kFormat>) tma_prefetch_map(&p.kvmap);
+    }
+    // The first part's query and page ids into L2 (the kernel before may yet write them: nothing is read here).
+    Walk ahead(p, pair, pairs);
+    if (ahead.next(part)) {
+        const uint32_t r = part.seg < p.groups ? min(2 * part.seg + rank, p.rows - 1) : part.seg - p.groups;
+        if (threadIdx.x < kQBytes / 128)
+            prefetch_l2(reinterpret_cast<const uint8_t*>(p.q) + (size_t)p.q_row[r] * kQBytes + threadIdx.x * 128);
+        else if (kFormat != kWidened && warp == 16 && lane < 2)
+            prefetch_l2(p.cache.table + (part.seg < p.groups ? 0 : (size_t)(part.seg - p.groups) * p.cache.table_stride) +
+                        ((part.start + (kTile - 1) * lane) >> p.cache.page_shift));
     }
     pdl_wait();
     pdl_trigger();
@@ -499,14 +513,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                         // A part begins O anew, once the part before has been read.
                         ok = ok && (i != 0 || n_part == 0 || wait_warp(&bar->o_read, (n_part - 1) & 1, p.status));
                         const uint64_t a_desc = smem_desc_sw128_kmajor(smem_u32(smem + L::p) + it % kPBufs<kFormat> * kPBytes);
-                        const uint32_t mine = 4 * it + (lane & 3);  // the lane's unit of all
+                        // The lane's unit of all. The last tile's lie in the units of the K form, which it has done with.
+                        const uint32_t mine = 4 * it + (lane & 3);
+                        const bool in_k = kByTma<kFormat> && it + 1 == n;
+                        uint64_t* bars = &bar->full[in_k ? lane & 3 : kKUnits + mine % kV];
+                        const uint32_t parity = (in_k ? n : mine / kV) & 1;
                         uint32_t full = 0;
 #pragma unroll
                         for (uint32_t v = 0; v < 4; ++v) {
-                            ok = ok && unit_full(&bar->full[kKUnits + mine % kV], mine / kV & 1, v, kV, full);
+                            ok = ok && unit_full(bars, parity, v, in_k ? kKUnits : kV, full);
                             if (!ok) break;
                             tc_fence_after();
-                            const uint32_t slot = kKUnits + (4 * it + v) % kV;
+                            const uint32_t slot = in_k ? v : kKUnits + (4 * it + v) % kV;
                             const uint64_t b_desc = smem_desc_sw128_mnmajor(ring + slot * kUnitBytes, 4096, 1024);
                             if (elect_one()) {
 #pragma unroll
@@ -731,13 +749,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             if (lane == 0) mbar_arrive(&bar->place_free[of % kPlaceBufs]);
         };
         if constexpr (kByTma<kFormat>) {
-            // Warp b fills unit b: of the K form one of every tile, of the V form every kV-th.
+            // Warp b fills unit b: of the K form one of every tile and then, when S of the last tile is done, one of its
+            // V form; of the other tiles' V form every kV-th.
             const uint32_t slot = warp - kBuildWarp, dst = ring + slot * kUnitBytes;
-            const bool v_form = slot >= kKUnits;
             const uint32_t box = kFormat == kWidened ? kBoxRows : min(1u << p.cache.page_shift, (uint32_t)kBoxRows);
             for (uint32_t lap = 0;; ++lap) {
-                const uint32_t g = v_form ? slot - kKUnits + lap * kV : 4 * lap + slot, of = g / 4, u = g % 4;
-                if (of >= n) break;
+                const bool v_unit = slot >= kKUnits;
+                const uint32_t g = v_unit ? slot - kKUnits + lap * kV : 4 * min(lap, n - 1) + slot, of = g / 4, u = g % 4;
+                if (n == 0 || (v_unit ? of + 1 >= n : lap > n)) break;
+                const bool v_form = v_unit || lap == n;
                 if (!looked_up(of) || !wait_warp(&bar->empty[slot], (lap & 1) ^ 1, p.status)) break;
                 const int32_t* at = place_s + of % kPlaceBufs * kTile + (v_form ? 32 * u : 64 * rank);
                 if (kFormat == kWidened || !(bar->form[of % kPlaceBufs] & kByThreads)) {
@@ -914,7 +934,10 @@ __global__ void __launch_bounds__(kJoinThreads, 3) prefix_join_kernel(const __gr
     constexpr uint32_t kLanes = kSplit ? 64 : 128, kWays = kJoinThreads / kLanes, kStep = kSplit ? kWays : 1;
     __shared__ float fac_s[kJoinParts][kHeads];
     __shared__ float m_s[kJoinWays][kHeads], l_s[kJoinWays][kHeads];
-    __shared__ float4 acc_s[kSplit ? kWays - 1 : 1][kLanes];
+    __shared__ union {
+        float sum[kJoinParts][kHeads];                      // of the parts, until the factors are known
+        float4 acc[kSplit ? kWays - 1 : 1][kLanes];
+    } u_s;
     pdl_trigger();
     const uint32_t r = blockIdx.x, way = threadIdx.x / kLanes;
     const uint32_t head = threadIdx.x & 63, head_way = threadIdx.x >> 6;
@@ -927,26 +950,29 @@ __global__ void __launch_bounds__(kJoinThreads, 3) prefix_join_kernel(const __gr
     float m = -INFINITY;
 #pragma unroll 4
     for (uint32_t i = head_way; i < parts.count; i += kJoinWays) {
-        const float x = __ldcg(parts.at(i) + head);
+        const float* part = parts.at(i);
+        const float x = __ldcg(part + head);
+        const float4 sums = __ldcg(reinterpret_cast<const float4*>(part + kHeads) + head);
         fac_s[i][head] = x;
+        u_s.sum[i][head] = (sums.x + sums.y) + (sums.z + sums.w);
         m = fmaxf(m, x);
     }
     m_s[head_way][head] = m;
     __syncthreads();
-    float top = sink * kLog2e;
+    const float sink2 = fminf(fmaxf(sink * kLog2e, -FLT_MAX), FLT_MAX);  // a finite sink stays finite
+    float top = sink2;
 #pragma unroll
     for (int k = 0; k < kJoinWays; ++k) top = fmaxf(top, m_s[k][head]);
     float l = 0.0f;
 #pragma unroll 4
     for (uint32_t i = head_way; i < parts.count; i += kJoinWays) {
         const float f = exp2f(fac_s[i][head] - top);
-        const float4 sums = __ldcg(reinterpret_cast<const float4*>(parts.at(i) + kHeads) + head);
         fac_s[i][head] = f;
-        l = fmaf((sums.x + sums.y) + (sums.z + sums.w), f, l);
+        l = fmaf(u_s.sum[i][head], f, l);
     }
     l_s[head_way][head] = l;
     __syncthreads();
-    float den = exp2f(sink * kLog2e - top);
+    float den = exp2f(sink2 - top);
 #pragma unroll
     for (int k = 0; k < kJoinWays; ++k) den += l_s[k][head];
     // A flagged part's sum is NaN.
@@ -969,11 +995,11 @@ __global__ void __launch_bounds__(kJoinThreads, 3) prefix_join_kernel(const __gr
         for (uint32_t i = i0; i < parts.count; i += kStep)
             add(acc, __ldcg(reinterpret_cast<const float4*>(parts.at(i) + o_at)), fac_s[i][head]);
         const uint32_t dim = 256 * (col >> 5) + 128 * (lane >> 6) + 4 * (col & 31);
-        if (kSplit && way > 0) acc_s[way - 1][head] = acc;
+        if (kSplit && way > 0) u_s.acc[way - 1][head] = acc;
         if (kSplit) __syncthreads();
         if (!kSplit || way == 0) {
             if (kSplit)
-                for (uint32_t k = 0; k < kWays - 1; ++k) add(acc, acc_s[k][head], 1.0f);
+                for (uint32_t k = 0; k < kWays - 1; ++k) add(acc, u_s.acc[k][head], 1.0f);
             const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
             __align__(8) __nv_bfloat16 y[4];
 #pragma unroll

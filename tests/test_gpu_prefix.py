@@ -365,3 +365,17 @@ def test_the_workspace_has_to_be_large_enough():
         with pytest.raises((TypeError, ValueError)):
             ds.ds_rows_prefix_attn(table(300, [1, 2]), 300, wrong, torch.zeros(64, device="cuda"), 0, SCALE,
                                    torch.zeros_like(q), cache, workspace_t=ws)
+
+
+def test_extreme_sinks():
+    """Finite sinks of any size: the heads are sound, and the largest leave nothing of the rows."""
+    cache, held = shared_cache(np.random.default_rng(3), 200, [1, 70], "bf16", 16)
+    q = queries(np.random.default_rng(4), 2, 512)
+    big = torch.finfo(torch.float32).max
+    sinks = torch.zeros(64, device="cuda")
+    sinks[:6] = torch.tensor([big, -big, 2.5e38, -2.5e38, 1e-45, 3000.0])
+    out, bad = torch.full_like(q, 4.0), torch.full((2, 64), 9, dtype=torch.int32, device="cuda")
+    ds.ds_rows_prefix_attn(table(200, [1, 70]), 200, q, sinks, 0, SCALE, out, cache, invalid=bad)
+    assert not bad.any()
+    check(out, q, held, sinks)
+    assert not out[:, [0, 2, 5]].any() and out[:, [1, 3, 4]].any()
