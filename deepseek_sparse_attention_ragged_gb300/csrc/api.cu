@@ -686,17 +686,26 @@ int check_prefix_rows(int rows, const ds_row_t* table, uint32_t prefix_len) {
 // segment's set-up (its query, the first tile's way through the pipeline, what it leaves in the workspace)
 // counts as four tiles, so that the pairs with the rows' short ends do not finish last (63 rows of 20001 and
 // up to 311 more: 157 us at two, 132 at three, 121 at four, 122 to 126 at five to eight).
+// A pair costs what it leaves and the join reads, about 0.1 us, and a tile 1.4 us (2.4 and 3.7 where 4 or 8 bits are
+// widened as they are used): with few segments the best number of pairs is near sqrt(14 tiles) (one row of 9728: 14.7 us
+// against 18.1 with 76 pairs, of 19456 18.3 against 20.6, of 38912 22.4 against 23.7) and sqrt(30 tiles). Many
+// segments keep all pairs (30 rows of 1216 and 100 more: 21.2 us against 25.6).
 size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t prefix_len, uint32_t most_pairs,
-                      bool& widen) {
+                      bool& widen, bool by_tma = true) {
     p.rows = (uint32_t)rows;
     p.groups = (p.rows + 1) / 2;
     p.prefix_len = prefix_len;
-    uint32_t tiles = 0;
     auto tiles_of = [](uint32_t slots) { return (slots + kPrefixTile - 1) / kPrefixTile; };  // at most 2^24
-    tiles += p.groups * tiles_of(prefix_len);
-    for (uint32_t e = 0; e < p.rows; ++e) tiles += tiles_of(table[e].kv_len - prefix_len);
+    uint32_t tiles = p.groups * tiles_of(prefix_len), filled = prefix_len ? p.groups : 0;
+    for (uint32_t e = 0; e < p.rows; ++e) {
+        tiles += tiles_of(table[e].kv_len - prefix_len);
+        filled += table[e].kv_len > prefix_len ? 1 : 0;
+    }
     p.pairs = tiles < most_pairs ? tiles : most_pairs;
-    p.seg_cost = tiles <= most_pairs ? 0 : 4;
+    const uint32_t parts = p.pairs + p.groups + p.rows - 1;
+    if (filled <= 4)
+        while (p.pairs > 1 && (uint64_t)(p.pairs - 1) * (p.pairs - 1) >= (by_tma ? 14 : 30) * (uint64_t)tiles) --p.pairs;
+    p.seg_cost = tiles <= p.pairs ? 0 : 4;
     uint32_t segs = 0, at = 0;
     auto add = [&](uint32_t slots) {
         p.begin[segs++] = at;
@@ -717,7 +726,7 @@ size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t
     p.wide_tiles = wide;
     // Packed rows are widened once, beforehand, where each is attended to by two pairs of entries or more on the average.
     widen = tiles >= 2 * wide && wide <= 0x7FFFFFFFu / kPrefixTile;
-    return 256 + align256((size_t)(p.pairs + segs - 1) * 2 * kPrefixPartFloats * 4);
+    return 256 + align256((size_t)parts * 2 * kPrefixPartFloats * 4);
 }
 constexpr size_t kWideTileBytes = (size_t)kPrefixTile * kDim * 2;
 
@@ -1290,8 +1299,10 @@ int ds_rows_prefix_attn(int rows, const ds_row_t* table, uint32_t prefix_len, co
     if (rc) return rc;
     const int sms = num_sms();
     if (sms <= 0) return fail(DS_ECUDA, "no CUDA device");
-    (void)lay_out_prefix(p, rows, table, prefix_len, std::min(kPrefixPairsMax, std::max((uint32_t)sms / 2, 1u)), widen);
     widen = widen && kv->format != DS_CACHE_BF16 && workspace_bytes - L.total >= p.wide_tiles * kWideTileBytes;
+    bool unused;
+    (void)lay_out_prefix(p, rows, table, prefix_len, std::min(kPrefixPairsMax, std::max((uint32_t)sms / 2, 1u)), unused,
+                         widen || kv->format == DS_CACHE_BF16);
     p.wide = widen ? reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + L.total) : nullptr;
     rc = get_encoder();
     if (rc) return rc;

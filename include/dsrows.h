@@ -577,7 +577,7 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
  * arguments are invalid (see ds_rows_last_error). 256-byte aligned, scratch between calls.
  * For DS_CACHE_FP8 and DS_CACHE_INT4 it holds the attended rows as bf16 (1 KB each) where
  * enough entries share them to widen them once beforehand; with DS_CACHE_BF16's
- * bytes the call works as well, and widens them as they are used (the same bits). */
+ * bytes the call works as well, and widens them as they are used. */
 size_t ds_rows_prefix_attn_workspace_bytes(int rows, const ds_row_t* table, uint32_t prefix_len, int format);
 
 /*
