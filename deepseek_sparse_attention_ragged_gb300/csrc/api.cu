@@ -1130,7 +1130,8 @@ int ds_rows_fetch(const ds_paged_cache_t* cache, const int32_t* seq, const int32
     p.seq = seq;
     p.slot = slot;
     p.invalid = invalid;
-    p.wide = aligned16(out) && (out_stride * elem) % 16 == 0 ? 1u : 0u;
+    const uint64_t starts = reinterpret_cast<uintptr_t>(out) | (tokens > 1 ? out_stride * elem : 0);
+    p.aligned = starts % 32 == 0 ? 2u : starts % 16 == 0 ? 1u : 0u;
     const int sms = num_sms();
     if (sms <= 0) return fail(DS_ECUDA, "no CUDA device");
     StageRange range("dsrows.fetch");

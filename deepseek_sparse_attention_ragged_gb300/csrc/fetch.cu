@@ -2,9 +2,9 @@
 // once to the output's type.
 //
 // Bound by the bytes read and written (for a few rows: by the launch and three dependent loads, the
-// indices, the page id and the row). A thread has 8 neighbouring elements of kUnroll rows, so that
-// neighbours store 16 bytes (32 for fp32) each without a gap, and the loads of its rows are in
-// flight together.
+// indices, the page id and the row). A thread has 16 neighbouring elements, a group of the 4-bit type and 16 bytes of the
+// 8-bit one, and stores them by 32 bytes; the indices of its rows are looked up two steps ahead and their page
+// ids one step, so that a row's load waits for neither.
 
 #include "cache_rows.cuh"
 #include "kernels.h"
@@ -14,50 +14,56 @@ namespace dsrows {
 namespace {
 
 constexpr int kFetchThreads = 256;
-constexpr int kFetchUnroll = 2;
+constexpr int kFetchUnroll = 1;
 constexpr int kFetchBlocks = 6;  // of a multiprocessor
 
-// 8 elements from 4 bf16 pairs.
-__device__ __forceinline__ void put8(__nv_bfloat16* out, const uint32_t (&w)[4], bool wide) {
-    if (wide) {
-        *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        reinterpret_cast<uint16_t*>(out)[i] = (uint16_t)(w[i / 2] >> 16 * (i % 2));
-}
-__device__ __forceinline__ float element(const uint32_t (&w)[4], int i) {
+// 16 elements from 8 bf16 pairs; `aligned`: to 32 bytes, 16 bytes or the type (2, 1, 0).
+__device__ __forceinline__ float element(const uint32_t (&w)[8], int i) {
     return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
 }
-__device__ __forceinline__ void put8(float* out, const uint32_t (&w)[4], bool wide) {
-    if (wide) {
+__device__ __forceinline__ void put_words(void* out, const uint32_t (&w)[8], uint32_t aligned) {
+    if (aligned == 2) {
+        st_global_v8(out, w);
+    } else if (aligned == 1) {
+        static_cast<uint4*>(out)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(out)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            reinterpret_cast<float4*>(out)[i] = make_float4(element(w, 4 * i), element(w, 4 * i + 1),
-                                                            element(w, 4 * i + 2), element(w, 4 * i + 3));
-        return;
+        for (int i = 0; i < 16; ++i) static_cast<uint16_t*>(out)[i] = (uint16_t)(w[i / 2] >> 16 * (i % 2));
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = element(w, i);
 }
-__device__ __forceinline__ void put8(__half* out, const uint32_t (&w)[4], bool wide) {
-    __align__(16) __half h[8];
+__device__ __forceinline__ void put16(__nv_bfloat16* out, const uint32_t (&w)[8], uint32_t aligned) {
+    put_words(out, w, aligned);
+}
+__device__ __forceinline__ void put16(__half* out, const uint32_t (&w)[8], uint32_t aligned) {
+    uint32_t h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = __float2half_rn(element(w, i));
-    if (wide) {
-        *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(h);
+    for (int i = 0; i < 8; ++i) {
+        const __half2 two = __floats2half2_rn(element(w, 2 * i), element(w, 2 * i + 1));
+        h[i] = *reinterpret_cast<const uint32_t*>(&two);
+    }
+    put_words(out, h, aligned);
+}
+__device__ __forceinline__ void put16(float* out, const uint32_t (&w)[8], uint32_t aligned) {
+    if (aligned == 0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) out[i] = element(w, i);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = h[i];
+    for (int k = 0; k < 2; ++k) {
+        uint32_t f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __float_as_uint(element(w, 8 * k + i));
+        put_words(out + 8 * k, f, aligned);
+    }
 }
 
 }  // namespace
 
 template <typename T, int kDimOf, int kFormat>
 __global__ void __launch_bounds__(kFetchThreads) fetch_kernel(const __grid_constant__ FetchCall p) {
-    constexpr int LANES = kDimOf / 8;  // threads of a row
+    constexpr int LANES = kDimOf / 16;  // threads of a row
     constexpr int ROWS = kFetchThreads / LANES;
     pdl_trigger();
     const int r = threadIdx.x / LANES, g = threadIdx.x % LANES;
@@ -93,12 +99,12 @@ __global__ void __launch_bounds__(kFetchThreads) fetch_kernel(const __grid_const
     page_of(now, id);
 #pragma unroll 1
     for (; first < p.tokens; first += step) {
-        Held8 held[kFetchUnroll];
+        Held16<kFormat> held[kFetchUnroll];
 #pragma unroll
         for (int u = 0; u < kFetchUnroll; ++u) {
             if ((uint32_t)id[u] >= p.cache.num_pages) id[u] = -1;
             if (id[u] >= 0)
-                held[u] = load8<kDimOf, kFormat>(p.cache, (uint32_t)id[u], (uint32_t)now.slot[u] & ((1u << shift) - 1), g);
+                load16<kDimOf, kFormat>(p.cache, (uint32_t)id[u], (uint32_t)now.slot[u] & ((1u << shift) - 1), g, held[u]);
         }
         int32_t next_id[kFetchUnroll];
         Place then;
@@ -110,9 +116,14 @@ __global__ void __launch_bounds__(kFetchThreads) fetch_kernel(const __grid_const
             const bool row = now.seq[u] != -1;  // also false past the last token
             if (g == 0 && p.invalid && token < p.tokens) p.invalid[token] = row && id[u] < 0 ? 1u : 0u;
             if (row) {
-                uint32_t w[4] = {0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};  // no page: NaN
-                if (id[u] >= 0) widen8<kFormat>(held[u], w);
-                put8(static_cast<T*>(p.out) + token * p.out_stride + 8 * g, w, p.wide != 0);
+                uint32_t w[8];
+                if (id[u] >= 0) {
+                    widen16(held[u], w);
+                } else {  // no page: NaN
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = 0x7FC07FC0u;
+                }
+                put16(static_cast<T*>(p.out) + token * p.out_stride + 16 * g, w, p.aligned);
             }
             id[u] = next_id[u];
         }
@@ -123,7 +134,7 @@ __global__ void __launch_bounds__(kFetchThreads) fetch_kernel(const __grid_const
 
 template <typename T, int kDimOf>
 static cudaError_t launch_rows(const FetchCall& p, int format, int num_sms, cudaStream_t stream, bool pdl) {
-    constexpr uint64_t rows = kFetchThreads / (kDimOf / 8) * kFetchUnroll;
+    constexpr uint64_t rows = kFetchThreads / (kDimOf / 16) * kFetchUnroll;
     // Blocks with the same number of steps each.
     const uint64_t work = (p.tokens + rows - 1) / rows, most = (uint64_t)num_sms * kFetchBlocks;
     const uint64_t steps = (work + most - 1) / most;

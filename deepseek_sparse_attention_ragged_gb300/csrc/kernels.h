@@ -184,7 +184,7 @@ struct FetchCall {
     const int32_t* seq;
     const int32_t* slot;
     uint32_t* invalid;
-    uint32_t wide;  // the rows of out start on 16-byte boundaries
+    uint32_t aligned;  // the rows of out start on 32-byte (2), 16-byte (1) or their type's boundaries (0)
 };
 
 // Indexer scores over a paged key cache, one query per entry.

@@ -851,7 +851,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
 
 namespace {
 constexpr int kWidenThreads = 256;
-constexpr int kWidenRows = 16;  // of a block: four a thread, in flight together
+constexpr int kWidenUnroll = 2;                                             // rows of a thread, in flight together
+constexpr int kWidenRows = kWidenThreads / (kDim / 16) * kWidenUnroll;      // of a block
 }  // namespace
 
 // The rows that a call attends to as bf16, each once: the prefix, then each entry's own, every run filled up with
@@ -860,39 +861,44 @@ constexpr int kWidenRows = 16;  // of a block: four a thread, in flight together
 template <int kFormat>
 __global__ void __launch_bounds__(kWidenThreads) prefix_widen_kernel(const __grid_constant__ PrefixParams p) {
     pdl_trigger();
-    const uint32_t g = threadIdx.x % (kDim / 8), shift = p.cache.page_shift;
+    constexpr uint32_t kLanes = kDim / 16, kRows = kWidenThreads / kLanes;
+    const uint32_t g = threadIdx.x % kLanes, shift = p.cache.page_shift;
     const uint32_t tile = blockIdx.x / (kTile / kWidenRows);
-    const uint32_t in_tile = blockIdx.x % (kTile / kWidenRows) * kWidenRows + threadIdx.x / (kDim / 8);
-    // The run: its entry, first slot, first tile and end.
+    const uint32_t in_tile = blockIdx.x % (kTile / kWidenRows) * kWidenRows + threadIdx.x / kLanes;
+    // The run: its entry (the last one that begins at the tile or before it), first slot, first tile and end.
     uint32_t entry = 0, first = 0, begin = 0, end = p.prefix_len;
     if (tile >= p.wide_begin[0]) {
-        while (entry + 1 < p.rows && tile >= p.wide_begin[entry + 1]) ++entry;
+        for (uint32_t step = kPrefixRowsMax / 2; step > 0; step /= 2)
+            if (entry + step < p.rows && p.wide_begin[entry + step] <= tile) entry += step;
         first = p.prefix_len;
         begin = p.wide_begin[entry];
         end = p.kv_len[entry];
     }
     const int32_t* table = p.cache.table + (size_t)entry * p.cache.table_stride;
+    const uint32_t slot = first + (tile - begin) * kTile + in_tile;
     pdl_wait();
-    Held8 held[4];
-    int32_t id[4];
+    Held16<kFormat> held[kWidenUnroll];
+    int32_t id[kWidenUnroll];
 #pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) {
-        const uint32_t j = first + (tile - begin) * kTile + in_tile + 4 * k;
+    for (uint32_t k = 0; k < kWidenUnroll; ++k) {
+        const uint32_t j = slot + kRows * k;
         id[k] = j < end ? table[j >> shift] : kNoRow;
         if (j < end && (uint32_t)id[k] >= p.cache.num_pages) id[k] = kBadRow;
     }
 #pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) {
-        const uint32_t j = first + (tile - begin) * kTile + in_tile + 4 * k;
-        if (id[k] >= 0) held[k] = load8<kDim, kFormat>(p.cache, (uint32_t)id[k], j & ((1u << shift) - 1), g);
-    }
+    for (uint32_t k = 0; k < kWidenUnroll; ++k)
+        if (id[k] >= 0)
+            load16<kDim, kFormat>(p.cache, (uint32_t)id[k], (slot + kRows * k) & ((1u << shift) - 1), g, held[k]);
 #pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) {
-        const uint32_t empty = id[k] == kBadRow ? 0x7FC07FC0u : 0u;
-        uint32_t w[4] = {empty, empty, empty, empty};
-        if (id[k] >= 0) widen8<kFormat>(held[k], w);
-        *reinterpret_cast<uint4*>(p.wide + ((size_t)tile * kTile + in_tile + 4 * k) * kDim + 8 * g) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+    for (uint32_t k = 0; k < kWidenUnroll; ++k) {
+        uint32_t w[8];
+        if (id[k] >= 0) {
+            widen16(held[k], w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = id[k] == kBadRow ? 0x7FC07FC0u : 0u;
+        }
+        st_global_v8(p.wide + ((size_t)tile * kTile + in_tile + kRows * k) * kDim + 16 * g, w);
     }
 }
 
