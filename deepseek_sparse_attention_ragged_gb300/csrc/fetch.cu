@@ -14,7 +14,6 @@ namespace dsrows {
 namespace {
 
 constexpr int kFetchThreads = 256;
-constexpr int kFetchUnroll = 1;
 constexpr int kFetchBlocks = 6;  // of a multiprocessor
 
 // 16 elements from 8 bf16 pairs; `aligned`: to 32 bytes, 16 bytes or the type (2, 1, 0).
@@ -68,64 +67,40 @@ __global__ void __launch_bounds__(kFetchThreads) fetch_kernel(const __grid_const
     pdl_trigger();
     const int r = threadIdx.x / LANES, g = threadIdx.x % LANES;
     const uint32_t shift = p.cache.page_shift;
-    const uint64_t step = (uint64_t)gridDim.x * (ROWS * kFetchUnroll);
+    const uint64_t step = (uint64_t)gridDim.x * ROWS;
     struct Place {
-        int32_t seq[kFetchUnroll], slot[kFetchUnroll];
+        int32_t seq, slot;
     };
-    auto look = [&](uint64_t first, Place& at) {
-#pragma unroll
-        for (int u = 0; u < kFetchUnroll; ++u) {
-            const uint64_t token = first + u * ROWS;
-            at.seq[u] = token < p.tokens ? p.seq[token] : -1;
-            at.slot[u] = token < p.tokens ? p.slot[token] : 0;
-        }
+    auto look = [&](uint64_t token) {
+        return token < p.tokens ? Place{p.seq[token], p.slot[token]} : Place{-1, 0};
     };
-    auto page_of = [&](const Place& at, int32_t (&id)[kFetchUnroll]) {
-#pragma unroll
-        for (int u = 0; u < kFetchUnroll; ++u) {
-            const uint32_t page_no = (uint32_t)at.slot[u] >> shift;
-            const bool in = at.seq[u] >= 0 && (uint32_t)at.seq[u] < p.cache.entries && at.slot[u] >= 0 &&
-                            page_no < p.cache.table_stride;
-            id[u] = in ? p.cache.table[(uint64_t)at.seq[u] * p.cache.table_stride + page_no] : -1;
-        }
+    auto page_of = [&](const Place& at) -> int32_t {
+        const uint32_t page_no = (uint32_t)at.slot >> shift;
+        const bool in = at.seq >= 0 && (uint32_t)at.seq < p.cache.entries && at.slot >= 0 && page_no < p.cache.table_stride;
+        return in ? p.cache.table[(uint64_t)at.seq * p.cache.table_stride + page_no] : -1;
     };
     pdl_wait();
-    // The indices are looked up two steps ahead, the page ids one.
-    uint64_t first = (uint64_t)blockIdx.x * (ROWS * kFetchUnroll) + r;
-    Place now, next;
-    int32_t id[kFetchUnroll];
-    look(first, now);
-    look(first + step, next);
-    page_of(now, id);
+    uint64_t token = (uint64_t)blockIdx.x * ROWS + r;
+    Place now = look(token), next = look(token + step);
+    int32_t id = page_of(now);
 #pragma unroll 1
-    for (; first < p.tokens; first += step) {
-        Held16<kFormat> held[kFetchUnroll];
+    for (; token < p.tokens; token += step) {
+        Held16<kFormat> held;
+        const bool there = id >= 0 && (uint32_t)id < p.cache.num_pages;
+        if (there)
+            load16<kDimOf, kFormat>(p.cache, (uint32_t)id, (uint32_t)now.slot & ((1u << shift) - 1), g, held);
+        id = page_of(next);
+        const Place then = look(token + 2 * step);
+        if (g == 0 && p.invalid) p.invalid[token] = now.seq != -1 && !there ? 1u : 0u;
+        if (now.seq != -1) {
+            uint32_t w[8];
+            if (there) {
+                widen16(held, w);
+            } else {  // no page: NaN
 #pragma unroll
-        for (int u = 0; u < kFetchUnroll; ++u) {
-            if ((uint32_t)id[u] >= p.cache.num_pages) id[u] = -1;
-            if (id[u] >= 0)
-                load16<kDimOf, kFormat>(p.cache, (uint32_t)id[u], (uint32_t)now.slot[u] & ((1u << shift) - 1), g, held[u]);
-        }
-        int32_t next_id[kFetchUnroll];
-        Place then;
-        page_of(next, next_id);
-        look(first + 2 * step, then);
-#pragma unroll
-        for (int u = 0; u < kFetchUnroll; ++u) {
-            const uint64_t token = first + u * ROWS;
-            const bool row = now.seq[u] != -1;  // also false past the last token
-            if (g == 0 && p.invalid && token < p.tokens) p.invalid[token] = row && id[u] < 0 ? 1u : 0u;
-            if (row) {
-                uint32_t w[8];
-                if (id[u] >= 0) {
-                    widen16(held[u], w);
-                } else {  // no page: NaN
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = 0x7FC07FC0u;
-                }
-                put16(static_cast<T*>(p.out) + token * p.out_stride + 16 * g, w, p.aligned);
+                for (int i = 0; i < 8; ++i) w[i] = 0x7FC07FC0u;
             }
-            id[u] = next_id[u];
+            put16(static_cast<T*>(p.out) + token * p.out_stride + 16 * g, w, p.aligned);
         }
         now = next;
         next = then;
@@ -134,7 +109,7 @@ __global__ void __launch_bounds__(kFetchThreads) fetch_kernel(const __grid_const
 
 template <typename T, int kDimOf>
 static cudaError_t launch_rows(const FetchCall& p, int format, int num_sms, cudaStream_t stream, bool pdl) {
-    constexpr uint64_t rows = kFetchThreads / (kDimOf / 16) * kFetchUnroll;
+    constexpr uint64_t rows = kFetchThreads / (kDimOf / 16);
     // Blocks with the same number of steps each.
     const uint64_t work = (p.tokens + rows - 1) / rows, most = (uint64_t)num_sms * kFetchBlocks;
     const uint64_t steps = (work + most - 1) / most;
