@@ -225,8 +225,9 @@ __device__ __forceinline__ void sync_softmax(uint32_t set) {
 __device__ __forceinline__ uint32_t v_dim(uint32_t d, uint32_t rank) { return 256 * (d >> 7) + 128 * rank + (d & 127); }
 
 // A lane's values of a step of a packed unit, eight rows of 128 dims: a 16-byte piece of one row (4 bits) or
-// two (8 bits). Four neighbouring pieces of each row are read together, and eight lanes store into
-// eight rows, which the swizzle puts into different banks.
+// two (8 bits). Eight lanes, whose 16-byte accesses are one turn of the load and store unit, have two rows by
+// four pieces (8 bits) or four by two (4 bits): few cache lines a turn, and chunks that the swizzle puts into
+// different banks. (With eight rows to eight lanes a load took 27 cycles, 3,500 a tile on 8 bits.)
 template <int kFormat>
 struct Piece {
     static constexpr uint32_t kValues = kFormat == DS_CACHE_FP8 ? 16 : 32;  // of 16 bytes
@@ -234,7 +235,12 @@ struct Piece {
     uint4 d[kN];
     uint32_t sc;
 
-    static __device__ __forceinline__ uint32_t first(uint32_t lane) { return kValues * (lane >> 3); }
+    static __device__ __forceinline__ uint32_t row(uint32_t lane) {
+        return kFormat == DS_CACHE_FP8 ? 2 * (lane >> 3) + (lane & 1) : 4 * (lane >> 3 & 1) + (lane & 3);
+    }
+    static __device__ __forceinline__ uint32_t first(uint32_t lane) {
+        return kValues * (kFormat == DS_CACHE_FP8 ? lane >> 1 & 3 : 2 * (lane >> 4) + (lane >> 2 & 1));
+    }
     // The pieces at dims dim and dim + 64 of the row at `place`; zeros without one.
     __device__ __forceinline__ void load(const PagedCache& cache, int32_t place, uint32_t dim) {
         const uint32_t where = (uint32_t)max(place, 0);
@@ -805,7 +811,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             auto v_form_of = [&](uint32_t f) { return f == 2 * n - 1 || (f > 0 && !(f & 1)); };
             auto fetch = [&](uint32_t f, uint32_t k) {
                 const uint32_t of = tile_of(f), u = team + 2 * k, d = Piece<kFormat>::first(lane);
-                const int32_t* at = place_s + of % kPlaceBufs * kTile + (lane & 7);
+                const int32_t* at = place_s + of % kPlaceBufs * kTile + Piece<kFormat>::row(lane);
                 if (v_form_of(f)) held[k].load(p.cache, at[32 * u + 8 * (s >> 1)], v_dim(128 * (s & 1), rank) + d);
                 else held[k].load(p.cache, at[64 * rank + 8 * s], 128 * u + d);
             };
@@ -817,7 +823,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             }
             for (uint32_t f = 0; ok && f < 2 * n; ++f) {
                 const bool v_form = v_form_of(f), then = f + 1 < 2 * n;
-                const uint32_t row = 8 * (v_form ? s >> 1 : s) + (lane & 7), size = v_form ? 4096 : 8192;
+                const uint32_t row = 8 * (v_form ? s >> 1 : s) + Piece<kFormat>::row(lane), size = v_form ? 4096 : 8192;
                 ok = !then || looked_up(tile_of(f + 1));
 #pragma unroll
                 for (uint32_t k = 0; k < 2; ++k) {
