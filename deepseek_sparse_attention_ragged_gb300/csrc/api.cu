@@ -686,10 +686,12 @@ int check_prefix_rows(int rows, const ds_row_t* table, uint32_t prefix_len) {
 // segment's set-up (its query, the first tile's way through the pipeline, what it leaves in the workspace)
 // counts as four tiles, so that the pairs with the rows' short ends do not finish last (63 rows of 20001 and
 // up to 311 more: 157 us at two, 132 at three, 121 at four, 122 to 126 at five to eight).
-// A pair costs what it leaves and the join reads, about 0.1 us, and a tile 1.4 us (2.4 and 3.7 where 4 or 8 bits are
-// widened as they are used): with few segments the best number of pairs is near sqrt(14 tiles) (one row of 9728: 14.7 us
-// against 18.1 with 76 pairs, of 19456 18.3 against 20.6, of 38912 22.4 against 23.7) and sqrt(30 tiles). Many
-// segments keep all pairs (30 rows of 1216 and 100 more: 21.2 us against 25.6).
+// A pair costs what it leaves and the join reads, so few segments are not dealt out to all of them: k tiles
+// to a pair cost k times a tile and the pairs that this takes, with a tile as much as 10 pairs for rows by TMA and as
+// 24 where packed rows are widened as they are used (of 6 to 40 the best over the sizes). One row, us with this
+// number against a pair for every tile, up to all: bf16 of 9728 14.3 / 17.8, of 19456 16.7 / 19.8, of 30000 22.5 / 23.3;
+// 8 bits of 9728 16.0 / 19.4, of 38912 28.8 / 31.1. Many segments keep all pairs (30 rows of 1216 and 100 more: 21.2 us against
+// 25.6). One segment alone has its set-up in every pair, which shifts nothing.
 size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t prefix_len, uint32_t most_pairs,
                       bool& widen, bool by_tma = true) {
     p.rows = (uint32_t)rows;
@@ -703,9 +705,17 @@ size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t
     }
     p.pairs = tiles < most_pairs ? tiles : most_pairs;
     const uint32_t parts = p.pairs + p.groups + p.rows - 1;
-    if (filled <= 4)
-        while (p.pairs > 1 && (uint64_t)(p.pairs - 1) * (p.pairs - 1) >= (by_tma ? 14 : 30) * (uint64_t)tiles) --p.pairs;
-    p.seg_cost = tiles <= p.pairs ? 0 : 4;
+    const uint32_t set_up = filled == 1 ? 0 : 4;
+    p.seg_cost = tiles <= p.pairs ? 0 : set_up;
+    if (filled <= 4) {
+        const uint32_t per_tile = by_tma ? 10 : 24, most = p.pairs;
+        uint32_t best = p.seg_cost == 0 && tiles <= most ? per_tile + tiles : ~0u;
+        const uint32_t line = tiles + set_up * filled;
+        for (uint32_t k = std::max((line - 1) / most + 1, 2u); k < best / per_tile; ++k) {
+            const uint32_t pairs = (line - 1) / k + 1, cost = per_tile * k + pairs;
+            if (cost < best) best = cost, p.pairs = pairs, p.seg_cost = set_up;
+        }
+    }
     uint32_t segs = 0, at = 0;
     auto add = [&](uint32_t slots) {
         p.begin[segs++] = at;

@@ -15,16 +15,30 @@
 // cta_group::2 MMAs of M = 128:
 //   S[128 heads x 128 slots] = Q . G^T      (K = 512; CTA c brings slots 64 c .. 64 c + 63)
 //   O[128 heads x 512 dims] += P . G        (K = 128 slots; CTA c brings dims 256 j + 128 c .. + 127)
-// O of 64 heads takes 256 TMEM columns in this layout, which leaves room for two S; with one CTA and
-// M = 128 it would fill TMEM alone. Each CTA keeps its own softmax: its 64 heads see every slot of the tile,
-// so nothing but the operands crosses the pair.
+// O of 64 heads takes 256 TMEM columns in this layout, which leaves room for four S; with one CTA and M = 128 it would
+// fill TMEM alone. A CTA has the 64 slots of the K form and the 256 dims of the V form that it brings, half of
+// what one CTA by itself would read. Each keeps its own softmax: its 64 heads see every slot of the tile, so
+// nothing but the operands crosses the pair.
 //
-// Warp roles: 0 looks up the tiles' rows, 1 and 2 issue the MMAs (in the pair's first CTA), 4 to 11
-// do the softmax (a thread has 64 slots of one head); 3 loads the queries, and the others
-// bring the operands, each one unit of a ring. The K form (64 slots
-// x 128 dims) and the V form (32 slots x 256 dims) of the rows go through one ring of 16 KB units in
-// the order in which the MMAs take them: S of the next tile comes before P . G of this one.
+// Warp roles: 0 looks up the tiles' rows, 1 issues S and 2 P . G (in the pair's first CTA), 3 loads the queries, 4 to 11
+// do the softmax, two sets on alternate tiles (a thread has 64 slots of one head), and the others bring the
+// operands. The K form (64 slots x 128 dims a unit) and the V form (32 slots x 256 dims) of the rows have rings of
+// their own, of 16 KB units: a tile of S comes ahead of P . G of the one before. bf16 rows come by TMA, in boxes of rows of one
+// page; packed rows are widened in registers on their way to shared memory, or, where enough rows of the batch share
+// them, once for all by a kernel beforehand.
 // Rows past a segment's end and rows without a page are zeros with probability 0.
+//
+// In a captured graph, all launches of a call (the time that its operations or its bytes alone would take):
+//   3 rows, 300 shared and up to 40 more, bf16 pages           12.0 us (0.1)
+//   1 row of 131073, bf16                                      42.0 us (19.9, bytes)
+//   8 rows, 65536 shared and up to 999 more, bf16              58.5 us (36.3, operations)
+//   5 rows, 40007 shared and up to 1000 more, 4 bits           40.3 us (13.9, operations)
+//   63 rows, 20001 shared and up to 311 more, 8 bits           120 us (87.5, operations)
+// A tile takes a pair 1.3 to 1.4 us on bf16 rows (its MMAs 1.0): the tensor cores are busy for two thirds of the
+// attention kernel at eight rows and three quarters at 63. The rest is fixed: some 12 to 16 us of launches, first
+// loads, the parts' 128 KB a CTA and their join, which a short call or a single row sees most. Packed rows
+// widened as they are used take 1.9 us (8 bits) or 1.7 us (4 bits) a tile: every value passes registers, and 36 KB of
+// stores a unit of the load and store pipe.
 
 #include <float.h>
 
@@ -408,7 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             prefetch_l2(reinterpret_cast<const uint8_t*>(p.q) + (size_t)p.q_row[r] * kQBytes + threadIdx.x * 128);
         else if (kFormat != kWidened && warp == 16 && lane < 2)
             prefetch_l2(p.cache.table + (part.seg < p.groups ? 0 : (size_t)(part.seg - p.groups) * p.cache.table_stride) +
-                        ((part.start + (kTile - 1) * lane) >> p.cache.page_shift));
+                        (min(part.start + (kTile - 1) * lane, part.end - 1) >> p.cache.page_shift));
     }
     pdl_wait();
     pdl_trigger();
