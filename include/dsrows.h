@@ -537,7 +537,7 @@ int ds_rows_append(const ds_paged_cache_t* cache, const void* x, uint64_t x_stri
  *              is. The same (seq, slot) may come up again.
  *   out        device, element type `dtype`, rows out_stride elements apart (the elements of
  *              a row contiguous; out_stride >= dim, at most 2^31; of a lone row: not looked
- *              at); must not share memory with the pages. 16-byte aligned rows are fastest.
+ *              at); must not share memory with the pages. 32-byte aligned rows are fastest.
  *   tokens     below 2^31; 0 enqueues nothing
  *   invalid    optional uint32 [tokens]: 1 where seq, slot or its page id is out of range
  *              (the row of out is NaN), else 0
