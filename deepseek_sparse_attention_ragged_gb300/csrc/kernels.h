@@ -216,7 +216,7 @@ constexpr uint32_t kPrefixRowsMax = DS_PREFIX_ROWS_MAX;
 constexpr uint32_t kPrefixSegsMax = kPrefixRowsMax / 2 + kPrefixRowsMax;
 constexpr uint32_t kPrefixPairsMax = 76;  // of this GPU's 152 multiprocessors
 constexpr uint32_t kPrefixTile = 128;
-constexpr uint32_t kPrefixBoxRows = 32;  // a TMA box of rows: this many, or a smaller page
+constexpr uint32_t kPrefixBoxRows = 64;  // a TMA box of rows: this many, or a smaller page
 // For each head the maximum that O refers to; the sums of its slots in four shares (softmax set, half
 // of a tile), NaN where one is flagged; then O [64 column groups][128 TMEM lanes (half, head)][4].
 constexpr size_t kPrefixHeadFloats = 5 * DS_HEADS;
@@ -224,8 +224,8 @@ constexpr size_t kPrefixPartFloats = kPrefixHeadFloats + (size_t)DS_HEADS * DS_D
 
 struct PrefixParams {
     CUtensorMap qmap;   // bf16 [Q * 64, 512], box {64, 64}, 128-B swizzle
-    // bf16 pages: [num_pages * page_size, 512], box {64, min(page_size, 32)}, 128-B swizzle; or the
-    // widened rows, box {64, 32}
+    // bf16 pages: [num_pages * page_size, 512], box {64, min(page_size, 64)}, 128-B swizzle; or the
+    // widened rows, box {64, 64}
     CUtensorMap kvmap;
     PagedCache cache;
     __nv_bfloat16* wide;    // packed pages: their rows widened before the attention, or null

@@ -22,8 +22,8 @@
 //
 // Warp roles: 0 looks up the tiles' rows, 1 issues S and 2 P . G (in the pair's first CTA), 3 loads the queries, 4 to 11
 // do the softmax, two sets on alternate tiles (a thread has 64 slots of one head), and the others bring the
-// operands. The K form (64 slots x 128 dims a unit) and the V form (32 slots x 256 dims) of the rows have rings of
-// their own, of 16 KB units: a tile of S comes ahead of P . G of the one before. bf16 rows come by TMA, in boxes of rows of one
+// operands. The K form (the CTA's 64 slots, 128 dims a unit) and the V form (64 slots and 128 of the CTA's dims a unit) of the
+// rows have rings of their own, of 16 KB units: a tile of S comes ahead of P . G of the one before. bf16 rows come by TMA, in boxes of rows of one
 // page; packed rows are widened in registers on their way to shared memory, or, where enough rows of the batch share
 // them, once for all by a kernel beforehand.
 // Rows past a segment's end and rows without a page are zeros with probability 0.
@@ -53,7 +53,7 @@ namespace dsrows {
 namespace {
 
 constexpr int kTile = kPrefixTile;            // slots of a tile
-constexpr int kUnitBytes = 16384;             // a ring unit: [64 slots][128 dims] or [32 slots][256 dims]
+constexpr int kUnitBytes = 16384;             // a ring unit: [64 slots][128 dims], two blocks of 64 dims
 constexpr int kQBytes = kHeads * kDim * 2;    // the CTA's query row, 8 blocks [64 heads][64 dims]
 constexpr int kPBytes = kHeads * kTile * 2;   // P of a tile: 2 blocks [64 heads][64 slots]
 constexpr int kBoxRows = kPrefixBoxRows;      // most rows of a TMA box
@@ -545,16 +545,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                             if (!ok) break;
                             tc_fence_after();
                             const uint32_t slot = in_k ? v : kKUnits + (4 * it + v) % kV;
-                            const uint64_t b_desc = smem_desc_sw128_mnmajor(ring + slot * kUnitBytes, 4096, 1024);
+                            const uint64_t b_desc = smem_desc_sw128_mnmajor(ring + slot * kUnitBytes, 8192, 1024);
                             if (elect_one()) {
 #pragma unroll
-                                for (uint32_t ks = 0; ks < 2; ++ks)
-#pragma unroll
-                                    for (uint32_t j = 0; j < 2; ++j)
-                                        umma2_bf16(tmem + kOCol + 128 * j,
-                                                   a_desc + (((v >> 1) * 8192 + (v & 1) * 64 + ks * 32) >> 4),
-                                                   b_desc + ((j * 8192 + ks * 2048) >> 4), idesc,
-                                                   i == 0 && v == 0 && ks == 0 ? 0u : 1u);
+                                for (uint32_t ks = 0; ks < 4; ++ks)
+                                    umma2_bf16(tmem + kOCol + 128 * (v & 1), a_desc + (((v >> 1) * 8192 + ks * 32) >> 4),
+                                               b_desc + (ks * 2048 >> 4), idesc, i == 0 && v < 2 && ks == 0 ? 0u : 1u);
                                 umma2_commit(&bar->empty[slot]);
                                 if (v == 3) umma2_commit(&bar->pv_done[it & 1]);
                             }
@@ -778,30 +774,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 const uint32_t g = v_unit ? slot - kKUnits + lap * kV : 4 * min(lap, n - 1) + slot, of = g / 4, u = g % 4;
                 if (n == 0 || (v_unit ? of + 1 >= n : lap > n)) break;
                 const bool v_form = v_unit || lap == n;
-                if (!looked_up(of) || !wait_warp(&bar->empty[slot], (lap & 1) ^ 1, p.status)) break;
-                const int32_t* at = place_s + of % kPlaceBufs * kTile + (v_form ? 32 * u : 64 * rank);
-                if (kFormat == kWidened || !(bar->form[of % kPlaceBufs] & kByThreads)) {
-                    // Boxes of rows: lane = (row group, 64 dims).
-                    const uint32_t groups = (v_form ? 32 : 64) / box;
-                    const uint32_t row = lane % groups * box, dims = lane / groups;
-                    // Widened runs end with zeros up to a whole tile.
-                    const int32_t y = kFormat == kWidened
-                                          ? place_s[of % kPlaceBufs * kTile] + (int32_t)((v_form ? 32 * u : 64 * rank) + row)
-                                          : at[row];
+                if (!looked_up(of)) break;
+                // Boxes of rows: lane = (64 dims, row group).
+                const uint32_t first = v_form ? 64 * (u >> 1) : 64 * rank, row = lane % (64 / box) * box, dims = lane / (64 / box);
+                const bool boxes = kFormat == kWidened || !(bar->form[of % kPlaceBufs] & kByThreads);
+                const int32_t* at = place_s + of % kPlaceBufs * kTile;
+                // Widened runs end with zeros up to a whole tile.
+                const int32_t y = kFormat == kWidened ? at[0] + (int32_t)(first + row) : at[first + row];
+                if (!wait_warp(&bar->empty[slot], (lap & 1) ^ 1, p.status)) break;
+                if (boxes) {
                     if (lane == 0) arrive_first_cta_expect(&bar->full[slot], kUnitBytes);
                     __syncwarp();
-                    if (dims < (v_form ? 4u : 2u))
-                        tma_load_pair(dst + dims * (v_form ? 4096 : 8192) + row * 128, &p.kvmap, &bar->full[slot],
-                                      (int)(v_form ? v_dim(64 * dims, rank) : 128 * u + 64 * dims), y);
+                    if (dims < 2)
+                        tma_load_pair(dst + dims * 8192 + row * 128, &p.kvmap, &bar->full[slot],
+                                      (int)(v_form ? v_dim(128 * (u & 1) + 64 * dims, rank) : 128 * u + 64 * dims), y);
                     read(of);
                 } else {
                     // Rows by 16 bytes, zeros for those that are missing.
 #pragma unroll 8
                     for (uint32_t k = lane; k < kUnitBytes / 16; k += 32) {
-                        const uint32_t row = v_form ? k >> 5 : k >> 4, ch = v_form ? k & 31 : k & 15;  // 8 dims
-                        const int32_t place = at[row];
-                        const uint32_t dim = v_form ? v_dim(8 * ch, rank) : 128 * u + 8 * ch;
-                        cp_async16_or_zero(dst + (ch >> 3) * (v_form ? 4096 : 8192) + swizzled(row, ch & 7),
+                        const uint32_t row = k >> 4, ch = k & 15;  // 8 dims
+                        const int32_t place = at[first + row];
+                        const uint32_t dim = v_form ? v_dim(128 * (u & 1) + 8 * ch, rank) : 128 * u + 8 * ch;
+                        cp_async16_or_zero(dst + (ch >> 3) * 8192 + swizzled(row, ch & 7),
                                            p.cache.pages + (size_t)max(place, 0) * (2 * kDim) + 2 * dim, place >= 0);
                     }
                     read(of);
@@ -814,8 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             }
         } else {
             // Packed rows are widened by two teams of eight warps: team t fills units t and t + 2 of each form, warp s
-            // of it the unit's step s, eight rows of 128 dims (K form: rows 8 s ..; V form: 8 (s / 2) .., 128 dims
-            // each). The loads of a form are issued as the form before it is stored. (Two warps to a unit, four
+            // of it the unit's step s, eight rows of 128 dims. The loads of a form are issued as the form before it is stored. (Two warps to a unit, four
             // steps each, took 4000 cycles from a free unit to a full one, and the ring holds no more than a tile.)
             const uint32_t team = (warp - kBuildWarp) >> 3, s = warp - kBuildWarp & 7;
             Piece<kFormat> held[2];
@@ -826,7 +820,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             auto fetch = [&](uint32_t f, uint32_t k) {
                 const uint32_t of = tile_of(f), u = team + 2 * k, d = Piece<kFormat>::first(lane);
                 const int32_t* at = place_s + of % kPlaceBufs * kTile + Piece<kFormat>::row(lane);
-                if (v_form_of(f)) held[k].load(p.cache, at[32 * u + 8 * (s >> 1)], v_dim(128 * (s & 1), rank) + d);
+                if (v_form_of(f)) held[k].load(p.cache, at[64 * (u >> 1) + 8 * s], v_dim(128 * (u & 1), rank) + d);
                 else held[k].load(p.cache, at[64 * rank + 8 * s], 128 * u + d);
             };
             bool ok = n > 0 && looked_up(0);
@@ -837,16 +831,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             }
             for (uint32_t f = 0; ok && f < 2 * n; ++f) {
                 const bool v_form = v_form_of(f), then = f + 1 < 2 * n;
-                const uint32_t row = 8 * (v_form ? s >> 1 : s) + Piece<kFormat>::row(lane), size = v_form ? 4096 : 8192;
+                const uint32_t row = 8 * s + Piece<kFormat>::row(lane);
                 ok = !then || looked_up(tile_of(f + 1));
 #pragma unroll
                 for (uint32_t k = 0; k < 2; ++k) {
                     const uint32_t slot = (v_form ? kKUnits : 0) + team + 2 * k;
                     ok = ok && wait_warp(&bar->empty[slot], (tile_of(f) & 1) ^ 1, p.status);
                     if (!ok) break;
-                    const uint32_t block = ring + slot * kUnitBytes + (v_form ? (s & 1) * 8192 : 0);
+                    const uint32_t unit = ring + slot * kUnitBytes;
                     held[k].store(Piece<kFormat>::first(lane),
-                                  [&](uint32_t ch) { return block + (ch >> 3) * size + swizzled(row, ch & 7); });
+                                  [&](uint32_t ch) { return unit + (ch >> 3) * 8192 + swizzled(row, ch & 7); });
                     if (then) fetch(f + 1, k);
                     fence_proxy_async_smem();
                     __syncwarp();
