@@ -4,7 +4,8 @@
 // Bound by the bytes of the rows read and written (and, for a few rows, by the
 // launch). A lane owns 16 consecutive elements, which is one group of the 4-bit
 // type, so its scale needs no exchange (a block of the 8-bit type is eight lanes, whose
-// magnitudes meet in three shuffles): a warp holds one 512-wide row or four 128-wide ones. The lanes of a row share its sines and cosines through shared
+// magnitudes meet in three shuffles): a warp holds one 512-wide row or four 128-wide
+// ones. The lanes of a row share its sines and cosines through shared
 // memory (each takes rot / 2 / lanes of them); in the half layout a pair's other
 // element comes from its lane by a shuffle where the halves are whole groups, and is
 // read again where they are not. The row is fetched while its place is looked up
@@ -13,6 +14,7 @@
 // Eight 512-wide rows: 2.5 us. Long runs, over three sets of inputs (most of them in L2) and over
 // sets of 300 MB and more, with the bytes' time at the measured copy bandwidth:
 //   32768 x 128, bf16 into 4-bit pages, half of each rotated, and the values   7.6 / 10.2 us (2.9)
+//   32768 x 128, bf16 into 8-bit pages, half of each rotated, and the values   7.3 us (3.2)
 //   32768 x 128, bf16 into bf16 pages                                          6.2 /  8.9 us (2.5)
 //   8191 x 512, bf16 into 4-bit pages, and the values                          6.3 /  8.9 us (2.8)
 //   8191 x 512, fp32 into bf16 pages                                           6.2 /  8.2 us (3.7)
