@@ -45,6 +45,8 @@
 
 #include <float.h>
 
+#include <algorithm>
+
 #include "cache_rows.cuh"
 #include "common.cuh"
 #include "fp8.cuh"
@@ -925,19 +927,20 @@ namespace {
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWays = kJoinThreads / kHeads;
 constexpr uint32_t kJoinParts = kPrefixPairsMax + 2;  // a row's, at most: its segments lie on one line of runs
+static_assert(kJoinParts <= 10 * kJoinWays, "parts that a thread holds");
 
 // A row's parts in their order: those of its group's prefix, then its own.
 struct RowParts {
     const float *shared, *own;  // of the first part of each
     uint32_t n0, count;
     static constexpr size_t kStep = 2 * kPrefixPartFloats;  // from one pair's to the next pair's
-    static __device__ __forceinline__ uint32_t runs(const PrefixParams& p, uint32_t seg, uint32_t& first) {
+    static __host__ __device__ __forceinline__ uint32_t runs(const PrefixParams& p, uint32_t seg, uint32_t& first) {
         const uint32_t begin = p.begin[seg], end = p.begin[seg + 1];
         auto pair_of = [&](uint32_t t) { return (uint32_t)(((uint64_t)(t + 1) * p.pairs - 1) / p.line); };
         first = begin < end ? pair_of(begin + p.seg_cost) : 0;
         return begin < end ? pair_of(end - 1) - first + 1 : 0;
     }
-    __device__ __forceinline__ RowParts(const PrefixParams& p, uint32_t r) {
+    __host__ __device__ __forceinline__ RowParts(const PrefixParams& p, uint32_t r) {
         uint32_t a, b;
         n0 = runs(p, r / 2, a);
         count = n0 + runs(p, p.groups + r, b);
@@ -948,28 +951,119 @@ struct RowParts {
 };
 }  // namespace
 
-// A block joins `units` units of one row. The factors exp(m_i - m) of the parts come first, for every head. Up to eight
-// rows (kSplit) have many parts each: a unit is half a column of the O layout (4 dims of 64 heads), and eight threads have
-// every eighth part each. More rows have few: a unit is four columns, a thread to a lane of each.
-// Bound by the parts' bytes in L2, and for few rows by its chain of loads.
-template <bool kSplit>
-__global__ void __launch_bounds__(kJoinThreads, 3) prefix_join_kernel(const __grid_constant__ PrefixParams p, uint32_t units) {
-    constexpr uint32_t kLanes = kSplit ? 64 : 128, kWays = kJoinThreads / kLanes, kStep = kSplit ? kWays : 1;
-    __shared__ float fac_s[kJoinParts][kHeads];
+// What a row's parts come to, once their maxima (with the sink's: `top`) and sums are known.
+struct Joined {
+    bool zero;
+    float inv;
+    __device__ __forceinline__ Joined(uint32_t stopped, float sink, float top, float den)  // a flagged part's sum is NaN
+        : zero(stopped || !finite_f(sink) || !finite_f(top) || !finite_f(den) || !(den > 0.0f)), inv(1.0f / den) {}
+    // Column `col` of the O layout, TMEM lane `lane`: four dims of a head.
+    __device__ __forceinline__ void store(const PrefixParams& p, size_t at, uint32_t col, uint32_t lane, float4 acc) const {
+        const uint32_t dim = 256 * (col >> 5) + 128 * (lane >> 6) + 4 * (col & 31);
+        const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+        __align__(8) __nv_bfloat16 y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = __float2bfloat16_rn(!zero && finite_f(x[k]) ? x[k] : 0.0f);
+        *reinterpret_cast<uint2*>(p.out + at * kDim + dim) = *reinterpret_cast<const uint2*>(y);
+    }
+};
+__device__ __forceinline__ float finite_sink2(float sink) {  // a finite sink stays finite
+    return fminf(fmaxf(sink * kLog2e, -FLT_MAX), FLT_MAX);
+}
+__device__ __forceinline__ void add_scaled(float4& acc, const float4& o, float f) {
+    acc.x = fmaf(o.x, f, acc.x);
+    acc.y = fmaf(o.y, f, acc.y);
+    acc.z = fmaf(o.z, f, acc.z);
+    acc.w = fmaf(o.w, f, acc.w);
+}
+
+// Up to eight rows, which have many parts each: a block joins `units` halves of a column of the O layout (4 dims of 64
+// heads) of one row. Eight threads have every eighth part each, up to kHeld of them, whose maxima, sums and first half
+// column are all in flight together.
+template <int kHeld>
+__global__ void __launch_bounds__(kJoinThreads, kHeld > 4 ? 1 : 2) prefix_join_split_kernel(const __grid_constant__ PrefixParams p,
+                                                                                            uint32_t units) {
     __shared__ float m_s[kJoinWays][kHeads], l_s[kJoinWays][kHeads];
-    __shared__ union {
-        float sum[kJoinParts][kHeads];                      // of the parts, until the factors are known
-        float4 acc[kSplit ? kWays - 1 : 1][kLanes];
-    } u_s;
+    __shared__ float4 acc_s[2][kJoinWays - 1][kHeads];
     pdl_trigger();
-    const uint32_t r = blockIdx.x, way = threadIdx.x / kLanes;
-    const uint32_t head = threadIdx.x & 63, head_way = threadIdx.x >> 6;
+    const uint32_t r = blockIdx.x, way = threadIdx.x / kHeads, head = threadIdx.x % kHeads;
+    const RowParts parts(p, r);
+    const size_t at = (size_t)p.q_row[r] * kHeads + head;
+    const uint32_t unit0 = blockIdx.y * units;
+    float m[kHeld], f[kHeld];
+    float4 sums[kHeld], o[kHeld];
+    auto load = [&](uint32_t unit) {
+        const size_t o_at = kPrefixHeadFloats + ((unit >> 1) * 128 + (unit & 1) * 64 + head) * 4;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (way + kJoinWays * k < parts.count)
+                o[k] = __ldcg(reinterpret_cast<const float4*>(parts.at(way + kJoinWays * k) + o_at));
+        }
+    };
+    pdl_wait();
+    const float sink = p.sinks[(size_t)p.q_row[r] * p.sinks_row_stride + head];
+    const uint32_t stopped = *p.status;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        m[k] = -INFINITY;
+        sums[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (way + kJoinWays * k < parts.count) {
+            const float* part = parts.at(way + kJoinWays * k);
+            m[k] = __ldcg(part + head);
+            sums[k] = __ldcg(reinterpret_cast<const float4*>(part + kHeads) + head);
+        }
+    }
+    load(unit0);
+    float top = m[0];
+#pragma unroll
+    for (int k = 1; k < kHeld; ++k) top = fmaxf(top, m[k]);
+    m_s[way][head] = top;
+    __syncthreads();
+    const float sink2 = finite_sink2(sink);
+    top = sink2;
+#pragma unroll
+    for (int k = 0; k < kJoinWays; ++k) top = fmaxf(top, m_s[k][head]);
+    float l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        f[k] = exp2f(m[k] - top);
+        l = fmaf((sums[k].x + sums[k].y) + (sums[k].z + sums[k].w), f[k], l);
+    }
+    l_s[way][head] = l;
+#pragma unroll 1
+    for (uint32_t u = 0; u < units; ++u) {
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) add_scaled(acc, o[k], f[k]);
+        if (way > 0) acc_s[u & 1][way - 1][head] = acc;
+        if (u + 1 < units) load(unit0 + u + 1);
+        __syncthreads();
+        if (way == 0) {
+            float den = exp2f(sink2 - top);
+#pragma unroll
+            for (int k = 0; k < kJoinWays; ++k) den += l_s[k][head];
+            const Joined joined(stopped, sink, top, den);
+            if (p.invalid && unit0 + u == 0) p.invalid[at] = joined.zero ? 1u : 0u;
+#pragma unroll
+            for (int k = 0; k < kJoinWays - 1; ++k) add_scaled(acc, acc_s[u & 1][k][head], 1.0f);
+            joined.store(p, at, (unit0 + u) >> 1, ((unit0 + u) & 1) * 64 + head, acc);
+        }
+    }
+}
+
+// More rows, with few parts each: a block joins `units` units of four columns of the O layout of one row, a thread to a lane
+// of each. The factors exp(m_i - m) of the parts come first, for every head. Bound by the parts' bytes in L2.
+__global__ void __launch_bounds__(kJoinThreads, 3) prefix_join_kernel(const __grid_constant__ PrefixParams p, uint32_t units) {
+    __shared__ float fac_s[kJoinParts][kHeads], sum_s[kJoinParts][kHeads];
+    __shared__ float m_s[kJoinWays][kHeads], l_s[kJoinWays][kHeads];
+    pdl_trigger();
+    const uint32_t r = blockIdx.x, head = threadIdx.x & 63, head_way = threadIdx.x >> 6;
     const RowParts parts(p, r);
     const size_t at = (size_t)p.q_row[r] * kHeads + head;
     pdl_wait();
     const float sink = p.sinks[(size_t)p.q_row[r] * p.sinks_row_stride + head];
     const uint32_t stopped = *p.status;
-    const uint32_t i0 = kSplit ? way : 0;
     float m = -INFINITY;
 #pragma unroll 4
     for (uint32_t i = head_way; i < parts.count; i += kJoinWays) {
@@ -977,12 +1071,12 @@ __global__ void __launch_bounds__(kJoinThreads, 3) prefix_join_kernel(const __gr
         const float x = __ldcg(part + head);
         const float4 sums = __ldcg(reinterpret_cast<const float4*>(part + kHeads) + head);
         fac_s[i][head] = x;
-        u_s.sum[i][head] = (sums.x + sums.y) + (sums.z + sums.w);
+        sum_s[i][head] = (sums.x + sums.y) + (sums.z + sums.w);
         m = fmaxf(m, x);
     }
     m_s[head_way][head] = m;
     __syncthreads();
-    const float sink2 = fminf(fmaxf(sink * kLog2e, -FLT_MAX), FLT_MAX);  // a finite sink stays finite
+    const float sink2 = finite_sink2(sink);
     float top = sink2;
 #pragma unroll
     for (int k = 0; k < kJoinWays; ++k) top = fmaxf(top, m_s[k][head]);
@@ -991,45 +1085,24 @@ __global__ void __launch_bounds__(kJoinThreads, 3) prefix_join_kernel(const __gr
     for (uint32_t i = head_way; i < parts.count; i += kJoinWays) {
         const float f = exp2f(fac_s[i][head] - top);
         fac_s[i][head] = f;
-        l = fmaf(u_s.sum[i][head], f, l);
+        l = fmaf(sum_s[i][head], f, l);
     }
     l_s[head_way][head] = l;
     __syncthreads();
     float den = exp2f(sink2 - top);
 #pragma unroll
     for (int k = 0; k < kJoinWays; ++k) den += l_s[k][head];
-    // A flagged part's sum is NaN.
-    const bool zero = stopped || !finite_f(sink) || !finite_f(top) || !finite_f(den) || !(den > 0.0f);
-    const float inv = 1.0f / den;
-    if (p.invalid && blockIdx.y == 0 && threadIdx.x < 64) p.invalid[at] = zero ? 1u : 0u;
-    auto add = [&](float4& acc, const float4& o, float f) {
-        acc.x = fmaf(o.x, f, acc.x);
-        acc.y = fmaf(o.y, f, acc.y);
-        acc.z = fmaf(o.z, f, acc.z);
-        acc.w = fmaf(o.w, f, acc.w);
-    };
+    const Joined joined(stopped, sink, top, den);
+    if (p.invalid && blockIdx.y == 0 && threadIdx.x < 64) p.invalid[at] = joined.zero ? 1u : 0u;
 #pragma unroll 1
     for (uint32_t unit = blockIdx.y * units; unit < (blockIdx.y + 1) * units; ++unit) {
-        const uint32_t col = kSplit ? unit >> 1 : 4 * unit + way;
-        const uint32_t lane = kSplit ? (unit & 1) * 64 + head : threadIdx.x & 127;
-        const size_t o_at = kPrefixHeadFloats + (col * 128 + lane) * 4;
+        const uint32_t lane = threadIdx.x & 127, col = 4 * unit + (threadIdx.x >> 7);
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 2
-        for (uint32_t i = i0; i < parts.count; i += kStep)
-            add(acc, __ldcg(reinterpret_cast<const float4*>(parts.at(i) + o_at)), fac_s[i][head]);
-        const uint32_t dim = 256 * (col >> 5) + 128 * (lane >> 6) + 4 * (col & 31);
-        if (kSplit && way > 0) u_s.acc[way - 1][head] = acc;
-        if (kSplit) __syncthreads();
-        if (!kSplit || way == 0) {
-            if (kSplit)
-                for (uint32_t k = 0; k < kWays - 1; ++k) add(acc, u_s.acc[k][head], 1.0f);
-            const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-            __align__(8) __nv_bfloat16 y[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = __float2bfloat16_rn(!zero && finite_f(x[k]) ? x[k] : 0.0f);
-            *reinterpret_cast<uint2*>(p.out + at * kDim + dim) = *reinterpret_cast<const uint2*>(y);
-        }
-        if (kSplit) __syncthreads();
+        for (uint32_t i = 0; i < parts.count; ++i)
+            add_scaled(acc, __ldcg(reinterpret_cast<const float4*>(parts.at(i) + kPrefixHeadFloats + (col * 128 + lane) * 4)),
+                       fac_s[i][head]);
+        joined.store(p, at, col, lane, acc);
     }
 }
 
@@ -1040,13 +1113,16 @@ static cudaError_t launch(const PrefixParams& p, cudaStream_t stream, bool pdl) 
     if (err != cudaSuccess) return err;
     err = launch_kernel(prefix_attn_kernel<kFormat>, dim3(2 * p.pairs), dim3(kThreads<kFormat>), kSmem<kFormat>, stream, pdl, p);
     if (err != cudaSuccess) return err;
-    // About four blocks for each multiprocessor (two, and a column of 64 threads a block, were up to 8 us slower).
+    uint32_t most = 0;  // parts of a row
+    for (uint32_t r = 0; r < p.rows; ++r) most = std::max(most, RowParts(p, r).count);
     uint32_t units = 1;
-    const uint32_t all = p.rows <= 8 ? 128 : 16;
-    while (p.rows * (all / units) > 8 * kPrefixPairsMax) units *= 2;
+    const uint32_t all = p.rows <= 8 ? 128 : 16, sms = 2 * kPrefixPairsMax, held = most <= 4 * kJoinWays ? 4 : 10;
+    // Blocks that run together; of the other kernel about four for each multiprocessor (two were up to 8 us slower).
+    while (p.rows * (all / units) > (p.rows > 8 ? 4 : held == 4 ? 2 : 1) * sms) units *= 2;
     const dim3 grid(p.rows, all / units), block(kJoinThreads);
-    if (p.rows <= 8) return launch_kernel(prefix_join_kernel<true>, grid, block, 0, stream, true, p, units);
-    return launch_kernel(prefix_join_kernel<false>, grid, block, 0, stream, true, p, units);
+    if (p.rows > 8) return launch_kernel(prefix_join_kernel, grid, block, 0, stream, true, p, units);
+    if (held == 4) return launch_kernel(prefix_join_split_kernel<4>, grid, block, 0, stream, true, p, units);
+    return launch_kernel(prefix_join_split_kernel<10>, grid, block, 0, stream, true, p, units);
 }
 
 template <int kFormat>
