@@ -685,15 +685,11 @@ int check_prefix_rows(int rows, const ds_row_t* table, uint32_t prefix_len) {
 // the workspace. With a tile for every pair, or less, each pair has one; else a
 // segment's set-up (its query, the first tile's way through the pipeline, what it leaves in the workspace)
 // counts as four tiles, so that the pairs with the rows' short ends do not finish last (63 rows of 20001 and
-// up to 311 more: 157 us at two, 132 at three, 121 at four, 122 to 126 at five to eight).
-// A pair costs what it leaves and the join reads, so few segments are not dealt out to all of them: k tiles
-// to a pair cost k times a tile and the pairs that this takes, with a tile as much as 10 pairs for rows by TMA and as
-// 24 where packed rows are widened as they are used (of 6 to 40 the best over the sizes). One row, us with this
-// number against a pair for every tile, up to all: bf16 of 9728 14.3 / 17.8, of 19456 16.7 / 19.8, of 30000 22.5 / 23.3;
-// 8 bits of 9728 16.0 / 19.4, of 38912 28.8 / 31.1. Many segments keep all pairs (30 rows of 1216 and 100 more: 21.2 us against
-// 25.6). One segment alone has its set-up in every pair, which shifts nothing.
+// up to 311 more: 155 us at two, 130 at three, 118 at four, 120 at six; 12 rows of 65536 and up to 12 more: 105, 87, 74, 72).
+// A segment alone is dealt out in equal runs: its set-up on the line would only shift them (one 8-bit row of 19456: 19.8 us
+// instead of 17.5). Fewer pairs than there are tiles for, which leave the join less to read, are no faster.
 size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t prefix_len, uint32_t most_pairs,
-                      bool& widen, bool by_tma = true) {
+                      bool& widen) {
     p.rows = (uint32_t)rows;
     p.groups = (p.rows + 1) / 2;
     p.prefix_len = prefix_len;
@@ -705,17 +701,7 @@ size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t
     }
     p.pairs = tiles < most_pairs ? tiles : most_pairs;
     const uint32_t parts = p.pairs + p.groups + p.rows - 1;
-    const uint32_t set_up = filled == 1 ? 0 : 4;
-    p.seg_cost = tiles <= p.pairs ? 0 : set_up;
-    if (filled <= 4) {
-        const uint32_t per_tile = by_tma ? 10 : 24, most = p.pairs;
-        uint32_t best = p.seg_cost == 0 && tiles <= most ? per_tile + tiles : ~0u;
-        const uint32_t line = tiles + set_up * filled;
-        for (uint32_t k = std::max((line - 1) / most + 1, 2u); k < best / per_tile; ++k) {
-            const uint32_t pairs = (line - 1) / k + 1, cost = per_tile * k + pairs;
-            if (cost < best) best = cost, p.pairs = pairs, p.seg_cost = set_up;
-        }
-    }
+    p.seg_cost = tiles <= p.pairs || filled == 1 ? 0 : 4;
     uint32_t segs = 0, at = 0;
     auto add = [&](uint32_t slots) {
         p.begin[segs++] = at;
@@ -1312,8 +1298,7 @@ int ds_rows_prefix_attn(int rows, const ds_row_t* table, uint32_t prefix_len, co
     if (sms <= 0) return fail(DS_ECUDA, "no CUDA device");
     widen = widen && kv->format != DS_CACHE_BF16 && workspace_bytes - L.total >= p.wide_tiles * kWideTileBytes;
     bool unused;
-    (void)lay_out_prefix(p, rows, table, prefix_len, std::min(kPrefixPairsMax, std::max((uint32_t)sms / 2, 1u)), unused,
-                         widen || kv->format == DS_CACHE_BF16);
+    (void)lay_out_prefix(p, rows, table, prefix_len, std::min(kPrefixPairsMax, std::max((uint32_t)sms / 2, 1u)), unused);
     p.wide = widen ? reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + L.total) : nullptr;
     rc = get_encoder();
     if (rc) return rc;

@@ -977,7 +977,7 @@ __device__ __forceinline__ void add_scaled(float4& acc, const float4& o, float f
     acc.w = fmaf(o.w, f, acc.w);
 }
 
-// Up to eight rows, which have many parts each: a block joins `units` halves of a column of the O layout (4 dims of 64
+// Up to eight rows with many parts each, or two: a block joins `units` halves of a column of the O layout (4 dims of 64
 // heads) of one row. Eight threads have every eighth part each, up to kHeld of them, whose maxima, sums and first half
 // column are all in flight together.
 template <int kHeld>
@@ -1052,7 +1052,7 @@ __global__ void __launch_bounds__(kJoinThreads, kHeld > 4 ? 1 : 2) prefix_join_s
     }
 }
 
-// More rows, with few parts each: a block joins `units` units of four columns of the O layout of one row, a thread to a lane
+// Many rows, or few parts each: a block joins `units` units of four columns of the O layout of one row, a thread to a lane
 // of each. The factors exp(m_i - m) of the parts come first, for every head. Bound by the parts' bytes in L2.
 __global__ void __launch_bounds__(kJoinThreads, 3) prefix_join_kernel(const __grid_constant__ PrefixParams p, uint32_t units) {
     __shared__ float fac_s[kJoinParts][kHeads], sum_s[kJoinParts][kHeads];
@@ -1116,11 +1116,14 @@ static cudaError_t launch(const PrefixParams& p, cudaStream_t stream, bool pdl) 
     uint32_t most = 0;  // parts of a row
     for (uint32_t r = 0; r < p.rows; ++r) most = std::max(most, RowParts(p, r).count);
     uint32_t units = 1;
-    const uint32_t all = p.rows <= 8 ? 128 : 16, sms = 2 * kPrefixPairsMax, held = most <= 4 * kJoinWays ? 4 : 10;
+    // (us, this kernel / the other: one row of 1216, 8 parts, 10.7 / 12.8; two rows of 500, 5 parts, 11.1 / 11.8; but three rows of 300,
+    // 4 parts, 12.0 / 11.5; eight of 500, 5 parts, 15.2 / 12.8; 20 of 40000, 9 parts, 80 / 74.)
+    const bool split = p.rows <= 2 || (p.rows <= 8 && most > 8);
+    const uint32_t all = split ? 128 : 16, sms = 2 * kPrefixPairsMax, held = most <= 4 * kJoinWays ? 4 : 10;
     // Blocks that run together; of the other kernel about four for each multiprocessor (two were up to 8 us slower).
-    while (p.rows * (all / units) > (p.rows > 8 ? 4 : held == 4 ? 2 : 1) * sms) units *= 2;
+    while (units < all && p.rows * (all / units) > (!split ? 4 : held == 4 ? 2 : 1) * sms) units *= 2;
     const dim3 grid(p.rows, all / units), block(kJoinThreads);
-    if (p.rows > 8) return launch_kernel(prefix_join_kernel, grid, block, 0, stream, true, p, units);
+    if (!split) return launch_kernel(prefix_join_kernel, grid, block, 0, stream, true, p, units);
     if (held == 4) return launch_kernel(prefix_join_split_kernel<4>, grid, block, 0, stream, true, p, units);
     return launch_kernel(prefix_join_split_kernel<10>, grid, block, 0, stream, true, p, units);
 }
