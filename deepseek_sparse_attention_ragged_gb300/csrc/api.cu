@@ -714,6 +714,8 @@ size_t lay_out_prefix(PrefixParams& p, int rows, const ds_row_t* table, uint32_t
         add(table[e].kv_len - prefix_len);
     }
     p.begin[segs] = p.line = at;
+    p.run = p.line / p.pairs;
+    p.rest = p.line % p.pairs;
     uint32_t wide = tiles_of(prefix_len);
     for (uint32_t e = 0; e < p.rows; ++e) {
         p.wide_begin[e] = wide;

@@ -244,7 +244,8 @@ struct PrefixParams {
     uint32_t prefix_len;
     uint32_t pairs;
     uint32_t seg_cost;  // units of the line for a segment's set-up, before its tiles
-    uint32_t line;      // its length
+    uint32_t line;      // its length: pairs * run + rest
+    uint32_t run, rest;
     uint32_t kv_len[kPrefixRowsMax];
     uint32_t q_row[kPrefixRowsMax];
     uint32_t begin[kPrefixSegsMax + 1];  // of each segment on the line (empty ones take nothing)

@@ -329,15 +329,16 @@ struct Part {
     uint32_t tiles;
 };
 
-// The parts of pair k in order: for (Walk w(p, k, pairs); w.next(part);). What is dealt out in equal runs
-// is a line on which a segment's tiles follow p.seg_cost units for its set-up.
+// The parts of pair k in order: for (Walk w(p, k); w.next(part);). What is dealt out in equal runs
+// (pair k's begins at floor(line k / pairs)) is a line on which a segment's tiles follow p.seg_cost units for its set-up.
 struct Walk {
     const PrefixParams& p;
     uint32_t t, end, seg;
-    __device__ __forceinline__ Walk(const PrefixParams& params, uint32_t pair, uint32_t pairs) : p(params) {
-        t = (uint32_t)((uint64_t)p.line * pair / pairs);
-        end = (uint32_t)((uint64_t)p.line * (pair + 1) / pairs);
+    __device__ __forceinline__ Walk(const PrefixParams& params, uint32_t pair) : p(params) {
+        t = p.run * pair + p.rest * pair / p.pairs;
+        end = p.run * (pair + 1) + p.rest * (pair + 1) / p.pairs;
         seg = 0;
+        while (t < end && p.begin[seg + 1] <= t) ++seg;
     }
     __device__ __forceinline__ bool next(Part& part) {
         while (t < end) {
@@ -372,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
     int32_t* place_s = reinterpret_cast<int32_t*>(smem + L::place);
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const uint32_t rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
     const uint32_t ring = smem_u32(smem + L::ring);
 
     if (threadIdx.x == 0) {
@@ -412,15 +413,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem_base, 0);
     // The pair's tiles. (What depends on the parameters alone comes before the wait for the kernel before this one.)
+    const Walk all(p, pair);
     Part part;
     uint32_t n = 0;
-    for (Walk w(p, pair, pairs); w.next(part);) n += part.tiles;
+    for (Walk w = all; w.next(part);) n += part.tiles;
     if (threadIdx.x == 32 * 3) {
         tma_prefetch_map(&p.qmap);
         if (kByTma<kFormat>) tma_prefetch_map(&p.kvmap);
     }
     // The first part's query and page ids into L2 (the kernel before may yet write them: nothing is read here).
-    Walk ahead(p, pair, pairs);
+    Walk ahead = all;
     if (ahead.next(part)) {
         const uint32_t r = part.seg < p.groups ? min(2 * part.seg + rank, p.rows - 1) : part.seg - p.groups;
         if (threadIdx.x < kQBytes / 128)
@@ -438,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
     if (warp == 0) {
         // ---- the tiles' rows: places in the pool ----------------------------------------------
         bool ok = true;
-        for (Walk w(p, pair, pairs); ok && w.next(part);) {
+        for (Walk w = all; ok && w.next(part);) {
             const uint32_t entry = part.seg < p.groups ? 0 : part.seg - p.groups;
             const int32_t* table = p.cache.table + (size_t)entry * p.cache.table_stride;
             const uint32_t shift = p.cache.page_shift;
@@ -501,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             if (warp == 1) {
                 constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
                 const uint64_t a_desc = smem_desc_sw128_kmajor(smem_u32(smem + L::q));
-                for (Walk w(p, pair, pairs); ok && w.next(part); ++n_part)
+                for (Walk w = all; ok && w.next(part); ++n_part)
                     for (uint32_t i = 0; i < part.tiles; ++i, ++it) {
                         ok = i != 0 || wait_warp(&bar->q_full, n_part & 1, p.status);
                         ok = ok && wait_warp(&bar->s_free[it % kSBufs], (it / kSBufs & 1) ^ 1, p.status);
@@ -532,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                     }
             } else {
                 constexpr uint32_t idesc = idesc_bf16_f32(128, 256) | 1u << 16;  // B is MN-major
-                for (Walk w(p, pair, pairs); ok && w.next(part); ++n_part)
+                for (Walk w = all; ok && w.next(part); ++n_part)
                     for (uint32_t i = 0; i < part.tiles; ++i, ++it) {
                         ok = wait_warp(&bar->p_full[it & 1], it >> 1 & 1, p.status);
                         // A part begins O anew, once the part before has been read.
@@ -581,7 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
         uint32_t met = 0;  // a set's warps meet once a tile
         bool ok = true;
-        for (Walk w(p, pair, pairs); ok && w.next(part);) {
+        for (Walk w = all; ok && w.next(part);) {
             float m = -INFINITY, sum = 0.0f;  // the maximum that the sum refers to
             uint32_t bad = 0;
             const uint32_t begin = it;
@@ -751,7 +753,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
     } else if (warp == 3) {
         // ---- each part's query, once the MMAs of the part before have read theirs --------------
         uint32_t n_part = 0;
-        for (Walk w(p, pair, pairs); w.next(part); ++n_part) {
+        for (Walk w = all; w.next(part); ++n_part) {
             if (n_part > 0 && !wait_warp(&bar->q_free, (n_part - 1) & 1, p.status)) break;
             const uint32_t r = part.seg < p.groups ? min(2 * part.seg + rank, p.rows - 1) : part.seg - p.groups;
             if (lane == 0) arrive_first_cta_expect(&bar->q_full, kQBytes);
