@@ -591,10 +591,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 if ((it & 1) != set) continue;
                 const uint32_t pbuf = it % kPlaceBufs;
                 const uint32_t sbuf = it % kSBufs, s_cols = lanes + s_col(it);
-                if (!(ok = wait_warp(&bar->s_full[sbuf], it / kSBufs & 1, p.status))) break;
-                tc_fence_after();
                 if (!(ok = wait_warp(&bar->place_full[pbuf], it / kPlaceBufs & 1, p.status))) break;
                 const bool masked = bar->form[pbuf] & kMasked;
+                if (!(ok = wait_warp(&bar->s_full[sbuf], it / kSBufs & 1, p.status))) break;
+                tc_fence_after();
                 const ::int4* at = reinterpret_cast<const ::int4*>(place_s + pbuf * kTile + half * 64);
                 // The largest logit. 0 * t is NaN exactly where one is not finite.
                 float top = -INFINITY;
