@@ -29,19 +29,19 @@
 // Rows past a segment's end and rows without a page are zeros with probability 0.
 //
 // In a captured graph, all launches of a call (the time that its operations or its bytes alone would take):
-//   3 rows, 300 shared and up to 40 more, bf16 pages           12.0 us (0.1)
-//   1 row of 131073, bf16                                      41.2 us (19.9, bytes)
-//   8 rows, 65536 shared and up to 999 more, bf16              58.6 us (36.3, operations)
-//   5 rows, 40007 shared and up to 1000 more, 4 bits           40.3 us (13.9, operations)
-//   63 rows, 20001 shared and up to 311 more, 8 bits           119 us (87.5, operations)
-// A tile takes a pair 1.3 us on bf16 rows (its MMAs 1.0): the tensor cores are busy for 68% of the attention kernel at
-// eight rows and 75% at 63. No unit is full; a ring unit's way round (commit, wait, 16 KB by TMA, wait, MMAs) takes about
+//   3 rows, 300 shared and up to 40 more, bf16 pages           11.1 us (0.1)
+//   1 row of 131073, bf16                                      37.1 us (19.9, bytes)
+//   8 rows, 65536 shared and up to 999 more, bf16              52.4 us (36.3, operations)
+//   5 rows, 40007 shared and up to 1000 more, 4 bits           37.8 us (13.9, operations)
+//   63 rows, 20001 shared and up to 311 more, 8 bits           115 us (87.5, operations)
+// A tile takes a pair 1.3 us on bf16 rows (its MMAs 1.0): the tensor cores are busy for 69% of the attention kernel at
+// eight rows and 76% at 63. No unit is full; a ring unit's way round (commit, wait, 16 KB by TMA, wait, MMAs) takes about
 // 2,000 cycles and the rings hold seven eighths of a tile, which is what shared memory has room for. Taken out one by
-// one, at 63 rows (119 us): the loads 109, seven of eight S MMAs 112, half of P . G 115, a quarter of the bytes 117, the
-// exponentials 119; 8 KB units 143, one P buffer 153, three K and four V units 128. The rest is fixed: some 11 us of
-// launches, first loads, the parts' 128 KB a CTA and their join, which a short call or a single row sees most. Packed
-// rows widened as they are used take 2.7 us (8 bits) or 2.5 us (4 bits) a tile: every value passes registers.
-// A single long row of bf16 takes 1.7 us a tile, which is 5.9 TB/s of DRAM.
+// one, at 63 rows (then 119 us): the loads 109, seven of eight S MMAs 112, half of P . G 115, a quarter of the bytes 117,
+// the exponentials 119; 8 KB units 143, one P buffer 153, three K and four V units 128. The rest is fixed: some 10 us of
+// launches, first loads, the parts (2 us: a multiprocessor stores 32 bytes a cycle, by bulk copies too) and their join,
+// which a short call or a single row sees most. Packed rows widened as they are used take 2.7 us (8 bits) or 2.5 us (4
+// bits) a tile: every value passes registers. A single long row of bf16 takes 1.7 us a tile, which is 5.9 TB/s of DRAM.
 
 #include <float.h>
 

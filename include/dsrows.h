@@ -547,7 +547,7 @@ int ds_rows_fetch(const ds_paged_cache_t* cache, const int32_t* seq, const int32
 
 /*
  * ds_rows_indexer_score with the keys in a paged cache (dim 128): entry e of the
- * table reads entry e of the cache. 4-bit keys are widened exactly, and the scores
+ * table reads entry e of the cache. 8- and 4-bit keys are widened exactly, and the scores
  * are bitwise those of the bf16 keys that the cache stands for. A key whose page id is
  * not in [0, num_pages), or with a NaN scale, scores -inf. DS_EINVAL when the
  * cache has fewer entries than rows, or a table row cannot reach kv_len; kv_len
@@ -560,7 +560,7 @@ int ds_rows_indexer_score_paged(int rows, const ds_row_t* table, const ds_paged_
 
 /*
  * ds_rows_sparse_attn with the KV rows in a paged cache (dim 512): entry e of the
- * table reads entry e of the cache. 4-bit rows are widened to bf16 exactly, so
+ * table reads entry e of the cache. 8- and 4-bit rows are widened to bf16 exactly, so
  * the output is bitwise that of ds_rows_sparse_attn on the bf16 rows that the
  * cache stands for. A selected row whose page id is not in [0, num_pages) zeroes
  * every head of its entry, as an index out of range does; a NaN scale zeroes the

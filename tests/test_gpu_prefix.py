@@ -328,7 +328,7 @@ def test_a_decode_step_of_samples_of_one_prompt():
 
 
 @pytest.mark.parametrize("fmt", ["fp8", "int4"])
-@pytest.mark.parametrize("prefix,tails", [(1000, [0, 1, 127, 128, 129, 300]), (1280, [5] * 9), (2049, [3] * 64)])
+@pytest.mark.parametrize("prefix,tails", [(5000, [0, 1, 127, 128, 129, 300]), (2560, [5] * 9), (2049, [3] * 64)])
 def test_rows_widened_beforehand_give_the_same_bits(fmt, prefix, tails):
     """With the smaller workspace the packed rows are widened as they are used; a page id out of range zeroes the same
     heads both ways."""

@@ -63,9 +63,9 @@ def test_workspace_bytes(lib):
     long = [((1 << 31) - 1, 1, 0, i) for i in range(64)], (1 << 31) - 200
     assert size(*long, "bf16") <= 512 + (76 + 96) * part
     # Packed rows that many entries share are also held as bf16, a kilobyte each, in whole tiles.
-    shared = [(1000 + i, 1, 0, i) for i in range(6)], 1000
+    shared = [(5000 + i, 1, 0, i) for i in range(6)], 5000
     for fmt in ("fp8", "int4", None):
-        assert size(*shared, fmt) == size(*shared, "bf16") + (8 + 5) * 128 * 1024
+        assert size(*shared, fmt) == size(*shared, "bf16") + (40 + 5) * 128 * 1024
         assert size([(1000, 1, 0, 0), (1001, 1, 0, 1)], 1000, fmt) == size([(1000, 1, 0, 0), (1001, 1, 0, 1)], 1000, "bf16")
     with pytest.raises(ValueError, match="one of"):
         size(*shared, "fp4")
