@@ -92,7 +92,8 @@ def test_prefix_attention(fmt, page, prefix, tails):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("prefix,tails", [(9999, [300] * 5), (20000, [0]), (3001, [1 + 7 * i for i in range(63)]),
-                                          (0, [9000, 1, 20000]), (130, [300 + i for i in range(64)])])
+                                          (0, [9000, 1, 20000]), (130, [300 + i for i in range(64)]), (30000, [0, 7]),
+                                          (20000, [5, 0, 9]), (7000, [0] * 4), (6000, [1] * 8), (512, [0] * 8)])
 def test_many_tiles_and_rows(fmt, prefix, tails):
     """More tiles than pairs of processors: parts that begin and end inside segments; rows in any order,
     each with its own sinks; the same bits again."""
