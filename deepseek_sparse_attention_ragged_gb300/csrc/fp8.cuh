@@ -22,11 +22,16 @@ __device__ __forceinline__ uint32_t factor(uint32_t byte) {
 
 // The 4 values of a word as bf16 pairs. A byte's exponent and mantissa in a bf16's places are
 // v 2^-120 (the types' biases are 7 and 127; subnormals agree too), so one exact product gives
-// v 2^e. There is no code for NaN: 0x7F is 480 (an append never writes it).
+// v 2^e. There is no code for NaN: 0x7F is 480 (an append never writes it). Even and odd bytes are placed
+// together and put in order at the end: six logical operations and two shifts to the left, which the FMA pipe does
+// (putting two neighbouring bytes in their places first takes eight).
 __device__ __forceinline__ void widen(uint32_t word, uint32_t f, uint32_t* out) {
-    const uint32_t t0 = __byte_perm(word, 0, 0x1404), t1 = __byte_perm(word, 0, 0x3424);  // bytes at bits 8 and 24
-    out[0] = int4::fma_bf16x2((t0 >> 4 & 0x07F007F0u) | (t0 & 0x80008000u), f, 0x80008000u);
-    out[1] = int4::fma_bf16x2((t1 >> 4 & 0x07F007F0u) | (t1 & 0x80008000u), f, 0x80008000u);
+    constexpr uint32_t kPlaces = 0x07F007F0u;
+    const uint32_t signs = word & 0x80808080u;
+    const uint32_t even = int4::fma_bf16x2((word * 16 & kPlaces) | (signs * 256 & ~kPlaces), f, 0x80008000u);
+    const uint32_t odd = int4::fma_bf16x2((word >> 4 & kPlaces) | (signs & ~kPlaces), f, 0x80008000u);
+    out[0] = __byte_perm(even, odd, 0x5410);
+    out[1] = __byte_perm(even, odd, 0x7632);
 }
 
 // The exponent byte of a block from the largest magnitude's bits: the least e with top <= 448 2^e,
