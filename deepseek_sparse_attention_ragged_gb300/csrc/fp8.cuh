@@ -22,14 +22,19 @@ __device__ __forceinline__ uint32_t factor(uint32_t byte) {
 
 // The 4 values of a word as bf16 pairs. A byte's exponent and mantissa in a bf16's places are
 // v 2^-120 (the types' biases are 7 and 127; subnormals agree too), so one exact product gives
-// v 2^e. There is no code for NaN: 0x7F is 480 (an append never writes it). Even and odd bytes are placed
-// together and put in order at the end: six logical operations and two shifts to the left, which the FMA pipe does
-// (putting two neighbouring bytes in their places first takes eight).
-__device__ __forceinline__ void widen(uint32_t word, uint32_t f, uint32_t* out) {
+// v 2^e. There is no code for NaN: 0x7F is 480 (an append never writes it). Here as (v0, v2) and (v1, v3): three or four
+// logical operations, and shifts to the left, which the FMA pipe does.
+__device__ __forceinline__ void widen_apart(uint32_t word, uint32_t f, uint32_t& even, uint32_t& odd) {
     constexpr uint32_t kPlaces = 0x07F007F0u;
     const uint32_t signs = word & 0x80808080u;
-    const uint32_t even = int4::fma_bf16x2((word * 16 & kPlaces) | (signs * 256 & ~kPlaces), f, 0x80008000u);
-    const uint32_t odd = int4::fma_bf16x2((word >> 4 & kPlaces) | (signs & ~kPlaces), f, 0x80008000u);
+    even = int4::fma_bf16x2((word * 16 & kPlaces) | (signs * 256 & ~kPlaces), f, 0x80008000u);
+    odd = int4::fma_bf16x2((word >> 4 & kPlaces) | (signs & ~kPlaces), f, 0x80008000u);
+}
+
+// ... in order. (Two neighbouring bytes put in their places first take two operations more.)
+__device__ __forceinline__ void widen(uint32_t word, uint32_t f, uint32_t* out) {
+    uint32_t even, odd;
+    widen_apart(word, f, even, odd);
     out[0] = __byte_perm(even, odd, 0x5410);
     out[1] = __byte_perm(even, odd, 0x7632);
 }

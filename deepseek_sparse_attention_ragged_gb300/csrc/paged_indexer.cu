@@ -30,10 +30,13 @@
 // and two issuers 25.3; the mask and exponent of a value in one instruction 23.1;
 // the polling loads 21.5; shared-space pointers and running indexes 20.8.
 //
-// 8-bit pages: 129 bytes a key and one exponent, the same way through TMEM. 8 x 131072 keys take 29.5 us (135 MB and the
-// scores: 20.7 us at the measured copy bandwidth). Without the head sums 25.7 us, without the widening 25.6 us, without
-// both 23.9 us: the stream behind its 3 us ramp, and the issue slots (2.3 of 4 a cycle, integer pipe 57%) on top of it. 12
-// stages instead of eight make no difference (29.2), four are slower (30.9).
+// 8-bit pages: 129 bytes a key, the same way through TMEM. Keys and query have the middle two of every four dims
+// exchanged, as the widening leaves them (the sum over the 16 dims of an MMA step does not depend on their order:
+// the scores are bitwise those of bf16 keys, by test). 8 x 131072 keys take 26.4 us (135 MB and the scores: 20.7 us at
+// the measured copy bandwidth); 29.4 us with the dims in order and two operations more for each value pair, 27.8 us with them put
+// in order behind the widening. The stream alone, with neither head sums nor widening, takes 23.9 us behind its 3 us
+// ramp; it was 25.7 us without the head sums and 25.6 us without the widening. 12 stages instead of eight made no
+// difference (29.2 against 29.4), four were slower (30.9).
 //
 // Warp roles: 0 loads, the next kIssuers issue the MMAs (warp 1 owns TMEM), then
 // kEpiSets epilogue sets of four warps and (packed pages) kWideSets widening sets.
@@ -206,7 +209,11 @@ __global__ void __launch_bounds__(Shape<kFormat>::kThreads, 1)
         const uint4* q = reinterpret_cast<const uint4*>(p.q + (size_t)p.q_row[e] * kIdxHeads * kIdxDim);
         for (int i = threadIdx.x; i < kIdxHeads * kIdxDim / 8; i += S::kThreads) {
             const int h = i >> 4, ch = i & 15;
-            *reinterpret_cast<uint4*>(q_s + (ch >> 3) * kQHalf + h * 128 + (((ch & 7) ^ (h & 7)) << 4)) = q[i];
+            uint4 v = q[i];
+            if constexpr (kFormat == DS_CACHE_FP8)  // in the order of the widened keys
+                v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
+                               __byte_perm(v.z, v.w, 0x7632));
+            *reinterpret_cast<uint4*>(q_s + (ch >> 3) * kQHalf + h * 128 + (((ch & 7) ^ (h & 7)) << 4)) = v;
         }
         if (threadIdx.x < kIdxHeads) {
             const float w = p.w[(size_t)p.q_row[e] * kIdxHeads + threadIdx.x];
@@ -398,10 +405,10 @@ __global__ void __launch_bounds__(Shape<kFormat>::kThreads, 1)
                     uint32_t r[16];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        fp8::widen(d[c + h].x, f, r + 8 * h);
-                        fp8::widen(d[c + h].y, f, r + 8 * h + 2);
-                        fp8::widen(d[c + h].z, f, r + 8 * h + 4);
-                        fp8::widen(d[c + h].w, f, r + 8 * h + 6);
+                        fp8::widen_apart(d[c + h].x, f, r[8 * h + 0], r[8 * h + 1]);
+                        fp8::widen_apart(d[c + h].y, f, r[8 * h + 2], r[8 * h + 3]);
+                        fp8::widen_apart(d[c + h].z, f, r[8 * h + 4], r[8 * h + 5]);
+                        fp8::widen_apart(d[c + h].w, f, r[8 * h + 6], r[8 * h + 7]);
                     }
                     tmem_st_x16(taddr + c * 8, r);
                 }
