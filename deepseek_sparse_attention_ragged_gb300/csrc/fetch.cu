@@ -7,7 +7,7 @@
 // ids one step, so that a row's load waits for neither.
 //
 // 37 4-bit rows 1.5 us. 262144 8-bit keys into bf16 (34 MB read, 67 MB written: 15.3 us at the measured copy bandwidth)
-// 19.5 us; 20001 8-bit rows of 512 into 32 bits (51 MB: 7.4 us) 9.2 us. Two rows a thread in flight made no difference;
+// 19.3 us; 20001 8-bit rows of 512 into 32 bits (51 MB: 7.4 us) 9.1 us. Two rows a thread in flight made no difference;
 // with each row's look-ups in front of it, and stores of 16 bytes, the two took 29.4 and 13.7 us. Waits for loads are the largest
 // stall; the widening uses half of the integer pipe.
 
