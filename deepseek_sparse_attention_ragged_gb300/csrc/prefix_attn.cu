@@ -480,8 +480,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
     } else if (warp <= 2) {
         // ---- the MMAs, issued in the first CTA for both: warp 1 S = Q G^T, warp 2 O += P G. (One warp for both took
         // 3,900 cycles a tile, twice the MMAs' time: waits of 100 to 200 cycles and 20 or so an MMA, one after another.
-        // The units of S are a loop and those of P G are not: 63 rows take 107 us so, 113 with both unrolled, 108 with neither.)
+        // The units of S are a loop and those of P G are not: 63 rows take 108 us so, 115 with both unrolled, 110 with neither.)
         if (rank == 0) {
+            // Unit u of a form, the lanes looking at all the form's units together: lane i at `full` in phase `parity`. Bits
+            // are the units known to be full; lane u + units and later ones look at a barrier before its time.
+            auto unit_full = [&](uint64_t* full, uint32_t parity, uint32_t u, uint32_t units, uint32_t& bits) -> bool {
+                uint64_t start = 0;
+                for (uint32_t tries = 1; !(bits >> u & 1); ++tries) {
+                    bits = __ballot_sync(0xFFFFFFFFu, mbar_try_wait(full, parity)) & 15 & ((1u << (u + units)) - 1);
+                    if (tries % 64 == 0) {
+                        const uint64_t now = __shfl_sync(0xFFFFFFFFu, global_timer_ns(), 0);
+                        if (start == 0) start = now;
+                        if (now - start > kWaitBudgetNs) {
+                            if (lane == 0) atomicOr(p.status, kStatusWaitTimeout);
+                            return false;
+                        }
+                    }
+                }
+                return true;
+            };
             uint32_t n_part = 0;
             bool ok = true;
             if (warp == 1) {
@@ -492,9 +509,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                         ok = i != 0 || wait_warp(&bar->q_full, n_part & 1, p.status);
                         ok = ok && wait_warp(&bar->s_free[it % kSBufs], (it / kSBufs & 1) ^ 1, p.status);
                         const uint32_t d = tmem + s_col(it);
+                        uint32_t full = 0;
 #pragma unroll 1
                         for (uint32_t u = 0; u < 4; ++u) {
-                            ok = ok && wait_warp(&bar->full[u], it & 1, p.status);
+                            ok = ok && unit_full(&bar->full[lane & 3], it & 1, u, kKUnits, full);
                             if (!ok) break;
                             tc_fence_after();
                             const uint64_t b_desc = smem_desc_sw128_kmajor(ring + u * kUnitBytes);
@@ -523,15 +541,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                         // A part begins O anew, once the part before has been read.
                         ok = ok && (i != 0 || n_part == 0 || wait_warp(&bar->o_read, (n_part - 1) & 1, p.status));
                         const uint64_t a_desc = smem_desc_sw128_kmajor(smem_u32(smem + L::p) + it % kPBufs<kFormat> * kPBytes);
-                        // The last tile's units lie in those of the K form, which it has done with. (P says so: before it is full,
-                        // a unit's barrier may still be a phase behind, with the parity that is waited for.)
+                        // The lane's unit of all. The last tile's lie in the units of the K form, which it has done with.
+                        const uint32_t mine = 4 * it + (lane & 3);
                         const bool in_k = kByTma<kFormat> && it + 1 == n;
+                        uint64_t* bars = &bar->full[in_k ? lane & 3 : kKUnits + mine % kV];
+                        const uint32_t parity = (in_k ? n : mine / kV) & 1;
+                        uint32_t full = 0;
 #pragma unroll
                         for (uint32_t v = 0; v < 4; ++v) {
-                            const uint32_t unit = 4 * it + v, slot = in_k ? v : kKUnits + unit % kV;
-                            ok = ok && wait_warp(&bar->full[slot], (in_k ? n : unit / kV) & 1, p.status);
+                            ok = ok && unit_full(bars, parity, v, in_k ? kKUnits : kV, full);
                             if (!ok) break;
                             tc_fence_after();
+                            const uint32_t slot = in_k ? v : kKUnits + (4 * it + v) % kV;
                             const uint64_t b_desc = smem_desc_sw128_mnmajor(ring + slot * kUnitBytes, 8192, 1024);
                             if (elect_one()) {
 #pragma unroll
