@@ -479,8 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
         }
     } else if (warp <= 2) {
         // ---- the MMAs, issued in the first CTA for both: warp 1 S = Q G^T, warp 2 O += P G. (One warp for both took
-        // 3,900 cycles a tile, twice the MMAs' time: waits of 100 to 200 cycles and 20 or so an MMA, one after another.
-        // The units of S are a loop and those of P G are not: 63 rows take 108 us so, 115 with both unrolled, 110 with neither.)
+        // 3,900 cycles a tile, twice the MMAs' time: waits of 100 to 200 cycles and 20 or so an MMA, one after another.)
         if (rank == 0) {
             // Unit u of a form, the lanes looking at all the form's units together: lane i at `full` in phase `parity`. Bits
             // are the units known to be full; lane u + units and later ones look at a barrier before its time.
@@ -510,7 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                         ok = ok && wait_warp(&bar->s_free[it % kSBufs], (it / kSBufs & 1) ^ 1, p.status);
                         const uint32_t d = tmem + s_col(it);
                         uint32_t full = 0;
-#pragma unroll 1
+#pragma unroll
                         for (uint32_t u = 0; u < 4; ++u) {
                             ok = ok && unit_full(&bar->full[lane & 3], it & 1, u, kKUnits, full);
                             if (!ok) break;
@@ -656,7 +655,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 // The weights, from S again: 64 logits and 64 weights at once are more registers than there are.
                 const float2 minus = make_float2(-m, -m);
                 float2 s2[2] = {};
-#pragma unroll 1
+#pragma unroll
                 for (uint32_t h = 0; h < 2; ++h) {
                     uint32_t v[32], w16[16];
                     tmem_ld_x32(s_cols + 32 * h, v);
