@@ -860,7 +860,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
 
     tc_fence_before();
     __syncthreads();
-    cluster_arrive_relaxed();  // neither CTA leaves while the other's MMAs or arrivals may reach it
+    // Neither CTA leaves while the other's MMAs or arrivals may reach it, for what lies there next would have them. The commits
+    // arrive in both CTAs by themselves, the last of each issuing warp's on `drained` (the first CTA has waited for its
+    // own). The threads' arrivals in the first CTA, the last ones of which nobody waits for, are performed before the
+    // release.
+    if (warp == 1) (void)wait_warp(&bar->drained, 0, p.status);
+    cluster_arrive_release();
     cluster_wait_acquire();
     if (warp == 1) {
         tc_fence_after();
