@@ -88,6 +88,9 @@ template <int kFormat>
 constexpr int kThreads = 32 * (kBuildWarp + kBuildWarps<kFormat>);
 constexpr uint32_t kOCol = 128;               // TMEM: two S of 64 columns, O, two more S
 constexpr uint32_t kSBufs = 4;
+// A set's warps meet once a tile, so a warp may write its largest logits of the set's next tile before another
+// has read those of this one, but not those of the one after.
+constexpr uint32_t kRedBufs = 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint16_t kBoth = 3;                 // the CTAs of a pair
 // The running maximum is raised only when a tile's exceeds it by more than this (in units of ln 2): the
@@ -105,8 +108,8 @@ struct Layout {
     static constexpr size_t q = ring + (size_t)(kKUnits + kVUnits<kFormat>) * kUnitBytes;
     static constexpr size_t p = q + kQBytes;
     static constexpr size_t place = p + kPBufs<kFormat> * (size_t)kPBytes;  // i32 [kPlaceBufs][128]
-    static constexpr size_t red = place + kPlaceBufs * kTile * 4;          // f32 [2][128]
-    static constexpr size_t maxima = red + 2 * 128 * 4;                    // f32 [2][128]
+    static constexpr size_t red = place + kPlaceBufs * kTile * 4;          // f32 [2][kRedBufs][128]
+    static constexpr size_t maxima = red + 2 * kRedBufs * 128 * 4;         // f32 [2][128]
     static constexpr size_t bars = maxima + 2 * 128 * 4;
 };
 
@@ -577,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
         const uint32_t set = (warp - kSoftmaxWarp) >> 2;
         const uint32_t row = (threadIdx.x - 32 * kSoftmaxWarp) & 127, head = row & 63, half = row >> 6;
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        float* red = reinterpret_cast<float*>(smem + L::red) + 128 * set;
+        float* red_s = reinterpret_cast<float*>(smem + L::red) + 128 * kRedBufs * set;
         float* m_s = reinterpret_cast<float*>(smem + L::maxima);  // [2][128]
         const uint32_t p_row = smem_u32(smem + L::p) + set % kPBufs<kFormat> * kPBytes + half * 8192;
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
@@ -629,6 +632,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                     top = fmaxf(top, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
                 }
                 if (!(odd.x + odd.y == 0.0f)) bad = 1;
+                float* red = red_s + 128 * (it / 2 % kRedBufs);
                 red[row] = top;
                 sync_softmax(set);
                 ++met;

@@ -40,7 +40,8 @@ def constants():
     end = SOURCE[:SOURCE.index("tcgen05.dealloc")]
     end = end[end.rindex("__syncthreads();"):]
     return dict(k_units=number("kKUnits"), v_units=by_form("kVUnits"), p_bufs=by_form("kPBufs"), s_bufs=number("kSBufs"),
-                place_bufs=number("kPlaceBufs"), release="cluster_arrive_release();" in end, both_drained="bar->drained" in end)
+                place_bufs=number("kPlaceBufs"), red_bufs=number("kRedBufs") if "kRedBufs =" in SOURCE else 1,
+                release="cluster_arrive_release();" in end, both_drained="bar->drained" in end)
 
 
 class Bar:
@@ -100,6 +101,7 @@ class Cta:
         self.p = [{} for _ in range(w.p_bufs)]
         self.s = [None] * w.s_bufs
         self.maxima = [{} for _ in range(2)]
+        self.red = [[{} for _ in range(w.red_bufs)] for _ in range(2)]
 
 
 class World:
@@ -313,9 +315,12 @@ class World:
             self.remote(c, first.o_read)
 
     def exchange(self, c, sm, w, it):
-        """The two threads of a head take the larger maximum."""
+        """The two threads of a head, in warps w and w ^ 2, take the larger maximum."""
+        red = c.red[sm][it // 2 % self.red_bufs]
+        red[w] = it
         c.met[sm].arrive()
         yield c.met[sm], it >> 1
+        check(red[w ^ 2] == it, f"the other half's largest logit is tile {red[w ^ 2]}'s, not {it}'s")
 
     @property
     def steps(self):
@@ -469,6 +474,12 @@ def test_every_order_of_the_roles_is_sound(tma):
 def test_an_exit_that_leaves_arrivals_behind_is_found(changed):
     with pytest.raises(Fault, match="has left"):
         many(True, 400, 2, **{**dict(release=True, both_drained=True), **changed})
+
+
+@pytest.mark.parametrize("tma", [True, False])
+def test_one_copy_of_the_largest_logits_is_overwritten(tma):
+    with pytest.raises(Fault, match="other half"):
+        many(tma, 400, 4, red_bufs=1)
 
 
 @pytest.mark.parametrize("wait", ["place_full", "place_free", "empty", "q_full", "q_free", "s_full", "p_full", "pv_done", "m_ready",
