@@ -288,7 +288,7 @@ def ds_rows_append(cache: PagedCache, x: torch.Tensor, seq: torch.Tensor, slot: 
     if x.dim() != 2 or x.shape[1] != cache.dim:
         raise ValueError(f"x must be [tokens, {cache.dim}], got {tuple(x.shape)}")
     row, element = x.stride()
-    if element != 1:
+    if element != 1 and x.shape[0]:  # no tokens: any strides (numpy's are 0)
         raise ValueError("the elements of a row of x must be contiguous")
     code = _code(_DTYPES, x.dtype, "the type of x")
     n = x.shape[0]
@@ -315,7 +315,7 @@ def ds_rows_fetch(cache: PagedCache, seq: torch.Tensor, slot: torch.Tensor, out:
     if out.dim() != 2 or out.shape[1] != cache.dim:
         raise ValueError(f"out must be [tokens, {cache.dim}], got {tuple(out.shape)}")
     row, element = out.stride()
-    if element != 1:
+    if element != 1 and out.shape[0]:
         raise ValueError("the elements of a row of out must be contiguous")
     code = _code(_DTYPES, out.dtype, "the type of out")
     n = out.shape[0]
