@@ -583,11 +583,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
         float* red_s = reinterpret_cast<float*>(smem + L::red) + 128 * kRedBufs * set;
         float* m_s = reinterpret_cast<float*>(smem + L::maxima);  // [2][128]
         const uint32_t p_row = smem_u32(smem + L::p) + set % kPBufs<kFormat> * kPBytes + half * 8192;
-        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+        const float scale = p.scale_log2;
+        const float2 scale2 = make_float2(scale, scale);
         uint32_t met = 0;  // a set's warps meet once a tile
         bool ok = true;
         for (Walk w = all; ok && w.next(part);) {
-            float m = -INFINITY, sum = 0.0f;  // the maximum that the sum refers to
+            float m = -INFINITY, sum = 0.0f;  // the maximum that the sum refers to, before the scale
             uint32_t bad = 0;
             const uint32_t begin = it;
             for (const uint32_t stop = it + part.tiles; it < stop; ++it) {
@@ -599,7 +600,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 if (!(ok = wait_warp(&bar->s_full[sbuf], it / kSBufs & 1, p.status))) break;
                 tc_fence_after();
                 const ::int4* at = reinterpret_cast<const ::int4*>(place_s + pbuf * kTile + half * 64);
-                // The largest logit. 0 * t is NaN exactly where one is not finite.
+                // The largest S (the scale is positive). 0 * S * scale is NaN exactly where a logit is not finite.
                 float top = -INFINITY;
                 float2 odd = make_float2(0.0f, 0.0f);
 #pragma unroll 1
@@ -610,8 +611,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                     float2 t[16];
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        t[c] = mul2(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), scale2);
-                        odd = fma2(t[c], make_float2(0.0f, 0.0f), odd);
+                        t[c] = make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
+                        odd = fma2(mul2(t[c], scale2), make_float2(0.0f, 0.0f), odd);
                     }
                     if (masked) {
 #pragma unroll
@@ -645,18 +646,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 } else {
                     const float before = m_s[128 * (set ^ 1) + row];
                     float now = before;
-                    if (top > before + kSlack && finite_f(top)) {
+                    if ((top - before) * scale > kSlack && finite_f(top)) {
                         now = top;
-                        f = exp2_fast(before - now);
+                        f = exp2_fast((before - now) * scale);
                     }
-                    if (now != m) sum *= exp2_fast(m - now);  // the set's sum, of its own tiles
+                    if (now != m) sum *= exp2_fast((m - now) * scale);  // the set's sum, of its own tiles
                     m = now;
                 }
                 m_s[128 * set + row] = m;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->m_ready[set]);
                 const bool moved = __any_sync(0xFFFFFFFFu, f != 1.0f);
-                // The weights, from S again: 64 logits and 64 weights at once are more registers than there are.
+                // The weights, from S again: 64 logits and 64 weights at once are more registers than there are. S less the
+                // maximum, then scaled: a product with the scale less a rounded maximum would be off by up to half a
+                // step of the maximum, which is past any weight for logits from 2^31 on.
                 const float2 minus = make_float2(-m, -m);
                 float2 s2[2] = {};
 #pragma unroll
@@ -666,8 +669,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        const float2 x = fma2(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), scale2,
-                                              minus);
+                        const float2 x =
+                            mul2(add2(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), minus), scale2);
                         float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
                         if (masked) {
                             const int2 a = reinterpret_cast<const int2*>(at)[16 * h + c];
@@ -726,10 +729,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
             if ((last & 1) != set) {
                 if (!(ok = wait_warp(&bar->m_ready[set ^ 1], last >> 1 & 1, p.status))) break;
                 const float now = m_s[128 * (set ^ 1) + row];
-                if (now != m) sum *= exp2_fast(m - now);
+                if (now != m) sum *= exp2_fast((m - now) * scale);
             }
             if (mine) out[kHeads + 4 * head + 2 * set + half] = bad ? __int_as_float(0x7FC00000) : sum;  // a flag is NaN
-            if (mine && half == 0 && (last & 1) == set) out[head] = m;
+            if (mine && half == 0 && (last & 1) == set) out[head] = m * scale;
             // The set that did not have the last tile waits for its own first, so that the other barrier is in that phase.
             if (kPBufs<kFormat> == 2 && (last & 1) != set && last > 0 &&
                 !(ok = wait_warp(&bar->pv_done[set], (last - 1) >> 1 & 1, p.status)))
