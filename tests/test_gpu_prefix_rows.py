@@ -1,4 +1,6 @@
-"""ds_rows_prefix_attn on rows made to show one thing each: that logits of any finite size are sound."""
+"""ds_rows_prefix_attn on rows made to show one thing each: that every slot is counted once, that what was
+accumulated is scaled when the maximum rises within a pair's run, and that logits of any finite size are sound.
+"""
 
 import numpy as np
 import pytest
@@ -7,9 +9,12 @@ import torch
 import deepseek_sparse_attention_ragged_gb300 as ds
 from test_gpu_fp8 import FORMATS
 from test_gpu_paged import BF16, SCALE, f64, i32
-from test_gpu_prefix import table
+from test_gpu_prefix import check, table
 
 pytestmark = pytest.mark.gpu
+
+PAIRS = 76  # of the chip's processors: with more tiles than these a pair has a run of several
+
 
 @pytest.fixture(scope="module", autouse=True)
 def _lib():
@@ -54,6 +59,68 @@ def attend(cache, prefix, tails, q, sinks, fmt):
         got.append((out, bad))
     assert torch.equal(got[0][0].view(torch.int16), got[-1][0].view(torch.int16)) and torch.equal(got[0][1], got[-1][1])
     return got[0]
+
+
+def tiles(prefix, tails):
+    up = lambda n: -(-n // 128)  # noqa: E731
+    return -(-len(tails) // 2) * up(prefix) + sum(map(up, tails))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("prefix,tails", [
+    (20000, [0]), (20009, [1]), (30000, [0, 7]), (20000, [5, 0, 9]), (10299, [0]), (0, [9000, 1, 20000]),
+    (130, [300 + i for i in range(64)]), (9999, [300] * 5), (3001, [1 + 7 * i for i in range(63)]), (6000, [1] * 8), (300, [1, 40]),
+    (0, [1000, 8192, 3000, 5001, 1, 129, 127, 128]), (40000, [0] * 2), (12800, [128] * 7),
+])
+def test_every_slot_counts_once(fmt, page, prefix, tails):
+    """With q = 0 every weight is 1. A row is 7 (exact in every type) at the dim of its tile, so an output is
+    7 count / (slots + 1): whole numbers in fp32, one reciprocal and one product (2^-24 each, and half as much again
+    for the reciprocal's use), rounded to bf16 (2^-8). A slot more or less in a tile of 128 changes it by 2^-7."""
+    rng = np.random.default_rng(prefix + page)
+
+    def marked(n, first):
+        x = np.zeros((n, 512), np.float32)
+        x[np.arange(n), (first + np.arange(n) // 128) % 512] = 7.0
+        return x
+    cache, held = cache_of(rng, marked(prefix, 0), [marked(n, 200 + 3 * e) for e, n in enumerate(tails)], fmt, page)
+    n = len(tails)
+    out, bad = attend(cache, prefix, tails, torch.zeros(n, 64, 512, dtype=BF16, device="cuda"),
+                      torch.zeros(64, device="cuda"), fmt)
+    assert not bad.any()
+    for e in range(n):
+        assert set(held[e].unique().tolist()) <= {0.0, 7.0}
+        want = held[e].double().sum(0) / (len(held[e]) + 1)
+        assert ((out[e].double() - want).abs() <= want * (2.0 ** -8 + 2.0 ** -22)).all(), f"row {e}"
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("prefix,tails", [(40000, [0]), (0, [9000, 12000, 30000]), (20000, [300] * 5), (31000, [0, 9]),
+                                          (4000, [1500] * 9), (0, [38000])])
+def test_the_maximum_rises_within_a_run(fmt, prefix, tails):
+    """Slots of nearly equal logits, and in a tile here and there one that stands 9.5 ln 2 (later 19 ln 2) above all before:
+    it weighs as much as some hundred of the others, so both what was accumulated and what comes count."""
+    assert tiles(prefix, tails) > 3 * PAIRS
+    rng = np.random.default_rng(prefix + len(tails))
+
+    def spiked(n, first):
+        x = rng.standard_normal((n, 512)).astype(np.float32)
+        x[:, :16] = 0  # the spikes' dims, a group of the 4-bit type
+        t = first + np.arange(n // 128)
+        at = 128 * np.arange(n // 128)
+        at += rng.integers(0, 128, len(at))
+        x[at, t % 8] = np.where(t % 16 < 8, 1.0, 2.0)
+        return x
+    cache, held = cache_of(rng, spiked(prefix, 0), [spiked(n, 5 * e) for e, n in enumerate(tails)], fmt, 64)
+    n = len(tails)
+    # Heads 8 k + d see the spikes of dim d; the others' dims add little.
+    q = torch.zeros(n, 64, 512)
+    q[:, torch.arange(64), torch.arange(64) % 8] = 9.5 / (SCALE * 1.4427)
+    q[:, :, 16:] = 0.02 * torch.randn(n, 64, 496, generator=torch.Generator().manual_seed(1))
+    q = q.to(BF16).cuda()
+    out, bad = attend(cache, prefix, tails, q, torch.zeros(64, device="cuda"), fmt)
+    assert not bad.any()
+    check(out, q, held, torch.zeros(64, device="cuda"))
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
