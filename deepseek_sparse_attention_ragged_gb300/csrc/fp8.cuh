@@ -47,8 +47,8 @@ __device__ __forceinline__ uint32_t exponent_byte(uint32_t top) {
     return (uint32_t)min(max(b, (int)kMinByte), (int)kMaxByte);
 }
 
-// 16 values of a block to 4 words: v = y 2^-e to the nearest e4m3 (ties to even, saturating).
-// The product is exact: it can only lose bits far below e4m3's smallest step.
+// 16 values of a block to 4 words: v = y 2^-e to the nearest e4m3 (ties to even, saturating); zeros in a block
+// that is stored as NaN. The product is exact: it can only lose bits far below e4m3's smallest step.
 __device__ __forceinline__ void quantise(const float (&y)[16], uint32_t byte, uint32_t (&word)[4]) {
     const float down = __uint_as_float((254u - (byte == kNanByte ? 127u : byte)) << 23);  // 2^-e
 #pragma unroll
@@ -57,7 +57,7 @@ __device__ __forceinline__ void quantise(const float (&y)[16], uint32_t byte, ui
                                                      __NV_E4M3);
         const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i + 2] * down, y[4 * i + 3] * down),
                                                      __NV_SATFINITE, __NV_E4M3);
-        word[i] = lo | hi << 16;
+        word[i] = byte == kNanByte ? 0u : lo | hi << 16;
     }
 }
 

@@ -523,7 +523,8 @@ size_t ds_rows_page_bytes(uint32_t page_size, uint32_t dim, int format);
  * (s = 0: n = 0); a group with a non-finite value is stored as NaN. n s is exact
  * in bf16 and in fp16. DS_CACHE_FP8, per block of 128 values y: e = the least of -100 .. 7
  * with max|y| <= 448 2^e (7 if there is none), v = y 2^-e to the nearest e4m3 (even on
- * ties, saturating at 448); a block with a non-finite value is stored as NaN.
+ * ties, saturating at 448); a block with a non-finite value is stored as NaN (exponent byte 255, its values
+ * zeros).
  */
 int ds_rows_append(const ds_paged_cache_t* cache, const void* x, uint64_t x_stride, int dtype, uint64_t tokens,
                    const int32_t* seq, const int32_t* slot, const ds_rope_t* rope, const int32_t* positions,

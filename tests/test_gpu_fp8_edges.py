@@ -7,8 +7,9 @@ import pytest
 import torch
 
 import deepseek_sparse_attention_ragged_gb300 as ds
-from test_gpu_fp8 import FORMATS, make_cache
-from test_gpu_paged import i32
+from oracle import paged as ref
+from test_gpu_fp8 import FORMATS, edge_blocks, make_cache
+from test_gpu_paged import TYPES, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +39,25 @@ def test_no_tokens_of_any_strides(fmt, dim):
                      lambda: ds.ds_rows_fetch(cache, i32([0] * 3), i32([0, 1, 2]), wrong)):
             with pytest.raises(ValueError, match="contiguous"):
                 call()
+
+
+@pytest.mark.parametrize("dim", [128, 512])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_block_stored_as_nan_holds_zeros(dim, dtype):
+    """Every byte that an append writes is the oracle's; e4m3's codes for NaN are not among them."""
+    rng = np.random.default_rng(dim)
+    n = 300
+    cache, _ = make_cache(rng, [n], dim, "fp8", 32)
+    y = edge_blocks(rng, n, dim)
+    for k, bad in enumerate((np.nan, -np.nan, np.inf, -np.inf) * 8):
+        y[k, rng.integers(0, dim)] = bad
+    y = torch.from_numpy(y).to(dtype)
+    ds.ds_rows_append(cache, y.cuda(), i32(np.zeros(n)), i32(np.arange(n)))
+    byte, ex = ref.fp8_quantise(y.float().numpy())
+    assert (ex == 255).any(1).sum() >= 32
+    pool = cache.pages.cpu().numpy().reshape(cache.num_pages, -1)[cache.page_table.cpu().numpy()[0, np.arange(n) // 32]]
+    v, sc = ref.fp8_places(dim, 32)
+    rows, at = np.arange(n)[:, None], np.arange(n) % 32
+    np.testing.assert_array_equal(pool[rows, v[at]], byte)
+    np.testing.assert_array_equal(pool[rows, sc[at]], ex)
+    assert not np.isin(pool[rows, v[at]], (0x7F, 0xFF)).any()
