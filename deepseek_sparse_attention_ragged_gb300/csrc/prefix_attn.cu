@@ -97,6 +97,12 @@ constexpr uint16_t kBoth = 3;                 // the CTAs of a pair
 // accumulated output is then scaled, and the weights stay below 2^8.
 constexpr float kSlack = 8.0f;
 
+// Tiles whose weights' products with the rows are summed in TMEM, at most: a longer run is folded into its part in the
+// workspace piece by piece. The tensor cores cut a product off at 2^-25 of the sum that it is added to (seen where a run of
+// ones stopped at 2^26), so the 16 of a step take up to 2^-21 of the sum and the 4096 steps of a piece 2^-9 of it, if all cuts
+// were largest; and no wait for a piece lasts for seconds. A piece costs about 6 us, beside some 660 of its tiles.
+constexpr uint32_t kPieceTiles = 512;
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kNoRow = -1, kBadRow = -2;
 constexpr uint32_t kMasked = 1;     // some slot of the tile has no row
@@ -324,23 +330,24 @@ __device__ __forceinline__ uint32_t s_col(uint32_t it) { return (it & 1) * 64 + 
 
 // ---- the pair's tiles --------------------------------------------------------------------------
 
-// A run of a pair's tiles within one segment.
+// A run of a pair's tiles within one segment, or a piece of it.
 struct Part {
     uint32_t seg;
     uint32_t start;   // its first tile's first slot
     uint32_t end;     // the segment's last slot + 1
     uint32_t tiles;
+    bool more;        // a piece behind the run's first
 };
 
-// The parts of pair k in order: for (Walk w(p, k); w.next(part);). What is dealt out in equal runs
+// The parts of pair k in order, by pieces: for (Walk w(p, k); w.next(part);). What is dealt out in equal runs
 // (pair k's begins at floor(line k / pairs)) is a line on which a segment's tiles follow p.seg_cost units for its set-up.
 struct Walk {
     const PrefixParams& p;
-    uint32_t t, end, seg;
+    uint32_t t, end, seg, had;  // had: the last part's segment + 1
     __device__ __forceinline__ Walk(const PrefixParams& params, uint32_t pair) : p(params) {
         t = p.run * pair + p.rest * pair / p.pairs;
         end = p.run * (pair + 1) + p.rest * (pair + 1) / p.pairs;
-        seg = 0;
+        seg = had = 0;
         while (t < end && p.begin[seg + 1] <= t) ++seg;
     }
     __device__ __forceinline__ bool next(Part& part) {
@@ -353,8 +360,10 @@ struct Walk {
                 part.seg = seg;
                 part.start = (shared ? 0u : p.prefix_len) + (t - first) * kTile;
                 part.end = shared ? p.prefix_len : p.kv_len[seg - p.groups];
-                part.tiles = stop - t;
-                t = stop;
+                part.tiles = min(stop - t, kPieceTiles);
+                part.more = had == seg + 1;
+                had = seg + 1;
+                t += part.tiles;
                 return true;
             }
             t = max(t, stop);
@@ -586,6 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
         const float scale = p.scale_log2;
         const float2 scale2 = make_float2(scale, scale);
         uint32_t met = 0;  // a set's warps meet once a tile
+        float m_run = 0.0f;  // the maximum that the run's pieces so far refer to
         bool ok = true;
         for (Walk w = all; ok && w.next(part);) {
             float m = -INFINITY, sum = 0.0f;  // the maximum that the sum refers to, before the scale
@@ -730,9 +740,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 if (!(ok = wait_warp(&bar->m_ready[set ^ 1], last >> 1 & 1, p.status))) break;
                 const float now = m_s[128 * (set ^ 1) + row];
                 if (now != m) sum *= exp2_fast((m - now) * scale);
+                m = now;
             }
-            if (mine) out[kHeads + 4 * head + 2 * set + half] = bad ? __int_as_float(0x7FC00000) : sum;  // a flag is NaN
-            if (mine && half == 0 && (last & 1) == set) out[head] = m * scale;
+            // What the run's pieces before left here and this one, by a common maximum. (A thread reads only what it wrote.)
+            const float top = part.more ? fmaxf(m_run, m) : m;
+            const float f_run = part.more ? exp2_fast((m_run - top) * scale) : 0.0f, f = exp2_fast((m - top) * scale);
+            m_run = top;
+            if (mine) {
+                float* to_sum = out + kHeads + 4 * head + 2 * set + half;
+                if (bad) sum = __int_as_float(0x7FC00000);  // a flag is NaN
+                *to_sum = part.more ? fmaf(*to_sum, f_run, sum * f) : sum;
+                if (half == 0 && (last & 1) == set) out[head] = m_run * scale;
+            }
             // The set that did not have the last tile waits for its own first, so that the other barrier is in that phase.
             if (kPBufs<kFormat> == 2 && (last & 1) != set && last > 0 &&
                 !(ok = wait_warp(&bar->pv_done[set], (last - 1) >> 1 & 1, p.status)))
@@ -745,11 +764,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 uint32_t o[32];
                 tmem_ld_x32(lanes + kOCol + 128 * set + c, o);
                 tmem_ld_wait();
-                if (mine)
+                if (mine) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        to[(c / 4 + k) * 128] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                            __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                    for (int k = 0; k < 8; ++k) {
+                        float4 v = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                               __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                        float4* at = to + (c / 4 + k) * 128;
+                        if (part.more) {
+                            const float4 was = *at;
+                            v = make_float4(fmaf(was.x, f_run, v.x * f), fmaf(was.y, f_run, v.y * f),
+                                            fmaf(was.z, f_run, v.z * f), fmaf(was.w, f_run, v.w * f));
+                        }
+                        *at = v;
+                    }
+                }
             }
             tc_fence_before();
             __syncwarp();

@@ -45,7 +45,7 @@ def cache_of(rng, shared, own, fmt, page):
         ds.ds_rows_append(cache, x, torch.full_like(slot, entry), slot, values=held)
         return held.float()
     head = put(shared, 0, 0)
-    return cache, [torch.cat([head, put(x, e, prefix)]) for e, x in enumerate(own)]
+    return cache, [torch.cat([head, put(x, e, prefix)]) if len(x) else head for e, x in enumerate(own)]
 
 
 def attend(cache, prefix, tails, q, sinks, fmt):
@@ -94,6 +94,25 @@ def test_every_slot_counts_once(fmt, page, prefix, tails):
         assert ((out[e].double() - want).abs() <= want * (2.0 ** -8 + 2.0 ** -22)).all(), f"row {e}"
 
 
+def spiked(rng, n, first):
+    """Rows of a run whose first tile is number `first`: a slot of each tile stands out in dim (tile mod 8)."""
+    x = rng.standard_normal((n, 512)).astype(np.float32)
+    x[:, :16] = 0  # the spikes' dims, a group of the 4-bit type
+    t = first + np.arange(n // 128)
+    at = 128 * np.arange(n // 128)
+    at += rng.integers(0, 128, len(at))
+    x[at, t % 8] = np.where(t % 16 < 8, 1.0, 2.0)
+    return x
+
+
+def spiked_queries(n):
+    """Heads 8 k + d see the spikes of dim d; the others' dims add little."""
+    q = torch.zeros(n, 64, 512)
+    q[:, torch.arange(64), torch.arange(64) % 8] = 9.5 / (SCALE * 1.4427)
+    q[:, :, 16:] = 0.02 * torch.randn(n, 64, 496, generator=torch.Generator().manual_seed(1))
+    return q.to(BF16).cuda()
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("prefix,tails", [(40000, [0]), (0, [9000, 12000, 30000]), (20000, [300] * 5), (31000, [0, 9]),
                                           (4000, [1500] * 9), (0, [38000])])
@@ -103,21 +122,9 @@ def test_the_maximum_rises_within_a_run(fmt, prefix, tails):
     assert tiles(prefix, tails) > 3 * PAIRS
     rng = np.random.default_rng(prefix + len(tails))
 
-    def spiked(n, first):
-        x = rng.standard_normal((n, 512)).astype(np.float32)
-        x[:, :16] = 0  # the spikes' dims, a group of the 4-bit type
-        t = first + np.arange(n // 128)
-        at = 128 * np.arange(n // 128)
-        at += rng.integers(0, 128, len(at))
-        x[at, t % 8] = np.where(t % 16 < 8, 1.0, 2.0)
-        return x
-    cache, held = cache_of(rng, spiked(prefix, 0), [spiked(n, 5 * e) for e, n in enumerate(tails)], fmt, 64)
+    cache, held = cache_of(rng, spiked(rng, prefix, 0), [spiked(rng, n, 5 * e) for e, n in enumerate(tails)], fmt, 64)
     n = len(tails)
-    # Heads 8 k + d see the spikes of dim d; the others' dims add little.
-    q = torch.zeros(n, 64, 512)
-    q[:, torch.arange(64), torch.arange(64) % 8] = 9.5 / (SCALE * 1.4427)
-    q[:, :, 16:] = 0.02 * torch.randn(n, 64, 496, generator=torch.Generator().manual_seed(1))
-    q = q.to(BF16).cuda()
+    q = spiked_queries(n)
     out, bad = attend(cache, prefix, tails, q, torch.zeros(64, device="cuda"), fmt)
     assert not bad.any()
     check(out, q, held, torch.zeros(64, device="cuda"))
@@ -152,3 +159,48 @@ def test_logits_of_any_finite_size(fmt, prefix, tails):
         for heads, at in ((slice(0, 32), first.argmax()), (slice(32, 64), first.argmin())):
             assert (first == first[at]).sum() == 1 and first[at].abs() > 1
             assert torch.equal(out[e, heads], held[e][at].to(BF16).expand(32, 512)), f"row {e}"
+
+
+def test_a_call_of_several_seconds():
+    """26 rows over 2^31 - 1 slots of the same four pages: a pair of processors works for seconds on a run of 2.9 million
+    tiles. No wait gives up, and the sums come out: with weights and rows of ones they are whole numbers, and those of a
+    piece of 512 tiles, 2^16, and of the pieces, multiples of it below 2^40, are exact in 32 bits."""
+    slots, page, n = (1 << 31) - 1, 256, 26
+    places = -(-slots // page)
+    assert tiles(slots, [0] * n) > 2800000 * PAIRS
+    table_ = torch.arange(places, dtype=torch.int32, device="cuda").remainder_(4).expand(n, places).contiguous()
+    cache = ds.PagedCache(torch.ones(4, page, 512, dtype=BF16, device="cuda"), table_, page, 512, "bf16")
+    rows = table(slots, [0] * n)
+    ws = ds.prefix_attn_workspace(rows, slots, "bf16")
+    out, bad = torch.zeros(n, 64, 512, dtype=BF16, device="cuda"), torch.full((n, 64), 9, dtype=torch.int32, device="cuda")
+    ds.ds_rows_prefix_attn(rows, slots, torch.zeros_like(out), torch.zeros(64, device="cuda"), 0, SCALE, out, cache,
+                           invalid=bad, workspace_t=ws)
+    assert ds.workspace_status(ws) == 0
+    assert not bad.any() and (out == 1).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_runs_of_several_pieces(fmt):
+    """64 rows over 170003 shared slots: a pair's run is longer than the 512 tiles of a piece. Once with marked rows and
+    weights of 1 (a slot more or less in a tile's dim, whose three tiles count 384, changes an output by 2^-8.6: the bound
+    shows a tile, 2^-1.6), once with maxima that rise."""
+    prefix, tails = 170003, [0] * 62 + [1, 300]
+    assert tiles(prefix, tails) > 520 * PAIRS
+    rng = np.random.default_rng(5)
+    n, sinks = len(tails), torch.zeros(64, device="cuda")
+    x = np.zeros((prefix, 512), np.float32)
+    x[np.arange(prefix), np.arange(prefix) // 128 % 512] = 7.0
+    own = [np.zeros((t, 512), np.float32) for t in tails]
+    own[-1][:, 5] = 7.0
+    cache, held = cache_of(rng, x, own, fmt, 128)
+    out, bad = attend(cache, prefix, tails, torch.zeros(n, 64, 512, dtype=BF16, device="cuda"), sinks, fmt)
+    assert not bad.any()
+    for e in range(n):
+        want = held[e].double().sum(0) / (len(held[e]) + 1)
+        assert ((out[e].double() - want).abs() <= want * (2.0 ** -8 + 2.0 ** -22)).all(), f"row {e}"
+    del cache, held
+    cache, held = cache_of(rng, spiked(rng, prefix, 0), [rng.standard_normal((t, 512)) for t in tails], fmt, 64)
+    q = spiked_queries(n)
+    out, bad = attend(cache, prefix, tails, q, sinks, fmt)
+    assert not bad.any()
+    check(out, q, held, sinks)
