@@ -29,13 +29,13 @@
 // Rows past a segment's end and rows without a page are zeros with probability 0.
 //
 // In a captured graph, all launches of a call (the time that its operations or its bytes alone would take):
-//   3 rows, 300 shared and up to 40 more, bf16 pages           11.1 us (0.1)
+//   3 rows, 300 shared and up to 40 more, bf16 pages           11.2 us (0.1)
 //   1 row of 131073, bf16                                      37.1 us (19.9, bytes)
-//   8 rows, 65536 shared and up to 999 more, bf16              52.4 us (36.3, operations)
-//   5 rows, 40007 shared and up to 1000 more, 4 bits           37.8 us (13.9, operations)
-//   63 rows, 20001 shared and up to 311 more, 8 bits           115 us (87.5, operations)
-// A tile takes a pair 1.3 us on bf16 rows (its MMAs 1.0): the tensor cores are busy for 69% of the attention kernel at
-// eight rows and 76% at 63. No unit is full; a ring unit's way round (commit, wait, 16 KB by TMA, wait, MMAs) takes about
+//   8 rows, 65536 shared and up to 999 more, bf16              54.0 us (36.3, operations)
+//   5 rows, 40007 shared and up to 1000 more, 4 bits           39.3 us (13.9, operations)
+//   63 rows, 20001 shared and up to 311 more, 8 bits           117 us (87.5, operations)
+// A tile takes a pair 1.3 us on bf16 rows (its MMAs 1.0): the tensor cores are busy for 65% of the attention kernel at
+// eight rows and 75% at 63. No unit is full; a ring unit's way round (commit, wait, 16 KB by TMA, wait, MMAs) takes about
 // 2,000 cycles and the rings hold seven eighths of a tile, which is what shared memory has room for. Taken out one by
 // one, at 63 rows (then 119 us): the loads 109, seven of eight S MMAs 112, half of P . G 115, a quarter of the bytes 117,
 // the exponentials 119; 8 KB units 143, one P buffer 153, three K and four V units 128. The rest is fixed: some 10 us of
@@ -100,7 +100,8 @@ constexpr float kSlack = 8.0f;
 // Tiles whose weights' products with the rows are summed in TMEM, at most: a longer run is folded into its part in the
 // workspace piece by piece. The tensor cores cut a product off at 2^-25 of the sum that it is added to (seen where a run of
 // ones stopped at 2^26), so the 16 of a step take up to 2^-21 of the sum and the 4096 steps of a piece 2^-9 of it, if all cuts
-// were largest; and no wait for a piece lasts for seconds. A piece costs about 6 us, beside some 660 of its tiles.
+// were largest; and no wait for a piece lasts for seconds. A piece costs less than 10 us, beside some
+// 900 of its tiles (64 rows over 155000 bf16 rows).
 constexpr uint32_t kPieceTiles = 512;
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -669,7 +670,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kFormat>, 1
                 const bool moved = __any_sync(0xFFFFFFFFu, f != 1.0f);
                 // The weights, from S again: 64 logits and 64 weights at once are more registers than there are. S less the
                 // maximum, then scaled: a product with the scale less a rounded maximum would be off by up to half a
-                // step of the maximum, which is past any weight for logits from 2^31 on.
+                // step of the maximum, which is past any weight for logits from 2^31 on. The product with the rows takes them
+                // rounded to bf16, 2^-8 of a weight at most (the sums are of the weights themselves): against 64 bits the
+                // output is off by 2.0e-3 (2-norm) where a row has some hundred slots and by 1.7e-3 where it has many,
+                // 1.7e-3 of both being its own rounding. Their low parts would be as many MMAs again.
                 const float2 minus = make_float2(-m, -m);
                 float2 s2[2] = {};
 #pragma unroll

@@ -578,7 +578,8 @@ int ds_rows_sparse_attn_paged(int rows, const ds_row_t* table, const ds_paged_ca
  * arguments are invalid (see ds_rows_last_error). 256-byte aligned, scratch between calls.
  * For DS_CACHE_FP8 and DS_CACHE_INT4 it holds the attended rows as bf16 (1 KB each) where
  * enough entries share them to widen them once beforehand; with DS_CACHE_BF16's
- * bytes the call works as well, and widens them as they are used. */
+ * bytes the call works as well, and widens them as they are used. DS_CACHE_BF16's are below 46 MB for any call;
+ * the others' are at most 128 KB more for each 128 rows, begun ones too, of the prefix and of each entry's own. */
 size_t ds_rows_prefix_attn_workspace_bytes(int rows, const ds_row_t* table, uint32_t prefix_len, int format);
 
 /*
@@ -605,7 +606,8 @@ size_t ds_rows_prefix_attn_workspace_bytes(int rows, const ds_row_t* table, uint
  * of every entry). A head is zeroed where a q element, the sink, an element of one of
  * the entry's rows or a logit (in units of ln 2) is not finite. Memory behind kv_len, and rows of
  * an entry's own pages before prefix_len, are not read. Weights exp(l_j - m) are rounded to bf16 for
- * the product with g_j; maxima, sums and outputs are kept in 32 bits. How the slots are split over the GPU
+ * the product with g_j; maxima, sums and outputs are kept in 32 bits (by the tensor cores for at most 65536 slots at a
+ * time). An element whose sum, with weights of up to 2^8, passes 32 bits is zero. How the slots are split over the GPU
  * depends on the whole call, and with it the last bits of a row: the same call gives the same bits, a
  * call with other rows beside it may not. Status bits as DS_STATUS_* in the workspace's
  * first word; after a wait that gave up every head of the call is zeros.
