@@ -599,7 +599,7 @@ size_t ds_rows_prefix_attn_workspace_bytes(int rows, const ds_row_t* table, uint
  *               inside a page: behind it each entry reads its own page.
  *   kv          dim 512, any format, with at least `rows` entries that reach kv_len
  *   q_attn      bf16 [Q, 64, 512], 16-B aligned; sinks, sinks_row_stride, scale, out and invalid
- *               as for ds_rows_sparse_attn (sinks and invalid 4-B aligned)
+ *               as for ds_rows_sparse_attn (sinks and invalid 4-B aligned); out may be q_attn
  *   workspace   at least ds_rows_prefix_attn_workspace_bytes(..., DS_CACHE_BF16) bytes, 256-byte
  *               aligned
  * A page id out of range under one of an entry's rows zeroes every head of it (under the prefix:

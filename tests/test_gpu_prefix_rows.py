@@ -204,3 +204,36 @@ def test_runs_of_several_pieces(fmt):
     out, bad = attend(cache, prefix, tails, q, sinks, fmt)
     assert not bad.any()
     check(out, q, held, sinks)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_in_place_and_captured_without_a_workspace(fmt):
+    """The output over the queries gives the same bits; so do replays of a capture that takes its workspace from the
+    graph's memory, between other captured work."""
+    rng = np.random.default_rng(6)
+    prefix, tails = 9000, [3, 700, 0, 1, 64]
+    make = lambda n: rng.standard_normal((n, 512)).astype(np.float32)  # noqa: E731
+    cache, held = cache_of(rng, make(prefix), [make(n) for n in tails], fmt, 64)
+    n, sinks = len(tails), torch.randn(64, device="cuda")
+    q = torch.randn(n, 64, 512, device="cuda").to(BF16)
+    want, _ = attend(cache, prefix, tails, q, sinks, fmt)
+    check(want, q, held, sinks)
+    rows = table(prefix, tails)
+    both = q.clone()
+    ds.ds_rows_prefix_attn(rows, prefix, both, sinks, 0, SCALE, both, cache)
+    assert torch.equal(both, want)
+    out, kept, graph = torch.zeros_like(q), q.clone(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        scratch = torch.full((1 << 20,), 7.0, device="cuda")
+        ds.ds_rows_prefix_attn(rows, prefix, q, sinks, 0, SCALE, out, cache)
+        more = scratch * 2  # may take the workspace's place, behind the call
+        total = more.sum()
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want) and total.item() == 14.0 * (1 << 20)
+        q.copy_(torch.randn_like(q))
+        graph.replay()
+        check(out, q, held, sinks)
+        q.copy_(kept)
